@@ -10,6 +10,7 @@ CPU fallback: if libw4.so is missing or a CUDA device is absent, calls raise.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import threading
 
@@ -24,6 +25,7 @@ __all__ = [
     "w4_packed_bytes", "w4_scales_bytes", "w4_last_device_status", "w4_wait_probe",
     "w4_status_string", "W4_PATH_AUTO", "W4_PATH_SMALL_M", "W4_PATH_TENSOR", "GROUP",
     "GroupedPlan", "w4_grouped_plan", "w4_gemm_grouped", "w4_gemm_grouped_noalloc",
+    "w4_kv_pages", "w4_kv_append", "w4_attn_decode", "w4_attn_decode_workspace_bytes",
 ]
 
 GROUP = 128
@@ -76,6 +78,36 @@ _SIGNATURES = {
     "w4_grouped_plan_init_affine": (ctypes.c_int, [ctypes.POINTER(_Plan), _vp, _sz, _i32, ctypes.POINTER(_Problem),
                                                    _i32, ctypes.POINTER(_vp)]),
 }
+
+
+class _KvCache(ctypes.Structure):
+    """w4_kv_cache of include/w4.h."""
+    _fields_ = [("k", _vp), ("v", _vp), ("k_scales", _vp), ("v_scales", _vp), ("pages", _i64), ("page_stride", _i64),
+                ("token_stride", _i64), ("head_stride", _i64), ("page_size", _i32), ("kv_heads", _i32),
+                ("head_dim", _i32), ("format", _i32)]
+
+
+class _Rows(ctypes.Structure):
+    """w4_rows of include/w4.h."""
+    _fields_ = [("data", _vp), ("token_stride", _i64), ("head_stride", _i64)]
+
+
+class _Rope(ctypes.Structure):
+    """w4_rope of include/w4.h."""
+    _fields_ = [("positions", _vp), ("axis_stride", _i64), ("cos", _vp), ("sin", _vp), ("rows", _i64),
+                ("rotary", _i32), ("axes", _i32), ("sections", _i32 * 4), ("cycled", _i32), ("paired", _i32)]
+
+
+_SIGNATURES.update({
+    "w4_kv_pages": (ctypes.c_int, [_vp, _vp, _i32, _i32, _vp, _i64, _vp, _vp, _i64, _i32, _i64, _vp, _vp, _vp, _vp,
+                                   _vp, _vp]),
+    "w4_kv_append": (ctypes.c_int, [ctypes.POINTER(_KvCache), ctypes.POINTER(_Rope), _i64, _i32, ctypes.POINTER(_Rows),
+                                    ctypes.POINTER(_Rows), ctypes.POINTER(_Rows), ctypes.POINTER(_Rows), _vp, _vp]),
+    "w4_attn_decode_workspace_bytes": (_sz, [ctypes.POINTER(_KvCache), _i32, _i64, _i32]),
+    "w4_attn_decode": (ctypes.c_int, [ctypes.POINTER(_KvCache), _i32, _i64, _i32, ctypes.POINTER(_Rows),
+                                      ctypes.POINTER(_Rows), _vp, _i64, _i32, _vp, _vp, ctypes.c_float, _i64, _vp, _sz,
+                                      _vp]),
+})
 
 
 class W4Error(RuntimeError):
@@ -447,3 +479,180 @@ def w4_wait_probe(limit_ns: int, arrive: bool, device=None) -> None:
     device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
     with torch.cuda.device(device):
         _check(load().w4_wait_probe(int(limit_ns), int(bool(arrive)), _stream(device)), "w4_wait_probe")
+
+
+def _vector(t: torch.Tensor, name: str, dtype: torch.dtype, n: int, device: torch.device) -> int:
+    """Address of a contiguous CUDA tensor of n values on `device`."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor of {n} values")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    return t.data_ptr()
+
+
+def _strided(t: torch.Tensor, name: str, dtype: torch.dtype, ndim: int, device: torch.device) -> torch.Tensor:
+    """A CUDA tensor with unit stride in its last dimension."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != ndim or (t.shape[-1] > 1 and t.stride(-1) != 1):
+        raise ValueError(f"{name} must be a {ndim}-D tensor with unit stride in its last dimension")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    return t
+
+
+def _rows(t: torch.Tensor, name: str, shape, device: torch.device) -> _Rows:
+    _strided(t, name, torch.bfloat16, 3, device)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    return _Rows(t.data_ptr(), t.stride(0), t.stride(1))
+
+
+def _kv_cache(k_cache, v_cache, k_scales, v_scales, device) -> _KvCache:
+    """The w4_kv_cache of key and value pages [pages, page_size, kv_heads, head_dim]
+    (bf16, or int8 with scales bf16 [pages, kv_heads, page_size])."""
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dtype not in (torch.bfloat16, torch.int8):
+        raise TypeError("k_cache must be a bfloat16 or int8 CUDA tensor")
+    _strided(k_cache, "k_cache", k_cache.dtype, 4, device)
+    _strided(v_cache, "v_cache", k_cache.dtype, 4, device)
+    if k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride():
+        raise ValueError("k_cache and v_cache must have one shape and the same strides")
+    pages, page_size, heads, dim = k_cache.shape
+    q8 = k_cache.dtype == torch.int8
+    if q8:
+        for t, name in ((k_scales, "k_scales"), (v_scales, "v_scales")):
+            _strided(t, name, torch.bfloat16, 3, device)
+            if tuple(t.shape) != (pages, heads, page_size) or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous [pages, kv_heads, page_size] tensor")
+    elif k_scales is not None or v_scales is not None:
+        raise ValueError("a bfloat16 cache has no scales")
+    s0, s1, s2, _ = k_cache.stride()
+    return _KvCache(k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr() if q8 else None,
+                    v_scales.data_ptr() if q8 else None, pages, s0, s1, s2, page_size, heads, dim, 8 if q8 else 16)
+
+
+def w4_kv_pages(lens: torch.Tensor, target: torch.Tensor, block_table: torch.Tensor, free_pages: torch.Tensor,
+                free_range: torch.Tensor, page_size: int, tokens: int, new_lens: torch.Tensor | None = None,
+                starts: torch.Tensor | None = None, slots: torch.Tensor | None = None,
+                positions: torch.Tensor | None = None, free_range_out: torch.Tensor | None = None):
+    """Moves requests from `lens` to `target` tokens (int32 [B]): takes pages from, and gives them back to, the
+    ring free_pages (int32 [pages]; entries free_range[0] to free_range[1], int64 [2]), updates block_table (int32
+    [B, width]) and returns (new_lens int32 [B], starts int32 [B + 1], slots int64 [tokens], positions int32
+    [tokens], free_range_out int64 [2]).  `tokens`: the new tokens of all requests together."""
+    if not isinstance(block_table, torch.Tensor) or not block_table.is_cuda:
+        raise TypeError("block_table must be a CUDA tensor")
+    dev = block_table.device
+    _strided(block_table, "block_table", torch.int32, 2, dev)
+    B, width = block_table.shape
+    if new_lens is None:
+        new_lens = torch.empty(B, dtype=torch.int32, device=dev)
+    if starts is None:
+        starts = torch.empty(B + 1, dtype=torch.int32, device=dev)
+    if slots is None:
+        slots = torch.empty(tokens, dtype=torch.int64, device=dev)
+    if positions is None:
+        positions = torch.empty(tokens, dtype=torch.int32, device=dev)
+    if free_range_out is None:
+        free_range_out = torch.empty(2, dtype=torch.int64, device=dev)
+    pages = free_pages.numel()
+    with torch.cuda.device(dev):
+        _check(load().w4_kv_pages(
+            _vector(lens, "lens", torch.int32, B, dev), _vector(target, "target", torch.int32, B, dev), B, page_size,
+            _vector(free_pages, "free_pages", torch.int32, pages, dev), pages,
+            _vector(free_range, "free_range", torch.int64, 2, dev), block_table.data_ptr(), block_table.stride(0), width,
+            tokens, _vector(new_lens, "new_lens", torch.int32, B, dev), _vector(starts, "starts", torch.int32, B + 1, dev),
+            _vector(slots, "slots", torch.int64, tokens, dev), _vector(positions, "positions", torch.int32, tokens, dev),
+            _vector(free_range_out, "free_range_out", torch.int64, 2, dev), _stream(dev)), "w4_kv_pages")
+    return new_lens, starts, slots, positions, free_range_out
+
+
+def w4_kv_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor | None,
+                 cos: torch.Tensor | None, sin: torch.Tensor | None, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                 slots: torch.Tensor, sections=None, cycled: bool = False, paired: bool = False,
+                 k_scales: torch.Tensor | None = None, v_scales: torch.Tensor | None = None,
+                 q_out: torch.Tensor | None = None) -> torch.Tensor | None:
+    """Rotates q (bf16 [T, q_heads, head_dim]) and k ([T, kv_heads, head_dim]) by the rows of cos and sin (fp32
+    [rows, rotary / 2]) at positions (int32 [T], or [axes, T] with `sections` frequencies per axis) and writes k
+    and v to their slots (int64 [T], −1: none) of the cache.  Returns the rotated queries (q_out; may be q).
+    cos None: no rotation; q None: keys and values only."""
+    if not isinstance(k, torch.Tensor) or not k.is_cuda:
+        raise TypeError("k must be a CUDA tensor")
+    dev = k.device
+    cache = _kv_cache(k_cache, v_cache, k_scales, v_scales, dev)
+    T = k.shape[0]
+    kv_shape = (T, cache.kv_heads, cache.head_dim)
+    rope = _Rope()
+    if cos is not None:
+        _cuda_tensor(cos, "cos", torch.float32, 2)
+        _cuda_tensor(sin, "sin", torch.float32, 2)
+        _strided(positions, "positions", torch.int32, positions.dim(), dev)
+        if sin.shape != cos.shape or cos.device != dev or sin.device != dev:
+            raise ValueError("cos and sin must have one shape, on the device of k")
+        sections = (cos.shape[1],) if sections is None else tuple(sections)
+        if positions.dim() not in (1, 2) or positions.shape[-1] != T or not 1 <= len(sections) <= 4 or \
+                (positions.dim() == 2 and positions.shape[0] != len(sections)):
+            raise ValueError("positions must be [T], or [axes, T] with one section for each of 1 to 4 axes")
+        rope = _Rope(positions.data_ptr(), positions.stride(0) if positions.dim() == 2 else 0, cos.data_ptr(),
+                     sin.data_ptr(), cos.shape[0], 2 * cos.shape[1], len(sections), (_i32 * 4)(*sections), int(cycled),
+                     int(paired))
+    rows_q = rows_out = None
+    q_heads = 0
+    if q is not None:
+        _strided(q, "q", torch.bfloat16, 3, dev)
+        q_heads = q.shape[1]
+        shape = (T, q_heads, cache.head_dim)
+        if q_out is None:
+            q_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        rows_q, rows_out = _rows(q, "q", shape, dev), _rows(q_out, "q_out", shape, dev)
+    with torch.cuda.device(dev):
+        _check(load().w4_kv_append(cache, rope, T, q_heads, rows_q, rows_out, _rows(k, "k", kv_shape, dev),
+                                   _rows(v, "v", kv_shape, dev), _vector(slots, "slots", torch.int64, T, dev),
+                                   _stream(dev)), "w4_kv_append")
+    return q_out
+
+
+def w4_attn_decode_workspace_bytes(q: torch.Tensor, k_cache: torch.Tensor, requests: int) -> int:
+    """Bytes of workspace of w4_attn_decode for these queries, cache pages and number of requests."""
+    cache = _KvCache(kv_heads=k_cache.shape[2], head_dim=k_cache.shape[3])
+    return load().w4_attn_decode_workspace_bytes(cache, requests, q.shape[0], q.shape[1])
+
+
+def w4_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
+                   lens: torch.Tensor, starts: torch.Tensor | None = None, k_scales: torch.Tensor | None = None,
+                   v_scales: torch.Tensor | None = None, scale: float | None = None, window: int = 0,
+                   out: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """Attention of the newest tokens q (bf16 [T, q_heads, head_dim]) of each request over its pages (block_table
+    int32 [B, width]; lens int32 [B], the new tokens counted) -> bf16 like q.  Rows starts[b] to starts[b + 1] − 1
+    (int32 [B + 1]) are request b's; without starts, T / B each.  scale: 1/√head_dim by default; window: tokens
+    each row sees, its own counted (0: all); out may be q."""
+    if not isinstance(q, torch.Tensor) or not q.is_cuda:
+        raise TypeError("q must be a CUDA tensor")
+    dev = q.device
+    cache = _kv_cache(k_cache, v_cache, k_scales, v_scales, dev)
+    _strided(q, "q", torch.bfloat16, 3, dev)
+    _strided(block_table, "block_table", torch.int32, 2, dev)
+    T, q_heads, dim = q.shape
+    B, width = block_table.shape
+    shape = (T, q_heads, cache.head_dim)
+    if out is None:
+        out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    rows_q, rows_out = _rows(q, "q", shape, dev), _rows(out, "out", shape, dev)
+    if scale is None:
+        scale = 1.0 / math.sqrt(dim)
+    with torch.cuda.device(dev):
+        if workspace is None:
+            workspace = torch.empty(load().w4_attn_decode_workspace_bytes(cache, B, T, q_heads), dtype=torch.uint8,
+                                    device=dev)
+        _check(load().w4_attn_decode(
+            cache, B, T, q_heads, rows_q, rows_out, block_table.data_ptr(), block_table.stride(0), width,
+            _vector(lens, "lens", torch.int32, B, dev),
+            None if starts is None else _vector(starts, "starts", torch.int32, B + 1, dev), scale, window,
+            _vector(workspace, "workspace", torch.uint8, workspace.numel(), dev), workspace.numel(), _stream(dev)),
+            "w4_attn_decode")
+    return out

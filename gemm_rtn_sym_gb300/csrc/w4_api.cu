@@ -11,6 +11,7 @@
 #include "w4.h"
 #include "w4_device.cuh"
 #include "w4_internal.h"
+#include "w4_kv.h"
 
 namespace w4 {
 namespace {
@@ -520,6 +521,267 @@ int w4_gemm_grouped_noalloc(int32_t count, const w4_gemm_problem* problems, void
         return W4_ERR_CUDA;
     p.device_plan = mem;
     return w4_gemm_grouped(&p, stream);
+}
+
+namespace {
+
+// Memory of strided rows: `bytes` in all; where period > 0, rows of `inner`
+// bytes (at most period) that repeat every `period` bytes.
+struct Region {
+    const void* p = nullptr;
+    size_t bytes = 0, period = 0, inner = 0;
+};
+
+Region plain(const void* p, size_t bytes) { return {p, p ? bytes : 0, 0, 0}; }
+
+// Whether two regions share a byte.  Regions of one period (slices of a fused
+// projection's output, keys and values side by side in one page) may interleave.
+bool meets(const Region& a, const Region& b) {
+    if (!overlaps(a.p, a.bytes, b.p, b.bytes)) return false;
+    if (a.period == 0 || a.period != b.period) return true;
+    const size_t T = a.period;
+    const size_t at = (reinterpret_cast<uintptr_t>(b.p) % T + T - reinterpret_cast<uintptr_t>(a.p) % T) % T;
+    return at < a.inner || at + b.inner > T;
+}
+
+struct Dim {
+    int64_t n, stride;
+};
+
+// The region of rows of `row` elements of `size` bytes over `count` (≤ 3)
+// dimensions, in any order of the strides.  W4_ERR_INVALID_ARG where two
+// places share memory or sizes overflow, W4_ERR_MISALIGNED where a row would
+// not start on 16 bytes.
+int strided(const void* p, Dim* dims, int count, int64_t row, int64_t size, Region* out) {
+    std::sort(dims, dims + count, [](const Dim& a, const Dim& b) { return a.stride < b.stride; });
+    int64_t extent = row, inner = 0, period = 0;
+    for (int i = 0; i < count; ++i) {
+        const Dim& d = dims[i];
+        if (d.n <= 1) continue;
+        if (d.stride < extent || d.stride > ((int64_t{1} << 59) - extent) / (d.n - 1)) return W4_ERR_INVALID_ARG;
+        if (d.stride * size % 16 != 0) return W4_ERR_MISALIGNED;
+        inner = extent;
+        period = d.stride;
+        extent += (d.n - 1) * d.stride;
+    }
+    if (!aligned(p, 16)) return W4_ERR_MISALIGNED;
+    *out = {p, static_cast<size_t>(extent * size), static_cast<size_t>(period * size), static_cast<size_t>(inner * size)};
+    return W4_OK;
+}
+
+int rows_region(const w4_rows* r, int64_t T, int32_t heads, int32_t head_dim, Region* out) {
+    if (!r || !r->data) return W4_ERR_INVALID_ARG;
+    Dim dims[2] = {{T, r->token_stride}, {heads, r->head_stride}};
+    return strided(r->data, dims, 2, head_dim, 2, out);
+}
+
+// k, v, k_scales, v_scales of a cache; the scales' regions are empty for format 16.
+int cache_regions(const w4_kv_cache* c, Region (&out)[4]) {
+    if (!c || c->pages < 1 || c->page_size < 1 || c->kv_heads < 1 || c->head_dim < 1) return W4_ERR_INVALID_ARG;
+    if (c->head_dim % 16 != 0 || c->head_dim > 256 || (c->format != 16 && c->format != 8)) return W4_ERR_UNSUPPORTED;
+    // Page ids are 32-bit; (pages · kv_heads · page_size) scales and every slot fit 62 bits.
+    if (c->pages > INT32_MAX || c->pages * c->page_size > (int64_t{1} << 61) / c->kv_heads) return W4_ERR_UNSUPPORTED;
+    const bool q8 = c->format == 8;
+    if (!c->k || !c->v || (q8 && (!c->k_scales || !c->v_scales))) return W4_ERR_INVALID_ARG;
+    for (int i = 0; i < 2; ++i) {
+        Dim dims[3] = {{c->pages, c->page_stride}, {c->page_size, c->token_stride}, {c->kv_heads, c->head_stride}};
+        if (const int s = strided(i ? c->v : c->k, dims, 3, c->head_dim, q8 ? 1 : 2, &out[i])) return s;
+    }
+    const size_t sb = q8 ? static_cast<size_t>(c->pages * c->page_size * c->kv_heads) * 2 : 0;
+    if (q8 && (!aligned(c->k_scales, 2) || !aligned(c->v_scales, 2))) return W4_ERR_MISALIGNED;
+    out[2] = plain(q8 ? c->k_scales : nullptr, sb);
+    out[3] = plain(q8 ? c->v_scales : nullptr, sb);
+    return W4_OK;
+}
+
+// Whether any output meets another or an input; `twin` (or −1) is the input
+// that output 0 may be.
+bool any_meet(const Region* outs, int n_out, const Region* ins, int n_in, int twin = -1) {
+    for (int i = 0; i < n_out; ++i) {
+        for (int j = i + 1; j < n_out; ++j)
+            if (meets(outs[i], outs[j])) return true;
+        for (int j = 0; j < n_in; ++j)
+            if (!(i == 0 && j == twin) && meets(outs[i], ins[j])) return true;
+    }
+    return false;
+}
+
+bool same_rows(const w4_rows* a, const w4_rows* b) {
+    return a->data == b->data && a->token_stride == b->token_stride && a->head_stride == b->head_stride;
+}
+
+Rows to_rows(const w4_rows* r) { return {static_cast<__nv_bfloat16*>(r->data), r->token_stride, r->head_stride}; }
+
+int usable_device(const DeviceInfo** dev) {
+    cudaError_t err;
+    *dev = device_info(&err);
+    if (!*dev) return W4_ERR_CUDA;
+    return (*dev)->cc_major < 10 ? W4_ERR_UNSUPPORTED : W4_OK;
+}
+
+}  // namespace
+
+int w4_kv_pages(const int32_t* lens, const int32_t* target, int32_t B, int32_t page_size, int32_t* free_pages,
+                int64_t pages, const int64_t* free_range, int32_t* block_table, int64_t table_stride, int32_t width,
+                int64_t T, int32_t* new_lens, int32_t* starts, int64_t* slots, int32_t* positions,
+                int64_t* free_range_out, void* stream) {
+    if (B < 0 || T < 0 || page_size < 1 || pages < 1 || width < 1) return W4_ERR_INVALID_ARG;
+    if (T > INT32_MAX || pages > INT32_MAX) return W4_ERR_UNSUPPORTED;
+    if (!free_pages || !free_range || !starts || !free_range_out) return W4_ERR_INVALID_ARG;
+    if (B > 0 && (!lens || !target || !block_table || !new_lens)) return W4_ERR_INVALID_ARG;
+    if (T > 0 && (!slots || !positions)) return W4_ERR_INVALID_ARG;
+    if (B > 1 && (table_stride < width || table_stride > (int64_t{1} << 59) / B)) return W4_ERR_INVALID_ARG;
+    const void* fours[] = {lens, target, free_pages, block_table, new_lens, starts, positions};
+    const void* eights[] = {free_range, slots, free_range_out};
+    for (const void* p : fours)
+        if (!aligned(p, 4)) return W4_ERR_MISALIGNED;
+    for (const void* p : eights)
+        if (!aligned(p, 8)) return W4_ERR_MISALIGNED;
+    const size_t b4 = static_cast<size_t>(B) * 4, t4 = static_cast<size_t>(T) * 4;
+    const size_t table_bytes = B > 0 ? (static_cast<size_t>(B - 1) * static_cast<size_t>(B > 1 ? table_stride : 0) + width) * 4 : 0;
+    const Region outs[] = {plain(block_table, table_bytes), plain(free_pages, static_cast<size_t>(pages) * 4),
+                           plain(new_lens, b4), plain(starts, b4 + 4), plain(slots, 2 * t4), plain(positions, t4),
+                           plain(free_range_out, 16)};
+    const Region ins[] = {plain(lens, b4), plain(target, b4), plain(free_range, 16)};
+    if (any_meet(outs, 7, ins, 3)) return W4_ERR_INVALID_ARG;
+    const DeviceInfo* dev;
+    if (const int s = usable_device(&dev)) return s;
+    const KvPagesArgs a = {lens, target, B, page_size, free_pages, pages, free_range, block_table, table_stride, width,
+                           T, new_lens, starts, slots, positions, free_range_out, dev->status};
+    return to_status(launch_kv_pages(a, *dev, static_cast<cudaStream_t>(stream)));
+}
+
+int w4_kv_append(const w4_kv_cache* cache, const w4_rope* rope, int64_t T, int32_t q_heads, const w4_rows* q,
+                 const w4_rows* q_out, const w4_rows* k, const w4_rows* v, const int64_t* slots, void* stream) {
+    if (T < 0 || q_heads < 0 || !rope) return W4_ERR_INVALID_ARG;
+    Region outs[5], ins[7];
+    if (const int s = cache_regions(cache, *reinterpret_cast<Region(*)[4]>(&outs[1]))) return s;
+    if (T > INT32_MAX || q_heads > 65536 || cache->kv_heads > 65536) return W4_ERR_UNSUPPORTED;
+    const w4_rope& r = *rope;
+    if (r.rotary < 0 || r.rotary > cache->head_dim) return W4_ERR_INVALID_ARG;
+    if (r.rotary % 16 != 0) return W4_ERR_UNSUPPORTED;
+    if (r.rotary > 0) {
+        if (r.axes < 1 || r.axes > 4) return W4_ERR_UNSUPPORTED;
+        int64_t sum = 0;
+        for (int i = 0; i < r.axes; ++i) {
+            if (r.sections[i] < 0) return W4_ERR_INVALID_ARG;
+            sum += r.sections[i];
+        }
+        if (sum != r.rotary / 2 || r.rows < 1 || r.rows > INT32_MAX || r.axis_stride < 0 ||
+            (r.axis_stride > 0 && r.axis_stride < T) || r.axis_stride > (int64_t{1} << 59))
+            return W4_ERR_INVALID_ARG;
+    }
+    if (T == 0) return W4_OK;
+    if (!slots || (r.rotary > 0 && (!r.positions || !r.cos || !r.sin))) return W4_ERR_INVALID_ARG;
+    if (!aligned(slots, 8)) return W4_ERR_MISALIGNED;
+    if (r.rotary > 0 && (!aligned(r.positions, 4) || !aligned(r.cos, 16) || !aligned(r.sin, 16)))
+        return W4_ERR_MISALIGNED;
+    const int32_t H = cache->kv_heads, d = cache->head_dim;
+    if (const int s = rows_region(k, T, H, d, &ins[0])) return s;
+    if (const int s = rows_region(v, T, H, d, &ins[1])) return s;
+    ins[2] = plain(slots, static_cast<size_t>(T) * 8);
+    const size_t table = r.rotary > 0 ? static_cast<size_t>(r.rows) * (r.rotary / 2) * 4 : 0;
+    ins[3] = plain(r.positions, r.rotary > 0 ? static_cast<size_t>((r.axes - 1) * r.axis_stride + T) * 4 : 0);
+    ins[4] = plain(r.cos, table);
+    ins[5] = plain(r.sin, table);
+    if (q_heads > 0) {
+        if (const int s = rows_region(q, T, q_heads, d, &ins[6])) return s;
+        if (const int s = rows_region(q_out, T, q_heads, d, &outs[0])) return s;
+    }
+    if (any_meet(outs, 5, ins, 7, q_heads > 0 && same_rows(q, q_out) ? 6 : -1)) return W4_ERR_INVALID_ARG;
+    const DeviceInfo* dev;
+    if (const int s = usable_device(&dev)) return s;
+    KvAppendArgs a = {};
+    if (q_heads > 0) {
+        a.q = to_rows(q);
+        a.q_out = to_rows(q_out);
+    }
+    a.k = to_rows(k);
+    a.v = to_rows(v);
+    a.q_heads = q_heads;
+    a.kv_heads = H;
+    a.head_dim = d;
+    a.T = T;
+    a.positions = r.positions;
+    a.axis_stride = r.axis_stride;
+    a.cos = r.cos;
+    a.sin = r.sin;
+    a.rows = r.rows;
+    a.rotary = r.rotary;
+    a.paired = r.paired != 0;
+    a.k_cache = cache->k;
+    a.v_cache = cache->v;
+    a.k_scales = static_cast<__nv_bfloat16*>(cache->k_scales);
+    a.v_scales = static_cast<__nv_bfloat16*>(cache->v_scales);
+    a.pages = cache->pages;
+    a.page_stride = cache->page_stride;
+    a.cache_token_stride = cache->token_stride;
+    a.cache_head_stride = cache->head_stride;
+    a.page_size = cache->page_size;
+    a.slots = slots;
+    a.status = dev->status;
+    return to_status(launch_kv_append(a, r.sections, r.axes, r.cycled != 0, cache->format == 8, *dev,
+                                      static_cast<cudaStream_t>(stream)));
+}
+
+size_t w4_attn_decode_workspace_bytes(const w4_kv_cache* cache, int32_t B, int64_t T, int32_t q_heads) {
+    if (!cache || B < 0 || T < 0 || q_heads < 1 || cache->kv_heads < 1 || cache->head_dim < 1 ||
+        cache->head_dim > 256 || cache->head_dim % 16 != 0 || q_heads % cache->kv_heads != 0)
+        return 0;
+    return attn_decode_workspace_bytes(B, T, q_heads, cache->kv_heads, cache->head_dim);
+}
+
+int w4_attn_decode(const w4_kv_cache* cache, int32_t B, int64_t T, int32_t q_heads, const w4_rows* q,
+                   const w4_rows* out, const int32_t* block_table, int64_t table_stride, int32_t width,
+                   const int32_t* lens, const int32_t* starts, float scale, int64_t window, void* workspace,
+                   size_t workspace_bytes, void* stream) {
+    if (B < 0 || T < 0 || q_heads < 1 || width < 1 || window < 0 || !(scale - scale == 0.f)) return W4_ERR_INVALID_ARG;
+    Region outs[2], ins[8];
+    if (const int s = cache_regions(cache, *reinterpret_cast<Region(*)[4]>(&ins[1]))) return s;
+    if (q_heads % cache->kv_heads != 0) return W4_ERR_INVALID_ARG;
+    if (q_heads > 65536 || T > INT32_MAX / q_heads) return W4_ERR_UNSUPPORTED;
+    if (B > 0 && !starts && T % B != 0) return W4_ERR_INVALID_ARG;
+    if (B == 0 || T == 0) return W4_OK;
+    if (!block_table || !lens || !workspace) return W4_ERR_INVALID_ARG;
+    if (B > 1 && (table_stride < width || table_stride > (int64_t{1} << 59) / B)) return W4_ERR_INVALID_ARG;
+    if (!aligned(block_table, 4) || !aligned(lens, 4) || !aligned(starts, 4) || !aligned(workspace, 256))
+        return W4_ERR_MISALIGNED;
+    if (workspace_bytes < w4_attn_decode_workspace_bytes(cache, B, T, q_heads)) return W4_ERR_INVALID_ARG;
+    if (const int s = rows_region(q, T, q_heads, cache->head_dim, &ins[0])) return s;
+    if (const int s = rows_region(out, T, q_heads, cache->head_dim, &outs[0])) return s;
+    outs[1] = plain(workspace, workspace_bytes);
+    ins[5] = plain(block_table, (static_cast<size_t>(B - 1) * static_cast<size_t>(B > 1 ? table_stride : 0) + width) * 4);
+    ins[6] = plain(lens, static_cast<size_t>(B) * 4);
+    ins[7] = plain(starts, static_cast<size_t>(B) * 4 + 4);
+    if (any_meet(outs, 2, ins, 8, same_rows(q, out) ? 0 : -1)) return W4_ERR_INVALID_ARG;
+    const DeviceInfo* dev;
+    if (const int s = usable_device(&dev)) return s;
+    AttnArgs a = {};
+    a.q = to_rows(q);
+    a.out = to_rows(out);
+    a.B = B;
+    a.T = T;
+    a.q_heads = q_heads;
+    a.kv_heads = cache->kv_heads;
+    a.head_dim = cache->head_dim;
+    a.k = cache->k;
+    a.v = cache->v;
+    a.k_scales = static_cast<const __nv_bfloat16*>(cache->k_scales);
+    a.v_scales = static_cast<const __nv_bfloat16*>(cache->v_scales);
+    a.pages = cache->pages;
+    a.page_stride = cache->page_stride;
+    a.token_stride = cache->token_stride;
+    a.head_stride = cache->head_stride;
+    a.page_size = cache->page_size;
+    a.table = block_table;
+    a.table_stride = table_stride;
+    a.width = width;
+    a.lens = lens;
+    a.starts = starts;
+    a.scale = scale;
+    a.window = window;
+    a.status = dev->status;
+    return to_status(launch_attn_decode(a, cache->format == 8, workspace, *dev, static_cast<cudaStream_t>(stream)));
 }
 
 int w4_last_device_status(void* stream) {

@@ -9,6 +9,7 @@ namespace w4 {
 
 // Mirrors w4_status in include/w4.h.
 constexpr unsigned kStatusOk = 0;
+constexpr unsigned kStatusInvalid = 1;
 constexpr unsigned kStatusTimeout = 5;
 
 // Default bound of every wait inside the library's kernels: about a second.

@@ -368,6 +368,168 @@ int w4_gemm_grouped(const w4_grouped_plan* plan, void* stream);
 int w4_gemm_grouped_noalloc(int32_t count, const w4_gemm_problem* problems, void* stream);
 
 /*
+ * Paged key-value cache — what a decode or a speculative-verify step of an
+ * attention layer runs between its 4-bit projections: block tables and slots
+ * from request lengths (w4_kv_pages), rotary positions and the new tokens'
+ * keys and values into the cache (w4_kv_append), attention of the newest
+ * tokens over it (w4_attn_decode).
+ *
+ * The cache is a pool of pages of page_size tokens.  A request's token at
+ * position p lies in page block_table[request][p / page_size], at place
+ * p % page_size; its slot is page · page_size + place.  The row of (page,
+ * place, head) starts at page · page_stride + place · token_stride + head ·
+ * head_stride elements from k (and v), so both [pages, page_size, kv_heads,
+ * head_dim] and [pages, kv_heads, page_size, head_dim] memory serve.
+ *   format 16: bf16 rows.
+ *   format 8 : int8 codes c and one bf16 scale d per row, [pages, kv_heads,
+ *              page_size]; the row stands for d·c.
+ * head_dim: a multiple of 16, at most 256.  k and v 16-byte aligned, strides
+ * multiples of 16 bytes, rows apart from each other; scales 2-byte aligned.
+ *
+ * Numbers that the kernels read from device memory (lengths, positions, page
+ * ids, slots) are checked there: one out of range records W4_ERR_INVALID_ARG
+ * in the status word (w4_last_device_status), and nothing out of bounds is
+ * read or written; what is done with it instead is said at each call.
+ */
+typedef struct w4_kv_cache {
+    void* k;
+    void* v;
+    void* k_scales;       /* format 8 only */
+    void* v_scales;
+    int64_t pages;
+    int64_t page_stride;  /* in elements, for k and v alike */
+    int64_t token_stride;
+    int64_t head_stride;
+    int32_t page_size;
+    int32_t kv_heads;
+    int32_t head_dim;
+    int32_t format;       /* 16: bf16, 8: int8 codes with scales */
+} w4_kv_cache;
+
+/* bf16 [tokens, heads, head_dim] with strides in elements (multiples of 8) and
+ * unit stride inside a row; 16-byte aligned.  Slices of a fused qkv
+ * projection's output are such rows. */
+typedef struct w4_rows {
+    void* data;
+    int64_t token_stride;
+    int64_t head_stride;
+} w4_rows;
+
+/*
+ * w4_kv_pages — moves every request from its present length to a target and
+ * says where its new tokens go.  A target above the length appends tokens; one
+ * below it drops the last ones (rejected drafts); 0 ends the request.
+ *   lens, target   in : int32 [B]
+ *   free_pages     in/out: int32 [pages], a ring of free page ids: entry
+ *                       i mod pages for i in [free_range[0], free_range[1])
+ *   free_range     in : int64 [2], counters that only grow
+ *   block_table    in/out: int32 [B, width], row stride table_stride
+ *   T              in : rows of slots and positions (all requests' new tokens)
+ *   new_lens       out: int32 [B]
+ *   starts         out: int32 [B + 1], a request's first row among the tokens
+ *   slots          out: int64 [T], −1: no slot (not granted, or past the last
+ *                       new token)
+ *   positions      out: int32 [T] (0 past the last new token)
+ *   free_range_out out: int64 [2]
+ * With have = ⌈len / page_size⌉ and want = ⌈target / page_size⌉, request b
+ * takes need = max(want − have, 0) pages from the head of the ring, in request
+ * order, and gives back max(have − want, 0) at its tail; those are free from
+ * the next call on.  A request whose target does not fit `width` pages is not
+ * granted and asks for none; one whose pages, with those asked by the requests
+ * before it, exceed the free ones is not granted.  A request that is not
+ * granted keeps its length, pages and table; its new tokens keep their rows
+ * in starts and positions, with slots of −1.
+ * Out of range: a negative length or target, or a length past the table, leaves
+ * the request as it is, with no new tokens; a request with new tokens past row
+ * T is not granted; a page id outside [0, pages) gives slots of −1.
+ * Deterministic; one launch.  lens, target and free_range must not overlap an
+ * output (calls in a row alternate between two sets).  B = 0 with T = 0 is a
+ * no-op apart from starts and free_range_out.
+ */
+int w4_kv_pages(const int32_t* lens, const int32_t* target, int32_t B, int32_t page_size, int32_t* free_pages,
+                int64_t pages, const int64_t* free_range, int32_t* block_table, int64_t table_stride, int32_t width,
+                int64_t T, int32_t* new_lens, int32_t* starts, int64_t* slots, int32_t* positions,
+                int64_t* free_range_out, void* stream);
+
+/*
+ * Rotary positions with several axes (time, height, width, ...): frequency i
+ * of a token turns by the table row of its position on axis(i).
+ *   positions  int32 [axes, T], axis_stride elements apart (0: one position
+ *              for every axis)
+ *   cos, sin   fp32 [rows, rotary / 2], 16-byte aligned
+ *   rotary     values of a row that turn, from its start: a multiple of 16,
+ *              at most head_dim; 0: none (the other members are then unused)
+ *   sections   frequencies of each axis, 1 to 4 axes, rotary / 2 in all
+ *   cycled     0: the axes' frequencies in blocks, one after another; 1: the
+ *              axes in turn (0, 1, 2, 0, 1, 2, ...), leaving out an axis whose
+ *              frequencies are used up
+ *   paired     0: value i turns with value i + rotary / 2; 1: 2i with 2i + 1
+ * (a, b) becomes (a·cos − b·sin, b·cos + a·sin): fp32 products, then an fp32
+ * difference or sum, rounded once to bf16.
+ */
+typedef struct w4_rope {
+    const int32_t* positions;
+    int64_t axis_stride;
+    const float* cos;
+    const float* sin;
+    int64_t rows;
+    int32_t rotary;
+    int32_t axes;
+    int32_t sections[4];
+    int32_t cycled;
+    int32_t paired;
+} w4_rope;
+
+/*
+ * w4_kv_append — rotates the queries and keys of T new tokens and writes the
+ * keys and values to the cache.
+ *   q, q_out  in/out: [T, q_heads, head_dim]; q_out may be q (in place); both
+ *                  NULL with q_heads = 0
+ *   k, v      in : [T, kv_heads, head_dim]
+ *   slots     in : int64 [T] from w4_kv_pages; a token with slot −1 is not
+ *                  stored, its queries are still turned
+ * Format 8 stores each row by the RTN rule of the weights at 8 bits:
+ * d = bf16_rne(fp32(max|x| / 127)) over the (rotated, bf16) row, c =
+ * clamp(round_half_even(fp32(x / d)), −128, 127), c = 0 where d = 0; a row
+ * with an infinity or NaN is stored as c = 0 with d = NaN.
+ * Two tokens with one slot leave either's row, not a defined one.  Out of
+ * range: a slot outside [−1, pages · page_size) is not stored; a position
+ * outside [0, rows) turns as position 0.
+ */
+int w4_kv_append(const w4_kv_cache* cache, const w4_rope* rope, int64_t T, int32_t q_heads, const w4_rows* q,
+                 const w4_rows* q_out, const w4_rows* k, const w4_rows* v, const int64_t* slots, void* stream);
+
+/*
+ * w4_attn_decode — attention of the newest tokens of B requests over their
+ * pages: one row per request in decode, K+1 in a verify pass.
+ *   q, out       [T, q_heads, head_dim]; q_heads a multiple of kv_heads, query
+ *                head h reading key-value head h / (q_heads / kv_heads)
+ *   block_table  int32 [B, width], row stride table_stride
+ *   lens         int32 [B], tokens in the cache with the new ones
+ *   starts       int32 [B + 1], first row of each request, rows
+ *                starts[b] .. starts[b+1] − 1; NULL: T / B rows each
+ *   scale        factor of the scores (1 / √head_dim for the usual rule)
+ *   window       0: every token up to the row's own; else the row's own and
+ *                the window − 1 before it
+ * Row j of a request with n rows and length L stands at position p = L − n + j
+ * and sees the tokens t with max(0, p − window + 1) ≤ t ≤ p:
+ *   out = Σ_t softmax_t(scale · q·k_t) · v_t,
+ * scores, maxima, sums and products in fp32, rounded once to bf16.  A row that
+ * sees no token (p < 0) is zeros.  What the masked and unused places of the
+ * cache hold, NaN and infinities included, changes nothing.  Rows past
+ * starts[B] are not written.
+ * Out of range: a length past width · page_size counts as that; starts that
+ * fall or pass T are cut; a page id outside [0, pages) reads as rows of zeros.
+ * workspace: w4_attn_decode_workspace_bytes(...) bytes, 256-byte aligned,
+ * contents unspecified before and after.  Deterministic.  out may be q.
+ */
+size_t w4_attn_decode_workspace_bytes(const w4_kv_cache* cache, int32_t B, int64_t T, int32_t q_heads);
+int w4_attn_decode(const w4_kv_cache* cache, int32_t B, int64_t T, int32_t q_heads, const w4_rows* q,
+                   const w4_rows* out, const int32_t* block_table, int64_t table_stride, int32_t width,
+                   const int32_t* lens, const int32_t* starts, float scale, int64_t window, void* workspace,
+                   size_t workspace_bytes, void* stream);
+
+/*
  * Every wait inside the library's kernels (mbarrier phases, TMA completion)
  * is bounded.  A wait that runs out records W4_ERR_TIMEOUT in a per-device
  * status word and the kernel returns early (its outputs are then undefined).
