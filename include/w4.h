@@ -518,7 +518,7 @@ int w4_kv_append(const w4_kv_cache* cache, const w4_rope* rope, int64_t T, int32
  * sees no token (p < 0) is zeros.  What the masked and unused places of the
  * cache hold, NaN and infinities included, changes nothing.  Rows past
  * starts[B] are not written.
- * Out of range: a length past width · page_size counts as that; starts that
+ * Out of range: a length past width · page_size (or 2³¹ − 2¹⁶) counts as that; starts that
  * fall or pass T are cut; a page id outside [0, pages) reads as rows of zeros.
  * workspace: w4_attn_decode_workspace_bytes(...) bytes, 256-byte aligned,
  * contents unspecified before and after.  Deterministic.  out may be q.
