@@ -10,7 +10,6 @@ CPU fallback: if libw4.so is missing or a CUDA device is absent, calls raise.
 from __future__ import annotations
 
 import ctypes
-import math
 import os
 import threading
 
@@ -481,60 +480,81 @@ def w4_wait_probe(limit_ns: int, arrive: bool, device=None) -> None:
         _check(load().w4_wait_probe(int(limit_ns), int(bool(arrive)), _stream(device)), "w4_wait_probe")
 
 
-def _vector(t: torch.Tensor, name: str, dtype: torch.dtype, n: int, device: torch.device) -> int:
-    """Address of a contiguous CUDA tensor of n values on `device`."""
+# The cache's calls come many to a step and their kernels last microseconds: their checks take each tensor's type, device
+# (one integer) and strides once, and the device is switched only where it is another.
+def _device_index(t: torch.Tensor, name: str) -> int:
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
+    return t.get_device()
+
+
+def _typed(t: torch.Tensor, name: str, dtype: torch.dtype, index: int) -> None:
+    if not isinstance(t, torch.Tensor) or t.get_device() < 0:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index}")
+
+
+def _vector(t: torch.Tensor, name: str, dtype: torch.dtype, n: int, index: int) -> int:
+    """Address of a contiguous tensor of n values."""
+    _typed(t, name, dtype, index)
+    if t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous tensor of {n} values")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}")
     return t.data_ptr()
 
 
-def _strided(t: torch.Tensor, name: str, dtype: torch.dtype, ndim: int, device: torch.device) -> torch.Tensor:
-    """A CUDA tensor with unit stride in its last dimension."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != ndim or (t.shape[-1] > 1 and t.stride(-1) != 1):
+def _strides(t: torch.Tensor, name: str, dtype: torch.dtype, ndim: int, index: int):
+    """Strides of a tensor with unit stride in its last dimension."""
+    _typed(t, name, dtype, index)
+    strides = t.stride()
+    if len(strides) != ndim or (strides[-1] != 1 and t.shape[-1] > 1):
         raise ValueError(f"{name} must be a {ndim}-D tensor with unit stride in its last dimension")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}")
-    return t
+    return strides
 
 
-def _rows(t: torch.Tensor, name: str, shape, device: torch.device) -> _Rows:
-    _strided(t, name, torch.bfloat16, 3, device)
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
-    return _Rows(t.data_ptr(), t.stride(0), t.stride(1))
+def _rows(t: torch.Tensor, name: str, shape, index: int) -> _Rows:
+    strides = _strides(t, name, torch.bfloat16, 3, index)
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {shape}, got {tuple(t.shape)}")
+    return _Rows(t.data_ptr(), strides[0], strides[1])
 
 
-def _kv_cache(k_cache, v_cache, k_scales, v_scales, device) -> _KvCache:
+def _kv_cache(k_cache, v_cache, k_scales, v_scales, index) -> _KvCache:
     """The w4_kv_cache of key and value pages [pages, page_size, kv_heads, head_dim]
     (bf16, or int8 with scales bf16 [pages, kv_heads, page_size])."""
-    if not isinstance(k_cache, torch.Tensor) or k_cache.dtype not in (torch.bfloat16, torch.int8):
+    dtype = k_cache.dtype if isinstance(k_cache, torch.Tensor) else None
+    if dtype is not torch.bfloat16 and dtype is not torch.int8:
         raise TypeError("k_cache must be a bfloat16 or int8 CUDA tensor")
-    _strided(k_cache, "k_cache", k_cache.dtype, 4, device)
-    _strided(v_cache, "v_cache", k_cache.dtype, 4, device)
-    if k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride():
+    strides = _strides(k_cache, "k_cache", dtype, 4, index)
+    shape = k_cache.shape
+    if _strides(v_cache, "v_cache", dtype, 4, index) != strides or v_cache.shape != shape:
         raise ValueError("k_cache and v_cache must have one shape and the same strides")
-    pages, page_size, heads, dim = k_cache.shape
-    q8 = k_cache.dtype == torch.int8
-    if q8:
+    pages, page_size, heads, dim = shape
+    k_scale = v_scale = None
+    if dtype is torch.int8:
         for t, name in ((k_scales, "k_scales"), (v_scales, "v_scales")):
-            _strided(t, name, torch.bfloat16, 3, device)
-            if tuple(t.shape) != (pages, heads, page_size) or not t.is_contiguous():
+            _typed(t, name, torch.bfloat16, index)
+            if t.shape != (pages, heads, page_size) or not t.is_contiguous():
                 raise ValueError(f"{name} must be a contiguous [pages, kv_heads, page_size] tensor")
+        k_scale, v_scale = k_scales.data_ptr(), v_scales.data_ptr()
     elif k_scales is not None or v_scales is not None:
         raise ValueError("a bfloat16 cache has no scales")
-    s0, s1, s2, _ = k_cache.stride()
-    return _KvCache(k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr() if q8 else None,
-                    v_scales.data_ptr() if q8 else None, pages, s0, s1, s2, page_size, heads, dim, 8 if q8 else 16)
+    return _KvCache(k_cache.data_ptr(), v_cache.data_ptr(), k_scale, v_scale, pages, strides[0], strides[1], strides[2],
+                    page_size, heads, dim, 16 if k_scale is None else 8)
+
+
+def _call(name: str, index: int, *args) -> None:
+    """Runs a library function on the current stream of the device."""
+    fn = getattr(_lib or load(), name)
+    if torch.cuda.current_device() == index:
+        status = fn(*args, torch.cuda.current_stream().cuda_stream)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, torch.cuda.current_stream().cuda_stream)
+    if status != W4_OK:
+        raise W4Error(status, name)
 
 
 def w4_kv_pages(lens: torch.Tensor, target: torch.Tensor, block_table: torch.Tensor, free_pages: torch.Tensor,
@@ -545,30 +565,23 @@ def w4_kv_pages(lens: torch.Tensor, target: torch.Tensor, block_table: torch.Ten
     ring free_pages (int32 [pages]; entries free_range[0] to free_range[1], int64 [2]), updates block_table (int32
     [B, width]) and returns (new_lens int32 [B], starts int32 [B + 1], slots int64 [tokens], positions int32
     [tokens], free_range_out int64 [2]).  `tokens`: the new tokens of all requests together."""
-    if not isinstance(block_table, torch.Tensor) or not block_table.is_cuda:
-        raise TypeError("block_table must be a CUDA tensor")
-    dev = block_table.device
-    _strided(block_table, "block_table", torch.int32, 2, dev)
+    index = _device_index(block_table, "block_table")
+    stride = _strides(block_table, "block_table", torch.int32, 2, index)[0]
     B, width = block_table.shape
-    if new_lens is None:
-        new_lens = torch.empty(B, dtype=torch.int32, device=dev)
-    if starts is None:
-        starts = torch.empty(B + 1, dtype=torch.int32, device=dev)
-    if slots is None:
-        slots = torch.empty(tokens, dtype=torch.int64, device=dev)
-    if positions is None:
-        positions = torch.empty(tokens, dtype=torch.int32, device=dev)
-    if free_range_out is None:
-        free_range_out = torch.empty(2, dtype=torch.int64, device=dev)
+    dev = block_table.device
+    i32, i64 = torch.int32, torch.int64
+    new_lens = torch.empty(B, dtype=i32, device=dev) if new_lens is None else new_lens
+    starts = torch.empty(B + 1, dtype=i32, device=dev) if starts is None else starts
+    slots = torch.empty(tokens, dtype=i64, device=dev) if slots is None else slots
+    positions = torch.empty(tokens, dtype=i32, device=dev) if positions is None else positions
+    free_range_out = torch.empty(2, dtype=i64, device=dev) if free_range_out is None else free_range_out
     pages = free_pages.numel()
-    with torch.cuda.device(dev):
-        _check(load().w4_kv_pages(
-            _vector(lens, "lens", torch.int32, B, dev), _vector(target, "target", torch.int32, B, dev), B, page_size,
-            _vector(free_pages, "free_pages", torch.int32, pages, dev), pages,
-            _vector(free_range, "free_range", torch.int64, 2, dev), block_table.data_ptr(), block_table.stride(0), width,
-            tokens, _vector(new_lens, "new_lens", torch.int32, B, dev), _vector(starts, "starts", torch.int32, B + 1, dev),
-            _vector(slots, "slots", torch.int64, tokens, dev), _vector(positions, "positions", torch.int32, tokens, dev),
-            _vector(free_range_out, "free_range_out", torch.int64, 2, dev), _stream(dev)), "w4_kv_pages")
+    _call("w4_kv_pages", index, _vector(lens, "lens", i32, B, index), _vector(target, "target", i32, B, index), B,
+          page_size, _vector(free_pages, "free_pages", i32, pages, index), pages,
+          _vector(free_range, "free_range", i64, 2, index), block_table.data_ptr(), stride, width, tokens,
+          _vector(new_lens, "new_lens", i32, B, index), _vector(starts, "starts", i32, B + 1, index),
+          _vector(slots, "slots", i64, tokens, index), _vector(positions, "positions", i32, tokens, index),
+          _vector(free_range_out, "free_range_out", i64, 2, index))
     return new_lens, starts, slots, positions, free_range_out
 
 
@@ -581,39 +594,38 @@ def w4_kv_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, posit
     [rows, rotary / 2]) at positions (int32 [T], or [axes, T] with `sections` frequencies per axis) and writes k
     and v to their slots (int64 [T], −1: none) of the cache.  Returns the rotated queries (q_out; may be q).
     cos None: no rotation; q None: keys and values only."""
-    if not isinstance(k, torch.Tensor) or not k.is_cuda:
-        raise TypeError("k must be a CUDA tensor")
-    dev = k.device
-    cache = _kv_cache(k_cache, v_cache, k_scales, v_scales, dev)
+    index = _device_index(k, "k")
+    cache = _kv_cache(k_cache, v_cache, k_scales, v_scales, index)
     T = k.shape[0]
-    kv_shape = (T, cache.kv_heads, cache.head_dim)
-    rope = _Rope()
-    if cos is not None:
-        _cuda_tensor(cos, "cos", torch.float32, 2)
-        _cuda_tensor(sin, "sin", torch.float32, 2)
-        _strided(positions, "positions", torch.int32, positions.dim(), dev)
-        if sin.shape != cos.shape or cos.device != dev or sin.device != dev:
-            raise ValueError("cos and sin must have one shape, on the device of k")
-        sections = (cos.shape[1],) if sections is None else tuple(sections)
-        if positions.dim() not in (1, 2) or positions.shape[-1] != T or not 1 <= len(sections) <= 4 or \
-                (positions.dim() == 2 and positions.shape[0] != len(sections)):
-            raise ValueError("positions must be [T], or [axes, T] with one section for each of 1 to 4 axes")
-        rope = _Rope(positions.data_ptr(), positions.stride(0) if positions.dim() == 2 else 0, cos.data_ptr(),
-                     sin.data_ptr(), cos.shape[0], 2 * cos.shape[1], len(sections), (_i32 * 4)(*sections), int(cycled),
-                     int(paired))
+    dim = cache.head_dim
+    kv_shape = (T, cache.kv_heads, dim)
+    if cos is None:
+        rope = _Rope()
+    else:
+        _typed(cos, "cos", torch.float32, index)
+        _typed(sin, "sin", torch.float32, index)
+        rows = cos.shape
+        if len(rows) != 2 or sin.shape != rows or not cos.is_contiguous() or not sin.is_contiguous():
+            raise ValueError("cos and sin must be contiguous [rows, rotary / 2] tensors of one shape")
+        sections = (rows[1],) if sections is None else tuple(sections)
+        axes = len(sections)
+        _typed(positions, "positions", torch.int32, index)
+        shape, strides = positions.shape, positions.stride()
+        if not 1 <= axes <= 4 or (shape != (axes, T) and shape != (T,)) or (strides[-1] != 1 and T > 1):
+            raise ValueError("positions must be [T], or [axes, T] with one section for each of 1 to 4 axes, with unit "
+                             "stride in the last dimension")
+        rope = _Rope(positions.data_ptr(), strides[0] if len(shape) == 2 else 0, cos.data_ptr(), sin.data_ptr(), rows[0],
+                     2 * rows[1], axes, sections, cycled, paired)
     rows_q = rows_out = None
     q_heads = 0
     if q is not None:
-        _strided(q, "q", torch.bfloat16, 3, dev)
         q_heads = q.shape[1]
-        shape = (T, q_heads, cache.head_dim)
+        shape = (T, q_heads, dim)
         if q_out is None:
-            q_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
-        rows_q, rows_out = _rows(q, "q", shape, dev), _rows(q_out, "q_out", shape, dev)
-    with torch.cuda.device(dev):
-        _check(load().w4_kv_append(cache, rope, T, q_heads, rows_q, rows_out, _rows(k, "k", kv_shape, dev),
-                                   _rows(v, "v", kv_shape, dev), _vector(slots, "slots", torch.int64, T, dev),
-                                   _stream(dev)), "w4_kv_append")
+            q_out = torch.empty(shape, dtype=torch.bfloat16, device=k.device)
+        rows_q, rows_out = _rows(q, "q", shape, index), _rows(q_out, "q_out", shape, index)
+    _call("w4_kv_append", index, cache, rope, T, q_heads, rows_q, rows_out, _rows(k, "k", kv_shape, index),
+          _rows(v, "v", kv_shape, index), _vector(slots, "slots", torch.int64, T, index))
     return q_out
 
 
@@ -631,28 +643,24 @@ def w4_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     int32 [B, width]; lens int32 [B], the new tokens counted) -> bf16 like q.  Rows starts[b] to starts[b + 1] − 1
     (int32 [B + 1]) are request b's; without starts, T / B each.  scale: 1/√head_dim by default; window: tokens
     each row sees, its own counted (0: all); out may be q."""
-    if not isinstance(q, torch.Tensor) or not q.is_cuda:
-        raise TypeError("q must be a CUDA tensor")
-    dev = q.device
-    cache = _kv_cache(k_cache, v_cache, k_scales, v_scales, dev)
-    _strided(q, "q", torch.bfloat16, 3, dev)
-    _strided(block_table, "block_table", torch.int32, 2, dev)
-    T, q_heads, dim = q.shape
+    index = _device_index(q, "q")
+    cache = _kv_cache(k_cache, v_cache, k_scales, v_scales, index)
+    stride = _strides(block_table, "block_table", torch.int32, 2, index)[0]
     B, width = block_table.shape
+    if q.dim() != 3:
+        raise ValueError("q must be a 3-D tensor")
+    T, q_heads, dim = q.shape
     shape = (T, q_heads, cache.head_dim)
     if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
-    rows_q, rows_out = _rows(q, "q", shape, dev), _rows(out, "out", shape, dev)
-    if scale is None:
-        scale = 1.0 / math.sqrt(dim)
-    with torch.cuda.device(dev):
-        if workspace is None:
-            workspace = torch.empty(load().w4_attn_decode_workspace_bytes(cache, B, T, q_heads), dtype=torch.uint8,
-                                    device=dev)
-        _check(load().w4_attn_decode(
-            cache, B, T, q_heads, rows_q, rows_out, block_table.data_ptr(), block_table.stride(0), width,
-            _vector(lens, "lens", torch.int32, B, dev),
-            None if starts is None else _vector(starts, "starts", torch.int32, B + 1, dev), scale, window,
-            _vector(workspace, "workspace", torch.uint8, workspace.numel(), dev), workspace.numel(), _stream(dev)),
-            "w4_attn_decode")
+        out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
+    rows_q, rows_out = _rows(q, "q", shape, index), _rows(out, "out", shape, index)
+    size = (_lib or load()).w4_attn_decode_workspace_bytes(cache, B, T, q_heads)
+    if workspace is None:
+        workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
+    else:
+        size = workspace.numel()
+    _call("w4_attn_decode", index, cache, B, T, q_heads, rows_q, rows_out, block_table.data_ptr(), stride, width,
+          _vector(lens, "lens", torch.int32, B, index),
+          None if starts is None else _vector(starts, "starts", torch.int32, B + 1, index),
+          dim ** -0.5 if scale is None else scale, window, _vector(workspace, "workspace", torch.uint8, size, index), size)
     return out
