@@ -647,7 +647,7 @@ int w4_kv_pages(const int32_t* lens, const int32_t* target, int32_t B, int32_t p
     const DeviceInfo* dev;
     if (const int s = usable_device(&dev)) return s;
     const KvPagesArgs a = {lens, target, B, page_size, free_pages, pages, free_range, block_table, table_stride, width,
-                           T, new_lens, starts, slots, positions, free_range_out, dev->status};
+                           T, new_lens, starts, slots, positions, free_range_out, dev->status, 0, 0};
     return to_status(launch_kv_pages(a, *dev, static_cast<cudaStream_t>(stream)));
 }
 
@@ -708,6 +708,7 @@ int w4_kv_append(const w4_kv_cache* cache, const w4_rope* rope, int64_t T, int32
     a.sin = r.sin;
     a.rows = r.rows;
     a.rotary = r.rotary;
+    a.axes = r.axes;
     a.paired = r.paired != 0;
     a.k_cache = cache->k;
     a.v_cache = cache->v;
@@ -720,7 +721,7 @@ int w4_kv_append(const w4_kv_cache* cache, const w4_rope* rope, int64_t T, int32
     a.page_size = cache->page_size;
     a.slots = slots;
     a.status = dev->status;
-    return to_status(launch_kv_append(a, r.sections, r.axes, r.cycled != 0, cache->format == 8, *dev,
+    return to_status(launch_kv_append(a, r.sections, r.cycled != 0, cache->format == 8, *dev,
                                       static_cast<cudaStream_t>(stream)));
 }
 

@@ -34,6 +34,7 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kTile = 64;       // tokens of a work item
+constexpr int kFixed = 3;       // an item's fixed cost (its first loads' latency, its sums' way out), in tiles
 constexpr int kMaxLength = 0x7fff0000;  // token numbers a little past a length stay below 2³¹
 constexpr int kMaxCtas = 1024;  // largest grid: bounds the workspace
 
@@ -55,8 +56,6 @@ struct SplitArgs {
     AttnArgs a;
     Carried* carried;   // [grid]
     float* partial;     // [grid][2][partial_floats]
-    uint32_t page_mul;  // token / page_size = (token · page_mul) >> page_shift, for token < 2³¹
-    int page_shift;
     float scale_log2;
 };
 
@@ -162,8 +161,10 @@ __device__ __forceinline__ Request request(const AttnArgs& a, int b, int rows_pe
     return r;
 }
 
-__device__ __forceinline__ long long items(const AttnArgs& a, const Request& r) {
-    return static_cast<long long>(a.kv_heads) * r.row_tiles * r.tiles;
+// Units of work of a request: each item (head, row tile) counts kFixed units
+// and then one for each of its tiles.
+__device__ __forceinline__ long long units(const AttnArgs& a, const Request& r) {
+    return static_cast<long long>(a.kv_heads) * r.row_tiles * (r.tiles + kFixed);
 }
 
 // ------------------------------------------------------------------ kernel
@@ -224,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 && !Q8 ? 1 : 2) attn_split_
     // thread sums a stretch of the requests, then one scan over the threads.
     const int per = (a.B + kThreads - 1) / kThreads;
     long long own = 0;
-    for (int b = tid * per; b < min((tid + 1) * per, a.B); ++b) own += items(a, request(a, b, 16 * R));
+    for (int b = tid * per; b < min((tid + 1) * per, a.B); ++b) own += units(a, request(a, b, 16 * R));
     s_sum[tid] = own;
     __syncthreads();
     for (int d = 1; d < kThreads; d <<= 1) {
@@ -243,7 +244,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 && !Q8 ? 1 : 2) attn_split_
         long long before = s_sum[tid] - own;
         int b = tid * per;
         for (; b < a.B - 1; ++b) {
-            const long long w = items(a, request(a, b, 16 * R));
+            const long long w = units(a, request(a, b, 16 * R));
             if (at < before + w) break;
             before += w;
         }
@@ -252,25 +253,28 @@ __global__ void __launch_bounds__(kThreads, D == 256 && !Q8 ? 1 : 2) attn_split_
     }
     __syncthreads();
     int b = s_at;
-    long long before = s_before;  // items of the requests before b
+    long long before = s_before;  // units of the requests before b
 
     const uint32_t ring = smem_addr(smem) + group * S::kStages * S::kStage;
     const int d_chunks = a.head_dim * S::kElt / 16;
 
     while (at < end && b < a.B) {
         const Request rq = request(a, b, 16 * R);
-        const long long mine = items(a, rq);
+        const long long mine = units(a, rq);
         if (at >= before + mine) {
             before += mine;
             ++b;
             continue;
         }
-        // The item: head h, row tile rt, tiles [tile0, tile1) of its own.
-        const long long in_request = at - before;
-        const int tile0 = static_cast<int>(in_request % rq.tiles);
-        const int line = static_cast<int>(in_request / rq.tiles);
+        // The item: head h, row tile rt, tiles [tile0, tile1) of its own; none where the run ends in the fixed units.
+        const int weight = rq.tiles + kFixed;
+        const int line = static_cast<int>((at - before) / weight);
+        const long long item = before + static_cast<long long>(line) * weight;
         const int rt = line % rq.row_tiles, h = line / rq.row_tiles;
-        const int tile1 = static_cast<int>(min(static_cast<long long>(rq.tiles), tile0 + (end - at)));
+        const int tile0 = max(0, static_cast<int>(at - item) - kFixed);
+        const int tile1 = static_cast<int>(min(static_cast<long long>(weight), end - item)) - kFixed;
+        at = item + weight;
+        if (tile1 <= tile0) continue;
         const int rows = rq.n * G, row0 = rt * 16 * R;
         const int low_tile = rq.low / kTile;
         const int tok0 = max(rq.low, (low_tile + tile0) * kTile);
@@ -284,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 && !Q8 ? 1 : 2) attn_split_
         auto page_of = [&](int i) {  // page id of the lane's token, −1 past the end
             const int tok = token_of(i);
             if (i >= stages || tok >= tok1) return -1;
-            return __ldg(table + static_cast<int>((static_cast<uint64_t>(tok) * sp.page_mul) >> sp.page_shift));
+            return __ldg(table + static_cast<int>((static_cast<uint64_t>(tok) * a.page_mul) >> a.page_shift));
         };
         // Scales of a token travel by register for one iteration, then through the stage's memory.
         float pend_k = 0.f, pend_v = 0.f;
@@ -299,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 && !Q8 ? 1 : 2) attn_split_
         auto load = [&](int i, int page) {  // stage i into its slot
             const int tok = token_of(i);
             const bool past = i >= stages || tok >= tok1;
-            const int pi = static_cast<int>((static_cast<uint64_t>(tok) * sp.page_mul) >> sp.page_shift);
+            const int pi = static_cast<int>((static_cast<uint64_t>(tok) * a.page_mul) >> a.page_shift);
             const int in_page = tok - pi * a.page_size;
             long long off = -1;
             if (!past) {
@@ -703,12 +707,11 @@ __global__ void __launch_bounds__(kThreads, D == 256 && !Q8 ? 1 : 2) attn_split_
             }
         }
         if (tid == 0 && tile0 == 0 && tile1 < rq.tiles) {
-            // The item's last tile is item at + tiles − 1; CTA c has those from c·total / ctas on.
-            const long long u = at + rq.tiles - 1;
+            // The item's last unit is that before the next item; CTA c has the units from ⌊c·total / ctas⌋ on.
+            const long long u = at - 1;
             sp.carried[blockIdx.x] = {static_cast<int>(((u + 1) * ctas - 1) / total), h, row0, rows, rq.start, rq.len - rq.n};
         }
         __syncthreads();
-        at += tile1 - tile0;
     }
 }
 
@@ -823,15 +826,10 @@ size_t attn_decode_workspace_bytes(int32_t B, int64_t T, int32_t q_heads, int32_
     return kMaxCtas * 32 + 2 * kMaxCtas * partial_floats(R, dim_of(head_dim)) * sizeof(float);
 }
 
-cudaError_t launch_attn_decode(const AttnArgs& a, bool q8, void* workspace, const DeviceInfo& dev,
-                               cudaStream_t stream) {
+cudaError_t launch_attn_decode(AttnArgs a, bool q8, void* workspace, const DeviceInfo& dev, cudaStream_t stream) {
+    divide_by(a.page_size, &a.page_mul, &a.page_shift);
     SplitArgs sp = {};
     sp.a = a;
-    // ⌈2^(31 + l) / page_size⌉ with 2^l ≥ page_size divides every token < 2³¹ exactly and fits 32 bits.
-    int l = 0;
-    while ((int64_t{1} << l) < a.page_size) ++l;
-    sp.page_shift = 31 + l;
-    sp.page_mul = static_cast<uint32_t>(((uint64_t{1} << sp.page_shift) + a.page_size - 1) / a.page_size);
     sp.scale_log2 = a.scale * 1.4426950408889634f;
     return q8 ? run_dim<true>(sp, workspace, dev, stream) : run_dim<false>(sp, workspace, dev, stream);
 }

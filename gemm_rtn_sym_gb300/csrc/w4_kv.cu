@@ -20,8 +20,12 @@ struct Sums {
 
 __device__ __forceinline__ Sums operator+(Sums a, Sums b) { return {a.grow + b.grow, a.need + b.need, a.back + b.back}; }
 
-__device__ __forceinline__ Sums shfl_up(Sums v, int d) {
-    return {__shfl_up_sync(~0u, v.grow, d), __shfl_up_sync(~0u, v.need, d), __shfl_up_sync(~0u, v.back, d)};
+__device__ __forceinline__ Sums warp_scan(Sums v, int lane) {
+    for (int d = 1; d < 32; d <<= 1) {
+        const Sums u = {__shfl_up_sync(~0u, v.grow, d), __shfl_up_sync(~0u, v.need, d), __shfl_up_sync(~0u, v.back, d)};
+        if (lane >= d) v = v + u;
+    }
+    return v;
 }
 
 constexpr int kPagesThreads = 1024;
@@ -39,22 +43,37 @@ __device__ __forceinline__ int last_at_most(const long long* v, int n, long long
     return lo;
 }
 
-// Every CTA scans all requests' sums, 1024 at a time, and writes every
-// gridDim.x-th block of 1024 tokens and of 1024 returned pages; CTA 0 writes
-// what there is one of for each request.  Reading the lengths again in every
-// CTA costs less than a second launch or a barrier over the grid.
+// Every CTA scans all requests' sums, one per thread at a time, and writes
+// every gridDim.x-th block of tokens and of returned pages; CTA 0 writes what
+// there is one of for each request.  Reading the lengths again in every CTA
+// costs less than a second launch or a barrier over the grid.  Bound by its
+// chain of latencies (two loads, two barriers, a search) at every size that
+// fits a cache.
 __global__ void __launch_bounds__(kPagesThreads) kv_pages_kernel(KvPagesArgs a) {
     __shared__ long long s_start[kPagesThreads], s_back[kPagesThreads], s_first[kPagesThreads];
-    __shared__ int s_len[kPagesThreads], s_want[kPagesThreads];
-    __shared__ Sums s_warp[kPagesThreads / 32];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const long long head = a.range[0], tail = a.range[1], P = a.page_size;
-    const long long most = static_cast<long long>(a.width) * P;
+    __shared__ int s_len[kPagesThreads], s_have[kPagesThreads], s_want[kPagesThreads];
+    __shared__ Sums s_warp[32];
+    __shared__ long long s_used[32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x;
+    const long long head = a.range[0], tail = a.range[1];
+    const long long most = static_cast<long long>(a.width) * a.page_size;
+    // Ring places of the counters; entries beyond wrap by one subtraction.
+    const long long head_at = static_cast<long long>(static_cast<uint64_t>(head) % static_cast<uint64_t>(a.pages));
+    const long long tail_at = static_cast<long long>(static_cast<uint64_t>(tail) % static_cast<uint64_t>(a.pages));
+    auto ring = [&](long long at, long long i) -> int* {
+        i += at;
+        if (i >= a.pages) i -= a.pages;
+        return a.ring + (i >= 0 && i < a.pages ? i : 0);
+    };
+    auto page_index = [&](int token) {  // token / page_size
+        return static_cast<int>((static_cast<uint64_t>(token) * a.page_mul) >> a.page_shift);
+    };
+    const long long free = min(max(tail - head, 0ll), static_cast<long long>(a.pages));
     Sums carry = {0, 0, 0};
     long long used = 0;
 
-    for (int base = 0; base < a.B; base += kPagesThreads) {
-        const int n = min(a.B - base, kPagesThreads);
+    for (int base = 0; base < a.B; base += threads) {
+        const int n = min(a.B - base, threads);
         int len = 0, target = 0;
         bool valid = false;
         if (tid < n) {
@@ -64,76 +83,76 @@ __global__ void __launch_bounds__(kPagesThreads) kv_pages_kernel(KvPagesArgs a) 
             if (!valid) record_status(a.status, kStatusInvalid);
         }
         const bool fits = valid && target <= most;
-        const long long have = valid ? (len + P - 1) / P : 0, want = valid ? (target + P - 1) / P : 0;
-        Sums own = {valid ? max(target - len, 0) : 0, fits ? max(want - have, 0ll) : 0, max(have - want, 0ll)};
-        Sums sum = own;
-        for (int d = 1; d < 32; d <<= 1) {
-            const Sums v = shfl_up(sum, d);
-            if (lane >= d) sum = sum + v;
-        }
+        const int have = valid && len > 0 ? page_index(len - 1) + 1 : 0;
+        const int want = valid && target > 0 ? page_index(target - 1) + 1 : 0;
+        const Sums own = {valid ? max(target - len, 0) : 0, fits ? max(want - have, 0) : 0, max(have - want, 0)};
+        Sums sum = warp_scan(own, lane);
         if (lane == 31) s_warp[warp] = sum;
         __syncthreads();
-        Sums before = carry, total = carry;
-        for (int w = 0; w < kPagesThreads / 32; ++w) {
-            if (w < warp) before = before + s_warp[w];
-            total = total + s_warp[w];
+        if (warp == 0) {
+            const Sums w = lane < threads / 32 ? s_warp[lane] : Sums{0, 0, 0};
+            s_warp[lane] = warp_scan(w, lane);
         }
-        sum = before + sum;
+        __syncthreads();
+        if (warp > 0) sum = sum + s_warp[warp - 1];
+        sum = sum + carry;
+        const Sums total = carry + s_warp[threads / 32 - 1];
         const bool roomy = own.grow == 0 || sum.grow <= a.T;
         if (!roomy) record_status(a.status, kStatusInvalid);
-        const bool granted = fits && roomy && (own.need == 0 || sum.need <= tail - head);
+        const bool granted = fits && roomy && (own.need == 0 || sum.need <= free);
         s_start[tid] = sum.grow - own.grow;
         s_back[tid] = sum.back - own.back;
-        // The ring position of the request's page 0, were all its pages new; −1: no slots.
-        s_first[tid] = granted ? head + sum.need - own.need : -1;
+        s_first[tid] = granted ? sum.need - own.need : -1;  // the request's first new page, from the ring's head; −1: no slots
         s_len[tid] = len;
-        s_want[tid] = static_cast<int>(want);
-        if (blockIdx.x == 0 && tid < n) {
-            a.starts[base + tid] = static_cast<int>(sum.grow - own.grow);
-            a.new_lens[base + tid] = granted ? target : len;
+        s_have[tid] = have;
+        s_want[tid] = want;
+        if (blockIdx.x == 0) {
+            if (tid < n) {
+                a.starts[base + tid] = static_cast<int>(sum.grow - own.grow);
+                a.new_lens[base + tid] = granted ? target : len;
+            }
+            // The sums grow, so the last granted request's sum is the most that is used.
+            long long u = granted && own.need > 0 ? sum.need : 0;
+            for (int d = 16; d > 0; d >>= 1) u = max(u, __shfl_xor_sync(~0u, u, d));
+            if (lane == 0) s_used[warp] = u;
         }
-        // The sums grow, so the last granted request's sum is the most that is used.
-        long long u = granted && own.need > 0 ? sum.need : 0;
-        for (int d = 16; d > 0; d >>= 1) u = max(u, __shfl_xor_sync(~0u, u, d));
         __syncthreads();
-        if (lane == 0) s_warp[warp].need = u;
-        __syncthreads();
-        for (int w = 0; w < kPagesThreads / 32; ++w) used = max(used, s_warp[w].need);
+        if (blockIdx.x == 0 && tid == 0)
+            for (int w = 0; w < threads / 32; ++w) used = max(used, s_used[w]);
 
+        const long long step = static_cast<long long>(gridDim.x) * threads;
         const long long t_end = min(total.grow, static_cast<long long>(a.T));
-        for (long long t = carry.grow + static_cast<long long>(blockIdx.x) * kPagesThreads + tid; t < t_end;
-             t += static_cast<long long>(gridDim.x) * kPagesThreads) {
+        for (long long t = carry.grow + static_cast<long long>(blockIdx.x) * threads + tid; t < t_end; t += step) {
             const int i = last_at_most(s_start, n, t);
-            const long long pos = s_len[i] + (t - s_start[i]), index = pos / P, have_i = (s_len[i] + P - 1) / P;
+            const int pos = s_len[i] + static_cast<int>(t - s_start[i]), index = page_index(pos);
+            const int place = pos - index * a.page_size;
             long long slot = -1;
             if (s_first[i] >= 0) {
                 int* entry = a.table + (base + i) * a.table_stride + index;
-                const int page = index >= have_i
-                                     ? a.ring[static_cast<uint64_t>(s_first[i] + (index - have_i)) % a.pages]
-                                     : *entry;
+                const int fresh = index - s_have[i];
+                const int page = fresh >= 0 ? *ring(head_at, s_first[i] + fresh) : *entry;
                 // The first token of a new page writes its table entry.  A
                 // request that grows past its last page has one such token in
                 // each new page, since its own last page is full by then.
-                if (index >= have_i && pos % P == 0) *entry = page;
+                if (fresh >= 0 && place == 0) *entry = page;
                 if (page >= 0 && page < a.pages)
-                    slot = page * P + pos % P;
+                    slot = static_cast<long long>(page) * a.page_size + place;
                 else
                     record_status(a.status, kStatusInvalid);
             }
             a.slots[t] = slot;
-            a.positions[t] = static_cast<int>(pos);
+            a.positions[t] = pos;
         }
-        for (long long r = carry.back + static_cast<long long>(blockIdx.x) * kPagesThreads + tid; r < total.back;
-             r += static_cast<long long>(gridDim.x) * kPagesThreads) {
+        for (long long r = carry.back + static_cast<long long>(blockIdx.x) * threads + tid; r < total.back; r += step) {
             const int i = last_at_most(s_back, n, r);
-            a.ring[static_cast<uint64_t>(tail + r) % a.pages] =
-                a.table[(base + i) * a.table_stride + s_want[i] + (r - s_back[i])];
+            // The table may claim more pages than the pool has; each entry of the ring is then written again.
+            *ring(tail_at, r < a.pages ? r : r % a.pages) = a.table[(base + i) * a.table_stride + s_want[i] + (r - s_back[i])];
         }
         carry = total;
         __syncthreads();
     }
-    for (long long t = carry.grow + static_cast<long long>(blockIdx.x) * kPagesThreads + tid; t < a.T;
-         t += static_cast<long long>(gridDim.x) * kPagesThreads) {
+    for (long long t = carry.grow + static_cast<long long>(blockIdx.x) * threads + tid; t < a.T;
+         t += static_cast<long long>(gridDim.x) * threads) {
         a.slots[t] = -1;
         a.positions[t] = 0;
     }
@@ -145,110 +164,160 @@ __global__ void __launch_bounds__(kPagesThreads) kv_pages_kernel(KvPagesArgs a) 
 }
 
 // ------------------------------------------------------------------ append
+// Axis of each frequency (rotary ≤ 256), two bits each, eight to a word.
 struct Axes {
-    uint8_t of[128];  // axis of each frequency (rotary ≤ 256)
+    uint16_t of[16];
 };
 
-// One CTA holds LPR lanes for each row it works on at a time; lane c of a row
-// has its values 8c..8c+7.  blockIdx.x is the token, whose tables' values are
-// read once per thread and used for every row the thread turns.
+constexpr int kAppendThreads = 256;
+constexpr int kBatch = 4;  // rows that a lane has in flight
+
+// LPR lanes work on a row, lane c of them on its values 8c..8c+7.  blockIdx.x
+// is the token, whose tables' values a thread reads once and uses for every
+// row that it turns; the rows' loads do not wait for the tables'.  Bound by
+// reading and writing each row once.
 template <int LPR, bool Q8>
-__global__ void __launch_bounds__(256) kv_append_kernel(KvAppendArgs a, Axes axes) {
+__global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const KvAppendArgs a, const Axes axes) {
     const long long t = blockIdx.x;
-    const int c = threadIdx.x % LPR, group = blockIdx.y * (blockDim.x / LPR) + threadIdx.x / LPR;
-    const int groups = gridDim.y * (blockDim.x / LPR);
+    constexpr int kGroups = kAppendThreads / LPR;
+    const int c = threadIdx.x % LPR, group = blockIdx.y * kGroups + threadIdx.x / LPR, groups = gridDim.y * kGroups;
     const int d = a.head_dim, H = a.kv_heads, F = a.rotary / 2, half = F / 8;
     const bool live = 8 * c < d, turned = 8 * c < a.rotary;
+    const int rows = 2 * H + a.q_heads;  // keys, values, queries
 
-    float cs[8], sn[8];
-    if (turned) {
-        // Halves: frequencies 8c.. of the first half, the same again for the second.  Pairs: 4c..4c+3.
-        const int first = a.paired ? 4 * c : 8 * (c < half ? c : c - half);
-        for (int i = 0; i < (a.paired ? 4 : 8); ++i) {
-            int row = a.positions[axes.of[first + i] * a.axis_stride + t];
-            if (row < 0 || row >= a.rows) {
-                record_status(a.status, kStatusInvalid);
-                row = 0;
-            }
-            cs[i] = a.cos[static_cast<long long>(row) * F + first + i];
-            sn[i] = a.sin[static_cast<long long>(row) * F + first + i];
-        }
-    }
     const long long slot = a.slots[t];
-    const bool stored = slot >= 0 && slot < a.pages * a.page_size;
-    if (!stored && slot != -1) record_status(a.status, kStatusInvalid);
-    const long long page = stored ? slot / a.page_size : 0, place = stored ? slot % a.page_size : 0;
-
-    // Rows in the order keys, values, queries; a warp's groups stay together for the shuffles.
-    const int rows = 2 * H + a.q_heads;
-    for (int r0 = group - group % (32 / LPR); r0 < rows; r0 += groups) {
-        const int r = r0 + group % (32 / LPR);
-        const bool is_q = r >= 2 * H, is_v = !is_q && r >= H;
-        const int h = is_q ? r - 2 * H : is_v ? r - H : r;
-        const bool work = live && r < rows && (is_q || stored);
-        uint4 x = {0, 0, 0, 0};
-        if (work) {
-            const Rows& src = is_q ? a.q : is_v ? a.v : a.k;
-            x = *reinterpret_cast<const uint4*>(src.data + t * src.token_stride + h * src.head_stride + 8 * c);
-        }
-        uint32_t w[4] = {x.x, x.y, x.z, x.w};
-        uint32_t other[4];
-        if (!a.paired) {
-            const int from = c < half ? c + half : c - half;
-            for (int i = 0; i < 4; ++i) other[i] = __shfl_sync(~0u, w[i], from & (LPR - 1), LPR);
-        }
-        if (turned && !is_v) {
-            for (int i = 0; i < 4; ++i) {
-                const float lo = bf16_lo(w[i]), hi = bf16_hi(w[i]);
-                float l, u;
-                if (a.paired) {
-                    l = __fsub_rn(__fmul_rn(lo, cs[i]), __fmul_rn(hi, sn[i]));
-                    u = __fadd_rn(__fmul_rn(hi, cs[i]), __fmul_rn(lo, sn[i]));
-                } else {
-                    const float ol = __fmul_rn(bf16_lo(other[i]), sn[2 * i]);
-                    const float oh = __fmul_rn(bf16_hi(other[i]), sn[2 * i + 1]);
-                    l = __fmul_rn(lo, cs[2 * i]);
-                    u = __fmul_rn(hi, cs[2 * i + 1]);
-                    l = c < half ? __fsub_rn(l, ol) : __fadd_rn(l, ol);
-                    u = c < half ? __fsub_rn(u, oh) : __fadd_rn(u, oh);
-                }
-                const __nv_bfloat162 v = __floats2bfloat162_rn(l, u);
-                w[i] = *reinterpret_cast<const uint32_t*>(&v);
+    bool stored = false;
+    long long at = 0, scale_at = 0;
+    float cs[8], sn[8];
+    for (int r0 = group; r0 - threadIdx.x / LPR < rows; r0 += kBatch * groups) {
+        uint4 x[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int r = r0 + i * groups;
+            x[i] = make_uint4(0, 0, 0, 0);
+            if (live && r < rows) {
+                const __nv_bfloat16* src = r < H ? a.k.data + t * a.k.token_stride + r * a.k.head_stride
+                                           : r < 2 * H ? a.v.data + t * a.v.token_stride + (r - H) * a.v.head_stride
+                                                       : a.q.data + t * a.q.token_stride + (r - 2 * H) * a.q.head_stride;
+                x[i] = *reinterpret_cast<const uint4*>(src + 8 * c);
             }
         }
-        if (Q8 && !is_q) {
-            // RTN at 8 bits over the row's LPR lanes (idle lanes hold zeros).
-            float most = 0.f;
-            bool finite = true;
-            for (int i = 0; i < 4; ++i) {
-                most = fmaxf(most, fmaxf(fabsf(bf16_lo(w[i])), fabsf(bf16_hi(w[i]))));
-                finite = finite && isfinite(bf16_lo(w[i])) && isfinite(bf16_hi(w[i]));
-            }
-            if (!finite) most = INFINITY;
-            for (int m = LPR / 2; m > 0; m >>= 1) most = fmaxf(most, __shfl_xor_sync(~0u, most, m));
-            if (work) {
-                const bool bad = isinf(most);
-                const __nv_bfloat16 scale = __float2bfloat16_rn(bad ? NAN : __fdiv_rn(most, 127.f));
-                const float s = __bfloat162float(scale);
-                uint32_t code[2] = {0, 0};
-                if (!bad && s > 0.f)
-                    for (int i = 0; i < 4; ++i) {
-                        const int q0 = __float2int_rn(fminf(fmaxf(rintf(__fdiv_rn(bf16_lo(w[i]), s)), -128.f), 127.f));
-                        const int q1 = __float2int_rn(fminf(fmaxf(rintf(__fdiv_rn(bf16_hi(w[i]), s)), -128.f), 127.f));
-                        code[i / 2] |= ((q0 & 0xFFu) | (q1 & 0xFFu) << 8) << (16 * (i & 1));
+        if (r0 == group) {
+            if (turned) {
+                // Halves: frequencies 8c.. of the first half, the same again for the second.  Pairs: 4c..4c+3.
+                const int n = a.paired ? 4 : 8, first = a.paired ? 4 * c : 8 * (c < half ? c : c - half);
+                const uint32_t code = axes.of[first >> 3] >> (2 * (first & 7)) & (n == 4 ? 0xFFu : 0xFFFFu);
+                const float* cos[4];
+                const float* sin[4];
+#pragma unroll
+                for (int axis = 0; axis < 4; ++axis) {
+                    int row = axis < a.axes ? a.positions[axis * a.axis_stride + t] : 0;
+                    if (row < 0 || row >= a.rows) {
+                        record_status(a.status, kStatusInvalid);
+                        row = 0;
                     }
-                int8_t* dst = static_cast<int8_t*>(is_v ? a.v_cache : a.k_cache) + page * a.page_stride +
-                              place * a.cache_token_stride + h * a.cache_head_stride + 8 * c;
-                *reinterpret_cast<uint2*>(dst) = make_uint2(code[0], code[1]);
-                if (c == 0)
-                    (is_v ? a.v_scales : a.k_scales)[(page * H + h) * a.page_size + place] = scale;
+                    cos[axis] = a.cos + static_cast<long long>(row) * F + first;
+                    sin[axis] = a.sin + static_cast<long long>(row) * F + first;
+                }
+                auto pick = [](const float* const(&p)[4], uint32_t axis) {
+                    return axis < 2 ? (axis ? p[1] : p[0]) : (axis == 2 ? p[2] : p[3]);
+                };
+                if (code == (code & 3) * (n == 4 ? 0x55u : 0x5555u)) {  // one axis
+                    const float4* u = reinterpret_cast<const float4*>(pick(cos, code & 3));
+                    const float4* w = reinterpret_cast<const float4*>(pick(sin, code & 3));
+                    *reinterpret_cast<float4*>(cs) = u[0];
+                    *reinterpret_cast<float4*>(sn) = w[0];
+                    if (n == 8) {
+                        *reinterpret_cast<float4*>(cs + 4) = u[1];
+                        *reinterpret_cast<float4*>(sn + 4) = w[1];
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (i < n) {
+                            cs[i] = pick(cos, code >> (2 * i) & 3)[i];
+                            sn[i] = pick(sin, code >> (2 * i) & 3)[i];
+                        }
+                }
             }
-        } else if (work) {
-            __nv_bfloat16* dst =
-                is_q ? a.q_out.data + t * a.q_out.token_stride + h * a.q_out.head_stride
-                     : static_cast<__nv_bfloat16*>(is_v ? a.v_cache : a.k_cache) + page * a.page_stride +
-                           place * a.cache_token_stride + h * a.cache_head_stride;
-            *reinterpret_cast<uint4*>(dst + 8 * c) = make_uint4(w[0], w[1], w[2], w[3]);
+            stored = slot >= 0 && slot < a.pages * a.page_size;
+            if (!stored && slot != -1) record_status(a.status, kStatusInvalid);
+            if (stored) {
+                const long long page = slot <= 0x7fffffff ? static_cast<long long>((static_cast<uint64_t>(slot) * a.page_mul) >> a.page_shift)
+                                                          : slot / a.page_size;
+                const long long place = slot - page * a.page_size;
+                at = page * a.page_stride + place * a.cache_token_stride;
+                scale_at = page * H * a.page_size + place;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int r = r0 + i * groups;
+            if (r - threadIdx.x / LPR >= rows) break;  // the same for the whole CTA
+            const bool is_q = r >= 2 * H, is_v = !is_q && r >= H;
+            const int h = is_q ? r - 2 * H : is_v ? r - H : r;
+            const bool work = live && r < rows && (is_q || stored);
+            uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+            uint32_t other[4];
+            if (!a.paired) {
+                const int from = c < half ? c + half : c - half;
+#pragma unroll
+                for (int y = 0; y < 4; ++y) other[y] = __shfl_sync(~0u, w[y], from & (LPR - 1), LPR);
+            }
+            if (turned && !is_v) {
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    const float lo = bf16_lo(w[y]), hi = bf16_hi(w[y]);
+                    float l, u;
+                    if (a.paired) {
+                        l = __fsub_rn(__fmul_rn(lo, cs[y]), __fmul_rn(hi, sn[y]));
+                        u = __fadd_rn(__fmul_rn(hi, cs[y]), __fmul_rn(lo, sn[y]));
+                    } else {
+                        const float ol = __fmul_rn(bf16_lo(other[y]), sn[2 * y]);
+                        const float oh = __fmul_rn(bf16_hi(other[y]), sn[2 * y + 1]);
+                        l = __fmul_rn(lo, cs[2 * y]);
+                        u = __fmul_rn(hi, cs[2 * y + 1]);
+                        l = c < half ? __fsub_rn(l, ol) : __fadd_rn(l, ol);
+                        u = c < half ? __fsub_rn(u, oh) : __fadd_rn(u, oh);
+                    }
+                    const __nv_bfloat162 v = __floats2bfloat162_rn(l, u);
+                    w[y] = *reinterpret_cast<const uint32_t*>(&v);
+                }
+            }
+            if (Q8 && r0 - threadIdx.x / LPR + i * groups < 2 * H) {
+                // RTN at 8 bits over the row's LPR lanes (idle lanes hold zeros); query rows go along unused.
+                float most = 0.f;
+                bool finite = true;
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    most = fmaxf(most, fmaxf(fabsf(bf16_lo(w[y])), fabsf(bf16_hi(w[y]))));
+                    finite = finite && isfinite(bf16_lo(w[y])) && isfinite(bf16_hi(w[y]));
+                }
+                if (!finite) most = INFINITY;
+#pragma unroll
+                for (int m = LPR / 2; m > 0; m >>= 1) most = fmaxf(most, __shfl_xor_sync(~0u, most, m));
+                if (work && !is_q) {
+                    const bool bad = isinf(most);
+                    const __nv_bfloat16 scale = __float2bfloat16_rn(bad ? NAN : __fdiv_rn(most, 127.f));
+                    const float s = __bfloat162float(scale);
+                    uint32_t code[2] = {0, 0};
+                    if (!bad && s > 0.f)
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
+                            const int q0 = __float2int_rn(fminf(fmaxf(rintf(__fdiv_rn(bf16_lo(w[y]), s)), -128.f), 127.f));
+                            const int q1 = __float2int_rn(fminf(fmaxf(rintf(__fdiv_rn(bf16_hi(w[y]), s)), -128.f), 127.f));
+                            code[y / 2] |= ((q0 & 0xFFu) | (q1 & 0xFFu) << 8) << (16 * (y & 1));
+                        }
+                    int8_t* dst = static_cast<int8_t*>(is_v ? a.v_cache : a.k_cache) + at + h * a.cache_head_stride + 8 * c;
+                    *reinterpret_cast<uint2*>(dst) = make_uint2(code[0], code[1]);
+                    if (c == 0) (is_v ? a.v_scales : a.k_scales)[scale_at + static_cast<long long>(h) * a.page_size] = scale;
+                }
+            }
+            if (work && (is_q || !Q8)) {
+                __nv_bfloat16* dst = is_q ? a.q_out.data + t * a.q_out.token_stride + h * a.q_out.head_stride
+                                          : static_cast<__nv_bfloat16*>(is_v ? a.v_cache : a.k_cache) + at + h * a.cache_head_stride;
+                *reinterpret_cast<uint4*>(dst + 8 * c) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
         }
     }
 }
@@ -256,38 +325,39 @@ __global__ void __launch_bounds__(256) kv_append_kernel(KvAppendArgs a, Axes axe
 template <int LPR>
 cudaError_t append(const KvAppendArgs& a, const Axes& axes, bool q8, dim3 grid, cudaStream_t stream) {
     if (q8)
-        kv_append_kernel<LPR, true><<<grid, 256, 0, stream>>>(a, axes);
+        kv_append_kernel<LPR, true><<<grid, kAppendThreads, 0, stream>>>(a, axes);
     else
-        kv_append_kernel<LPR, false><<<grid, 256, 0, stream>>>(a, axes);
+        kv_append_kernel<LPR, false><<<grid, kAppendThreads, 0, stream>>>(a, axes);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_kv_pages(const KvPagesArgs& a, const DeviceInfo& dev, cudaStream_t stream) {
-    const int64_t blocks = (a.T + kPagesThreads - 1) / kPagesThreads;
-    const int grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(blocks, dev.sm_count)));
-    kv_pages_kernel<<<grid, kPagesThreads, 0, stream>>>(a);
+cudaError_t launch_kv_pages(KvPagesArgs a, const DeviceInfo& dev, cudaStream_t stream) {
+    divide_by(a.page_size, &a.page_mul, &a.page_shift);
+    // Few requests: smaller CTAs, whose barriers cost less.
+    const int threads = a.B <= 256 ? 256 : kPagesThreads;
+    const int64_t blocks = (a.T + threads - 1) / threads;
+    const int grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(blocks, dev.sm_count * (kPagesThreads / threads))));
+    kv_pages_kernel<<<grid, threads, 0, stream>>>(a);
     return cudaGetLastError();
 }
 
-cudaError_t launch_kv_append(const KvAppendArgs& a, const int32_t sections[4], int32_t n_axes, bool cycled, bool q8,
-                             const DeviceInfo& dev, cudaStream_t stream) {
+cudaError_t launch_kv_append(KvAppendArgs a, const int32_t sections[4], bool cycled, bool q8, const DeviceInfo& dev,
+                             cudaStream_t stream) {
+    divide_by(a.page_size, &a.page_mul, &a.page_shift);
     Axes axes = {};
     int used[4] = {0, 0, 0, 0};
     for (int i = 0, turn = 0; i < a.rotary / 2; ++i) {
-        if (cycled) {
-            while (used[turn % n_axes] == sections[turn % n_axes]) ++turn;
-        } else {
-            while (used[turn] == sections[turn]) ++turn;
-        }
-        axes.of[i] = static_cast<uint8_t>(turn % n_axes);
-        ++used[axes.of[i]];
+        while (used[turn % a.axes] == sections[turn % a.axes]) ++turn;
+        const int axis = turn % a.axes;
+        axes.of[i >> 3] |= static_cast<uint16_t>(axis << (2 * (i & 7)));
+        ++used[axis];
         if (cycled) ++turn;
     }
     const int lpr = a.head_dim <= 64 ? 8 : a.head_dim <= 128 ? 16 : 32;
-    const int per_cta = 256 / lpr, rows = 2 * a.kv_heads + a.q_heads;
-    // Few tokens: one CTA per 256/LPR rows, so that every SM has some.
+    const int per_cta = kAppendThreads / lpr, rows = 2 * a.kv_heads + a.q_heads;
+    // Few tokens: a CTA for every 256 / LPR rows, so that the rows of a token are in flight at once.
     const int split = a.T * 2 >= dev.sm_count ? 1 : (rows + per_cta - 1) / per_cta;
     const dim3 grid(static_cast<unsigned>(a.T), static_cast<unsigned>(split));
     if (lpr == 8) return append<8>(a, axes, q8, grid, stream);

@@ -30,6 +30,8 @@ struct KvPagesArgs {
     int32_t* positions;
     int64_t* range_out;
     unsigned* status;
+    uint32_t page_mul;  // divide_by(page_size)
+    int32_t page_shift;
 };
 
 // bf16 rows [tokens, heads, head_dim], strides in elements.
@@ -49,6 +51,7 @@ struct KvAppendArgs {
     const float* sin;
     int64_t rows;
     int32_t rotary;
+    int32_t axes;
     int32_t paired;
     void* k_cache;
     void* v_cache;
@@ -59,6 +62,8 @@ struct KvAppendArgs {
     int32_t page_size;
     const int64_t* slots;
     unsigned* status;
+    uint32_t page_mul;  // divide_by(page_size)
+    int32_t page_shift;
 };
 
 struct AttnArgs {
@@ -81,14 +86,25 @@ struct AttnArgs {
     float scale;
     int64_t window;
     unsigned* status;
+    uint32_t page_mul;  // divide_by(page_size)
+    int32_t page_shift;
 };
 
-// Arguments are already validated by the C ABI layer.
-cudaError_t launch_kv_pages(const KvPagesArgs& a, const DeviceInfo& dev, cudaStream_t stream);
-cudaError_t launch_kv_append(const KvAppendArgs& a, const int32_t sections[4], int32_t n_axes, bool cycled, bool q8,
-                             const DeviceInfo& dev, cudaStream_t stream);
+// n / by = (n · mul) >> shift for every n < 2³¹: mul = ⌈2^shift / by⌉ with shift
+// = 31 + l and 2^l ≥ by errs by less than n / 2^(31 + l) < 1 / by, and fits 32 bits.
+inline void divide_by(int32_t by, uint32_t* mul, int32_t* shift) {
+    int l = 0;
+    while ((int64_t{1} << l) < by) ++l;
+    *shift = 31 + l;
+    *mul = static_cast<uint32_t>(((uint64_t{1} << *shift) + static_cast<uint64_t>(by) - 1) / static_cast<uint64_t>(by));
+}
+
+// Arguments are already validated by the C ABI layer; the divisors are filled in here.
+cudaError_t launch_kv_pages(KvPagesArgs a, const DeviceInfo& dev, cudaStream_t stream);
+cudaError_t launch_kv_append(KvAppendArgs a, const int32_t sections[4], bool cycled, bool q8, const DeviceInfo& dev,
+                             cudaStream_t stream);
 size_t attn_decode_workspace_bytes(int32_t B, int64_t T, int32_t q_heads, int32_t kv_heads, int32_t head_dim);
-cudaError_t launch_attn_decode(const AttnArgs& a, bool q8, void* workspace, const DeviceInfo& dev,
+cudaError_t launch_attn_decode(AttnArgs a, bool q8, void* workspace, const DeviceInfo& dev,
                                cudaStream_t stream);
 
 }  // namespace w4
