@@ -545,14 +545,18 @@ def _kv_cache(k_cache, v_cache, k_scales, v_scales, index) -> _KvCache:
                     page_size, heads, dim, 16 if k_scale is None else 8)
 
 
+# The address of a device's current stream (what torch.cuda.current_stream(i).cuda_stream gives, without the objects).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
+
+
 def _call(name: str, index: int, *args) -> None:
     """Runs a library function on the current stream of the device."""
     fn = getattr(_lib or load(), name)
     if torch.cuda.current_device() == index:
-        status = fn(*args, torch.cuda.current_stream().cuda_stream)
+        status = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(index):
-            status = fn(*args, torch.cuda.current_stream().cuda_stream)
+            status = fn(*args, _raw_stream(index))
     if status != W4_OK:
         raise W4Error(status, name)
 
@@ -570,19 +574,20 @@ def w4_kv_pages(lens: torch.Tensor, target: torch.Tensor, block_table: torch.Ten
     B, width = block_table.shape
     dev = block_table.device
     i32, i64 = torch.int32, torch.int64
-    new_lens = torch.empty(B, dtype=i32, device=dev) if new_lens is None else new_lens
-    starts = torch.empty(B + 1, dtype=i32, device=dev) if starts is None else starts
-    slots = torch.empty(tokens, dtype=i64, device=dev) if slots is None else slots
-    positions = torch.empty(tokens, dtype=i32, device=dev) if positions is None else positions
-    free_range_out = torch.empty(2, dtype=i64, device=dev) if free_range_out is None else free_range_out
+    outs, addresses = [], []
+    for t, name, dtype, n in ((new_lens, "new_lens", i32, B), (starts, "starts", i32, B + 1), (slots, "slots", i64, tokens),
+                              (positions, "positions", i32, tokens), (free_range_out, "free_range_out", i64, 2)):
+        if t is None:
+            t = torch.empty(n, dtype=dtype, device=dev)
+            addresses.append(t.data_ptr())
+        else:
+            addresses.append(_vector(t, name, dtype, n, index))
+        outs.append(t)
     pages = free_pages.numel()
     _call("w4_kv_pages", index, _vector(lens, "lens", i32, B, index), _vector(target, "target", i32, B, index), B,
           page_size, _vector(free_pages, "free_pages", i32, pages, index), pages,
-          _vector(free_range, "free_range", i64, 2, index), block_table.data_ptr(), stride, width, tokens,
-          _vector(new_lens, "new_lens", i32, B, index), _vector(starts, "starts", i32, B + 1, index),
-          _vector(slots, "slots", i64, tokens, index), _vector(positions, "positions", i32, tokens, index),
-          _vector(free_range_out, "free_range_out", i64, 2, index))
-    return new_lens, starts, slots, positions, free_range_out
+          _vector(free_range, "free_range", i64, 2, index), block_table.data_ptr(), stride, width, tokens, *addresses)
+    return tuple(outs)
 
 
 def w4_kv_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor | None,
@@ -654,13 +659,15 @@ def w4_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     if out is None:
         out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
     rows_q, rows_out = _rows(q, "q", shape, index), _rows(out, "out", shape, index)
-    size = (_lib or load()).w4_attn_decode_workspace_bytes(cache, B, T, q_heads)
     if workspace is None:
+        size = (_lib or load()).w4_attn_decode_workspace_bytes(cache, B, T, q_heads)
         workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
+        scratch = workspace.data_ptr()
     else:
         size = workspace.numel()
+        scratch = _vector(workspace, "workspace", torch.uint8, size, index)
     _call("w4_attn_decode", index, cache, B, T, q_heads, rows_q, rows_out, block_table.data_ptr(), stride, width,
           _vector(lens, "lens", torch.int32, B, index),
           None if starts is None else _vector(starts, "starts", torch.int32, B + 1, index),
-          dim ** -0.5 if scale is None else scale, window, _vector(workspace, "workspace", torch.uint8, size, index), size)
+          dim ** -0.5 if scale is None else scale, window, scratch, size)
     return out

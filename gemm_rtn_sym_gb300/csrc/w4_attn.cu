@@ -19,6 +19,7 @@
 // whole CTA stands in the loop; products run on m16n8k16 MMAs from registers,
 // rows (at most 16·R) as their M, padded with zeros.
 #include <algorithm>
+#include <atomic>
 #include <cstdint>
 
 #include <cuda_bf16.h>
@@ -36,6 +37,7 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kTile = 64;       // tokens of a work item
 constexpr int kFixed = 3;       // an item's fixed cost (its first loads' latency, its sums' way out), in tiles
 constexpr int kMaxLength = 0x7fff0000;  // token numbers a little past a length stay below 2³¹
+constexpr int kMaxDevices = 64;  // as many as the library knows (device_info refuses others)
 constexpr int kMaxCtas = 1024;  // largest grid: bounds the workspace
 
 // What the join needs to know of a CTA's last item where other CTAs carry it on.
@@ -778,12 +780,20 @@ int row_warps(int32_t B, int64_t T, int G) {
 template <int D, bool Q8, int R>
 cudaError_t run(SplitArgs sp, void* workspace, const DeviceInfo& dev, cudaStream_t stream) {
     using S = Shape<D, Q8, R>;
-    cudaError_t err = cudaFuncSetAttribute(attn_split_kernel<D, Q8, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    // CTAs that an SM holds, asked once per device.
+    static std::atomic<int> known[kMaxDevices];
+    int device = 0;
+    cudaError_t err = cudaGetDevice(&device);
     if (err != cudaSuccess) return err;
-    int per_sm = 0;
-    err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, attn_split_kernel<D, Q8, R>, kThreads, S::kSmem);
-    if (err != cudaSuccess) return err;
-    if (per_sm < 1) return cudaErrorInvalidConfiguration;
+    int per_sm = known[device & (kMaxDevices - 1)].load(std::memory_order_relaxed);
+    if (per_sm == 0) {
+        err = cudaFuncSetAttribute(attn_split_kernel<D, Q8, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+        if (err != cudaSuccess) return err;
+        err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, attn_split_kernel<D, Q8, R>, kThreads, S::kSmem);
+        if (err != cudaSuccess) return err;
+        if (per_sm < 1) return cudaErrorInvalidConfiguration;
+        known[device & (kMaxDevices - 1)].store(per_sm, std::memory_order_relaxed);
+    }
     const int grid = std::min(per_sm * dev.sm_count, kMaxCtas);
     sp.carried = static_cast<Carried*>(workspace);
     sp.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kMaxCtas * 32);
