@@ -15,8 +15,8 @@
 // the workspace, and a second small kernel joins them.
 //
 // Inside a CTA each group of R warps (16 query rows each) streams its own
-// tokens through its own ring of cp.async stages, so that no barrier of the
-// whole CTA stands in the loop; products run on m16n8k16 MMAs from registers,
+// tokens through its own ring of cp.async copies, keys and values in turn, so
+// that no barrier of the whole CTA stands in the loop; products run on m16n8k16 MMAs from registers,
 // rows (at most 16·R) as their M, padded with zeros.
 #include <algorithm>
 #include <atomic>
@@ -179,15 +179,21 @@ struct Shape {
     static constexpr int kTokens = 16 * kSub;
     static constexpr int kRow = D * kElt;            // bytes
     static constexpr int kChunks = kRow / 16;
-    static constexpr int kHalf = kTokens * kRow;     // keys, then values
-    static constexpr int kScales = Q8 ? kTokens * 8 : 0;  // (key scale, log2 of value scale) of each token
-    static constexpr int kStage = 2 * kHalf + kScales;
-    static constexpr int kBudget = 104 * 1024;
-    static constexpr int kFit = kBudget / (kGroups * kStage);
-    static constexpr int kStages = kFit < 3 ? 3 : kFit > 8 ? 8 : kFit;
-    static constexpr int kRing = kGroups * kStages * kStage;
+    static constexpr int kHalf = kTokens * kRow;     // a slot of the ring: a stage's keys or values
+    // Three CTAs of 168 registers on an SM, where the outputs' D / 2 leave that; else two.
+    static constexpr int kCtas = D == 256 ? 2 : 3;
+    static constexpr int kBudget = (kCtas == 3 ? 72 : 108) * 1024;
+    static constexpr int kFit = kBudget / (kGroups * (kHalf + (Q8 ? kTokens * 8 : 0)));
+    static constexpr int kSlots = kFit > 12 ? 12 : kFit;
+    static constexpr int kAhead = (kSlots + 1) / 2;  // stages whose keys may be under way or in use
+    static constexpr int kRing = kSlots * kHalf;
+    // (key scale, log2 of value scale) of each token, for the stages on the way and the one in use
+    static constexpr int kScaleSlots = kAhead + 1;
+    static constexpr int kScales = Q8 ? kScaleSlots * kTokens * 8 : 0;
+    static constexpr int kGroup = kRing + kScales;
     static constexpr int kMerge = kWarps * 16 * (D + 3) * 4;
-    static constexpr int kSmem = kRing > kMerge ? kRing : kMerge;
+    static constexpr int kSmem = kGroups * kGroup > kMerge ? kGroups * kGroup : kMerge;
+    static_assert(kSlots >= 3, "a slot in use, two on the way");
 };
 
 // Where 16-byte chunk c of token row r lies in a stage's keys (KEY) or values:
@@ -209,12 +215,12 @@ __device__ __forceinline__ void group_sync(int group) {
 }
 
 template <int D, bool Q8, int R>
-__global__ void __launch_bounds__(kThreads, D == 256 && !Q8 ? 1 : 2) attn_split_kernel(const SplitArgs sp) {
+__global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_kernel(const __grid_constant__ SplitArgs sp) {
     using S = Shape<D, Q8, R>;
     constexpr int NT = D / 8;   // output tiles of 8 columns
     constexpr int KS = D / 16;  // k-steps of 16
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ long long s_sum[kThreads];
+    __shared__ long long s_sum[kWarps];
     __shared__ int s_at;
     __shared__ long long s_before;
     const AttnArgs& a = sp.a;
@@ -228,22 +234,25 @@ __global__ void __launch_bounds__(kThreads, D == 256 && !Q8 ? 1 : 2) attn_split_
     const int per = (a.B + kThreads - 1) / kThreads;
     long long own = 0;
     for (int b = tid * per; b < min((tid + 1) * per, a.B); ++b) own += units(a, request(a, b, 16 * R));
-    s_sum[tid] = own;
-    __syncthreads();
-    for (int d = 1; d < kThreads; d <<= 1) {
-        const long long v = tid >= d ? s_sum[tid - d] : 0;
-        __syncthreads();
-        s_sum[tid] += v;
-        __syncthreads();
+    long long sum = own;
+    for (int d = 1; d < 32; d <<= 1) {
+        const long long v = __shfl_up_sync(~0u, sum, d);
+        if (lane >= d) sum += v;
     }
-    const long long total = s_sum[kThreads - 1];
+    if (lane == 31) s_sum[warp] = sum;
+    __syncthreads();
+    long long total = 0;
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) sum += s_sum[w];
+        total += s_sum[w];
+    }
     const long long ctas = min(static_cast<long long>(gridDim.x), total);
     if (tid == 0) sp.carried[blockIdx.x].last = -1;
     if (blockIdx.x >= ctas) return;
     long long at = blockIdx.x * total / ctas;
     const long long end = (blockIdx.x + 1) * total / ctas;
-    if (at >= s_sum[tid] - own && at < s_sum[tid]) {
-        long long before = s_sum[tid] - own;
+    if (at >= sum - own && at < sum) {
+        long long before = sum - own;
         int b = tid * per;
         for (; b < a.B - 1; ++b) {
             const long long w = units(a, request(a, b, 16 * R));
@@ -257,7 +266,8 @@ __global__ void __launch_bounds__(kThreads, D == 256 && !Q8 ? 1 : 2) attn_split_
     int b = s_at;
     long long before = s_before;  // units of the requests before b
 
-    const uint32_t ring = smem_addr(smem) + group * S::kStages * S::kStage;
+    const uint32_t ring = smem_addr(smem) + group * S::kGroup;
+    float2* scales = reinterpret_cast<float2*>(smem + group * S::kGroup + S::kRing);
     const int d_chunks = a.head_dim * S::kElt / 16;
 
     while (at < end && b < a.B) {
@@ -292,23 +302,20 @@ __global__ void __launch_bounds__(kThreads, D == 256 && !Q8 ? 1 : 2) attn_split_
             if (i >= stages || tok >= tok1) return -1;
             return __ldg(table + static_cast<int>((static_cast<uint64_t>(tok) * a.page_mul) >> a.page_shift));
         };
-        // Scales of a token travel by register for one iteration, then through the stage's memory.
+        // Scales of a token travel by register for one iteration, then through shared memory.
         float pend_k = 0.f, pend_v = 0.f;
-        int pend_slot = -1;
+        int pend_at = -1;
         auto put_scales = [&]() {
-            if (Q8 && pend_slot >= 0 && rw == 0 && lane < S::kTokens) {
-                float2* to = reinterpret_cast<float2*>(smem + group * S::kStages * S::kStage + pend_slot * S::kStage +
-                                                       2 * S::kHalf) + lane;
-                *to = make_float2(pend_k, __log2f(pend_v));
-            }
+            if (Q8 && pend_at >= 0 && rw == 0 && lane < S::kTokens)
+                scales[pend_at * S::kTokens + lane] = make_float2(pend_k, __log2f(pend_v));
         };
-        auto load = [&](int i, int page) {  // stage i into its slot
+        long long off = -1;     // of the lane's token, in the stage whose keys were asked for last; −1: none
+        auto find = [&](int i, int page) {  // stage i
             const int tok = token_of(i);
-            const bool past = i >= stages || tok >= tok1;
             const int pi = static_cast<int>((static_cast<uint64_t>(tok) * a.page_mul) >> a.page_shift);
             const int in_page = tok - pi * a.page_size;
-            long long off = -1;
-            if (!past) {
+            off = -1;
+            if (i < stages && tok < tok1) {
                 if (page >= 0 && page < a.pages)
                     off = page * a.page_stride + in_page * a.token_stride + h * a.head_stride;
                 else
@@ -321,10 +328,14 @@ __global__ void __launch_bounds__(kThreads, D == 256 && !Q8 ? 1 : 2) attn_split_
                     pend_k = __bfloat162float(a.k_scales[s]);
                     pend_v = __bfloat162float(a.v_scales[s]);
                 }
-                pend_slot = i < stages ? i % S::kStages : -1;
+                pend_at = i < stages ? i % S::kScaleSlots : -1;
             }
-            if (i < stages) {
-                const uint32_t dst = ring + (i % S::kStages) * S::kStage;
+        };
+        int put = 0;  // ring slot of the next copy
+        auto load = [&](bool key, bool any) {  // keys or values of the stage found last
+            if (any) {
+                const uint32_t dst = ring + put * S::kHalf;
+                const uint8_t* src = static_cast<const uint8_t*>(key ? a.k : a.v);
                 constexpr int kPerPass = 32 * R / S::kChunks;  // token rows of one pass of the group's lanes
                 const int c = (rw * 32 + lane) % S::kChunks, r0 = (rw * 32 + lane) / S::kChunks;
 #pragma unroll
@@ -332,29 +343,39 @@ __global__ void __launch_bounds__(kThreads, D == 256 && !Q8 ? 1 : 2) attn_split_
                     const int r = p + r0;
                     const long long o = __shfl_sync(~0u, off, r & 31);
                     const bool there = o >= 0 && c < d_chunks;
-                    const long long byte = there ? o * S::kElt + c * 16 : 0;
-                    if (kPerPass <= S::kTokens || r < S::kTokens) {
-                        cp_async16_zfill(dst + place<D, Q8, true>(r, c), static_cast<const uint8_t*>(a.k) + byte, there ? 16 : 0);
-                        cp_async16_zfill(dst + S::kHalf + place<D, Q8, false>(r, c), static_cast<const uint8_t*>(a.v) + byte,
-                                         there ? 16 : 0);
-                    }
+                    const uint8_t* from = src + (there ? o * S::kElt + c * 16 : 0);
+                    cp_async16_zfill(dst + (key ? place<D, Q8, true>(r, c) : place<D, Q8, false>(r, c)), from, there ? 16 : 0);
                 }
             }
+            if (++put == S::kSlots) put = 0;
             cp_async_commit();
         };
-
-        int page_next = -1;
-        {
-            int first[S::kStages];
-#pragma unroll
-            for (int i = 0; i < S::kStages; ++i) first[i] = page_of(i);
-#pragma unroll
-            for (int i = 0; i < S::kStages - 1; ++i) {
-                load(i, first[i]);
-                put_scales();
+        // Copy n holds the keys (n even) or values of stage n / 2; copy n + kSlots − 1 is asked for when copy n is
+        // there, into the slot of copy n − 1.  asked: the next stage to find.
+        int page_next = -1, asked = 0;
+        auto load_next = [&](int n) {
+            if ((n & 1) == 0) {
+                find(asked, page_next);
+                ++asked;
+                page_next = page_of(asked);
             }
-            pend_slot = -1;
-            page_next = first[S::kStages - 1];
+            load((n & 1) == 0, (n >> 1) < stages);
+        };
+        {
+            int first[S::kAhead];
+#pragma unroll
+            for (int i = 0; i < S::kAhead; ++i) first[i] = page_of(i);
+#pragma unroll
+            for (int n = 0; n < S::kSlots - 1; ++n) {
+                if ((n & 1) == 0) {
+                    find(n >> 1, first[n >> 1]);
+                    put_scales();
+                }
+                load((n & 1) == 0, (n >> 1) < stages);
+            }
+            asked = S::kSlots / 2;
+            pend_at = -1;
+            page_next = page_of(asked);
         }
 
         // ---- queries of the thread's rows g and g + 8
@@ -424,18 +445,19 @@ __global__ void __launch_bounds__(kThreads, D == 256 && !Q8 ? 1 : 2) attn_split_
         float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
         float mw[2] = {-INFINITY, -INFINITY};  // Q8: largest score + log2(value scale), the weights' reference
 
+        int get = 0;
         for (int i = 0; i < stages; ++i) {
-            cp_async_wait<S::kStages - 2>();
+            cp_async_wait<S::kSlots - 2>();
             put_scales();
             group_sync<R>(group);
-            {
-                const int page = page_next;
-                page_next = page_of(i + S::kStages);
-                load(i + S::kStages - 1, page);
-            }
-            const int slot = i % S::kStages, base = tok0 + (i * S::kGroups + group) * S::kTokens;
-            const uint32_t keys = ring + slot * S::kStage, vals = keys + S::kHalf;
-            const float2* scales = reinterpret_cast<const float2*>(smem + group * S::kStages * S::kStage + slot * S::kStage + 2 * S::kHalf);
+            pend_at = -1;
+            load_next(2 * i + S::kSlots - 1);
+            const int base = tok0 + (i * S::kGroups + group) * S::kTokens;
+            const uint32_t keys = ring + get * S::kHalf;
+            if (++get == S::kSlots) get = 0;
+            const uint32_t vals = ring + get * S::kHalf;
+            if (++get == S::kSlots) get = 0;
+            const float2* stage_scales = scales + i % S::kScaleSlots * S::kTokens;
 
             // ---- scores: s[2·sub + nt][x] of row g + 8·(x >> 1), token 16·sub + 8·nt + 2·t4 + (x & 1)
             float s[2 * S::kSub][4];
@@ -471,7 +493,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 && !Q8 ? 1 : 2) attn_split_
             for (int y = 0; y < 2 * S::kSub; ++y) {
                 float ks0 = 1.f, ks1 = 1.f;
                 if (Q8) {
-                    const float4 f = *reinterpret_cast<const float4*>(scales + y * 8 + 2 * t4);
+                    const float4 f = *reinterpret_cast<const float4*>(stage_scales + y * 8 + 2 * t4);
                     ks0 = f.x, lv[y][0] = f.y, ks1 = f.z, lv[y][1] = f.w;
                 }
                 s[y][0] *= row_scale[0] * ks0;
@@ -537,6 +559,11 @@ __global__ void __launch_bounds__(kThreads, D == 256 && !Q8 ? 1 : 2) attn_split_
                     s[y][x] = !Q8 ? p : s[y][x] == -INFINITY ? 0.f : ex2(s[y][x] + lv[y][x & 1] - refw[x >> 1]);
                 }
             // ---- values
+            cp_async_wait<S::kSlots - 2>();
+            if (S::kSlots % 2 != 0) put_scales();
+            group_sync<R>(group);
+            if (S::kSlots % 2 != 0) pend_at = -1;
+            load_next(2 * i + S::kSlots);
             if (!Q8) {
                 bool odd = false;  // a value that is not finite, in tokens that some rows do not see
                 if (hidden) {
@@ -718,53 +745,58 @@ __global__ void __launch_bounds__(kThreads, D == 256 && !Q8 ? 1 : 2) attn_split_
 }
 
 // Joins the parts of the item that begins in CTA blockIdx.x and ends in a
-// later one: its own second part, the later CTAs' first.  blockIdx.y takes
-// every fourth row.
+// later one: its own second part, the later CTAs' first.  A CTA takes one row;
+// its warps take the parts in turn, each with a running maximum of its own.
 template <int D, int R>
-__global__ void __launch_bounds__(kThreads) attn_join_kernel(const SplitArgs sp) {
+__global__ void __launch_bounds__(kThreads) attn_join_kernel(const __grid_constant__ SplitArgs sp) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const Carried c = sp.carried[blockIdx.x];
-    if (c.last < 0) return;
+    const int r = blockIdx.y;
+    if (c.last < 0 || c.row0 + r >= c.rows) return;
     const AttnArgs& a = sp.a;
     const int G = a.q_heads / a.kv_heads;
-    const size_t size = partial_floats(R, D);
-    const float* first = sp.partial + (2 * static_cast<size_t>(blockIdx.x) + 1) * size;
-    auto part = [&](int k) { return k == 0 ? first : sp.partial + 2 * (static_cast<size_t>(blockIdx.x) + k) * size; };
+    constexpr int V = D / 32;
+    constexpr size_t size = partial_floats(R, D);
     const int parts = c.last - static_cast<int>(blockIdx.x) + 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int r = blockIdx.y * kWarps + warp;
-    if (r >= 16 * R || c.row0 + r >= c.rows) return;
-    float mm = -INFINITY, mmw = -INFINITY;
-    for (int k = lane; k < parts; k += 32) {
-        mm = fmaxf(mm, part(k)[r]);
-        mmw = fmaxf(mmw, part(k)[16 * R + r]);
-    }
-    for (int x = 16; x > 0; x >>= 1) {
-        mm = fmaxf(mm, __shfl_xor_sync(~0u, mm, x));
-        mmw = fmaxf(mmw, __shfl_xor_sync(~0u, mmw, x));
-    }
-    const float rm = mm == -INFINITY ? 0.f : mm, rmw = mmw == -INFINITY ? 0.f : mmw;
-    float ll = 0.f, v[D / 32];
+    __shared__ float s_m[kWarps], s_mw[kWarps], s_l[kWarps], s_v[kWarps][D];
+    float mm = -INFINITY, mmw = -INFINITY, ll = 0.f, v[V];
 #pragma unroll
-    for (int x = 0; x < D / 32; ++x) v[x] = 0.f;
+    for (int x = 0; x < V; ++x) v[x] = 0.f;
 #pragma unroll 4
-    for (int k = 0; k < parts; ++k) {
-        const float* p = part(k);
-        ll += ex2(p[r] - rm) * p[32 * R + r];
-        const float f = ex2(p[16 * R + r] - rmw);
+    for (int k = warp; k < parts; k += kWarps) {
+        const float* p = sp.partial + (2 * (static_cast<size_t>(blockIdx.x) + k) + (k == 0)) * size;
+        const float pm = p[r], pmw = p[16 * R + r], pl = p[32 * R + r];
+        float pv[V];
 #pragma unroll
-        for (int x = 0; x < D / 32; ++x) {
-            const int col = lane + 32 * x;
-            if (col < a.head_dim) v[x] += f * p[48 * R + r * D + col];
-        }
+        for (int x = 0; x < V; ++x) pv[x] = lane + 32 * x < a.head_dim ? p[48 * R + r * D + lane + 32 * x] : 0.f;
+        const float nm = fmaxf(mm, pm), nw = fmaxf(mmw, pmw);
+        const float rm = nm == -INFINITY ? 0.f : nm, rw = nw == -INFINITY ? 0.f : nw;
+        ll = ll * ex2(mm - rm) + pl * ex2(pm - rm);
+        const float keep = ex2(mmw - rw), f = ex2(pmw - rw);
+#pragma unroll
+        for (int x = 0; x < V; ++x) v[x] = v[x] * keep + pv[x] * f;
+        mm = nm, mmw = nw;
     }
+    if (lane == 0) s_m[warp] = mm, s_mw[warp] = mmw, s_l[warp] = ll;
+#pragma unroll
+    for (int x = 0; x < V; ++x) s_v[warp][lane + 32 * x] = v[x];
+    __syncthreads();
+    mm = mmw = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, s_m[w]), mmw = fmaxf(mmw, s_mw[w]);
+    const float rm = mm == -INFINITY ? 0.f : mm, rw = mmw == -INFINITY ? 0.f : mmw;
+    ll = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) ll += s_l[w] * ex2(s_m[w] - rm);
     const int row = c.row0 + r, j = row / G;
     const float f = c.before + j < 0 ? 0.f : (mmw == -INFINITY ? 0.f : ex2(mmw - mm)) / ll;
     __nv_bfloat16* out = a.out.data + (c.start + j) * a.out.token_stride + (c.head * G + row % G) * a.out.head_stride;
+    for (int col = threadIdx.x; col < a.head_dim; col += kThreads) {
+        float y = 0.f;
 #pragma unroll
-    for (int x = 0; x < D / 32; ++x) {
-        const int col = lane + 32 * x;
-        if (col < a.head_dim) out[col] = __float2bfloat16_rn(v[x] * f);
+        for (int w = 0; w < kWarps; ++w) y += s_v[w][col] * ex2(s_mw[w] - rw);
+        out[col] = __float2bfloat16_rn(y * f);
     }
 }
 
@@ -801,7 +833,7 @@ cudaError_t run(SplitArgs sp, void* workspace, const DeviceInfo& dev, cudaStream
     err = cudaGetLastError();
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid, 16 * R / kWarps);
+    cfg.gridDim = dim3(grid, 16 * R);
     cfg.blockDim = dim3(kThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr;
