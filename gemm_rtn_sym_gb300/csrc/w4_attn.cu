@@ -2,25 +2,34 @@
 // key-value cache.
 //
 // For a row at position p: o = Σ_t 2^(s_t − m) v_t / Σ_t 2^(s_t − m) over the
-// tokens it sees, s_t = scale · log2(e) · q·k_t and m the largest s_t, in one
-// pass over the tokens: where the running maximum grows from m to m', sums and
-// values so far are multiplied by 2^(m − m').
+// tokens it sees, s_t = scale · log2(e) · q·k_t, in one pass over the tokens.
+// m is a reference near the largest score so far: where a score exceeds it by
+// more than 8, it moves up to the largest, from m to m', and sums and values
+// so far are multiplied by 2^(m − m'); weights stay below 2⁸ and fp32 sums
+// carry them as well as those below 1.
 //
 // Every byte of keys and values is used for a few rows only (query heads per
 // key-value head × new tokens), so the pass is bound by reading the cache.
 // The work is the list of all (request, key-value head, row tile, 64 tokens),
-// in that order, cut into equal runs, one for each CTA of a grid that is
-// resident at once: requests of any lengths load every SM alike.  A run's
-// first and last items may belong to several CTAs; those leave their sums in
-// the workspace, and a second small kernel joins them.
+// in that order, cut into equal pieces, one for each CTA of a grid that is
+// resident at once: requests of any lengths load every SM alike.  Items that
+// several pieces share leave their sums in the workspace, and the CTA that
+// finishes last joins them, sixteen at a time.  (SMs differ in how fast they
+// read, ±12 % here; two further rounds of smaller pieces evened that out but
+// cost more in starts and ends of pieces: 121 against 106 µs for 131071
+// tokens.)
 //
 // Inside a CTA each group of R warps (16 query rows each) streams its own
 // tokens through its own ring of cp.async copies, keys and values in turn, so
-// that no barrier of the whole CTA stands in the loop; products run on m16n8k16 MMAs from registers,
-// rows (at most 16·R) as their M, padded with zeros.
+// that no barrier of the whole CTA stands in the loop; products run on
+// m16n8k16 MMAs from registers, rows (at most 16·R) as their M, padded with
+// zeros.  Every warp loads for itself: one warp that issued TMA copies for
+// eight moved 3.5 TB/s, eight warps' cp.async 6.4.
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -34,32 +43,30 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kTile = 64;       // tokens of a work item
-constexpr int kFixed = 3;       // an item's fixed cost (its first loads' latency, its sums' way out), in tiles
+constexpr int kTile = 64;       // tokens of a unit of work
+constexpr int kFixed = 3;       // an item's fixed cost (its first loads' latency, its sums' way out), in units
+constexpr int kJoinGroup = 16;  // parts of an item that are joined at once
 constexpr int kMaxLength = 0x7fff0000;  // token numbers a little past a length stay below 2³¹
-constexpr int kMaxDevices = 64;  // as many as the library knows (device_info refuses others)
-constexpr int kMaxCtas = 1024;  // largest grid: bounds the workspace
+constexpr int kMaxDevices = 64;         // as many as the library knows (device_info refuses others)
+constexpr int kMaxCtas = 512;           // bounds the workspace
 
-// What the join needs to know of a CTA's last item where other CTAs carry it on.
-struct Carried {
-    int last;     // last CTA of the item; −1: no item of this CTA is carried on
-    int head;     // key-value head
-    int row0;     // first row of the row tile
-    int rows;     // rows of the request (new tokens × query heads per key-value head)
-    int start;    // first token row of the request
-    int before;   // tokens before the new ones (may be negative)
-};
-
-// Largest score, largest weight's exponent (score + log2 of the value's scale),
-// sum: 16·R of each, then 16·R rows of D values.
-__host__ __device__ constexpr size_t partial_floats(int R, int D) { return static_cast<size_t>(16 * R) * (3 + D); }
+// The weights' reference and their sum, 16·R of each, then 16·R rows of D values.
+__host__ __device__ constexpr size_t partial_floats(int R, int D) { return static_cast<size_t>(16 * R) * (2 + D); }
 
 struct SplitArgs {
     AttnArgs a;
-    Carried* carried;   // [grid]
-    float* partial;     // [grid][2][partial_floats]
-    float scale_log2;
+    unsigned long long* arrived;  // [2][kMaxCtas] parts there of a group, groups there of an item
+    float* partial;               // [kMaxCtas][2][partial_floats]
+    int G;                        // query heads per key-value head
+    uint32_t G_mul;               // divide_by(G)
+    int G_shift;
+    int rows_each;                // rows of each request, where starts is null
+    float scale_log2;             // |scale| · log2(e)
+    uint32_t flip;                // sign bits of a pair of queries to turn over: scale < 0
 };
+
+// A value scale of zero stands for this one, whose logarithm is a number.
+constexpr float kTiny = 1.17549435e-38f;
 
 // ------------------------------------------------------------- small pieces
 __device__ __forceinline__ float ex2(float x) {
@@ -138,28 +145,26 @@ struct Request {
     int row_tiles;
 };
 
-__device__ __forceinline__ Request request(const AttnArgs& a, int b, int rows_per_tile) {
+__device__ __forceinline__ Request request(const SplitArgs& sp, int b, int rows_per_tile) {
+    const AttnArgs& a = sp.a;
     Request r;
+    const int len = a.lens[b];
     if (a.starts) {
-        const long long T = a.T;
-        const long long s = min(max(static_cast<long long>(a.starts[b]), 0ll), T);
-        const long long e = min(max(static_cast<long long>(a.starts[b + 1]), s), T);
-        r.start = static_cast<int>(s);
-        r.n = static_cast<int>(e - s);
+        const int T = static_cast<int>(a.T);
+        r.start = min(max(a.starts[b], 0), T);
+        r.n = min(max(a.starts[b + 1], r.start), T) - r.start;
     } else {
-        r.n = static_cast<int>(a.T / a.B);
+        r.n = sp.rows_each;
         r.start = b * r.n;
     }
-    const long long most = min(static_cast<long long>(a.width) * a.page_size, static_cast<long long>(kMaxLength));
-    const int len = a.lens[b];
+    const int most = static_cast<int>(min(static_cast<long long>(a.width) * a.page_size, static_cast<long long>(kMaxLength)));
     if (len < 0 || len > most) record_status(a.status, kStatusInvalid);
-    r.len = len < 0 ? 0 : static_cast<int>(min(static_cast<long long>(len), most));
+    r.len = min(max(len, 0), most);
     const long long low = a.window > 0 ? static_cast<long long>(r.len) - r.n - a.window + 1 : 0;
     r.low = static_cast<int>(max(low, 0ll));
-    const int rows = r.n * (a.q_heads / a.kv_heads);
     // A request without tokens still has its rows of zeros to write: one tile.
     r.tiles = max(1, (r.len + kTile - 1) / kTile - r.low / kTile);
-    r.row_tiles = (rows + rows_per_tile - 1) / rows_per_tile;
+    r.row_tiles = (r.n * sp.G + rows_per_tile - 1) / rows_per_tile;
     return r;
 }
 
@@ -168,6 +173,25 @@ __device__ __forceinline__ Request request(const AttnArgs& a, int b, int rows_pe
 __device__ __forceinline__ long long units(const AttnArgs& a, const Request& r) {
     return static_cast<long long>(a.kv_heads) * r.row_tiles * (r.tiles + kFixed);
 }
+
+__device__ __forceinline__ long long quotient(long long x, int y) {
+    return x >> 32 ? static_cast<long long>(static_cast<unsigned long long>(x) / static_cast<unsigned>(y))
+                   : static_cast<long long>(static_cast<unsigned>(x) / static_cast<unsigned>(y));
+}
+
+// How `total` units are cut into n pieces: the first `longer` of them have one
+// unit more than the others' `size`.
+struct Cut {
+    long long size, longer;
+
+    __device__ __forceinline__ Cut(long long total, int n) : size(quotient(total, n)) { longer = total - size * n; }
+    __device__ __forceinline__ long long begin(int p) const { return p * size + min(static_cast<long long>(p), longer); }
+    __device__ __forceinline__ int piece(long long unit) const {  // that a unit lies in
+        const long long head = longer * (size + 1);
+        return static_cast<int>(unit < head ? quotient(unit, static_cast<int>(size) + 1)
+                                            : longer + quotient(unit - head, static_cast<int>(size)));
+    }
+};
 
 // ------------------------------------------------------------------ kernel
 // Shapes of the pass for head_dim ≤ D, R warps (16 rows each) per group.
@@ -191,19 +215,18 @@ struct Shape {
     static constexpr int kScaleSlots = kAhead + 1;
     static constexpr int kScales = Q8 ? kScaleSlots * kTokens * 8 : 0;
     static constexpr int kGroup = kRing + kScales;
-    static constexpr int kMerge = kWarps * 16 * (D + 3) * 4;
+    static constexpr int kMerge = kWarps * 16 * (D + 2) * 4;
     static constexpr int kSmem = kGroups * kGroup > kMerge ? kGroups * kGroup : kMerge;
     static_assert(kSlots >= 3, "a slot in use, two on the way");
 };
 
-// Where 16-byte chunk c of token row r lies in a stage's keys (KEY) or values:
+// Chunk c (of 16 bytes) of token row r lies at r · row + ((c ^ turn(r)) · 16):
 // the loads of eight lanes that a shared-memory access serves at once fall in
-// different banks.
-template <int D, bool Q8, bool KEY>
-__device__ __forceinline__ uint32_t place(int r, int c) {
-    constexpr int row = D * (Q8 ? 1 : 2);
-    const int x = row == 64 ? (KEY ? 0 : (r >> 1) & 3) : Q8 && KEY ? ((r & 1) << 2) | ((r >> 1) & 3) : r & 7;
-    return static_cast<uint32_t>(r * row + ((c ^ x) << 4));
+// different banks.  turn(r) < 8 (4 for rows of 64 bytes) moves a chunk within
+// 128 (64) bytes.
+template <int ROW, bool Q8, bool KEY>
+__device__ __forceinline__ int turn(int r) {
+    return ROW == 64 ? (KEY ? 0 : (r >> 1) & 3) : Q8 && KEY ? ((r & 1) << 2) | ((r >> 1) & 3) : r & 7;
 }
 
 template <int R>
@@ -214,26 +237,55 @@ __device__ __forceinline__ void group_sync(int group) {
         asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(R * 32) : "memory");
 }
 
+// Counts an arrival at `word`; true for the last of `need`.  The upper 48 bits
+// mark a word that counts, and the last arrival leaves the count 0, for the
+// next launch; a word without the mark (what the workspace held before its
+// first use) counts as none.  What the CTA wrote before its barrier is then
+// visible to the CTA of the last arrival.
+constexpr unsigned long long kMark = 0x77346B765F61ull << 16;
+
+__device__ __forceinline__ bool arrive(unsigned long long* word, int need) {
+    __threadfence();
+    unsigned long long seen = atomicAdd(word, 1ull);
+    bool counted = (seen & ~0xFFFFull) == kMark;
+    int count = static_cast<int>(seen & 0xFFFF) + 1;
+    if (!counted) {
+        ++seen;
+        do {
+            count = (seen & ~0xFFFFull) == kMark ? static_cast<int>(seen & 0xFFFF) + 1 : 1;
+            const unsigned long long prev = atomicCAS(word, seen, kMark | count);
+            counted = prev == seen;
+            seen = prev;
+        } while (!counted);
+    }
+    if (count != need) return false;
+    __threadfence();
+    atomicExch(word, kMark);
+    return true;
+}
+
 template <int D, bool Q8, int R>
 __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_kernel(const __grid_constant__ SplitArgs sp) {
     using S = Shape<D, Q8, R>;
     constexpr int NT = D / 8;   // output tiles of 8 columns
     constexpr int KS = D / 16;  // k-steps of 16
+    constexpr int kRow = S::kRow;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ long long s_sum[kWarps];
-    __shared__ int s_at;
     __shared__ long long s_before;
+    __shared__ int s_at;
+    __shared__ bool s_last;
     const AttnArgs& a = sp.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
-    const int group = warp / R, rw = warp % R;
-    const int G = a.q_heads / a.kv_heads;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int group = warp / R, rw = warp % R, G = sp.G;
+    auto over_G = [&](int r) { return static_cast<int>((static_cast<uint64_t>(r) * sp.G_mul) >> sp.G_shift); };
+    pdl_start();
 
-    // The total work, and the request that this CTA's run begins in: each
+    // The total work, and the request that this CTA's piece begins in: each
     // thread sums a stretch of the requests, then one scan over the threads.
     const int per = (a.B + kThreads - 1) / kThreads;
     long long own = 0;
-    for (int b = tid * per; b < min((tid + 1) * per, a.B); ++b) own += units(a, request(a, b, 16 * R));
+    for (int b = tid * per; b < min((tid + 1) * per, a.B); ++b) own += units(a, request(sp, b, 16 * R));
     long long sum = own;
     for (int d = 1; d < 32; d <<= 1) {
         const long long v = __shfl_up_sync(~0u, sum, d);
@@ -246,16 +298,15 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
         if (w < warp) sum += s_sum[w];
         total += s_sum[w];
     }
-    const long long ctas = min(static_cast<long long>(gridDim.x), total);
-    if (tid == 0) sp.carried[blockIdx.x].last = -1;
-    if (blockIdx.x >= ctas) return;
-    long long at = blockIdx.x * total / ctas;
-    const long long end = (blockIdx.x + 1) * total / ctas;
+    const Cut cut(total, gridDim.x);
+    long long at = cut.begin(blockIdx.x);
+    const long long end = cut.begin(blockIdx.x + 1);
+    if (at >= end) return;
     if (at >= sum - own && at < sum) {
         long long before = sum - own;
         int b = tid * per;
-        for (; b < a.B - 1; ++b) {
-            const long long w = units(a, request(a, b, 16 * R));
+        for (const int stop = min(b + per, a.B) - 1; b < stop; ++b) {
+            const long long w = units(a, request(sp, b, 16 * R));
             if (at < before + w) break;
             before += w;
         }
@@ -269,20 +320,23 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
     const uint32_t ring = smem_addr(smem) + group * S::kGroup;
     float2* scales = reinterpret_cast<float2*>(smem + group * S::kGroup + S::kRing);
     const int d_chunks = a.head_dim * S::kElt / 16;
+    // The lane's places in a slot: of its 16 bytes of a copy's pass, and of what it reads.
+    constexpr int kPerPass = 32 * R / S::kChunks;  // token rows of one pass of the group's lanes
+    const int load_c = (rw * 32 + lane) % S::kChunks, load_r = (rw * 32 + lane) / S::kChunks;
 
     while (at < end && b < a.B) {
-        const Request rq = request(a, b, 16 * R);
+        const Request rq = request(sp, b, 16 * R);
         const long long mine = units(a, rq);
         if (at >= before + mine) {
             before += mine;
             ++b;
             continue;
         }
-        // The item: head h, row tile rt, tiles [tile0, tile1) of its own; none where the run ends in the fixed units.
+        // The item: head h, row tile rt, tiles [tile0, tile1) of its own; none where the piece ends in the fixed units.
         const int weight = rq.tiles + kFixed;
-        const int line = static_cast<int>((at - before) / weight);
+        const int line = static_cast<int>(quotient(at - before, weight));
         const long long item = before + static_cast<long long>(line) * weight;
-        const int rt = line % rq.row_tiles, h = line / rq.row_tiles;
+        const int h = rq.row_tiles == 1 ? line : line / rq.row_tiles, rt = line - h * rq.row_tiles;
         const int tile0 = max(0, static_cast<int>(at - item) - kFixed);
         const int tile1 = static_cast<int>(min(static_cast<long long>(weight), end - item)) - kFixed;
         at = item + weight;
@@ -290,11 +344,11 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
         const int rows = rq.n * G, row0 = rt * 16 * R;
         const int low_tile = rq.low / kTile;
         const int tok0 = max(rq.low, (low_tile + tile0) * kTile);
-        const int tok1 = min(static_cast<long long>(rq.len), (low_tile + tile1) * static_cast<long long>(kTile));
+        const int tok1 = static_cast<int>(min(static_cast<long long>(rq.len), (low_tile + tile1) * static_cast<long long>(kTile)));
         const int count = tok1 - tok0 - group * S::kTokens;
         const int stages = count <= 0 ? 0 : (count + S::kGroups * S::kTokens - 1) / (S::kGroups * S::kTokens);
 
-        // ---- loads: lane l knows token l of a stage
+        // ---- page ids of the first stages: lane l knows token l of a stage
         const int* table = a.table + b * a.table_stride;
         auto token_of = [&](int i) { return tok0 + (i * S::kGroups + group) * S::kTokens + (lane & (S::kTokens - 1)); };
         auto page_of = [&](int i) {  // page id of the lane's token, −1 past the end
@@ -302,14 +356,48 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
             if (i >= stages || tok >= tok1) return -1;
             return __ldg(table + static_cast<int>((static_cast<uint64_t>(tok) * a.page_mul) >> a.page_shift));
         };
+        int first[S::kAhead];
+#pragma unroll
+        for (int i = 0; i < S::kAhead; ++i) first[i] = page_of(i);
+
+        // ---- queries of the thread's rows g and g + 8, asked for ahead of the tokens' bytes
+        uint32_t q[KS][4];
+        int see_lo[2], see_hi[2];   // tokens that a row sees
+        uint2 raw[Q8 ? 2 : 1][Q8 ? KS : 1];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int r = row0 + rw * 16 + g + 8 * x, j = over_G(r);
+            const bool live = r < rows;
+            see_hi[x] = live ? rq.len - rq.n + j + 1 : 0x7fffffff;
+            see_lo[x] = live && a.window > 0 ? static_cast<int>(max(0ll, static_cast<long long>(see_hi[x]) - a.window)) : 0;
+            const __nv_bfloat16* src = a.q.data + (live ? (rq.start + j) * a.q.token_stride + (h * G + r - j * G) * a.q.head_stride : 0);
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+                if (!Q8) {
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const int k = ks * 16 + 2 * t4 + 8 * y;
+                        q[ks][x + 2 * y] = live && k < a.head_dim ? *reinterpret_cast<const uint32_t*>(src + k) : 0u;
+                    }
+                } else {
+                    // four values in a row for each k-step and lane, like the keys' codes below
+                    const int k = (ks >> 2) * 64 + t4 * 16 + (ks & 3) * 4;
+                    raw[Q8 ? x : 0][Q8 ? ks : 0] = live && k < a.head_dim ? *reinterpret_cast<const uint2*>(src + k) : make_uint2(0, 0);
+                }
+            }
+        }
+
+        // ---- loads
         // Scales of a token travel by register for one iteration, then through shared memory.
         float pend_k = 0.f, pend_v = 0.f;
         int pend_at = -1;
         auto put_scales = [&]() {
             if (Q8 && pend_at >= 0 && rw == 0 && lane < S::kTokens)
-                scales[pend_at * S::kTokens + lane] = make_float2(pend_k, __log2f(pend_v));
+                scales[pend_at * S::kTokens + lane] = make_float2(pend_k, __log2f(pend_v < kTiny ? kTiny : pend_v));
         };
         long long off = -1;     // of the lane's token, in the stage whose keys were asked for last; −1: none
+        long long off0 = 0;     // of the stage's first token
+        bool even = false;      // the tokens are all there, token_stride apart, with rows of D values
         auto find = [&](int i, int page) {  // stage i
             const int tok = token_of(i);
             const int pi = static_cast<int>((static_cast<uint64_t>(tok) * a.page_mul) >> a.page_shift);
@@ -330,21 +418,33 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
                 }
                 pend_at = i < stages ? i % S::kScaleSlots : -1;
             }
+            off0 = __shfl_sync(~0u, off, 0);
+            even = __all_sync(~0u, off0 >= 0 && off == off0 + (lane & (S::kTokens - 1)) * a.token_stride) &&
+                   d_chunks == S::kChunks;
         };
         int put = 0;  // ring slot of the next copy
-        auto load = [&](bool key, bool any) {  // keys or values of the stage found last
+        auto load = [&](auto key, bool any) {  // keys or values of the stage found last
+            constexpr bool KEY = decltype(key)::value;
             if (any) {
-                const uint32_t dst = ring + put * S::kHalf;
-                const uint8_t* src = static_cast<const uint8_t*>(key ? a.k : a.v);
-                constexpr int kPerPass = 32 * R / S::kChunks;  // token rows of one pass of the group's lanes
-                const int c = (rw * 32 + lane) % S::kChunks, r0 = (rw * 32 + lane) / S::kChunks;
+                // place of (load_r, load_c); rows p further on keep it but for the turn of p's low bits
+                const uint32_t dst = ring + put * S::kHalf + load_r * kRow + ((load_c ^ turn<kRow, Q8, KEY>(load_r)) << 4);
+                const uint8_t* src = static_cast<const uint8_t*>(KEY ? a.k : a.v);
+                auto to = [&](int p) { return (dst ^ (turn<kRow, Q8, KEY>(p) << 4)) + p * kRow; };
+                if (even) {
+                    const uint8_t* from = src + off0 * S::kElt + load_r * a.token_stride * S::kElt + load_c * 16;
 #pragma unroll
-                for (int p = 0; p < S::kTokens; p += kPerPass) {
-                    const int r = p + r0;
-                    const long long o = __shfl_sync(~0u, off, r & 31);
-                    const bool there = o >= 0 && c < d_chunks;
-                    const uint8_t* from = src + (there ? o * S::kElt + c * 16 : 0);
-                    cp_async16_zfill(dst + (key ? place<D, Q8, true>(r, c) : place<D, Q8, false>(r, c)), from, there ? 16 : 0);
+                    for (int p = 0; p < S::kTokens; p += kPerPass) {
+                        cp_async16(to(p), from);
+                        from += kPerPass * S::kElt * a.token_stride;
+                    }
+                } else {
+#pragma unroll
+                    for (int p = 0; p < S::kTokens; p += kPerPass) {
+                        const long long o = __shfl_sync(~0u, off, (p + load_r) & 31);
+                        const bool there = o >= 0 && load_c < d_chunks;
+                        const uint8_t* from = src + (there ? o * S::kElt + load_c * 16 : 0);
+                        cp_async16_zfill(to(p), from, there ? 16 : 0);
+                    }
                 }
             }
             if (++put == S::kSlots) put = 0;
@@ -352,87 +452,63 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
         };
         // Copy n holds the keys (n even) or values of stage n / 2; copy n + kSlots − 1 is asked for when copy n is
         // there, into the slot of copy n − 1.  asked: the next stage to find.
-        int page_next = -1, asked = 0;
-        auto load_next = [&](int n) {
-            if ((n & 1) == 0) {
-                find(asked, page_next);
+        int asked = S::kSlots / 2;
+        auto load_next = [&](auto key, int& page, int n) {
+            if (decltype(key)::value) {
+                find(asked, page);
                 ++asked;
-                page_next = page_of(asked);
+                page = page_of(asked);
             }
-            load((n & 1) == 0, (n >> 1) < stages);
+            load(key, (n >> 1) < stages);
         };
-        {
-            int first[S::kAhead];
+        constexpr bool kOdd = S::kSlots % 2 != 0;
+        using First = std::integral_constant<bool, kOdd>;    // keys where kSlots is odd: copy 2i + kSlots − 1
+        using Second = std::integral_constant<bool, !kOdd>;  // copy 2i + kSlots
 #pragma unroll
-            for (int i = 0; i < S::kAhead; ++i) first[i] = page_of(i);
-#pragma unroll
-            for (int n = 0; n < S::kSlots - 1; ++n) {
-                if ((n & 1) == 0) {
-                    find(n >> 1, first[n >> 1]);
-                    put_scales();
-                }
-                load((n & 1) == 0, (n >> 1) < stages);
+        for (int n = 0; n < S::kSlots - 1; ++n) {
+            if ((n & 1) == 0) {
+                find(n >> 1, first[n >> 1]);
+                put_scales();
+                load(std::true_type(), (n >> 1) < stages);
+            } else {
+                load(std::false_type(), (n >> 1) < stages);
             }
-            asked = S::kSlots / 2;
-            pend_at = -1;
-            page_next = page_of(asked);
         }
+        pend_at = -1;
+        int page_next = page_of(asked);
 
-        // ---- queries of the thread's rows g and g + 8
-        uint32_t q[KS][4];
-        int see_lo[2], see_hi[2];   // tokens that a row sees
-        float row_scale[2] = {sp.scale_log2, sp.scale_log2};
-        {
-            const __nv_bfloat16* src[2];
-            bool live[2];
+        float row_scale[2] = {sp.scale_log2, sp.scale_log2};  // of scores, to base 2
+        if (!Q8) {
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) q[ks][x] ^= sp.flip;
+        } else {
+            // As fp16, after a division of the row by a power of two near its largest value.
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-                const int r = row0 + rw * 16 + g + 8 * x, j = r / G;
-                live[x] = r < rows;
-                see_hi[x] = live[x] ? rq.len - rq.n + j + 1 : 0x7fffffff;
-                see_lo[x] = live[x] && a.window > 0 ? static_cast<int>(max(0ll, static_cast<long long>(see_hi[x]) - a.window)) : 0;
-                src[x] = a.q.data + (live[x] ? (rq.start + j) * a.q.token_stride + (h * G + r % G) * a.q.head_stride : 0);
-            }
-            if (!Q8) {
+                float most = 0.f;
 #pragma unroll
-                for (int ks = 0; ks < KS; ++ks)
+                for (int ks = 0; ks < KS; ++ks) {
+                    const uint2 w = raw[Q8 ? x : 0][Q8 ? ks : 0];
+                    most = fmaxf(most, fmaxf(fmaxf(fabsf(bf16_lo(w.x)), fabsf(bf16_hi(w.x))), fmaxf(fabsf(bf16_lo(w.y)), fabsf(bf16_hi(w.y)))));
+                }
+                most = quad_max(most);
+                const int e = min(max(static_cast<int>(__float_as_uint(most) >> 23), 7), 247) - 127;
+                const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+                row_scale[x] *= __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const int k = ks * 16 + 2 * t4 + 8 * (x >> 1);
-                        q[ks][x] = live[x & 1] && k < a.head_dim ? *reinterpret_cast<const uint32_t*>(src[x & 1] + k) : 0u;
-                    }
-            } else {
-                // Four values in a row for each k-step and lane, like the keys' codes below; as fp16 after a
-                // division of the row by a power of two near its largest value.
-                uint2 w[2][KS];
-                float most[2] = {0.f, 0.f};
-#pragma unroll
-                for (int x = 0; x < 2; ++x)
-#pragma unroll
-                    for (int ks = 0; ks < KS; ++ks) {
-                        const int k = (ks >> 2) * 64 + t4 * 16 + (ks & 3) * 4;
-                        w[x][ks] = live[x] && k < a.head_dim ? *reinterpret_cast<const uint2*>(src[x] + k) : make_uint2(0, 0);
-                        most[x] = fmaxf(most[x], fmaxf(fmaxf(fabsf(bf16_lo(w[x][ks].x)), fabsf(bf16_hi(w[x][ks].x))),
-                                                       fmaxf(fabsf(bf16_lo(w[x][ks].y)), fabsf(bf16_hi(w[x][ks].y)))));
-                    }
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    most[x] = quad_max(most[x]);
-                    const int e = min(max(static_cast<int>(__float_as_uint(most[x]) >> 23), 7), 247) - 127;
-                    const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-                    row_scale[x] *= __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-#pragma unroll
-                    for (int ks = 0; ks < KS; ++ks) {
-                        q[ks][x] = pack_f16(bf16_lo(w[x][ks].x) * down, bf16_hi(w[x][ks].x) * down);
-                        q[ks][x + 2] = pack_f16(bf16_lo(w[x][ks].y) * down, bf16_hi(w[x][ks].y) * down);
-                    }
+                for (int ks = 0; ks < KS; ++ks) {
+                    const uint2 w = raw[Q8 ? x : 0][Q8 ? ks : 0];
+                    q[ks][x] = pack_f16(bf16_lo(w.x) * down, bf16_hi(w.x) * down) ^ sp.flip;
+                    q[ks][x + 2] = pack_f16(bf16_lo(w.y) * down, bf16_hi(w.y) * down) ^ sp.flip;
                 }
             }
         }
         // Tokens before all_hi and from all_lo on are seen by every row of the warp.
         int all_hi, all_lo;
         {
-            const int j0 = (row0 + rw * 16) / G, j1 = max(min(row0 + rw * 16 + 15, rows - 1), 0) / G;
+            const int j0 = over_G(row0 + rw * 16), j1 = over_G(max(min(row0 + rw * 16 + 15, rows - 1), 0));
             all_hi = rq.len - rq.n + j0 + 1;
             all_lo = a.window > 0 ? static_cast<int>(max(0ll, static_cast<long long>(rq.len) - rq.n + j1 + 1 - a.window)) : 0;
         }
@@ -442,16 +518,17 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
         for (int i = 0; i < NT; ++i)
 #pragma unroll
             for (int x = 0; x < 4; ++x) o[i][x] = 0.f;
+        // Format 16: the reference score, unscaled, and the sum of the weights 2^(row_scale · (s − m)).
+        // Format 8: the reference of score + log2(value scale), to base 2: the weights times their value scales are
+        // near 1 whatever the scales; the sum is that of the weights by the same reference.
         float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-        float mw[2] = {-INFINITY, -INFINITY};  // Q8: largest score + log2(value scale), the weights' reference
 
         int get = 0;
         for (int i = 0; i < stages; ++i) {
             cp_async_wait<S::kSlots - 2>();
-            put_scales();
+            if (!kOdd) put_scales();
             group_sync<R>(group);
-            pend_at = -1;
-            load_next(2 * i + S::kSlots - 1);
+            load_next(First(), page_next, 2 * i + S::kSlots - 1);
             const int base = tok0 + (i * S::kGroups + group) * S::kTokens;
             const uint32_t keys = ring + get * S::kHalf;
             if (++get == S::kSlots) get = 0;
@@ -466,104 +543,101 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
 #pragma unroll
                 for (int x = 0; x < 4; ++x) s[y][x] = 0.f;
             if (!Q8) {
+                // token (lane >> 4) · 8 + (lane & 7), chunk 2·ks + ((lane >> 3) & 1)
+                const uint32_t from = keys + ((lane >> 4) * 8 + (lane & 7)) * kRow + ((((lane >> 3) & 1) ^ (lane & 7)) << 4);
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
                     for (int sub = 0; sub < S::kSub; ++sub) {
                         uint32_t k[4];
-                        const int r = sub * 16 + (lane >> 4) * 8 + (lane & 7), c = ks * 2 + ((lane >> 3) & 1);
-                        ldmatrix_x4(keys + place<D, Q8, true>(r, c), k);
+                        ldmatrix_x4((from ^ ((ks & 3) << 5)) + (ks >> 2) * 128 + sub * 16 * kRow, k);
                         mma16816<false>(s[2 * sub], q[ks], k[0], k[1]);
                         mma16816<false>(s[2 * sub + 1], q[ks], k[2], k[3]);
                     }
             } else {
+                // token 8·y + g, chunk 4·kb + t4: four k-steps of two pairs
+                const uint32_t from = keys + g * kRow + ((t4 ^ turn<kRow, Q8, true>(g)) << 4);
 #pragma unroll
                 for (int kb = 0; kb < KS / 4; ++kb)
 #pragma unroll
                     for (int y = 0; y < 2 * S::kSub; ++y) {
-                        uint4 w = lds128(keys + place<D, Q8, true>(y * 8 + g, kb * 4 + t4));
+                        const uint4 w = lds128((from ^ ((kb & 1) << 6)) + (kb >> 1) * 128 + y * 8 * kRow);
                         const uint32_t u[4] = {w.x ^ 0x80808080u, w.y ^ 0x80808080u, w.z ^ 0x80808080u, w.w ^ 0x80808080u};
 #pragma unroll
                         for (int x = 0; x < 4; ++x)
                             mma16816<true>(s[y], q[kb * 4 + x], codes_f16(u[x], 0x4140), codes_f16(u[x], 0x4342));
                     }
             }
-            float lv[2 * S::kSub][2];  // log2 of the value scales of the lane's tokens
+            float inv[2 * S::kSub][2];  // 1 / value scale of the lane's tokens
+            if (Q8) {
 #pragma unroll
-            for (int y = 0; y < 2 * S::kSub; ++y) {
-                float ks0 = 1.f, ks1 = 1.f;
-                if (Q8) {
+                for (int y = 0; y < 2 * S::kSub; ++y) {
                     const float4 f = *reinterpret_cast<const float4*>(stage_scales + y * 8 + 2 * t4);
-                    ks0 = f.x, lv[y][0] = f.y, ks1 = f.z, lv[y][1] = f.w;
+                    s[y][0] = fmaf(s[y][0], row_scale[0] * f.x, f.y);
+                    s[y][1] = fmaf(s[y][1], row_scale[0] * f.z, f.w);
+                    s[y][2] = fmaf(s[y][2], row_scale[1] * f.x, f.y);
+                    s[y][3] = fmaf(s[y][3], row_scale[1] * f.z, f.w);
+                    // A number even where the scale is none: a hidden token's weight of 0 makes it 0 then.
+                    inv[y][0] = fminf(ex2(-f.y), 3e38f);
+                    inv[y][1] = fminf(ex2(-f.w), 3e38f);
                 }
-                s[y][0] *= row_scale[0] * ks0;
-                s[y][1] *= row_scale[0] * ks1;
-                s[y][2] *= row_scale[1] * ks0;
-                s[y][3] *= row_scale[1] * ks1;
             }
             // Some row does not see some token of the stage; there are such tokens, too, past the end.
             const bool hidden = min(base + S::kTokens, tok1) > all_hi || base < all_lo;
             const bool partly = hidden || base + S::kTokens > tok1;
-            auto sees = [&](int y, int x) {
-                const int tok = base + y * 8 + 2 * t4 + (x & 1);
-                return tok < min(see_hi[x >> 1], tok1) && tok >= see_lo[x >> 1];
-            };
             if (partly) {
 #pragma unroll
                 for (int y = 0; y < 2 * S::kSub; ++y)
 #pragma unroll
-                    for (int x = 0; x < 4; ++x)
-                        if (!sees(y, x)) s[y][x] = -INFINITY;
+                    for (int x = 0; x < 4; ++x) {
+                        const int tok = base + y * 8 + 2 * t4 + (x & 1);
+                        if (tok >= min(see_hi[x >> 1], tok1) || tok < see_lo[x >> 1]) s[y][x] = -INFINITY;
+                    }
             }
 
-            // ---- running maximum
-            float grown[2] = {m[0], m[1]}, grown_w[2] = {mw[0], mw[1]};
+            // ---- reference
+            float grown[2] = {m[0], m[1]};
 #pragma unroll
             for (int y = 0; y < 2 * S::kSub; ++y)
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    grown[x >> 1] = fmaxf(grown[x >> 1], s[y][x]);
-                    if (Q8) grown_w[x >> 1] = fmaxf(grown_w[x >> 1], s[y][x] == -INFINITY ? -INFINITY : s[y][x] + lv[y][x & 1]);
-                }
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                grown[x] = quad_max(grown[x]);
-                if (Q8) grown_w[x] = quad_max(grown_w[x]);
-            }
-            // It grows in the first few stages and seldom after them.
-            const bool grew = grown[0] > m[0] || grown[1] > m[1] || (Q8 && (grown_w[0] > mw[0] || grown_w[1] > mw[1]));
-            if (__any_sync(~0u, grew)) {
+                for (int x = 0; x < 4; ++x) grown[x >> 1] = fmaxf(grown[x >> 1], s[y][x]);
+            grown[0] = quad_max(grown[0]);
+            grown[1] = quad_max(grown[1]);
+            const float by0 = (grown[0] - m[0]) * (Q8 ? 1.f : row_scale[0]), by1 = (grown[1] - m[1]) * (Q8 ? 1.f : row_scale[1]);
+            if (__any_sync(~0u, by0 > 8.f || by1 > 8.f)) {
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    const float keep_l = m[x] == -INFINITY ? 0.f : ex2(m[x] - grown[x]);
-                    const float keep_o = !Q8 ? keep_l : mw[x] == -INFINITY ? 0.f : ex2(mw[x] - grown_w[x]);
-                    l[x] *= keep_l;
+                    const float keep = m[x] == -INFINITY ? 0.f : ex2(x ? -by1 : -by0);
+                    l[x] = fminf(l[x], 3e38f) * keep;
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
-                        o[n][2 * x] *= keep_o;
-                        o[n][2 * x + 1] *= keep_o;
+                        o[n][2 * x] *= keep;
+                        o[n][2 * x + 1] *= keep;
                     }
                     m[x] = grown[x];
-                    mw[x] = grown_w[x];
                 }
             }
             // ---- weights
-            const float ref[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
-            const float refw[2] = {mw[0] == -INFINITY ? 0.f : mw[0], mw[1] == -INFINITY ? 0.f : mw[1]};
+            const float ref[2] = {m[0] == -INFINITY ? 0.f : m[0] * (Q8 ? 1.f : row_scale[0]),
+                                  m[1] == -INFINITY ? 0.f : m[1] * (Q8 ? 1.f : row_scale[1])};
 #pragma unroll
             for (int y = 0; y < 2 * S::kSub; ++y)
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
-                    const float p = ex2(s[y][x] - ref[x >> 1]);
-                    l[x >> 1] += p;
-                    s[y][x] = !Q8 ? p : s[y][x] == -INFINITY ? 0.f : ex2(s[y][x] + lv[y][x & 1] - refw[x >> 1]);
+                    if (Q8) {
+                        s[y][x] = ex2(s[y][x] - ref[x >> 1]);
+                        l[x >> 1] = fmaf(s[y][x], inv[y][x & 1], l[x >> 1]);
+                    } else {
+                        s[y][x] = ex2(fmaf(s[y][x], row_scale[x >> 1], -ref[x >> 1]));
+                        l[x >> 1] += s[y][x];
+                    }
                 }
+
             // ---- values
             cp_async_wait<S::kSlots - 2>();
-            if (S::kSlots % 2 != 0) put_scales();
+            if (kOdd) put_scales();
             group_sync<R>(group);
-            if (S::kSlots % 2 != 0) pend_at = -1;
-            load_next(2 * i + S::kSlots);
+            load_next(Second(), page_next, 2 * i + S::kSlots);
             if (!Q8) {
                 bool odd = false;  // a value that is not finite, in tokens that some rows do not see
                 if (hidden) {
@@ -589,14 +663,15 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
 #pragma unroll
                                 for (int e = 0; e < 2; ++e)
                                     if (y == tk >> 3 && e == (tk & 1)) v = s[y][2 * x + e];
-                            // The shuffle's source lane holds the same column's parity, so v is chosen alike there.
                             p[x] = __shfl_sync(~0u, v, from);
                             seen[x] = base + tk < min(see_hi[x], tok1) && base + tk >= see_lo[x];
                         }
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
                             uint32_t w;
-                            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(vals + place<D, Q8, false>(tk, n) + 4 * t4));
+                            asm volatile("ld.shared.u32 %0, [%1];"
+                                         : "=r"(w)
+                                         : "r"(vals + tk * kRow + ((n ^ turn<kRow, Q8, false>(tk)) << 4) + 4 * t4));
 #pragma unroll
                             for (int x = 0; x < 2; ++x)
                                 if (seen[x]) {
@@ -616,13 +691,14 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
                             hi[sub][x] = pack_bf16(p0, p1);
                             lo[sub][x] = pack_bf16(p0 - bf16_lo(hi[sub][x]), p1 - bf16_hi(hi[sub][x]));
                         }
+                    // token ((lane >> 3) & 1) · 8 + (lane & 7), chunk 2·n + (lane >> 4)
+                    const uint32_t from = vals + (((lane >> 3) & 1) * 8 + (lane & 7)) * kRow + (((lane >> 4) ^ (lane & 7)) << 4);
 #pragma unroll
                     for (int n = 0; n < NT / 2; ++n)
 #pragma unroll
                         for (int sub = 0; sub < S::kSub; ++sub) {
                             uint32_t v[4];
-                            const int r = sub * 16 + ((lane >> 3) & 1) * 8 + (lane & 7), c = n * 2 + (lane >> 4);
-                            ldmatrix_x4_trans(vals + place<D, Q8, false>(r, c), v);
+                            ldmatrix_x4_trans((from ^ ((n & 3) << 5)) + (n >> 2) * 128 + sub * 16 * kRow, v);
                             mma16816<false>(o[2 * n], hi[sub], v[0], v[1]);
                             mma16816<false>(o[2 * n + 1], hi[sub], v[2], v[3]);
                             mma16816<false>(o[2 * n], lo[sub], v[0], v[1]);
@@ -630,33 +706,33 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
                         }
                 }
             } else {
-                // Weights times value scales, at most 1 by their own reference, as fp16 (2⁻¹¹): an eighth of the
-                // result's rounding.
+                // Weights times value scales as fp16 (2⁻¹¹): an eighth of the result's rounding.
 #pragma unroll
                 for (int sub = 0; sub < S::kSub; ++sub) {
                     uint32_t p[4];
 #pragma unroll
                     for (int x = 0; x < 4; ++x)
                         p[x] = pack_f16(s[2 * sub + (x >> 1)][2 * (x & 1)], s[2 * sub + (x >> 1)][2 * (x & 1) + 1]);
-                    // Column n of output tile i is value 16·n + i (8·n + i for D = 64) of the row: a lane's
+                    // Column n of output tile i is value 16·n + i (8·n + i for D = 64) of the row's 128: a lane's
                     // 16 (8) bytes of a token row are its column of 16 (8) tiles.
                     constexpr int kBytes = D == 64 ? 8 : 16;
+                    const int chunk = D == 64 ? g >> 1 : g;
+                    const uint32_t from = vals + 2 * t4 * kRow + ((chunk ^ turn<kRow, Q8, false>(2 * t4)) << 4) + (D == 64 ? 8 * (g & 1) : 0);
 #pragma unroll
                     for (int hb = 0; hb < NT / kBytes; ++hb) {
                         uint32_t w[4][kBytes / 4];
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            const int r = sub * 16 + 2 * t4 + (x & 1) + 8 * (x >> 1);
+                        for (int x = 0; x < 4; ++x) {  // token 16·sub + 2·t4 + (x & 1) + 8·(x >> 1)
+                            const int r = (x & 1) + 8 * (x >> 1);
+                            const uint32_t at = (from ^ (turn<kRow, Q8, false>(r & 1) << 4)) + (sub * 16 + r) * kRow + hb * 128;
                             if (kBytes == 16) {
-                                const uint4 v = lds128(vals + place<D, Q8, false>(r, hb * 8 + g));
+                                const uint4 v = lds128(at);
                                 w[x][0] = v.x ^ 0x80808080u;
                                 w[x][1] = v.y ^ 0x80808080u;
                                 w[x][kBytes / 4 - 2] = v.z ^ 0x80808080u;
                                 w[x][kBytes / 4 - 1] = v.w ^ 0x80808080u;
                             } else {
-                                asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
-                                             : "=r"(w[x][0]), "=r"(w[x][1])
-                                             : "r"(vals + place<D, Q8, false>(r, g >> 1) + 8 * (g & 1)));
+                                asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[x][0]), "=r"(w[x][1]) : "r"(at));
                                 w[x][0] ^= 0x80808080u;
                                 w[x][1] ^= 0x80808080u;
                             }
@@ -677,17 +753,16 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
         }
         cp_async_wait<0>();
 
-        // ---- the groups' sums meet in shared memory: [warp][16 rows][D], then m, mw, l of each row
+        // ---- the groups' sums meet in shared memory: [warp][16 rows][D], then the reference and sum of each row
         __syncthreads();
         float* s_o = reinterpret_cast<float*>(smem);
-        float* s_stat = s_o + kWarps * 16 * D;  // [3][warp][16]
+        float* s_stat = s_o + kWarps * 16 * D;  // [2][warp][16]
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
             l[x] = quad_sum(l[x]);
             if (t4 == 0) {
-                s_stat[warp * 16 + g + 8 * x] = m[x];
-                s_stat[kWarps * 16 + warp * 16 + g + 8 * x] = Q8 ? mw[x] : m[x];
-                s_stat[2 * kWarps * 16 + warp * 16 + g + 8 * x] = l[x];
+                s_stat[warp * 16 + g + 8 * x] = m[x] * (Q8 ? 1.f : row_scale[x]);
+                s_stat[kWarps * 16 + warp * 16 + g + 8 * x] = fminf(l[x], 3e38f);
             }
         }
 #pragma unroll
@@ -699,104 +774,139 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
                 s_o[(warp * 16 + g + 8 * (x >> 1)) * D + col] = o[n][x];
             }
         __syncthreads();
+
+        // A row's output: `v` its values times the sum `l` of its weights.  A row that sees nothing is zeros; one
+        // whose scores are all −∞ has no value (0 / 0).
+        auto put_row = [&](int row, int col, const float* v, int n, float l) {
+            const int j = over_G(row);
+            const float f = rq.len - rq.n + j < 0 ? 0.f : 1.f / l;
+            __nv_bfloat16* to = a.out.data + (rq.start + j) * a.out.token_stride + (h * G + row - j * G) * a.out.head_stride + col;
+            for (int x = 0; x < n; x += 2) *reinterpret_cast<uint32_t*>(to + x) = pack_bf16(v[x] * f, v[x + 1] * f);
+        };
         const bool whole = tile0 == 0 && tile1 == rq.tiles;
-        float* part = sp.partial + (2 * static_cast<size_t>(blockIdx.x) + (tile0 > 0 ? 0 : 1)) * partial_floats(R, D);
+        // Parts of a shared item: piece p0 (which has its first tile) and those after it; a piece's first item
+        // leaves its sums in slot 0, its last in slot 1.
+        const int p0 = whole ? 0 : cut.piece(item + kFixed), k_own = static_cast<int>(blockIdx.x) - p0;
+        const int parts = whole ? 1 : cut.piece(item + weight - 1) - p0 + 1;
+        auto part = [&](int k) { return sp.partial + (2 * static_cast<size_t>(p0 + k) + (k == 0)) * partial_floats(R, D); };
         for (int x = tid; x < 16 * R * (D / 4); x += kThreads) {
             const int r = x / (D / 4), col = x % (D / 4) * 4, row = row0 + r;
             if (row >= rows || col >= a.head_dim) continue;
-            float mm = -INFINITY, mmw = -INFINITY;
+            float mm = -INFINITY;
 #pragma unroll
-            for (int k = 0; k < S::kGroups; ++k) {
-                mm = fmaxf(mm, s_stat[(k * R * 16) + r]);
-                mmw = fmaxf(mmw, s_stat[kWarps * 16 + k * R * 16 + r]);
-            }
-            const float rm = mm == -INFINITY ? 0.f : mm, rmw = mmw == -INFINITY ? 0.f : mmw;
+            for (int k = 0; k < S::kGroups; ++k) mm = fmaxf(mm, s_stat[k * R * 16 + r]);
+            const float rm = mm == -INFINITY ? 0.f : mm;
             float ll = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int k = 0; k < S::kGroups; ++k) {
-                ll += ex2(s_stat[k * R * 16 + r] - rm) * s_stat[2 * kWarps * 16 + k * R * 16 + r];
-                const float f = ex2(s_stat[kWarps * 16 + k * R * 16 + r] - rmw);
+                const float f = ex2(s_stat[k * R * 16 + r] - rm);
                 const float4 w = *reinterpret_cast<const float4*>(s_o + (k * R * 16 + r) * D + col);
+                ll += f * s_stat[kWarps * 16 + k * R * 16 + r];
                 v[0] += f * w.x, v[1] += f * w.y, v[2] += f * w.z, v[3] += f * w.w;
             }
             if (whole) {
-                const int j = row / G;
-                // A row that sees nothing is zeros; one whose scores are all −∞ has no value (0 / 0).
-                const float f = rq.len - rq.n + j < 0 ? 0.f : (mmw == -INFINITY ? 0.f : ex2(mmw - mm)) / ll;
-                uint2 y = make_uint2(pack_bf16(v[0] * f, v[1] * f), pack_bf16(v[2] * f, v[3] * f));
-                *reinterpret_cast<uint2*>(a.out.data + (rq.start + j) * a.out.token_stride +
-                                          (h * G + row % G) * a.out.head_stride + col) = y;
+                put_row(row, col, v, 4, ll);
             } else {
+                float* to = part(k_own);
                 if (col == 0) {
-                    part[r] = mm;
-                    part[16 * R + r] = mmw;
-                    part[32 * R + r] = ll;
+                    to[r] = mm;
+                    to[16 * R + r] = fminf(ll, 3e38f);
                 }
-                *reinterpret_cast<float4*>(part + 48 * R + r * D + col) = make_float4(v[0], v[1], v[2], v[3]);
+                *reinterpret_cast<float4*>(to + 32 * R + r * D + col) = make_float4(v[0], v[1], v[2], v[3]);
             }
         }
-        if (tid == 0 && tile0 == 0 && tile1 < rq.tiles) {
-            // The item's last unit is that before the next item; CTA c has the units from ⌊c·total / ctas⌋ on.
-            const long long u = at - 1;
-            sp.carried[blockIdx.x] = {static_cast<int>(((u + 1) * ctas - 1) / total), h, row0, rows, rq.start, rq.len - rq.n};
-        }
         __syncthreads();
-    }
-}
+        if (whole) continue;
 
-// Joins the parts of the item that begins in CTA blockIdx.x and ends in a
-// later one: its own second part, the later CTAs' first.  A CTA takes one row;
-// its warps take the parts in turn, each with a running maximum of its own.
-template <int D, int R>
-__global__ void __launch_bounds__(kThreads) attn_join_kernel(const __grid_constant__ SplitArgs sp) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const Carried c = sp.carried[blockIdx.x];
-    const int r = blockIdx.y;
-    if (c.last < 0 || c.row0 + r >= c.rows) return;
-    const AttnArgs& a = sp.a;
-    const int G = a.q_heads / a.kv_heads;
-    constexpr int V = D / 32;
-    constexpr size_t size = partial_floats(R, D);
-    const int parts = c.last - static_cast<int>(blockIdx.x) + 1;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    __shared__ float s_m[kWarps], s_mw[kWarps], s_l[kWarps], s_v[kWarps][D];
-    float mm = -INFINITY, mmw = -INFINITY, ll = 0.f, v[V];
+        // ---- the last part of a group of sixteen to get here joins the group, the last group the item
+        constexpr int V = D / 32;  // neighbouring values of a lane
+        // A warp joins NP parts of 16 / NP rows at a time, all loads at once: parts k0, k0 + step, ... (n of them) into
+        // the output or into part k0.
+        auto join_rows = [&](auto np, int k0, int n, int step, bool last) {
+            constexpr int NP = decltype(np)::value, NR = 16 / NP;
+            const int y_lane = (lane & 15) / NP, i_lane = lane & (NP - 1);
+            for (int r = warp * NR; r < 16 * R && row0 + r < rows; r += kWarps * NR) {
+                float mm = -INFINITY, ll = 0.f, v[NR][V];  // mm, ll: of the lane's row
 #pragma unroll
-    for (int x = 0; x < V; ++x) v[x] = 0.f;
-#pragma unroll 4
-    for (int k = warp; k < parts; k += kWarps) {
-        const float* p = sp.partial + (2 * (static_cast<size_t>(blockIdx.x) + k) + (k == 0)) * size;
-        const float pm = p[r], pmw = p[16 * R + r], pl = p[32 * R + r];
-        float pv[V];
+                for (int y = 0; y < NR; ++y)
 #pragma unroll
-        for (int x = 0; x < V; ++x) pv[x] = lane + 32 * x < a.head_dim ? p[48 * R + r * D + lane + 32 * x] : 0.f;
-        const float nm = fmaxf(mm, pm), nw = fmaxf(mmw, pmw);
-        const float rm = nm == -INFINITY ? 0.f : nm, rw = nw == -INFINITY ? 0.f : nw;
-        ll = ll * ex2(mm - rm) + pl * ex2(pm - rm);
-        const float keep = ex2(mmw - rw), f = ex2(pmw - rw);
+                    for (int x = 0; x < V; ++x) v[y][x] = 0.f;
+                for (int i0 = 0; i0 < n; i0 += NP) {
+                    // lanes 0 to 15: the references, 16 to 31: the sums
+                    const bool there = i0 + i_lane < n;
+                    const float stat = there ? __ldcg(part(k0 + (i0 + i_lane) * step) + (lane < 16 ? 0 : 16 * R) + r + y_lane) : -INFINITY;
+                    float w[NR][NP][V];
 #pragma unroll
-        for (int x = 0; x < V; ++x) v[x] = v[x] * keep + pv[x] * f;
-        mm = nm, mmw = nw;
-    }
-    if (lane == 0) s_m[warp] = mm, s_mw[warp] = mmw, s_l[warp] = ll;
+                    for (int i = 0; i < NP; ++i) {
+                        const float* p = part(k0 + min(i0 + i, n - 1) * step) + 32 * R + r * D + lane * V;
 #pragma unroll
-    for (int x = 0; x < V; ++x) s_v[warp][lane + 32 * x] = v[x];
-    __syncthreads();
-    mm = mmw = -INFINITY;
+                        for (int y = 0; y < NR; ++y)
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, s_m[w]), mmw = fmaxf(mmw, s_mw[w]);
-    const float rm = mm == -INFINITY ? 0.f : mm, rw = mmw == -INFINITY ? 0.f : mmw;
-    ll = 0.f;
+                            for (int x = 0; x < V; x += 2) {
+                                const float2 f = __ldcg(reinterpret_cast<const float2*>(p + y * D + x));
+                                w[y][i][x] = f.x, w[y][i][x + 1] = f.y;
+                            }
+                    }
+                    const float pm = __shfl_sync(~0u, stat, lane & 15), pl = __shfl_sync(~0u, stat, (lane & 15) + 16);
+                    float nm = fmaxf(mm, pm);
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) ll += s_l[w] * ex2(s_m[w] - rm);
-    const int row = c.row0 + r, j = row / G;
-    const float f = c.before + j < 0 ? 0.f : (mmw == -INFINITY ? 0.f : ex2(mmw - mm)) / ll;
-    __nv_bfloat16* out = a.out.data + (c.start + j) * a.out.token_stride + (c.head * G + row % G) * a.out.head_stride;
-    for (int col = threadIdx.x; col < a.head_dim; col += kThreads) {
-        float y = 0.f;
+                    for (int d = 1; d < NP; d <<= 1) nm = fmaxf(nm, __shfl_xor_sync(~0u, nm, d));
+                    const float rm = nm == -INFINITY ? 0.f : nm, keep = ex2(mm - rm), f = there ? ex2(pm - rm) : 0.f;
+                    float fl = there ? f * pl : 0.f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) y += s_v[w][col] * ex2(s_mw[w] - rw);
-        out[col] = __float2bfloat16_rn(y * f);
+                    for (int d = 1; d < NP; d <<= 1) fl += __shfl_xor_sync(~0u, fl, d);
+                    ll = ll * keep + fl;
+                    mm = nm;
+#pragma unroll
+                    for (int y = 0; y < NR; ++y) {
+                        const float k = __shfl_sync(~0u, keep, y * NP);
+#pragma unroll
+                        for (int x = 0; x < V; ++x) v[y][x] *= k;
+#pragma unroll
+                        for (int i = 0; i < NP; ++i) {
+                            const float fi = __shfl_sync(~0u, f, y * NP + i);
+#pragma unroll
+                            for (int x = 0; x < V; ++x) v[y][x] = i0 + i < n ? fmaf(fi, w[y][i][x], v[y][x]) : v[y][x];
+                        }
+                    }
+                }
+#pragma unroll
+                for (int y = 0; y < NR; ++y) {
+                    const float l_row = __shfl_sync(~0u, ll, y * NP), m_row = __shfl_sync(~0u, mm, y * NP);
+                    if (row0 + r + y >= rows) continue;
+                    if (last) {
+                        if (lane * V < a.head_dim) put_row(row0 + r + y, lane * V, v[y], V, l_row);
+                    } else {
+                        float* to = part(k0);
+                        if (lane == 0) to[r + y] = m_row, to[16 * R + r + y] = fminf(l_row, 3e38f);
+#pragma unroll
+                        for (int x = 0; x < V; ++x) to[32 * R + (r + y) * D + lane * V + x] = v[y][x];
+                    }
+                }
+            }
+        };
+        auto join = [&](int k0, int n, int step, bool last) {
+            if (n <= 4)
+                join_rows(std::integral_constant<int, 4>(), k0, n, step, last);
+            else
+                join_rows(std::integral_constant<int, 16>(), k0, n, step, last);
+        };
+        const int k_group = k_own / kJoinGroup * kJoinGroup, in_group = min(kJoinGroup, parts - k_group);
+        const int groups = (parts + kJoinGroup - 1) / kJoinGroup;
+        if (in_group > 1) {
+            if (tid == 0) s_last = arrive(sp.arrived + p0 + k_group, in_group);
+            __syncthreads();
+            const bool last = s_last;
+            if (last) join(k_group, in_group, 1, groups == 1);
+            __syncthreads();
+            if (!last) continue;
+        }
+        if (groups > 1) {
+            if (tid == 0) s_last = arrive(sp.arrived + kMaxCtas + p0, groups);
+            __syncthreads();
+            if (s_last) join(0, groups, kJoinGroup, true);
+            __syncthreads();
+        }
     }
 }
 
@@ -826,27 +936,29 @@ cudaError_t run(SplitArgs sp, void* workspace, const DeviceInfo& dev, cudaStream
         if (per_sm < 1) return cudaErrorInvalidConfiguration;
         known[device & (kMaxDevices - 1)].store(per_sm, std::memory_order_relaxed);
     }
-    const int grid = std::min(per_sm * dev.sm_count, kMaxCtas);
-    sp.carried = static_cast<Carried*>(workspace);
-    sp.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kMaxCtas * 32);
-    attn_split_kernel<D, Q8, R><<<grid, kThreads, S::kSmem, stream>>>(sp);
-    err = cudaGetLastError();
-    if (err != cudaSuccess) return err;
+    sp.arrived = static_cast<unsigned long long*>(workspace);
+    sp.partial = reinterpret_cast<float*>(sp.arrived + 2 * kMaxCtas);
+    // At least as many units as the batch can have: a CTA for each, where they are few.
+    const AttnArgs& a = sp.a;
+    const double reach = std::min(static_cast<double>(a.width) * a.page_size, a.window > 0 ? static_cast<double>(a.window) + a.T : 1e18);
+    const double most = static_cast<double>(a.kv_heads) * (a.B + static_cast<double>(a.T) * sp.G / (16 * R)) * (reach / kTile + 2 + kFixed);
+    const int grid = static_cast<int>(std::min<double>(std::min(per_sm * dev.sm_count, kMaxCtas), most));
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid, 16 * R);
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
     cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = S::kSmem;
     cfg.stream = stream;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attn_join_kernel<D, R>, sp);
+    return cudaLaunchKernelEx(&cfg, attn_split_kernel<D, Q8, R>, sp);
 }
 
 template <int D, bool Q8>
 cudaError_t run_rows(const SplitArgs& sp, void* workspace, const DeviceInfo& dev, cudaStream_t stream) {
-    const int R = row_warps(sp.a.B, sp.a.T, sp.a.q_heads / sp.a.kv_heads);
+    const int R = row_warps(sp.a.B, sp.a.T, sp.G);
     if (R == 1) return run<D, Q8, 1>(sp, workspace, dev, stream);
     if (R == 2) return run<D, Q8, 2>(sp, workspace, dev, stream);
     return run<D, Q8, 4>(sp, workspace, dev, stream);
@@ -863,16 +975,21 @@ cudaError_t run_dim(const SplitArgs& sp, void* workspace, const DeviceInfo& dev,
 }  // namespace
 
 size_t attn_decode_workspace_bytes(int32_t B, int64_t T, int32_t q_heads, int32_t kv_heads, int32_t head_dim) {
-    static_assert(sizeof(Carried) <= 32, "a CTA's record fits its place in the workspace");
     const int R = B > 0 ? row_warps(B, T, q_heads / kv_heads) : 1;
-    return kMaxCtas * 32 + 2 * kMaxCtas * partial_floats(R, dim_of(head_dim)) * sizeof(float);
+    return 2 * kMaxCtas * (sizeof(unsigned long long) + partial_floats(R, dim_of(head_dim)) * sizeof(float));
 }
 
 cudaError_t launch_attn_decode(AttnArgs a, bool q8, void* workspace, const DeviceInfo& dev, cudaStream_t stream) {
     divide_by(a.page_size, &a.page_mul, &a.page_shift);
     SplitArgs sp = {};
     sp.a = a;
-    sp.scale_log2 = a.scale * 1.4426950408889634f;
+    sp.G = a.q_heads / a.kv_heads;
+    divide_by(sp.G, &sp.G_mul, &sp.G_shift);
+    sp.rows_each = static_cast<int>(a.T / a.B);
+    // A factor below zero turns the queries' signs over, and one of zero is one so small that every weight is 1: the
+    // largest score is then that of the unscaled products, and hidden ones stay at −∞.
+    sp.scale_log2 = std::max(std::fabs(a.scale) * 1.4426950408889634f, 1e-30f);
+    sp.flip = a.scale < 0.f ? 0x80008000u : 0u;
     return q8 ? run_dim<true>(sp, workspace, dev, stream) : run_dim<false>(sp, workspace, dev, stream);
 }
 
