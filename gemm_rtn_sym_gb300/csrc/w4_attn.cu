@@ -44,7 +44,6 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kTile = 64;       // tokens of a unit of work
-constexpr int kFixed = 3;       // an item's fixed cost (its first loads' latency, its sums' way out), in units
 constexpr int kJoinGroup = 16;  // parts of an item that are joined at once
 constexpr int kMaxLength = 0x7fff0000;  // token numbers a little past a length stay below 2³¹
 constexpr int kMaxDevices = 64;         // as many as the library knows (device_info refuses others)
@@ -168,10 +167,10 @@ __device__ __forceinline__ Request request(const SplitArgs& sp, int b, int rows_
     return r;
 }
 
-// Units of work of a request: each item (head, row tile) counts kFixed units
+// Units of work of a request: each item (head, row tile) counts `fixed` units
 // and then one for each of its tiles.
-__device__ __forceinline__ long long units(const AttnArgs& a, const Request& r) {
-    return static_cast<long long>(a.kv_heads) * r.row_tiles * (r.tiles + kFixed);
+__device__ __forceinline__ long long units(const AttnArgs& a, const Request& r, int fixed) {
+    return static_cast<long long>(a.kv_heads) * r.row_tiles * (r.tiles + fixed);
 }
 
 __device__ __forceinline__ long long quotient(long long x, int y) {
@@ -203,6 +202,10 @@ struct Shape {
     static constexpr int kTokens = 16 * kSub;
     static constexpr int kRow = D * kElt;            // bytes
     static constexpr int kChunks = kRow / 16;
+    // An item's fixed cost (its first loads' latency, its sums' way out) in units of 64 tokens: about that of 96 KB of
+    // keys and values.  64 ragged requests in 8 bits (16 KB a unit): 107, 93, 84, 86, 92 µs with 2, 3, 5, 8, 12;
+    // in bf16 115, 116, 116, 117, 117; a window at head_dim 256 (64 KB): 48, 47, 50, 52, 56.
+    static constexpr int kFixed = kRow >= 512 ? 2 : kRow == 256 ? 3 : kRow == 128 ? 6 : 10;
     static constexpr int kHalf = kTokens * kRow;     // a slot of the ring: a stage's keys or values
     // Three CTAs of 168 registers on an SM, where the outputs' D / 2 leave that; else two.
     static constexpr int kCtas = D == 256 ? 2 : 3;
@@ -269,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
     using S = Shape<D, Q8, R>;
     constexpr int NT = D / 8;   // output tiles of 8 columns
     constexpr int KS = D / 16;  // k-steps of 16
-    constexpr int kRow = S::kRow;
+    constexpr int kRow = S::kRow, kFixed = S::kFixed;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ long long s_sum[kWarps];
     __shared__ long long s_before;
@@ -279,13 +282,12 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
     const int group = warp / R, rw = warp % R, G = sp.G;
     auto over_G = [&](int r) { return static_cast<int>((static_cast<uint64_t>(r) * sp.G_mul) >> sp.G_shift); };
-    pdl_start();
 
     // The total work, and the request that this CTA's piece begins in: each
     // thread sums a stretch of the requests, then one scan over the threads.
     const int per = (a.B + kThreads - 1) / kThreads;
     long long own = 0;
-    for (int b = tid * per; b < min((tid + 1) * per, a.B); ++b) own += units(a, request(sp, b, 16 * R));
+    for (int b = tid * per; b < min((tid + 1) * per, a.B); ++b) own += units(a, request(sp, b, 16 * R), kFixed);
     long long sum = own;
     for (int d = 1; d < 32; d <<= 1) {
         const long long v = __shfl_up_sync(~0u, sum, d);
@@ -306,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
         long long before = sum - own;
         int b = tid * per;
         for (const int stop = min(b + per, a.B) - 1; b < stop; ++b) {
-            const long long w = units(a, request(sp, b, 16 * R));
+            const long long w = units(a, request(sp, b, 16 * R), kFixed);
             if (at < before + w) break;
             before += w;
         }
@@ -326,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
 
     while (at < end && b < a.B) {
         const Request rq = request(sp, b, 16 * R);
-        const long long mine = units(a, rq);
+        const long long mine = units(a, rq, kFixed);
         if (at >= before + mine) {
             before += mine;
             ++b;
@@ -345,15 +347,16 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
         const int low_tile = rq.low / kTile;
         const int tok0 = max(rq.low, (low_tile + tile0) * kTile);
         const int tok1 = static_cast<int>(min(static_cast<long long>(rq.len), (low_tile + tile1) * static_cast<long long>(kTile)));
-        const int count = tok1 - tok0 - group * S::kTokens;
+        // Stages begin at multiples of 16 tokens, so that they lie in one page where pages are such multiples.
+        const int base0 = tok0 & ~15, count = tok1 - base0 - group * S::kTokens;
         const int stages = count <= 0 ? 0 : (count + S::kGroups * S::kTokens - 1) / (S::kGroups * S::kTokens);
 
         // ---- page ids of the first stages: lane l knows token l of a stage
         const int* table = a.table + b * a.table_stride;
-        auto token_of = [&](int i) { return tok0 + (i * S::kGroups + group) * S::kTokens + (lane & (S::kTokens - 1)); };
-        auto page_of = [&](int i) {  // page id of the lane's token, −1 past the end
+        auto token_of = [&](int i) { return base0 + (i * S::kGroups + group) * S::kTokens + (lane & (S::kTokens - 1)); };
+        auto page_of = [&](int i) {  // page id of the lane's token, −1 outside the piece
             const int tok = token_of(i);
-            if (i >= stages || tok >= tok1) return -1;
+            if (i >= stages || tok < tok0 || tok >= tok1) return -1;
             return __ldg(table + static_cast<int>((static_cast<uint64_t>(tok) * a.page_mul) >> a.page_shift));
         };
         int first[S::kAhead];
@@ -396,14 +399,14 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
                 scales[pend_at * S::kTokens + lane] = make_float2(pend_k, __log2f(pend_v < kTiny ? kTiny : pend_v));
         };
         long long off = -1;     // of the lane's token, in the stage whose keys were asked for last; −1: none
-        long long off0 = 0;     // of the stage's first token
-        bool even = false;      // the tokens are all there, token_stride apart, with rows of D values
+        long long off0[S::kSub];  // of the first token of each 16
+        bool even = false;      // the tokens are all there, those of a 16 token_stride apart, with rows of D values
         auto find = [&](int i, int page) {  // stage i
             const int tok = token_of(i);
             const int pi = static_cast<int>((static_cast<uint64_t>(tok) * a.page_mul) >> a.page_shift);
             const int in_page = tok - pi * a.page_size;
             off = -1;
-            if (i < stages && tok < tok1) {
+            if (i < stages && tok >= tok0 && tok < tok1) {
                 if (page >= 0 && page < a.pages)
                     off = page * a.page_stride + in_page * a.token_stride + h * a.head_stride;
                 else
@@ -418,9 +421,10 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
                 }
                 pend_at = i < stages ? i % S::kScaleSlots : -1;
             }
-            off0 = __shfl_sync(~0u, off, 0);
-            even = __all_sync(~0u, off0 >= 0 && off == off0 + (lane & (S::kTokens - 1)) * a.token_stride) &&
-                   d_chunks == S::kChunks;
+#pragma unroll
+            for (int sub = 0; sub < S::kSub; ++sub) off0[sub] = __shfl_sync(~0u, off, 16 * sub);
+            const long long mine = S::kSub == 2 && (lane & 16) ? off0[S::kSub - 1] : off0[0];
+            even = __all_sync(~0u, mine >= 0 && off == mine + (lane & 15) * a.token_stride) && d_chunks == S::kChunks;
         };
         int put = 0;  // ring slot of the next copy
         auto load = [&](auto key, bool any) {  // keys or values of the stage found last
@@ -431,9 +435,13 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
                 const uint8_t* src = static_cast<const uint8_t*>(KEY ? a.k : a.v);
                 auto to = [&](int p) { return (dst ^ (turn<kRow, Q8, KEY>(p) << 4)) + p * kRow; };
                 if (even) {
-                    const uint8_t* from = src + off0 * S::kElt + load_r * a.token_stride * S::kElt + load_c * 16;
+                    // (a pass may reach into the second 16 tokens)
+                    const uint8_t* from = src + (kPerPass > 16 && load_r >= 16 ? off0[S::kSub - 1] : off0[0]) * S::kElt +
+                                          (load_r & 15) * a.token_stride * S::kElt + load_c * 16;
 #pragma unroll
                     for (int p = 0; p < S::kTokens; p += kPerPass) {
+                        if (S::kSub == 2 && p == 16)
+                            from = src + off0[S::kSub - 1] * S::kElt + load_r * a.token_stride * S::kElt + load_c * 16;
                         cp_async16(to(p), from);
                         from += kPerPass * S::kElt * a.token_stride;
                     }
@@ -529,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
             if (!kOdd) put_scales();
             group_sync<R>(group);
             load_next(First(), page_next, 2 * i + S::kSlots - 1);
-            const int base = tok0 + (i * S::kGroups + group) * S::kTokens;
+            const int base = base0 + (i * S::kGroups + group) * S::kTokens;
             const uint32_t keys = ring + get * S::kHalf;
             if (++get == S::kSlots) get = 0;
             const uint32_t vals = ring + get * S::kHalf;
@@ -584,14 +592,14 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
             }
             // Some row does not see some token of the stage; there are such tokens, too, past the end.
             const bool hidden = min(base + S::kTokens, tok1) > all_hi || base < all_lo;
-            const bool partly = hidden || base + S::kTokens > tok1;
+            const bool partly = hidden || base + S::kTokens > tok1 || base < tok0;
             if (partly) {
 #pragma unroll
                 for (int y = 0; y < 2 * S::kSub; ++y)
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
                         const int tok = base + y * 8 + 2 * t4 + (x & 1);
-                        if (tok >= min(see_hi[x >> 1], tok1) || tok < see_lo[x >> 1]) s[y][x] = -INFINITY;
+                        if (tok >= min(see_hi[x >> 1], tok1) || tok < max(see_lo[x >> 1], tok0)) s[y][x] = -INFINITY;
                     }
             }
 
@@ -664,7 +672,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
                                 for (int e = 0; e < 2; ++e)
                                     if (y == tk >> 3 && e == (tk & 1)) v = s[y][2 * x + e];
                             p[x] = __shfl_sync(~0u, v, from);
-                            seen[x] = base + tk < min(see_hi[x], tok1) && base + tk >= see_lo[x];
+                            seen[x] = base + tk < min(see_hi[x], tok1) && base + tk >= max(see_lo[x], tok0);
                         }
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
@@ -941,19 +949,10 @@ cudaError_t run(SplitArgs sp, void* workspace, const DeviceInfo& dev, cudaStream
     // At least as many units as the batch can have: a CTA for each, where they are few.
     const AttnArgs& a = sp.a;
     const double reach = std::min(static_cast<double>(a.width) * a.page_size, a.window > 0 ? static_cast<double>(a.window) + a.T : 1e18);
-    const double most = static_cast<double>(a.kv_heads) * (a.B + static_cast<double>(a.T) * sp.G / (16 * R)) * (reach / kTile + 2 + kFixed);
+    const double most = static_cast<double>(a.kv_heads) * (a.B + static_cast<double>(a.T) * sp.G / (16 * R)) * (reach / kTile + 2 + S::kFixed);
     const int grid = static_cast<int>(std::min<double>(std::min(per_sm * dev.sm_count, kMaxCtas), most));
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(grid));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = S::kSmem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attn_split_kernel<D, Q8, R>, sp);
+    attn_split_kernel<D, Q8, R><<<grid, kThreads, S::kSmem, stream>>>(sp);
+    return cudaGetLastError();
 }
 
 template <int D, bool Q8>

@@ -172,151 +172,151 @@ struct Axes {
 constexpr int kAppendThreads = 256;
 constexpr int kBatch = 4;  // rows that a lane has in flight
 
-// LPR lanes work on a row, lane c of them on its values 8c..8c+7.  blockIdx.x
-// is the token, whose tables' values a thread reads once and uses for every
-// row that it turns; the rows' loads do not wait for the tables'.  Bound by
-// reading and writing each row once.
+// x·c + y·s for the two values of a word, every operation rounded on its own
+// (as packed pairs, products and sums came back fused).
+__device__ __forceinline__ uint32_t turn_pair(uint32_t x, uint32_t y, float2 c, float2 s) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(__fadd_rn(__fmul_rn(bf16_lo(x), c.x), __fmul_rn(bf16_lo(y), s.x)),
+                                                   __fadd_rn(__fmul_rn(bf16_hi(x), c.y), __fmul_rn(bf16_hi(y), s.y)));
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// LPR lanes work on a row, lane c of them on its values 8c..8c+7.  A CTA takes
+// every gridDim.x-th token: its threads ask for the token's rows (keys,
+// values, queries), fetch its cosines and sines once for all of them into
+// shared memory, and turn and write the rows.  blockIdx.y shares a token's rows
+// among CTAs where there are few tokens.  Bound by reading and writing each row
+// once.
 template <int LPR, bool Q8>
-__global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const KvAppendArgs a, const Axes axes) {
-    const long long t = blockIdx.x;
+__global__ void __launch_bounds__(kAppendThreads, 4) kv_append_kernel(const __grid_constant__ KvAppendArgs a,
+                                                                       const __grid_constant__ Axes axes) {
     constexpr int kGroups = kAppendThreads / LPR;
-    const int c = threadIdx.x % LPR, group = blockIdx.y * kGroups + threadIdx.x / LPR, groups = gridDim.y * kGroups;
+    __shared__ __align__(16) float s_cos[2][128], s_sin[2][128];
+    const int c = threadIdx.x % LPR, group0 = blockIdx.y * kGroups, group = group0 + threadIdx.x / LPR;
+    const int groups = gridDim.y * kGroups;
     const int d = a.head_dim, H = a.kv_heads, F = a.rotary / 2, half = F / 8;
     const bool live = 8 * c < d, turned = 8 * c < a.rotary;
-    const int rows = 2 * H + a.q_heads;  // keys, values, queries
+    const int rows = 2 * H + a.q_heads;
+    // Rows r of a token: keys from 0, values from H, queries from 2H, so that r · head_stride counts from there.
+    const __nv_bfloat16* const k_from = a.k.data + 8 * c;
+    const __nv_bfloat16* const v_from = a.v.data - H * a.v.head_stride + 8 * c;
+    const __nv_bfloat16* const q_from = a.q.data - 2 * H * a.q.head_stride + 8 * c;
 
-    const long long slot = a.slots[t];
-    bool stored = false;
-    long long at = 0, scale_at = 0;
-    float cs[8], sn[8];
-    for (int r0 = group; r0 - threadIdx.x / LPR < rows; r0 += kBatch * groups) {
-        uint4 x[kBatch];
+    for (int t = blockIdx.x, turn = 0; t < a.T; t += gridDim.x, turn ^= 1) {
+        long long slot = 0, at = 0, scale_at = 0;
+        bool stored = false;
+        float2 C[4], S[4];
+        for (int r0 = group, base = group0; base < rows; r0 += kBatch * groups, base += kBatch * groups) {
+            uint4 x[kBatch];
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            const int r = r0 + i * groups;
-            x[i] = make_uint4(0, 0, 0, 0);
-            if (live && r < rows) {
-                const __nv_bfloat16* src = r < H ? a.k.data + t * a.k.token_stride + r * a.k.head_stride
-                                           : r < 2 * H ? a.v.data + t * a.v.token_stride + (r - H) * a.v.head_stride
-                                                       : a.q.data + t * a.q.token_stride + (r - 2 * H) * a.q.head_stride;
-                x[i] = *reinterpret_cast<const uint4*>(src + 8 * c);
+            for (int i = 0; i < kBatch; ++i) {
+                const int r = r0 + i * groups;
+                x[i] = make_uint4(0, 0, 0, 0);
+                if (live && r < rows) {
+                    const __nv_bfloat16* src = r < H       ? k_from + t * a.k.token_stride + r * a.k.head_stride
+                                               : r < 2 * H ? v_from + t * a.v.token_stride + r * a.v.head_stride
+                                                           : q_from + t * a.q.token_stride + r * a.q.head_stride;
+                    x[i] = *reinterpret_cast<const uint4*>(src);
+                }
             }
-        }
-        if (r0 == group) {
-            if (turned) {
-                // Halves: frequencies 8c.. of the first half, the same again for the second.  Pairs: 4c..4c+3.
-                const int n = a.paired ? 4 : 8, first = a.paired ? 4 * c : 8 * (c < half ? c : c - half);
-                const uint32_t code = axes.of[first >> 3] >> (2 * (first & 7)) & (n == 4 ? 0xFFu : 0xFFFFu);
-                const float* cos[4];
-                const float* sin[4];
-#pragma unroll
-                for (int axis = 0; axis < 4; ++axis) {
-                    int row = axis < a.axes ? a.positions[axis * a.axis_stride + t] : 0;
+            if (base == group0) {
+                slot = a.slots[t];
+                if (threadIdx.x < F) {
+                    const int axis = axes.of[threadIdx.x >> 3] >> (2 * (threadIdx.x & 7)) & 3;
+                    int row = a.positions[axis * a.axis_stride + t];
                     if (row < 0 || row >= a.rows) {
                         record_status(a.status, kStatusInvalid);
                         row = 0;
                     }
-                    cos[axis] = a.cos + static_cast<long long>(row) * F + first;
-                    sin[axis] = a.sin + static_cast<long long>(row) * F + first;
+                    s_cos[turn][threadIdx.x] = a.cos[static_cast<long long>(row) * F + threadIdx.x];
+                    s_sin[turn][threadIdx.x] = a.sin[static_cast<long long>(row) * F + threadIdx.x];
                 }
-                auto pick = [](const float* const(&p)[4], uint32_t axis) {
-                    return axis < 2 ? (axis ? p[1] : p[0]) : (axis == 2 ? p[2] : p[3]);
-                };
-                if (code == (code & 3) * (n == 4 ? 0x55u : 0x5555u)) {  // one axis
-                    const float4* u = reinterpret_cast<const float4*>(pick(cos, code & 3));
-                    const float4* w = reinterpret_cast<const float4*>(pick(sin, code & 3));
-                    *reinterpret_cast<float4*>(cs) = u[0];
-                    *reinterpret_cast<float4*>(sn) = w[0];
-                    if (n == 8) {
-                        *reinterpret_cast<float4*>(cs + 4) = u[1];
-                        *reinterpret_cast<float4*>(sn + 4) = w[1];
+                __syncthreads();
+                if (turned && !a.paired) {
+                    // The first half takes −sin of its partner's values, the second +sin.
+                    const int first = 8 * (c < half ? c : c - half);
+                    const float sign = c < half ? -1.f : 1.f;
+#pragma unroll
+                    for (int y = 0; y < 4; y += 2) {
+                        const float4 u = *reinterpret_cast<const float4*>(&s_cos[turn][first + 2 * y]);
+                        const float4 w = *reinterpret_cast<const float4*>(&s_sin[turn][first + 2 * y]);
+                        C[y] = make_float2(u.x, u.y), C[y + 1] = make_float2(u.z, u.w);
+                        S[y] = make_float2(sign * w.x, sign * w.y), S[y + 1] = make_float2(sign * w.z, sign * w.w);
                     }
+                } else if (turned) {
+                    const float4 u = *reinterpret_cast<const float4*>(&s_cos[turn][4 * c]);
+                    const float4 w = *reinterpret_cast<const float4*>(&s_sin[turn][4 * c]);
+                    C[0] = make_float2(u.x, u.x), C[1] = make_float2(u.y, u.y), C[2] = make_float2(u.z, u.z), C[3] = make_float2(u.w, u.w);
+                    S[0] = make_float2(-w.x, w.x), S[1] = make_float2(-w.y, w.y), S[2] = make_float2(-w.z, w.z), S[3] = make_float2(-w.w, w.w);
+                }
+                stored = slot >= 0 && slot < a.pages * a.page_size;
+                if (!stored && slot != -1) record_status(a.status, kStatusInvalid);
+                if (stored) {
+                    const long long page = slot <= 0x7fffffff
+                                               ? static_cast<long long>((static_cast<uint64_t>(slot) * a.page_mul) >> a.page_shift)
+                                               : slot / a.page_size;
+                    const long long place = slot - page * a.page_size;
+                    at = page * a.page_stride + place * a.cache_token_stride + 8 * c;
+                    scale_at = page * H * a.page_size + place;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                if (base + i * groups >= rows) break;  // the same for the whole CTA
+                const int r = r0 + i * groups;
+                const bool is_q = r >= 2 * H, is_v = !is_q && r >= H;
+                const bool work = live && r < rows && (is_q || stored);
+                uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+                uint32_t other[4];
+                if (!a.paired) {
+                    const int from = c < half ? c + half : c - half;
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) other[y] = __shfl_sync(~0u, w[y], from & (LPR - 1), LPR);
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (i < n) {
-                            cs[i] = pick(cos, code >> (2 * i) & 3)[i];
-                            sn[i] = pick(sin, code >> (2 * i) & 3)[i];
-                        }
+                    for (int y = 0; y < 4; ++y) other[y] = __byte_perm(w[y], 0, 0x1032);
                 }
-            }
-            stored = slot >= 0 && slot < a.pages * a.page_size;
-            if (!stored && slot != -1) record_status(a.status, kStatusInvalid);
-            if (stored) {
-                const long long page = slot <= 0x7fffffff ? static_cast<long long>((static_cast<uint64_t>(slot) * a.page_mul) >> a.page_shift)
-                                                          : slot / a.page_size;
-                const long long place = slot - page * a.page_size;
-                at = page * a.page_stride + place * a.cache_token_stride;
-                scale_at = page * H * a.page_size + place;
-            }
-        }
+                if (turned && !is_v)
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            const int r = r0 + i * groups;
-            if (r - threadIdx.x / LPR >= rows) break;  // the same for the whole CTA
-            const bool is_q = r >= 2 * H, is_v = !is_q && r >= H;
-            const int h = is_q ? r - 2 * H : is_v ? r - H : r;
-            const bool work = live && r < rows && (is_q || stored);
-            uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-            uint32_t other[4];
-            if (!a.paired) {
-                const int from = c < half ? c + half : c - half;
+                    for (int y = 0; y < 4; ++y)
+                        w[y] = turn_pair(w[y], other[y], C[y], S[y]);
+                if (Q8 && base + i * groups < 2 * H) {
+                    // RTN at 8 bits over the row's LPR lanes (idle lanes hold zeros); query rows go along unused.
+                    float most = 0.f;
+                    bool finite = true;
 #pragma unroll
-                for (int y = 0; y < 4; ++y) other[y] = __shfl_sync(~0u, w[y], from & (LPR - 1), LPR);
-            }
-            if (turned && !is_v) {
-#pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                    const float lo = bf16_lo(w[y]), hi = bf16_hi(w[y]);
-                    float l, u;
-                    if (a.paired) {
-                        l = __fsub_rn(__fmul_rn(lo, cs[y]), __fmul_rn(hi, sn[y]));
-                        u = __fadd_rn(__fmul_rn(hi, cs[y]), __fmul_rn(lo, sn[y]));
-                    } else {
-                        const float ol = __fmul_rn(bf16_lo(other[y]), sn[2 * y]);
-                        const float oh = __fmul_rn(bf16_hi(other[y]), sn[2 * y + 1]);
-                        l = __fmul_rn(lo, cs[2 * y]);
-                        u = __fmul_rn(hi, cs[2 * y + 1]);
-                        l = c < half ? __fsub_rn(l, ol) : __fadd_rn(l, ol);
-                        u = c < half ? __fsub_rn(u, oh) : __fadd_rn(u, oh);
+                    for (int y = 0; y < 4; ++y) {
+                        most = fmaxf(most, fmaxf(fabsf(bf16_lo(w[y])), fabsf(bf16_hi(w[y]))));
+                        finite = finite && isfinite(bf16_lo(w[y])) && isfinite(bf16_hi(w[y]));
                     }
-                    const __nv_bfloat162 v = __floats2bfloat162_rn(l, u);
-                    w[y] = *reinterpret_cast<const uint32_t*>(&v);
-                }
-            }
-            if (Q8 && r0 - threadIdx.x / LPR + i * groups < 2 * H) {
-                // RTN at 8 bits over the row's LPR lanes (idle lanes hold zeros); query rows go along unused.
-                float most = 0.f;
-                bool finite = true;
+                    if (!finite) most = INFINITY;
 #pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                    most = fmaxf(most, fmaxf(fabsf(bf16_lo(w[y])), fabsf(bf16_hi(w[y]))));
-                    finite = finite && isfinite(bf16_lo(w[y])) && isfinite(bf16_hi(w[y]));
-                }
-                if (!finite) most = INFINITY;
+                    for (int m = LPR / 2; m > 0; m >>= 1) most = fmaxf(most, __shfl_xor_sync(~0u, most, m));
+                    if (work && !is_q) {
+                        const bool bad = isinf(most);
+                        const __nv_bfloat16 scale = __float2bfloat16_rn(bad ? NAN : __fdiv_rn(most, 127.f));
+                        const float s = __bfloat162float(scale);
+                        uint32_t code[2] = {0, 0};
+                        if (!bad && s > 0.f)
 #pragma unroll
-                for (int m = LPR / 2; m > 0; m >>= 1) most = fmaxf(most, __shfl_xor_sync(~0u, most, m));
-                if (work && !is_q) {
-                    const bool bad = isinf(most);
-                    const __nv_bfloat16 scale = __float2bfloat16_rn(bad ? NAN : __fdiv_rn(most, 127.f));
-                    const float s = __bfloat162float(scale);
-                    uint32_t code[2] = {0, 0};
-                    if (!bad && s > 0.f)
-#pragma unroll
-                        for (int y = 0; y < 4; ++y) {
-                            const int q0 = __float2int_rn(fminf(fmaxf(rintf(__fdiv_rn(bf16_lo(w[y]), s)), -128.f), 127.f));
-                            const int q1 = __float2int_rn(fminf(fmaxf(rintf(__fdiv_rn(bf16_hi(w[y]), s)), -128.f), 127.f));
-                            code[y / 2] |= ((q0 & 0xFFu) | (q1 & 0xFFu) << 8) << (16 * (y & 1));
-                        }
-                    int8_t* dst = static_cast<int8_t*>(is_v ? a.v_cache : a.k_cache) + at + h * a.cache_head_stride + 8 * c;
-                    *reinterpret_cast<uint2*>(dst) = make_uint2(code[0], code[1]);
-                    if (c == 0) (is_v ? a.v_scales : a.k_scales)[scale_at + static_cast<long long>(h) * a.page_size] = scale;
+                            for (int y = 0; y < 4; ++y) {
+                                const int q0 = __float2int_rn(fminf(fmaxf(rintf(__fdiv_rn(bf16_lo(w[y]), s)), -128.f), 127.f));
+                                const int q1 = __float2int_rn(fminf(fmaxf(rintf(__fdiv_rn(bf16_hi(w[y]), s)), -128.f), 127.f));
+                                code[y / 2] |= ((q0 & 0xFFu) | (q1 & 0xFFu) << 8) << (16 * (y & 1));
+                            }
+                        const int h = is_v ? r - H : r;
+                        int8_t* dst = static_cast<int8_t*>(is_v ? a.v_cache : a.k_cache) + at + h * a.cache_head_stride;
+                        *reinterpret_cast<uint2*>(dst) = make_uint2(code[0], code[1]);
+                        if (c == 0) (is_v ? a.v_scales : a.k_scales)[scale_at + static_cast<long long>(h) * a.page_size] = scale;
+                    }
                 }
-            }
-            if (work && (is_q || !Q8)) {
-                __nv_bfloat16* dst = is_q ? a.q_out.data + t * a.q_out.token_stride + h * a.q_out.head_stride
-                                          : static_cast<__nv_bfloat16*>(is_v ? a.v_cache : a.k_cache) + at + h * a.cache_head_stride;
-                *reinterpret_cast<uint4*>(dst + 8 * c) = make_uint4(w[0], w[1], w[2], w[3]);
+                if (work && (is_q || !Q8)) {
+                    __nv_bfloat16* dst;
+                    if (is_q)
+                        dst = a.q_out.data + t * a.q_out.token_stride + (r - 2 * H) * a.q_out.head_stride + 8 * c;
+                    else
+                        dst = static_cast<__nv_bfloat16*>(is_v ? a.v_cache : a.k_cache) + at + (is_v ? r - H : r) * a.cache_head_stride;
+                    *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+                }
             }
         }
     }
@@ -359,7 +359,9 @@ cudaError_t launch_kv_append(KvAppendArgs a, const int32_t sections[4], bool cyc
     const int per_cta = kAppendThreads / lpr, rows = 2 * a.kv_heads + a.q_heads;
     // Few tokens: a CTA for every 256 / LPR rows, so that the rows of a token are in flight at once.
     const int split = a.T * 2 >= dev.sm_count ? 1 : (rows + per_cta - 1) / per_cta;
-    const dim3 grid(static_cast<unsigned>(a.T), static_cast<unsigned>(split));
+    // Many tokens: CTAs that stay, four to an SM.
+    const int64_t tokens = std::min<int64_t>(a.T, std::max(1, 4 * dev.sm_count));
+    const dim3 grid(static_cast<unsigned>(tokens), static_cast<unsigned>(split));
     if (lpr == 8) return append<8>(a, axes, q8, grid, stream);
     if (lpr == 16) return append<16>(a, axes, q8, grid, stream);
     return append<32>(a, axes, q8, grid, stream);
