@@ -636,7 +636,7 @@ def w4_kv_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, posit
 
 def w4_attn_decode_workspace_bytes(q: torch.Tensor, k_cache: torch.Tensor, requests: int) -> int:
     """Bytes of workspace of w4_attn_decode for these queries, cache pages and number of requests."""
-    cache = _KvCache(kv_heads=k_cache.shape[2], head_dim=k_cache.shape[3])
+    cache = _KvCache(kv_heads=k_cache.shape[2], head_dim=k_cache.shape[3], format=8 if k_cache.dtype == torch.int8 else 16)
     return load().w4_attn_decode_workspace_bytes(cache, requests, q.shape[0], q.shape[1])
 
 

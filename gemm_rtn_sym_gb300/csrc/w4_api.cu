@@ -729,7 +729,7 @@ size_t w4_attn_decode_workspace_bytes(const w4_kv_cache* cache, int32_t B, int64
     if (!cache || B < 0 || T < 0 || q_heads < 1 || cache->kv_heads < 1 || cache->head_dim < 1 ||
         cache->head_dim > 256 || cache->head_dim % 16 != 0 || q_heads % cache->kv_heads != 0)
         return 0;
-    return attn_decode_workspace_bytes(B, T, q_heads, cache->kv_heads, cache->head_dim);
+    return attn_decode_workspace_bytes(B, T, q_heads, cache->kv_heads, cache->head_dim, cache->format == 8);
 }
 
 int w4_attn_decode(const w4_kv_cache* cache, int32_t B, int64_t T, int32_t q_heads, const w4_rows* q,

@@ -35,6 +35,8 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include "w4_attn_common.cuh"
+#include "w4_attn_tc.h"
 #include "w4_device.cuh"
 #include "w4_kv.h"
 
@@ -44,40 +46,10 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kTile = 64;       // tokens of a unit of work
-constexpr int kJoinGroup = 16;  // parts of an item that are joined at once
-constexpr int kMaxLength = 0x7fff0000;  // token numbers a little past a length stay below 2³¹
-constexpr int kMaxDevices = 64;         // as many as the library knows (device_info refuses others)
-constexpr int kMaxCtas = 512;           // bounds the workspace
-
-// The weights' reference and their sum, 16·R of each, then 16·R rows of D values.
-__host__ __device__ constexpr size_t partial_floats(int R, int D) { return static_cast<size_t>(16 * R) * (2 + D); }
-
-struct SplitArgs {
-    AttnArgs a;
-    unsigned long long* arrived;  // [2][kMaxCtas] parts there of a group, groups there of an item
-    float* partial;               // [kMaxCtas][2][partial_floats]
-    int G;                        // query heads per key-value head
-    uint32_t G_mul;               // divide_by(G)
-    int G_shift;
-    int rows_each;                // rows of each request, where starts is null
-    float scale_log2;             // |scale| · log2(e)
-    uint32_t flip;                // sign bits of a pair of queries to turn over: scale < 0
-};
-
 // A value scale of zero stands for this one, whose logarithm is a number.
 constexpr float kTiny = 1.17549435e-38f;
 
 // ------------------------------------------------------------- small pieces
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, int bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-
 __device__ __forceinline__ void ldmatrix_x4(uint32_t addr, uint32_t (&r)[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -107,10 +79,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&v);
-}
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     const __half2 v = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&v);
@@ -133,64 +101,6 @@ __device__ __forceinline__ uint32_t codes_f16(uint32_t w, uint32_t sel) {
     const __half2 v = __hsub2(*reinterpret_cast<const __half2*>(&u), bias);
     return *reinterpret_cast<const uint32_t*>(&v);
 }
-
-// --------------------------------------------------------------- work list
-// A request's part of the work: rows and tokens, clipped to what is there.
-struct Request {
-    int start, n;     // token rows
-    int len;          // tokens in the cache
-    int low;          // first token that any row sees
-    int tiles;        // 64-token tiles from the one of `low`
-    int row_tiles;
-};
-
-__device__ __forceinline__ Request request(const SplitArgs& sp, int b, int rows_per_tile) {
-    const AttnArgs& a = sp.a;
-    Request r;
-    const int len = a.lens[b];
-    if (a.starts) {
-        const int T = static_cast<int>(a.T);
-        r.start = min(max(a.starts[b], 0), T);
-        r.n = min(max(a.starts[b + 1], r.start), T) - r.start;
-    } else {
-        r.n = sp.rows_each;
-        r.start = b * r.n;
-    }
-    const int most = static_cast<int>(min(static_cast<long long>(a.width) * a.page_size, static_cast<long long>(kMaxLength)));
-    if (len < 0 || len > most) record_status(a.status, kStatusInvalid);
-    r.len = min(max(len, 0), most);
-    const long long low = a.window > 0 ? static_cast<long long>(r.len) - r.n - a.window + 1 : 0;
-    r.low = static_cast<int>(max(low, 0ll));
-    // A request without tokens still has its rows of zeros to write: one tile.
-    r.tiles = max(1, (r.len + kTile - 1) / kTile - r.low / kTile);
-    r.row_tiles = (r.n * sp.G + rows_per_tile - 1) / rows_per_tile;
-    return r;
-}
-
-// Units of work of a request: each item (head, row tile) counts `fixed` units
-// and then one for each of its tiles.
-__device__ __forceinline__ long long units(const AttnArgs& a, const Request& r, int fixed) {
-    return static_cast<long long>(a.kv_heads) * r.row_tiles * (r.tiles + fixed);
-}
-
-__device__ __forceinline__ long long quotient(long long x, int y) {
-    return x >> 32 ? static_cast<long long>(static_cast<unsigned long long>(x) / static_cast<unsigned>(y))
-                   : static_cast<long long>(static_cast<unsigned>(x) / static_cast<unsigned>(y));
-}
-
-// How `total` units are cut into n pieces: the first `longer` of them have one
-// unit more than the others' `size`.
-struct Cut {
-    long long size, longer;
-
-    __device__ __forceinline__ Cut(long long total, int n) : size(quotient(total, n)) { longer = total - size * n; }
-    __device__ __forceinline__ long long begin(int p) const { return p * size + min(static_cast<long long>(p), longer); }
-    __device__ __forceinline__ int piece(long long unit) const {  // that a unit lies in
-        const long long head = longer * (size + 1);
-        return static_cast<int>(unit < head ? quotient(unit, static_cast<int>(size) + 1)
-                                            : longer + quotient(unit - head, static_cast<int>(size)));
-    }
-};
 
 // ------------------------------------------------------------------ kernel
 // Shapes of the pass for head_dim ≤ D, R warps (16 rows each) per group.
@@ -240,33 +150,6 @@ __device__ __forceinline__ void group_sync(int group) {
         asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(R * 32) : "memory");
 }
 
-// Counts an arrival at `word`; true for the last of `need`.  The upper 48 bits
-// mark a word that counts, and the last arrival leaves the count 0, for the
-// next launch; a word without the mark (what the workspace held before its
-// first use) counts as none.  What the CTA wrote before its barrier is then
-// visible to the CTA of the last arrival.
-constexpr unsigned long long kMark = 0x77346B765F61ull << 16;
-
-__device__ __forceinline__ bool arrive(unsigned long long* word, int need) {
-    __threadfence();
-    unsigned long long seen = atomicAdd(word, 1ull);
-    bool counted = (seen & ~0xFFFFull) == kMark;
-    int count = static_cast<int>(seen & 0xFFFF) + 1;
-    if (!counted) {
-        ++seen;
-        do {
-            count = (seen & ~0xFFFFull) == kMark ? static_cast<int>(seen & 0xFFFF) + 1 : 1;
-            const unsigned long long prev = atomicCAS(word, seen, kMark | count);
-            counted = prev == seen;
-            seen = prev;
-        } while (!counted);
-    }
-    if (count != need) return false;
-    __threadfence();
-    atomicExch(word, kMark);
-    return true;
-}
-
 template <int D, bool Q8, int R>
 __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_kernel(const __grid_constant__ SplitArgs sp) {
     using S = Shape<D, Q8, R>;
@@ -274,50 +157,12 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
     constexpr int KS = D / 16;  // k-steps of 16
     constexpr int kRow = S::kRow, kFixed = S::kFixed;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ long long s_sum[kWarps];
-    __shared__ long long s_before;
-    __shared__ int s_at;
     __shared__ bool s_last;
     const AttnArgs& a = sp.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
     const int group = warp / R, rw = warp % R, G = sp.G;
-    auto over_G = [&](int r) { return static_cast<int>((static_cast<uint64_t>(r) * sp.G_mul) >> sp.G_shift); };
-
-    // The total work, and the request that this CTA's piece begins in: each
-    // thread sums a stretch of the requests, then one scan over the threads.
-    const int per = (a.B + kThreads - 1) / kThreads;
-    long long own = 0;
-    for (int b = tid * per; b < min((tid + 1) * per, a.B); ++b) own += units(a, request(sp, b, 16 * R), kFixed);
-    long long sum = own;
-    for (int d = 1; d < 32; d <<= 1) {
-        const long long v = __shfl_up_sync(~0u, sum, d);
-        if (lane >= d) sum += v;
-    }
-    if (lane == 31) s_sum[warp] = sum;
-    __syncthreads();
-    long long total = 0;
-    for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) sum += s_sum[w];
-        total += s_sum[w];
-    }
-    const Cut cut(total, gridDim.x);
-    long long at = cut.begin(blockIdx.x);
-    const long long end = cut.begin(blockIdx.x + 1);
-    if (at >= end) return;
-    if (at >= sum - own && at < sum) {
-        long long before = sum - own;
-        int b = tid * per;
-        for (const int stop = min(b + per, a.B) - 1; b < stop; ++b) {
-            const long long w = units(a, request(sp, b, 16 * R), kFixed);
-            if (at < before + w) break;
-            before += w;
-        }
-        s_at = b;
-        s_before = before;
-    }
-    __syncthreads();
-    int b = s_at;
-    long long before = s_before;  // units of the requests before b
+    Walk<kTile, 16 * R, kFixed> walk;
+    if (!walk.template find<kThreads>(sp)) return;
 
     const uint32_t ring = smem_addr(smem) + group * S::kGroup;
     float2* scales = reinterpret_cast<float2*>(smem + group * S::kGroup + S::kRing);
@@ -326,38 +171,19 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
     constexpr int kPerPass = 32 * R / S::kChunks;  // token rows of one pass of the group's lanes
     const int load_c = (rw * 32 + lane) % S::kChunks, load_r = (rw * 32 + lane) / S::kChunks;
 
-    while (at < end && b < a.B) {
-        const Request rq = request(sp, b, 16 * R);
-        const long long mine = units(a, rq, kFixed);
-        if (at >= before + mine) {
-            before += mine;
-            ++b;
-            continue;
-        }
-        // The item: head h, row tile rt, tiles [tile0, tile1) of its own; none where the piece ends in the fixed units.
-        const int weight = rq.tiles + kFixed;
-        const int line = static_cast<int>(quotient(at - before, weight));
-        const long long item = before + static_cast<long long>(line) * weight;
-        const int h = rq.row_tiles == 1 ? line : line / rq.row_tiles, rt = line - h * rq.row_tiles;
-        const int tile0 = max(0, static_cast<int>(at - item) - kFixed);
-        const int tile1 = static_cast<int>(min(static_cast<long long>(weight), end - item)) - kFixed;
-        at = item + weight;
-        if (tile1 <= tile0) continue;
-        const int rows = rq.n * G, row0 = rt * 16 * R;
-        const int low_tile = rq.low / kTile;
-        const int tok0 = max(rq.low, (low_tile + tile0) * kTile);
-        const int tok1 = static_cast<int>(min(static_cast<long long>(rq.len), (low_tile + tile1) * static_cast<long long>(kTile)));
+    for (Item it; walk.next(sp, it);) {
+        const int h = it.h, row0 = it.row0, rows = it.rows, tok0 = it.tok0, tok1 = it.tok1;
         // Stages begin at multiples of 16 tokens, so that they lie in one page where pages are such multiples.
         const int base0 = tok0 & ~15, count = tok1 - base0 - group * S::kTokens;
         const int stages = count <= 0 ? 0 : (count + S::kGroups * S::kTokens - 1) / (S::kGroups * S::kTokens);
 
         // ---- page ids of the first stages: lane l knows token l of a stage
-        const int* table = a.table + b * a.table_stride;
+        const int* table = a.table + it.b * a.table_stride;
         auto token_of = [&](int i) { return base0 + (i * S::kGroups + group) * S::kTokens + (lane & (S::kTokens - 1)); };
         auto page_of = [&](int i) {  // page id of the lane's token, −1 outside the piece
             const int tok = token_of(i);
             if (i >= stages || tok < tok0 || tok >= tok1) return -1;
-            return __ldg(table + static_cast<int>((static_cast<uint64_t>(tok) * a.page_mul) >> a.page_shift));
+            return __ldg(table + sp.page_index(tok));
         };
         int first[S::kAhead];
 #pragma unroll
@@ -369,11 +195,11 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
         uint2 raw[Q8 ? 2 : 1][Q8 ? KS : 1];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-            const int r = row0 + rw * 16 + g + 8 * x, j = over_G(r);
+            const int r = row0 + rw * 16 + g + 8 * x, j = sp.over_G(r);
             const bool live = r < rows;
-            see_hi[x] = live ? rq.len - rq.n + j + 1 : 0x7fffffff;
+            see_hi[x] = live ? it.len - it.n + j + 1 : 0x7fffffff;
             see_lo[x] = live && a.window > 0 ? static_cast<int>(max(0ll, static_cast<long long>(see_hi[x]) - a.window)) : 0;
-            const __nv_bfloat16* src = a.q.data + (live ? (rq.start + j) * a.q.token_stride + (h * G + r - j * G) * a.q.head_stride : 0);
+            const __nv_bfloat16* src = a.q.data + (live ? (it.start + j) * a.q.token_stride + (h * G + r - j * G) * a.q.head_stride : 0);
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
                 if (!Q8) {
@@ -403,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
         bool even = false;      // the tokens are all there, those of a 16 token_stride apart, with rows of D values
         auto find = [&](int i, int page) {  // stage i
             const int tok = token_of(i);
-            const int pi = static_cast<int>((static_cast<uint64_t>(tok) * a.page_mul) >> a.page_shift);
+            const int pi = sp.page_index(tok);
             const int in_page = tok - pi * a.page_size;
             off = -1;
             if (i < stages && tok >= tok0 && tok < tok1) {
@@ -516,9 +342,9 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
         // Tokens before all_hi and from all_lo on are seen by every row of the warp.
         int all_hi, all_lo;
         {
-            const int j0 = over_G(row0 + rw * 16), j1 = over_G(max(min(row0 + rw * 16 + 15, rows - 1), 0));
-            all_hi = rq.len - rq.n + j0 + 1;
-            all_lo = a.window > 0 ? static_cast<int>(max(0ll, static_cast<long long>(rq.len) - rq.n + j1 + 1 - a.window)) : 0;
+            const int j0 = sp.over_G(row0 + rw * 16), j1 = sp.over_G(max(min(row0 + rw * 16 + 15, rows - 1), 0));
+            all_hi = it.len - it.n + j0 + 1;
+            all_lo = a.window > 0 ? static_cast<int>(max(0ll, static_cast<long long>(it.len) - it.n + j1 + 1 - a.window)) : 0;
         }
 
         float o[NT][4];
@@ -783,20 +609,9 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
             }
         __syncthreads();
 
-        // A row's output: `v` its values times the sum `l` of its weights.  A row that sees nothing is zeros; one
-        // whose scores are all −∞ has no value (0 / 0).
-        auto put_row = [&](int row, int col, const float* v, int n, float l) {
-            const int j = over_G(row);
-            const float f = rq.len - rq.n + j < 0 ? 0.f : 1.f / l;
-            __nv_bfloat16* to = a.out.data + (rq.start + j) * a.out.token_stride + (h * G + row - j * G) * a.out.head_stride + col;
-            for (int x = 0; x < n; x += 2) *reinterpret_cast<uint32_t*>(to + x) = pack_bf16(v[x] * f, v[x + 1] * f);
-        };
-        const bool whole = tile0 == 0 && tile1 == rq.tiles;
-        // Parts of a shared item: piece p0 (which has its first tile) and those after it; a piece's first item
-        // leaves its sums in slot 0, its last in slot 1.
-        const int p0 = whole ? 0 : cut.piece(item + kFixed), k_own = static_cast<int>(blockIdx.x) - p0;
-        const int parts = whole ? 1 : cut.piece(item + weight - 1) - p0 + 1;
-        auto part = [&](int k) { return sp.partial + (2 * static_cast<size_t>(p0 + k) + (k == 0)) * partial_floats(R, D); };
+        const bool whole = it.whole();
+        const Parts<16 * R, D> parts(sp, walk, it, kFixed);
+        float* const part = parts.at(static_cast<int>(blockIdx.x) - parts.first);
         for (int x = tid; x < 16 * R * (D / 4); x += kThreads) {
             const int r = x / (D / 4), col = x % (D / 4) * 4, row = row0 + r;
             if (row >= rows || col >= a.head_dim) continue;
@@ -813,112 +628,24 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
                 v[0] += f * w.x, v[1] += f * w.y, v[2] += f * w.z, v[3] += f * w.w;
             }
             if (whole) {
-                put_row(row, col, v, 4, ll);
+                put_row(sp, it, row, col, v, 4, ll);
             } else {
-                float* to = part(k_own);
                 if (col == 0) {
-                    to[r] = mm;
-                    to[16 * R + r] = fminf(ll, 3e38f);
+                    part[r] = mm;
+                    part[16 * R + r] = fminf(ll, 3e38f);
                 }
-                *reinterpret_cast<float4*>(to + 32 * R + r * D + col) = make_float4(v[0], v[1], v[2], v[3]);
+                *reinterpret_cast<float4*>(part + 32 * R + r * D + col) = make_float4(v[0], v[1], v[2], v[3]);
             }
         }
         __syncthreads();
-        if (whole) continue;
-
-        // ---- the last part of a group of sixteen to get here joins the group, the last group the item
-        constexpr int V = D / 32;  // neighbouring values of a lane
-        // A warp joins NP parts of 16 / NP rows at a time, all loads at once: parts k0, k0 + step, ... (n of them) into
-        // the output or into part k0.
-        auto join_rows = [&](auto np, int k0, int n, int step, bool last) {
-            constexpr int NP = decltype(np)::value, NR = 16 / NP;
-            const int y_lane = (lane & 15) / NP, i_lane = lane & (NP - 1);
-            for (int r = warp * NR; r < 16 * R && row0 + r < rows; r += kWarps * NR) {
-                float mm = -INFINITY, ll = 0.f, v[NR][V];  // mm, ll: of the lane's row
-#pragma unroll
-                for (int y = 0; y < NR; ++y)
-#pragma unroll
-                    for (int x = 0; x < V; ++x) v[y][x] = 0.f;
-                for (int i0 = 0; i0 < n; i0 += NP) {
-                    // lanes 0 to 15: the references, 16 to 31: the sums
-                    const bool there = i0 + i_lane < n;
-                    const float stat = there ? __ldcg(part(k0 + (i0 + i_lane) * step) + (lane < 16 ? 0 : 16 * R) + r + y_lane) : -INFINITY;
-                    float w[NR][NP][V];
-#pragma unroll
-                    for (int i = 0; i < NP; ++i) {
-                        const float* p = part(k0 + min(i0 + i, n - 1) * step) + 32 * R + r * D + lane * V;
-#pragma unroll
-                        for (int y = 0; y < NR; ++y)
-#pragma unroll
-                            for (int x = 0; x < V; x += 2) {
-                                const float2 f = __ldcg(reinterpret_cast<const float2*>(p + y * D + x));
-                                w[y][i][x] = f.x, w[y][i][x + 1] = f.y;
-                            }
-                    }
-                    const float pm = __shfl_sync(~0u, stat, lane & 15), pl = __shfl_sync(~0u, stat, (lane & 15) + 16);
-                    float nm = fmaxf(mm, pm);
-#pragma unroll
-                    for (int d = 1; d < NP; d <<= 1) nm = fmaxf(nm, __shfl_xor_sync(~0u, nm, d));
-                    const float rm = nm == -INFINITY ? 0.f : nm, keep = ex2(mm - rm), f = there ? ex2(pm - rm) : 0.f;
-                    float fl = there ? f * pl : 0.f;
-#pragma unroll
-                    for (int d = 1; d < NP; d <<= 1) fl += __shfl_xor_sync(~0u, fl, d);
-                    ll = ll * keep + fl;
-                    mm = nm;
-#pragma unroll
-                    for (int y = 0; y < NR; ++y) {
-                        const float k = __shfl_sync(~0u, keep, y * NP);
-#pragma unroll
-                        for (int x = 0; x < V; ++x) v[y][x] *= k;
-#pragma unroll
-                        for (int i = 0; i < NP; ++i) {
-                            const float fi = __shfl_sync(~0u, f, y * NP + i);
-#pragma unroll
-                            for (int x = 0; x < V; ++x) v[y][x] = i0 + i < n ? fmaf(fi, w[y][i][x], v[y][x]) : v[y][x];
-                        }
-                    }
-                }
-#pragma unroll
-                for (int y = 0; y < NR; ++y) {
-                    const float l_row = __shfl_sync(~0u, ll, y * NP), m_row = __shfl_sync(~0u, mm, y * NP);
-                    if (row0 + r + y >= rows) continue;
-                    if (last) {
-                        if (lane * V < a.head_dim) put_row(row0 + r + y, lane * V, v[y], V, l_row);
-                    } else {
-                        float* to = part(k0);
-                        if (lane == 0) to[r + y] = m_row, to[16 * R + r + y] = fminf(l_row, 3e38f);
-#pragma unroll
-                        for (int x = 0; x < V; ++x) to[32 * R + (r + y) * D + lane * V + x] = v[y][x];
-                    }
-                }
-            }
-        };
-        auto join = [&](int k0, int n, int step, bool last) {
-            if (n <= 4)
-                join_rows(std::integral_constant<int, 4>(), k0, n, step, last);
-            else
-                join_rows(std::integral_constant<int, 16>(), k0, n, step, last);
-        };
-        const int k_group = k_own / kJoinGroup * kJoinGroup, in_group = min(kJoinGroup, parts - k_group);
-        const int groups = (parts + kJoinGroup - 1) / kJoinGroup;
-        if (in_group > 1) {
-            if (tid == 0) s_last = arrive(sp.arrived + p0 + k_group, in_group);
-            __syncthreads();
-            const bool last = s_last;
-            if (last) join(k_group, in_group, 1, groups == 1);
-            __syncthreads();
-            if (!last) continue;
-        }
-        if (groups > 1) {
-            if (tid == 0) s_last = arrive(sp.arrived + kMaxCtas + p0, groups);
-            __syncthreads();
-            if (s_last) join(0, groups, kJoinGroup, true);
-            __syncthreads();
-        }
+        if (!whole) parts.template finish<kWarps>(sp, it, s_last, [] { __syncthreads(); });
     }
 }
 
 int dim_of(int head_dim) { return head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256; }
+
+// Whether the tensor-core kernel takes the call: more than 32 rows to a key-value head, on the average.
+bool many_rows(int32_t B, int64_t T, int G, bool q8) { return !q8 && (T + B - 1) / B * G > 32; }
 
 // Warps (of 16 rows) that share a stage: what the requests' rows need on the
 // average, at most 4.
@@ -928,7 +655,7 @@ int row_warps(int32_t B, int64_t T, int G) {
 }
 
 template <int D, bool Q8, int R>
-cudaError_t run(SplitArgs sp, void* workspace, const DeviceInfo& dev, cudaStream_t stream) {
+cudaError_t run(const SplitArgs& sp, const DeviceInfo& dev, cudaStream_t stream) {
     using S = Shape<D, Q8, R>;
     // CTAs that an SM holds, asked once per device.
     static std::atomic<int> known[kMaxDevices];
@@ -944,8 +671,6 @@ cudaError_t run(SplitArgs sp, void* workspace, const DeviceInfo& dev, cudaStream
         if (per_sm < 1) return cudaErrorInvalidConfiguration;
         known[device & (kMaxDevices - 1)].store(per_sm, std::memory_order_relaxed);
     }
-    sp.arrived = static_cast<unsigned long long*>(workspace);
-    sp.partial = reinterpret_cast<float*>(sp.arrived + 2 * kMaxCtas);
     // At least as many units as the batch can have: a CTA for each, where they are few.
     const AttnArgs& a = sp.a;
     const double reach = std::min(static_cast<double>(a.width) * a.page_size, a.window > 0 ? static_cast<double>(a.window) + a.T : 1e18);
@@ -956,32 +681,36 @@ cudaError_t run(SplitArgs sp, void* workspace, const DeviceInfo& dev, cudaStream
 }
 
 template <int D, bool Q8>
-cudaError_t run_rows(const SplitArgs& sp, void* workspace, const DeviceInfo& dev, cudaStream_t stream) {
+cudaError_t run_rows(const SplitArgs& sp, const DeviceInfo& dev, cudaStream_t stream) {
     const int R = row_warps(sp.a.B, sp.a.T, sp.G);
-    if (R == 1) return run<D, Q8, 1>(sp, workspace, dev, stream);
-    if (R == 2) return run<D, Q8, 2>(sp, workspace, dev, stream);
-    return run<D, Q8, 4>(sp, workspace, dev, stream);
+    if (R == 1) return run<D, Q8, 1>(sp, dev, stream);
+    if (R == 2) return run<D, Q8, 2>(sp, dev, stream);
+    return run<D, Q8, 4>(sp, dev, stream);
 }
 
 template <bool Q8>
-cudaError_t run_dim(const SplitArgs& sp, void* workspace, const DeviceInfo& dev, cudaStream_t stream) {
+cudaError_t run_dim(const SplitArgs& sp, const DeviceInfo& dev, cudaStream_t stream) {
     const int D = dim_of(sp.a.head_dim);
-    if (D == 64) return run_rows<64, Q8>(sp, workspace, dev, stream);
-    if (D == 128) return run_rows<128, Q8>(sp, workspace, dev, stream);
-    return run_rows<256, Q8>(sp, workspace, dev, stream);
+    if (D == 64) return run_rows<64, Q8>(sp, dev, stream);
+    if (D == 128) return run_rows<128, Q8>(sp, dev, stream);
+    return run_rows<256, Q8>(sp, dev, stream);
 }
 
 }  // namespace
 
-size_t attn_decode_workspace_bytes(int32_t B, int64_t T, int32_t q_heads, int32_t kv_heads, int32_t head_dim) {
-    const int R = B > 0 ? row_warps(B, T, q_heads / kv_heads) : 1;
-    return 2 * kMaxCtas * (sizeof(unsigned long long) + partial_floats(R, dim_of(head_dim)) * sizeof(float));
+size_t attn_decode_workspace_bytes(int32_t B, int64_t T, int32_t q_heads, int32_t kv_heads, int32_t head_dim, bool q8) {
+    const int G = q_heads / kv_heads;
+    const size_t part = B > 0 && many_rows(B, T, G, q8) ? attn_tc_partial_floats(head_dim)
+                                                        : partial_floats(16 * (B > 0 ? row_warps(B, T, G) : 1), dim_of(head_dim));
+    return 2 * kMaxCtas * (sizeof(unsigned long long) + part * sizeof(float));
 }
 
 cudaError_t launch_attn_decode(AttnArgs a, bool q8, void* workspace, const DeviceInfo& dev, cudaStream_t stream) {
     divide_by(a.page_size, &a.page_mul, &a.page_shift);
     SplitArgs sp = {};
     sp.a = a;
+    sp.arrived = static_cast<unsigned long long*>(workspace);
+    sp.partial = reinterpret_cast<float*>(sp.arrived + 2 * kMaxCtas);
     sp.G = a.q_heads / a.kv_heads;
     divide_by(sp.G, &sp.G_mul, &sp.G_shift);
     sp.rows_each = static_cast<int>(a.T / a.B);
@@ -989,7 +718,8 @@ cudaError_t launch_attn_decode(AttnArgs a, bool q8, void* workspace, const Devic
     // largest score is then that of the unscaled products, and hidden ones stay at −∞.
     sp.scale_log2 = std::max(std::fabs(a.scale) * 1.4426950408889634f, 1e-30f);
     sp.flip = a.scale < 0.f ? 0x80008000u : 0u;
-    return q8 ? run_dim<true>(sp, workspace, dev, stream) : run_dim<false>(sp, workspace, dev, stream);
+    if (many_rows(a.B, a.T, sp.G, q8)) return launch_attn_tc(sp, dev, stream);
+    return q8 ? run_dim<true>(sp, dev, stream) : run_dim<false>(sp, dev, stream);
 }
 
 }  // namespace w4

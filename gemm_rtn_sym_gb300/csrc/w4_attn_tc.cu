@@ -1,0 +1,493 @@
+// Attention over the paged cache where many rows read each key-value head
+// (verify passes of several drafts): tcgen05 products, one CTA to an SM.
+//
+// The pass is that of the kernel for few rows: o = Σ_t 2^(s_t − m) v_t /
+// Σ_t 2^(s_t − m) in one pass over the tokens, the work in equal pieces, parts
+// of shared items joined by the CTA that finishes last.  What differs is what
+// bounds it: with R rows a byte of keys and values takes 2·R operations, and
+// the m16n8k16 MMAs of the other kernel reach a quarter of the tensor cores'
+// rate (104 rows of 128 over 16 requests: 196 µs, the cache's bytes 39 µs).
+//
+//   S [128 rows, TT tokens] = Q [rows, D] · Kᵀ     both from shared memory
+//   O [128 rows, D]        += P [rows, tokens] · V  P from tensor memory
+//
+// A tile is TT = 128 tokens (64 at D = 256: 64 KB of keys and values either
+// way).  Warps 0 to 3 hold a row per thread: they read S from tensor memory,
+// twice (the largest score, then the weights), so that a row's statistics need
+// no exchange between threads, and write the weights over it, as two bf16 each
+// (one alone would err as much as the result's rounding).  Warps 4 to 7 copy
+// the tokens' rows by cp.async, from pages of any size, into a ring of six
+// slots, keys and values in turn.  Warp 8 issues the products: the scores of
+// tile i + 1 while the weights of tile i are made.
+// Tensor memory: S of two tiles in columns 0 to 2·TT, O from column 256.
+#include <algorithm>
+#include <atomic>
+#include <cmath>
+#include <cstdint>
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "w4_attn_common.cuh"
+#include "w4_attn_tc.h"
+#include "w4_device.cuh"
+#include "w4_kv.h"
+#include "w4_tcgen05.cuh"
+
+namespace w4 {
+namespace {
+
+constexpr int kRows = 128;
+constexpr int kSoftmaxWarps = 4, kLoadWarps = 4;
+constexpr int kMmaWarp = kSoftmaxWarps + kLoadWarps;
+constexpr int kThreads = 32 * (kMmaWarp + 1);
+constexpr int kSlots = 6;
+constexpr int kFixed = 2;  // an item's fixed cost in tiles
+constexpr uint32_t kColO = 256, kTmemCols = 512;
+
+template <int D>
+struct Shape {
+    static constexpr int kTile = D == 256 ? 64 : 128;
+    static constexpr int kBlocks = D / 64;            // 128-byte columns of a row
+    static constexpr int kSlot = kTile * D * 2;       // keys or values of a tile
+    static constexpr int kSlotsHere = D == 256 ? 4 : kSlots;
+    static constexpr int kQ = kRows * D * 2;
+    // At least what keeps a second CTA, which would wait for tensor memory, off the SM.
+    static constexpr int kNeed = 1024 + kQ + kSlotsHere * kSlot, kSmem = kNeed > 120 * 1024 ? kNeed : 120 * 1024;
+};
+
+// Byte of 16-byte chunk c of row r in a tile of ROWS rows: columns of 128 bytes, 128-byte swizzle.
+template <int ROWS>
+__device__ __forceinline__ uint32_t place(int r, int c) {
+    return static_cast<uint32_t>((c >> 3) * ROWS * 128 + r * 128 + (((c ^ r) & 7) << 4));
+}
+
+// Descriptor of values as the B operand: tokens along K, values along N, in
+// blocks of 64 values `block` bytes apart, eight tokens 1024 bytes apart.
+__device__ __forceinline__ uint64_t values_desc(uint32_t saddr, uint32_t block) {
+    return static_cast<uint64_t>((saddr & 0x3FFFF) >> 4) | static_cast<uint64_t>(block >> 4) << 16 |
+           static_cast<uint64_t>(1024 >> 4) << 32 | static_cast<uint64_t>(1) << 46 | static_cast<uint64_t>(2) << 61;
+}
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
+          "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
+          "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(taddr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+// Waits, as a warp, for a phase; where the wait runs out, reports it, gives what is in
+// flight once more as long, and lets the caller go on without waiting.
+__device__ __forceinline__ void wait_or_report(uint32_t bar, uint32_t parity, bool& alive, unsigned* status) {
+    if (!alive || __all_sync(~0u, mbar_wait(bar, parity))) return;
+    record_status(status, kStatusTimeout);
+    alive = false;
+    mbar_wait(bar, parity);
+    __syncwarp();
+}
+
+__device__ __forceinline__ void rows_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kSoftmaxWarps * 32) : "memory"); }
+
+// A ring position that goes round `n` places: the place, and the parity of the round.
+struct Turn {
+    int place = 0;
+    uint32_t round = 0;
+    __device__ __forceinline__ void step(int n) {
+        if (++place == n) place = 0, round ^= 1;
+    }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_constant__ SplitArgs sp) {
+    using S = Shape<D>;
+    constexpr int TT = S::kTile, NS = S::kSlotsHere;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t s_full[NS], s_empty[NS], s_scores[2], s_weights[2], s_values, s_queries;
+    __shared__ uint32_t s_tmem;
+    __shared__ bool s_last;
+    const AttnArgs& a = sp.a;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t q_smem = (smem_addr(smem_raw) + 1023) & ~1023u, ring = q_smem + S::kQ;
+
+    if (tid == 0) {
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(smem_addr(&s_full[i]), kLoadWarps * 32);
+            mbar_init(smem_addr(&s_empty[i]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_addr(&s_scores[i]), 1);
+            mbar_init(smem_addr(&s_weights[i]), kSoftmaxWarps * 32);
+        }
+        mbar_init(smem_addr(&s_values), 1);
+        mbar_init(smem_addr(&s_queries), kSoftmaxWarps * 32);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    Walk<TT, kRows, kFixed> walk;
+    if (!walk.template find<kThreads>(sp)) return;
+    if (warp == kMmaWarp) tmem_alloc(smem_addr(&s_tmem), kTmemCols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    bool alive = true;
+
+    if (warp == kMmaWarp) {
+        // ------------------------------------------------------ products
+        const uint32_t qk_idesc = idesc_bf16(TT), pv_idesc = idesc_bf16(D) | 1u << 16;  // B (values) N-major
+        Turn slot;            // of the next tile's keys or values, as they come
+        uint32_t tile = 0, items = 0;
+        for (Item it; walk.next(sp, it);) {
+            const int tiles = max(0, (it.tok1 - (it.tok0 & ~15) + TT - 1) / TT);
+            if (tiles == 0) continue;
+            wait_or_report(smem_addr(&s_queries), items++ & 1, alive, a.status);
+            auto scores = [&](uint32_t n) {  // of tile n, whose keys come next
+                wait_or_report(smem_addr(&s_full[slot.place]), slot.round, alive, a.status);
+                fence_async_smem();  // the copies were made through the generic proxy
+                tc_fence_after();
+                const uint32_t keys = ring + slot.place * S::kSlot;
+                if (elect_one()) {
+#pragma unroll
+                    for (int ks = 0; ks < D / 16; ++ks)
+                        mma_bf16(tmem + (n & 1) * TT, sw128_desc(q_smem + (ks >> 2) * kRows * 128 + (ks & 3) * 32),
+                                 sw128_desc(keys + (ks >> 2) * TT * 128 + (ks & 3) * 32), qk_idesc, ks > 0);
+                    mma_commit(smem_addr(&s_empty[slot.place]));
+                    mma_commit(smem_addr(&s_scores[n & 1]));
+                }
+                __syncwarp();
+                slot.step(NS);
+            };
+            scores(tile);
+            for (int i = 0; i < tiles; ++i, ++tile) {
+                // The tile's values lie after its keys; the next tile's keys after those.
+                const Turn values = slot;
+                slot.step(NS);
+                if (i + 1 < tiles) {
+                    // Its scores go where the weights of tile − 1 are, which must have been used.
+                    if (i > 0) wait_or_report(smem_addr(&s_values), (tile - 1) & 1, alive, a.status);
+                    scores(tile + 1);
+                }
+                wait_or_report(smem_addr(&s_full[values.place]), values.round, alive, a.status);
+                wait_or_report(smem_addr(&s_weights[tile & 1]), tile >> 1 & 1, alive, a.status);
+                fence_async_smem();
+                tc_fence_after();
+                const uint32_t vals = ring + values.place * S::kSlot, weights = tmem + (tile & 1) * TT;
+                if (elect_one()) {
+                    // Sixteen tokens' weights: 8 columns of their upper halves, 16 columns further the lower ones.
+#pragma unroll
+                    for (int ks = 0; ks < TT / 16; ++ks) {
+                        const uint64_t desc = values_desc(vals + ks * 2048, TT * 128);
+                        mma_bf16_tmem_a(tmem + kColO, weights + (ks >> 1) * 32 + (ks & 1) * 8, desc, pv_idesc, 1);
+                        mma_bf16_tmem_a(tmem + kColO, weights + (ks >> 1) * 32 + (ks & 1) * 8 + 16, desc, pv_idesc, 1);
+                    }
+                    mma_commit(smem_addr(&s_empty[values.place]));
+                    mma_commit(smem_addr(&s_values));
+                }
+                __syncwarp();
+            }
+        }
+    } else if (warp >= kSoftmaxWarps) {
+        // -------------------------------------------------------- copies
+        // A warp copies TT / 4 tokens of each tile; lane l knows token l of them.
+        constexpr int kMine = TT / kLoadWarps, kSub = kMine / 16, kChunks = D / 8;
+        constexpr int kPerPass = 32 / kChunks;  // token rows of one pass of the warp's lanes (D ≤ 256)
+        const int my_row = (warp - kSoftmaxWarps) * kMine, d_chunks = a.head_dim / 8;
+        const int load_c = lane % kChunks, load_r = lane / kChunks;
+        Turn slot;
+        slot.round = 1;  // the ring's first round finds its slots free
+        for (Item it; walk.next(sp, it);) {
+            const int base0 = it.tok0 & ~15, tiles = max(0, (it.tok1 - base0 + TT - 1) / TT);
+            const int* table = a.table + it.b * a.table_stride;
+            auto page_of = [&](int i) {  // page id of the lane's token, −1 outside the piece
+                const int tok = base0 + i * TT + my_row + (lane & (kMine - 1));
+                return i < tiles && tok >= it.tok0 && tok < it.tok1 ? __ldg(table + sp.page_index(tok)) : -1;
+            };
+            int page_next = page_of(0);
+            for (int i = 0; i < tiles; ++i) {
+                const int tok = base0 + i * TT + my_row + (lane & (kMine - 1)), page = page_next;
+                page_next = page_of(i + 1);
+                long long off = -1;
+                if (tok >= it.tok0 && tok < it.tok1) {
+                    if (page >= 0 && page < a.pages)
+                        off = page * a.page_stride + (tok - sp.page_index(tok) * a.page_size) * a.token_stride + it.h * a.head_stride;
+                    else
+                        record_status(a.status, kStatusInvalid);
+                }
+                long long off0[kSub];  // of the first token of each 16
+#pragma unroll
+                for (int sub = 0; sub < kSub; ++sub) off0[sub] = __shfl_sync(~0u, off, 16 * sub);
+                const long long mine = kSub == 2 && (lane & 16) ? off0[kSub - 1] : off0[0];
+                const bool even = __all_sync(~0u, mine >= 0 && off == mine + (lane & 15) * a.token_stride) && d_chunks == kChunks;
+#pragma unroll
+                for (int key = 1; key >= 0; --key) {
+                    wait_or_report(smem_addr(&s_empty[slot.place]), slot.round, alive, a.status);
+                    const uint32_t dst = ring + slot.place * S::kSlot;
+                    const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(key ? a.k : a.v);
+                    if (even) {
+#pragma unroll
+                        for (int sub = 0; sub < kSub; ++sub) {
+                            const __nv_bfloat16* from = src + off0[sub] + load_r * a.token_stride + load_c * 8;
+#pragma unroll
+                            for (int p = 0; p < 16; p += kPerPass) {
+                                cp_async16(dst + place<TT>(my_row + sub * 16 + p + load_r, load_c), from);
+                                from += kPerPass * a.token_stride;
+                            }
+                        }
+                    } else {
+#pragma unroll 4
+                        for (int p = 0; p < kMine; p += kPerPass) {
+                            const long long o = __shfl_sync(~0u, off, p + load_r);
+                            const bool there = o >= 0 && load_c < d_chunks;
+                            cp_async16_zfill(dst + place<TT>(my_row + p + load_r, load_c), src + (there ? o + load_c * 8 : 0), there ? 16 : 0);
+                        }
+                    }
+                    cp_async_arrive(smem_addr(&s_full[slot.place]));
+                    slot.step(NS);
+                }
+            }
+        }
+        cp_async_wait_all();
+    } else {
+        // ------------------------------------------- a row in every thread
+        const uint32_t mine = tmem + (static_cast<uint32_t>(warp * 32) << 16);  // the warp's lanes
+        Turn slot;  // of the tile's values
+        slot.step(NS);
+        uint32_t tile = 0;
+        for (Item it; walk.next(sp, it);) {
+            const int base0 = it.tok0 & ~15, tiles = max(0, (it.tok1 - base0 + TT - 1) / TT);
+            const int row = it.row0 + tid, j = sp.over_G(row);
+            const bool live = row < it.rows;
+            const int see_hi = live ? it.len - it.n + j + 1 : 0x7fffffff;  // tokens that the row sees
+            const int see_lo = live && a.window > 0 ? static_cast<int>(max(0ll, static_cast<long long>(see_hi) - a.window)) : 0;
+            // Tokens before all_hi and from all_lo on are seen by every row of the item.
+            const int all_hi = it.len - it.n + sp.over_G(it.row0) + 1;
+            const int all_lo = a.window > 0 ? static_cast<int>(max(0ll, static_cast<long long>(it.len) - it.n +
+                                                                          sp.over_G(min(it.row0 + kRows, it.rows) - 1) + 1 - a.window)) : 0;
+            if (tiles > 0) {
+                const __nv_bfloat16* src = a.q.data + (live ? (it.start + j) * a.q.token_stride + (it.h * sp.G + row - j * sp.G) * a.q.head_stride : 0);
+#pragma unroll 8
+                for (int c = 0; c < D / 8; ++c) {
+                    uint4 v = make_uint4(0, 0, 0, 0);
+                    if (live && 8 * c < a.head_dim) {
+                        v = *reinterpret_cast<const uint4*>(src + 8 * c);
+                        v.x ^= sp.flip, v.y ^= sp.flip, v.z ^= sp.flip, v.w ^= sp.flip;
+                    }
+                    sts128(q_smem + place<kRows>(tid, c), v);
+                }
+                fence_async_smem();
+                uint32_t zero[32];
+#pragma unroll
+                for (int x = 0; x < 32; ++x) zero[x] = 0;
+#pragma unroll
+                for (int c = 0; c < D; c += 32) tmem_st32(mine + kColO + c, zero);
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(smem_addr(&s_queries));
+            }
+            float m = -INFINITY, l = 0.f;  // reference score, unscaled; sum of the weights
+            for (int i = 0; i < tiles; ++i, ++tile, slot.step(NS), slot.step(NS)) {
+                const int base = base0 + i * TT;
+                const bool hidden = min(base + TT, it.tok1) > all_hi || max(base, it.tok0) < all_lo;
+                const bool partly = hidden || base + TT > it.tok1 || base < it.tok0;
+                const int lo = max(see_lo, it.tok0) - base, hi = min(see_hi, it.tok1) - base;  // columns that the row sees
+                const uint32_t scores = mine + (tile & 1) * TT;
+                wait_or_report(smem_addr(&s_scores[tile & 1]), tile >> 1 & 1, alive, a.status);
+                tc_fence_after();
+                // ---- reference
+                float grown = m;
+#pragma unroll
+                for (int c = 0; c < TT; c += 32) {
+                    uint32_t v[32];
+                    tmem_ld32(scores + c, v);
+                    if (partly) {
+#pragma unroll
+                        for (int x = 0; x < 32; ++x) grown = fmaxf(grown, c + x >= lo && c + x < hi ? __uint_as_float(v[x]) : -INFINITY);
+                    } else {
+#pragma unroll
+                        for (int x = 0; x < 32; ++x) grown = fmaxf(grown, __uint_as_float(v[x]));
+                    }
+                }
+                auto values_so_far = [&]() {  // the products before this tile's are in O
+                    if (i > 0) wait_or_report(smem_addr(&s_values), (tile - 1) & 1, alive, a.status);
+                    tc_fence_after();
+                };
+                const float by = (grown - m) * sp.scale_log2;
+                if (__any_sync(~0u, by > 8.f)) {
+                    const float keep = m == -INFINITY ? 0.f : ex2(-by);
+                    if (i > 0) {
+                        values_so_far();
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 32) {
+                            uint32_t v[32];
+                            tmem_ld32(mine + kColO + c, v);
+#pragma unroll
+                            for (int x = 0; x < 32; ++x) v[x] = __float_as_uint(__uint_as_float(v[x]) * keep);
+                            tmem_st32(mine + kColO + c, v);
+                        }
+                        tmem_wait_st();
+                    }
+                    l *= keep;
+                    m = grown;
+                }
+                const float ref = m == -INFINITY ? 0.f : m * sp.scale_log2;
+
+                // ---- values that are not finite, of tokens that some rows do not see: 0 · ∞ would spoil those rows.
+                // They are made 0 for the product and added here to the rows that see them.
+                if (hidden) {
+                    const uint32_t vals = ring + slot.place * S::kSlot;
+                    wait_or_report(smem_addr(&s_full[slot.place]), slot.round, alive, a.status);
+                    bool odd = false;
+                    for (int x = tid; x < TT * S::kBlocks * 8; x += kSoftmaxWarps * 32) {
+                        const uint4 w = lds128(vals + x * 16);
+                        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) odd |= (u[y] & 0x7F80u) == 0x7F80u || (u[y] & 0x7F800000u) == 0x7F800000u;
+                    }
+                    if (tid == 0) s_last = false;
+                    rows_sync();
+                    if (odd) s_last = true;
+                    rows_sync();
+                    if (s_last) {
+                        values_so_far();
+#pragma unroll 1
+                        for (int tk = 0; tk < TT; ++tk) {
+                            bool bad = false;  // the token's row has such a value: the same for all threads
+                            for (int c = 0; c < D / 8; ++c) {
+                                const uint4 w = lds128(vals + place<TT>(tk, c));
+                                const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                                for (int y = 0; y < 4; ++y) bad |= (u[y] & 0x7F80u) == 0x7F80u || (u[y] & 0x7F800000u) == 0x7F800000u;
+                            }
+                            if (!bad) continue;
+                            uint32_t sv[32];
+                            tmem_ld32(scores + (tk & ~31), sv);
+                            float score = 0.f;
+#pragma unroll
+                            for (int x = 0; x < 32; ++x)
+                                if (x == (tk & 31)) score = __uint_as_float(sv[x]);
+                            const bool sees = tk >= lo && tk < hi;
+                            const float p = sees ? ex2(fmaf(score, sp.scale_log2, -ref)) : 0.f;
+#pragma unroll 1
+                            for (int c = 0; c < D; c += 32) {
+                                uint32_t v[32];
+                                tmem_ld32(mine + kColO + c, v);
+#pragma unroll
+                                for (int x = 0; x < 32; x += 8) {
+                                    const uint4 w = lds128(vals + place<TT>(tk, (c + x) / 8));
+                                    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                                    for (int y = 0; y < 8; ++y) {
+                                        const float value = y & 1 ? bf16_hi(u[y >> 1]) : bf16_lo(u[y >> 1]);
+                                        if (sees) v[x + y] = __float_as_uint(__uint_as_float(v[x + y]) + p * value);
+                                    }
+                                }
+                                tmem_st32(mine + kColO + c, v);
+                            }
+                            tmem_wait_st();
+                            rows_sync();  // every row has read the token's values
+                            for (int c = tid; c < D / 8; c += kSoftmaxWarps * 32) sts128(vals + place<TT>(tk, c), make_uint4(0, 0, 0, 0));
+                        }
+                        fence_async_smem();
+                    }
+                }
+                // ---- weights, over the scores: of 32 tokens the upper halves in 16 columns, then the lower ones
+#pragma unroll
+                for (int c = 0; c < TT; c += 32) {
+                    uint32_t v[32], w[32];
+                    tmem_ld32(scores + c, v);
+#pragma unroll
+                    for (int x = 0; x < 32; x += 2) {
+                        float p0 = ex2(fmaf(__uint_as_float(v[x]), sp.scale_log2, -ref));
+                        float p1 = ex2(fmaf(__uint_as_float(v[x + 1]), sp.scale_log2, -ref));
+                        if (partly) {
+                            p0 = c + x >= lo && c + x < hi ? p0 : 0.f;
+                            p1 = c + x + 1 >= lo && c + x + 1 < hi ? p1 : 0.f;
+                        }
+                        l += p0;
+                        l += p1;
+                        const uint32_t up = pack_bf16(p0, p1);
+                        w[x >> 1] = up;
+                        w[16 + (x >> 1)] = pack_bf16(p0 - bf16_lo(up), p1 - bf16_hi(up));
+                    }
+                    tmem_st32(scores + c, w);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(smem_addr(&s_weights[tile & 1]));
+            }
+            // ---- the row's sums
+            if (tiles > 0) wait_or_report(smem_addr(&s_values), (tile - 1) & 1, alive, a.status);
+            tc_fence_after();
+            const Parts<kRows, D> parts(sp, walk, it, kFixed);
+            float* const part = parts.at(static_cast<int>(blockIdx.x) - parts.first);
+            const bool whole = it.whole();
+            if (!whole && live) {
+                part[tid] = m * sp.scale_log2;
+                part[kRows + tid] = fminf(l, 3e38f);
+            }
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+                uint32_t v[32];
+                tmem_ld32(mine + kColO + c, v);
+                if (live) {
+#pragma unroll
+                    for (int x = 0; x < 32; x += 4) {
+                        const float4 f = make_float4(__uint_as_float(v[x]), __uint_as_float(v[x + 1]), __uint_as_float(v[x + 2]), __uint_as_float(v[x + 3]));
+                        if (!whole)
+                            *reinterpret_cast<float4*>(part + 2 * kRows + tid * D + c + x) = f;
+                        else if (c + x < a.head_dim)
+                            put_row(sp, it, row, c + x, &f.x, 4, l);
+                    }
+                }
+                __syncwarp();
+            }
+            tc_fence_before();
+            rows_sync();
+            if (!whole) parts.template finish<kSoftmaxWarps>(sp, it, s_last, rows_sync);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+template <int D>
+cudaError_t run(const SplitArgs& sp, int grid, cudaStream_t stream) {
+    using S = Shape<D>;
+    static std::atomic<bool> ready[kMaxDevices];  // the kernel may use its shared memory on this device
+    int device = 0;
+    cudaError_t err = cudaGetDevice(&device);
+    if (err != cudaSuccess) return err;
+    if (!ready[device & (kMaxDevices - 1)].load(std::memory_order_relaxed)) {
+        err = cudaFuncSetAttribute(attn_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+        if (err != cudaSuccess) return err;
+        ready[device & (kMaxDevices - 1)].store(true, std::memory_order_relaxed);
+    }
+    attn_tc_kernel<D><<<grid, kThreads, S::kSmem, stream>>>(sp);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t attn_tc_partial_floats(int head_dim) { return partial_floats(kRows, head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256); }
+
+cudaError_t launch_attn_tc(const SplitArgs& sp, const DeviceInfo& dev, cudaStream_t stream) {
+    const AttnArgs& a = sp.a;
+    const int tile = a.head_dim <= 128 ? 128 : 64;
+    // At least as many units as the batch can have: a CTA for each, where they are few.
+    const double reach = std::min(static_cast<double>(a.width) * a.page_size, a.window > 0 ? static_cast<double>(a.window) + a.T : 1e18);
+    const double most = static_cast<double>(a.kv_heads) * (a.B + static_cast<double>(a.T) * sp.G / kRows) * (reach / tile + 2 + kFixed);
+    const int grid = static_cast<int>(std::min<double>(std::min(dev.sm_count, kMaxCtas), most));
+    if (a.head_dim <= 64) return run<64>(sp, grid, stream);
+    if (a.head_dim <= 128) return run<128>(sp, grid, stream);
+    return run<256>(sp, grid, stream);
+}
+
+}  // namespace w4
