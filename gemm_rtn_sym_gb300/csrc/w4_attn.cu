@@ -638,7 +638,13 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
             }
         }
         __syncthreads();
-        if (!whole) parts.template finish<kWarps>(sp, it, s_last, [] { __syncthreads(); });
+        if (!whole)
+            parts.finish(sp, s_last, [] { __syncthreads(); }, [&](int k0, int n, int step, bool last) {
+                if (n <= 4)
+                    parts.template join_rows<kWarps, 4>(sp, it, warp, lane, k0, n, step, last);
+                else
+                    parts.template join_rows<kWarps, 16>(sp, it, warp, lane, k0, n, step, last);
+            });
     }
 }
 

@@ -287,22 +287,26 @@ struct Parts {
 #pragma unroll
                 for (int x = 0; x < V; ++x) v[y][x] = 0.f;
             for (int i0 = 0; i0 < n; i0 += NP) {
-                // lanes 0 to 15: the references, 16 to 31: the sums
                 const bool there = i0 + i_lane < n;
-                const float stat = there ? __ldcg(at(k0 + (i0 + i_lane) * step) + (lane < 16 ? 0 : ROWS) + r + y_lane) : -INFINITY;
+                const float* mine = at(k0 + min(i0 + i_lane, n - 1) * step) + r + y_lane;
+                const float pm = there ? __ldcg(mine) : -INFINITY, pl = __ldcg(mine + ROWS);
                 float w[NR][NP][V];
 #pragma unroll
                 for (int i = 0; i < NP; ++i) {
                     const float* p = at(k0 + min(i0 + i, n - 1) * step) + 2 * ROWS + r * D + lane * V;
 #pragma unroll
                     for (int y = 0; y < NR; ++y)
+                        if constexpr (V == 2) {
+                            const float2 f = __ldcg(reinterpret_cast<const float2*>(p + y * D));
+                            w[y][i][0] = f.x, w[y][i][1] = f.y;
+                        } else {
 #pragma unroll
-                        for (int x = 0; x < V; x += 2) {
-                            const float2 f = __ldcg(reinterpret_cast<const float2*>(p + y * D + x));
-                            w[y][i][x] = f.x, w[y][i][x + 1] = f.y;
+                            for (int x = 0; x < V; x += 4) {
+                                const float4 f = __ldcg(reinterpret_cast<const float4*>(p + y * D + x));
+                                w[y][i][x] = f.x, w[y][i][x + 1] = f.y, w[y][i][x + 2] = f.z, w[y][i][x + 3] = f.w;
+                            }
                         }
                 }
-                const float pm = __shfl_sync(~0u, stat, lane & 15), pl = __shfl_sync(~0u, stat, (lane & 15) + 16);
                 float nm = fmaxf(mm, pm);
 #pragma unroll
                 for (int d = 1; d < NP; d <<= 1) nm = fmaxf(nm, __shfl_xor_sync(~0u, nm, d));
@@ -342,29 +346,24 @@ struct Parts {
     }
 
     // After this CTA has left its part: the last part of a group of sixteen to get here joins the group, the last
-    // group the item.  `sync` is a barrier of the WARPS warps that take part (numbered from 0), `s_last` shared by them.
-    template <int WARPS, class Sync>
-    __device__ __forceinline__ void finish(const SplitArgs& sp, const Item& it, bool& s_last, Sync sync) const {
-        const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    // group the item.  `sync` is a barrier of the warps that take part (thread 0 among them), `s_last` shared by them;
+    // `join` (parts k0, k0 + step, ..., n of them, into the output if `last`, else into part k0) is called by all.
+    template <class Sync, class Join>
+    __device__ __forceinline__ void finish(const SplitArgs& sp, bool& s_last, Sync sync, Join join) const {
         const int own = static_cast<int>(blockIdx.x) - first;
         const int k0 = own / kJoinGroup * kJoinGroup, in_group = min(kJoinGroup, count - k0), groups = (count + kJoinGroup - 1) / kJoinGroup;
         if (in_group > 1) {
-            if (tid == 0) s_last = arrive(sp.arrived + first + k0, in_group);
+            if (threadIdx.x == 0) s_last = arrive(sp.arrived + first + k0, in_group);
             sync();
             const bool last = s_last;
-            if (last) {
-                if (in_group <= 4)
-                    join_rows<WARPS, 4>(sp, it, warp, lane, k0, in_group, 1, groups == 1);
-                else
-                    join_rows<WARPS, 16>(sp, it, warp, lane, k0, in_group, 1, groups == 1);
-            }
+            if (last) join(k0, in_group, 1, groups == 1);
             sync();
             if (!last) return;
         }
         if (groups > 1) {
-            if (tid == 0) s_last = arrive(sp.arrived + kMaxCtas + first, groups);
+            if (threadIdx.x == 0) s_last = arrive(sp.arrived + kMaxCtas + first, groups);
             sync();
-            if (s_last) join_rows<WARPS, 16>(sp, it, warp, lane, 0, groups, kJoinGroup, true);
+            if (s_last) join(0, groups, kJoinGroup, true);
             sync();
         }
     }

@@ -19,11 +19,12 @@
 // the tokens' rows by cp.async, from pages of any size, into a ring of six
 // slots, keys and values in turn.  Warp 8 issues the products: the scores of
 // tile i + 1 while the weights of tile i are made.
-// Tensor memory: S of two tiles in columns 0 to 2·TT, O from column 256.
+// Tensor memory: S of three tiles from column 0, then O.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -43,11 +44,12 @@ constexpr int kMmaWarp = kSoftmaxWarps + kLoadWarps;
 constexpr int kThreads = 32 * (kMmaWarp + 1);
 constexpr int kSlots = 6;
 constexpr int kFixed = 2;  // an item's fixed cost in tiles
-constexpr uint32_t kColO = 256, kTmemCols = 512;
+constexpr uint32_t kTmemCols = 512;
 
 template <int D>
 struct Shape {
     static constexpr int kTile = D == 256 ? 64 : 128;
+    static constexpr uint32_t kColO = D == 256 ? 256 : 384;
     static constexpr int kBlocks = D / 64;            // 128-byte columns of a row
     static constexpr int kSlot = kTile * D * 2;       // keys or values of a tile
     static constexpr int kSlotsHere = D == 256 ? 4 : kSlots;
@@ -107,7 +109,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     using S = Shape<D>;
     constexpr int TT = S::kTile, NS = S::kSlotsHere;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t s_full[NS], s_empty[NS], s_scores[2], s_weights[2], s_values, s_queries;
+    // s_values: the products of even and of odd tiles are in O; apart, since a wait may look two tiles back.
+    __shared__ __align__(8) uint64_t s_full[NS], s_empty[NS], s_scores[3], s_weights[3], s_values[2], s_queries;
     __shared__ uint32_t s_tmem;
     __shared__ bool s_last;
     const AttnArgs& a = sp.a;
@@ -119,11 +122,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             mbar_init(smem_addr(&s_full[i]), kLoadWarps * 32);
             mbar_init(smem_addr(&s_empty[i]), 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 3; ++i) {
             mbar_init(smem_addr(&s_scores[i]), 1);
             mbar_init(smem_addr(&s_weights[i]), kSoftmaxWarps * 32);
         }
-        mbar_init(smem_addr(&s_values), 1);
+        mbar_init(smem_addr(&s_values[0]), 1);
+        mbar_init(smem_addr(&s_values[1]), 1);
         mbar_init(smem_addr(&s_queries), kSoftmaxWarps * 32);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -138,14 +142,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
 
     if (warp == kMmaWarp) {
         // ------------------------------------------------------ products
-        const uint32_t qk_idesc = idesc_bf16(TT), pv_idesc = idesc_bf16(D) | 1u << 16;  // B (values) N-major
+        // A factor below zero turns the queries' signs over.
+        const uint32_t qk_idesc = idesc_bf16(TT) | (sp.flip ? 1u << 13 : 0u), pv_idesc = idesc_bf16(D) | 1u << 16;  // B (values) N-major
         Turn slot;            // of the next tile's keys or values, as they come
+        Turn next, now;       // score buffers of the tile to be scored next and of the one whose values are next
         uint32_t tile = 0, items = 0;
         for (Item it; walk.next(sp, it);) {
             const int tiles = max(0, (it.tok1 - (it.tok0 & ~15) + TT - 1) / TT);
             if (tiles == 0) continue;
             wait_or_report(smem_addr(&s_queries), items++ & 1, alive, a.status);
-            auto scores = [&](uint32_t n) {  // of tile n, whose keys come next
+            auto scores = [&]() {  // of the tile whose keys come next
                 wait_or_report(smem_addr(&s_full[slot.place]), slot.round, alive, a.status);
                 fence_async_smem();  // the copies were made through the generic proxy
                 tc_fence_after();
@@ -153,41 +159,43 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                 if (elect_one()) {
 #pragma unroll
                     for (int ks = 0; ks < D / 16; ++ks)
-                        mma_bf16(tmem + (n & 1) * TT, sw128_desc(q_smem + (ks >> 2) * kRows * 128 + (ks & 3) * 32),
+                        mma_bf16(tmem + next.place * TT, sw128_desc(q_smem + (ks >> 2) * kRows * 128 + (ks & 3) * 32),
                                  sw128_desc(keys + (ks >> 2) * TT * 128 + (ks & 3) * 32), qk_idesc, ks > 0);
                     mma_commit(smem_addr(&s_empty[slot.place]));
-                    mma_commit(smem_addr(&s_scores[n & 1]));
+                    mma_commit(smem_addr(&s_scores[next.place]));
                 }
                 __syncwarp();
                 slot.step(NS);
+                next.step(3);
             };
-            scores(tile);
+            scores();
             for (int i = 0; i < tiles; ++i, ++tile) {
                 // The tile's values lie after its keys; the next tile's keys after those.
                 const Turn values = slot;
                 slot.step(NS);
                 if (i + 1 < tiles) {
-                    // Its scores go where the weights of tile − 1 are, which must have been used.
-                    if (i > 0) wait_or_report(smem_addr(&s_values), (tile - 1) & 1, alive, a.status);
-                    scores(tile + 1);
+                    // Its scores go where the weights of tile − 2 are, which must have been used.
+                    if (i > 1) wait_or_report(smem_addr(&s_values[tile & 1]), (tile - 2) >> 1 & 1, alive, a.status);
+                    scores();
                 }
                 wait_or_report(smem_addr(&s_full[values.place]), values.round, alive, a.status);
-                wait_or_report(smem_addr(&s_weights[tile & 1]), tile >> 1 & 1, alive, a.status);
+                wait_or_report(smem_addr(&s_weights[now.place]), now.round, alive, a.status);
                 fence_async_smem();
                 tc_fence_after();
-                const uint32_t vals = ring + values.place * S::kSlot, weights = tmem + (tile & 1) * TT;
+                const uint32_t vals = ring + values.place * S::kSlot, weights = tmem + now.place * TT;
                 if (elect_one()) {
                     // Sixteen tokens' weights: 8 columns of their upper halves, 16 columns further the lower ones.
 #pragma unroll
                     for (int ks = 0; ks < TT / 16; ++ks) {
                         const uint64_t desc = values_desc(vals + ks * 2048, TT * 128);
-                        mma_bf16_tmem_a(tmem + kColO, weights + (ks >> 1) * 32 + (ks & 1) * 8, desc, pv_idesc, 1);
-                        mma_bf16_tmem_a(tmem + kColO, weights + (ks >> 1) * 32 + (ks & 1) * 8 + 16, desc, pv_idesc, 1);
+                        mma_bf16_tmem_a(tmem + S::kColO, weights + (ks >> 1) * 32 + (ks & 1) * 8, desc, pv_idesc, 1);
+                        mma_bf16_tmem_a(tmem + S::kColO, weights + (ks >> 1) * 32 + (ks & 1) * 8 + 16, desc, pv_idesc, 1);
                     }
                     mma_commit(smem_addr(&s_empty[values.place]));
-                    mma_commit(smem_addr(&s_values));
+                    mma_commit(smem_addr(&s_values[tile & 1]));
                 }
                 __syncwarp();
+                now.step(3);
             }
         }
     } else if (warp >= kSoftmaxWarps) {
@@ -257,7 +265,23 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         Turn slot;  // of the tile's values
         slot.step(NS);
         uint32_t tile = 0;
-        for (Item it; walk.next(sp, it);) {
+        Turn now;  // of the tile's scores
+        // The queries of an item are asked for before the sums of the one before it go out: a row by D / 8 lanes.
+        auto ask = [&](const Item& n) {
+            constexpr int kChunks = D / 8, kPerPass = kSoftmaxWarps * 32 / kChunks;
+            const int c = tid % kChunks;
+#pragma unroll 4
+            for (int p = 0; p < kRows; p += kPerPass) {
+                const int r = p + tid / kChunks, row = n.row0 + r, jr = sp.over_G(row);
+                const bool there = row < n.rows && 8 * c < a.head_dim;
+                const __nv_bfloat16* src = a.q.data + (there ? (n.start + jr) * a.q.token_stride + (n.h * sp.G + row - jr * sp.G) * a.q.head_stride + 8 * c : 0);
+                cp_async16_zfill(q_smem + place<kRows>(r, c), src, there ? 16 : 0);
+            }
+        };
+        Item it;
+        bool more = walk.next(sp, it);
+        if (more) ask(it);
+        while (more) {
             const int base0 = it.tok0 & ~15, tiles = max(0, (it.tok1 - base0 + TT - 1) / TT);
             const int row = it.row0 + tid, j = sp.over_G(row);
             const bool live = row < it.rows;
@@ -268,51 +292,48 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             const int all_lo = a.window > 0 ? static_cast<int>(max(0ll, static_cast<long long>(it.len) - it.n +
                                                                           sp.over_G(min(it.row0 + kRows, it.rows) - 1) + 1 - a.window)) : 0;
             if (tiles > 0) {
-                const __nv_bfloat16* src = a.q.data + (live ? (it.start + j) * a.q.token_stride + (it.h * sp.G + row - j * sp.G) * a.q.head_stride : 0);
-#pragma unroll 8
-                for (int c = 0; c < D / 8; ++c) {
-                    uint4 v = make_uint4(0, 0, 0, 0);
-                    if (live && 8 * c < a.head_dim) {
-                        v = *reinterpret_cast<const uint4*>(src + 8 * c);
-                        v.x ^= sp.flip, v.y ^= sp.flip, v.z ^= sp.flip, v.w ^= sp.flip;
-                    }
-                    sts128(q_smem + place<kRows>(tid, c), v);
-                }
+                cp_async_wait_all();
                 fence_async_smem();
                 uint32_t zero[32];
 #pragma unroll
                 for (int x = 0; x < 32; ++x) zero[x] = 0;
 #pragma unroll
-                for (int c = 0; c < D; c += 32) tmem_st32(mine + kColO + c, zero);
+                for (int c = 0; c < D; c += 32) tmem_st32(mine + S::kColO + c, zero);
                 tmem_wait_st();
                 tc_fence_before();
                 mbar_arrive(smem_addr(&s_queries));
             }
             float m = -INFINITY, l = 0.f;  // reference score, unscaled; sum of the weights
-            for (int i = 0; i < tiles; ++i, ++tile, slot.step(NS), slot.step(NS)) {
+            for (int i = 0; i < tiles; ++i, ++tile, now.step(3), slot.step(NS), slot.step(NS)) {
                 const int base = base0 + i * TT;
                 const bool hidden = min(base + TT, it.tok1) > all_hi || max(base, it.tok0) < all_lo;
                 const bool partly = hidden || base + TT > it.tok1 || base < it.tok0;
-                const int lo = max(see_lo, it.tok0) - base, hi = min(see_hi, it.tok1) - base;  // columns that the row sees
-                const uint32_t scores = mine + (tile & 1) * TT;
-                wait_or_report(smem_addr(&s_scores[tile & 1]), tile >> 1 & 1, alive, a.status);
+                // Columns that the row sees: from lo on, `wide` of them.
+                const int lo = max(see_lo, it.tok0) - base, wide = max(min(see_hi, it.tok1) - base - lo, 0);
+                auto sees = [&](int column) { return static_cast<unsigned>(column - lo) < static_cast<unsigned>(wide); };
+                const uint32_t scores = mine + now.place * TT;
+                wait_or_report(smem_addr(&s_scores[now.place]), now.round, alive, a.status);
                 tc_fence_after();
                 // ---- reference
                 float grown = m;
+                auto largest = [&](auto some) {  // of the scores that the row sees: all of the tile's, or some
+#pragma unroll 1
+                    for (int c = 0; c < TT; c += 32) {
+                        uint32_t v[32];
+                        tmem_ld32(scores + c, v);
 #pragma unroll
-                for (int c = 0; c < TT; c += 32) {
-                    uint32_t v[32];
-                    tmem_ld32(scores + c, v);
-                    if (partly) {
-#pragma unroll
-                        for (int x = 0; x < 32; ++x) grown = fmaxf(grown, c + x >= lo && c + x < hi ? __uint_as_float(v[x]) : -INFINITY);
-                    } else {
-#pragma unroll
-                        for (int x = 0; x < 32; ++x) grown = fmaxf(grown, __uint_as_float(v[x]));
+                        for (int x = 0; x < 32; ++x) {
+                            const float f = __uint_as_float(v[x]);
+                            grown = fmaxf(grown, !decltype(some)::value || sees(c + x) ? f : -INFINITY);
+                        }
                     }
-                }
+                };
+                if (partly)
+                    largest(std::true_type());
+                else
+                    largest(std::false_type());
                 auto values_so_far = [&]() {  // the products before this tile's are in O
-                    if (i > 0) wait_or_report(smem_addr(&s_values), (tile - 1) & 1, alive, a.status);
+                    if (i > 0) wait_or_report(smem_addr(&s_values[(tile - 1) & 1]), (tile - 1) >> 1 & 1, alive, a.status);
                     tc_fence_after();
                 };
                 const float by = (grown - m) * sp.scale_log2;
@@ -323,10 +344,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
 #pragma unroll 1
                         for (int c = 0; c < D; c += 32) {
                             uint32_t v[32];
-                            tmem_ld32(mine + kColO + c, v);
+                            tmem_ld32(mine + S::kColO + c, v);
 #pragma unroll
                             for (int x = 0; x < 32; ++x) v[x] = __float_as_uint(__uint_as_float(v[x]) * keep);
-                            tmem_st32(mine + kColO + c, v);
+                            tmem_st32(mine + S::kColO + c, v);
                         }
                         tmem_wait_st();
                     }
@@ -369,12 +390,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
 #pragma unroll
                             for (int x = 0; x < 32; ++x)
                                 if (x == (tk & 31)) score = __uint_as_float(sv[x]);
-                            const bool sees = tk >= lo && tk < hi;
-                            const float p = sees ? ex2(fmaf(score, sp.scale_log2, -ref)) : 0.f;
+                            const bool seen = sees(tk);
+                            const float p = seen ? ex2(fmaf(score, sp.scale_log2, -ref)) : 0.f;
 #pragma unroll 1
                             for (int c = 0; c < D; c += 32) {
                                 uint32_t v[32];
-                                tmem_ld32(mine + kColO + c, v);
+                                tmem_ld32(mine + S::kColO + c, v);
 #pragma unroll
                                 for (int x = 0; x < 32; x += 8) {
                                     const uint4 w = lds128(vals + place<TT>(tk, (c + x) / 8));
@@ -382,10 +403,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
 #pragma unroll
                                     for (int y = 0; y < 8; ++y) {
                                         const float value = y & 1 ? bf16_hi(u[y >> 1]) : bf16_lo(u[y >> 1]);
-                                        if (sees) v[x + y] = __float_as_uint(__uint_as_float(v[x + y]) + p * value);
+                                        if (seen) v[x + y] = __float_as_uint(__uint_as_float(v[x + y]) + p * value);
                                     }
                                 }
-                                tmem_st32(mine + kColO + c, v);
+                                tmem_st32(mine + S::kColO + c, v);
                             }
                             tmem_wait_st();
                             rows_sync();  // every row has read the token's values
@@ -395,59 +416,125 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                     }
                 }
                 // ---- weights, over the scores: of 32 tokens the upper halves in 16 columns, then the lower ones
+                float sums[4] = {l, 0.f, 0.f, 0.f};
+                auto weights = [&](auto some) {
+#pragma unroll 1
+                    for (int c = 0; c < TT; c += 32) {
+                        uint32_t v[32], w[32];
+                        tmem_ld32(scores + c, v);
 #pragma unroll
-                for (int c = 0; c < TT; c += 32) {
-                    uint32_t v[32], w[32];
-                    tmem_ld32(scores + c, v);
-#pragma unroll
-                    for (int x = 0; x < 32; x += 2) {
-                        float p0 = ex2(fmaf(__uint_as_float(v[x]), sp.scale_log2, -ref));
-                        float p1 = ex2(fmaf(__uint_as_float(v[x + 1]), sp.scale_log2, -ref));
-                        if (partly) {
-                            p0 = c + x >= lo && c + x < hi ? p0 : 0.f;
-                            p1 = c + x + 1 >= lo && c + x + 1 < hi ? p1 : 0.f;
+                        for (int x = 0; x < 32; x += 2) {
+                            float s0 = __uint_as_float(v[x]), s1 = __uint_as_float(v[x + 1]);
+                            if (decltype(some)::value) {
+                                s0 = sees(c + x) ? s0 : -INFINITY;
+                                s1 = sees(c + x + 1) ? s1 : -INFINITY;
+                            }
+                            const float p0 = ex2(fmaf(s0, sp.scale_log2, -ref)), p1 = ex2(fmaf(s1, sp.scale_log2, -ref));
+                            sums[x & 2] += p0;
+                            sums[(x & 2) + 1] += p1;
+                            // Upper halves cut off, not rounded: the lower ones take what is left, to 16 bits in all
+                            // (roundings to bf16 would share the exponentials' slow pipe).
+                            const uint32_t u0 = __float_as_uint(p0), u1 = __float_as_uint(p1);
+                            w[x >> 1] = __byte_perm(u0, u1, 0x7632);
+                            w[16 + (x >> 1)] = __byte_perm(__float_as_uint(p0 - __uint_as_float(u0 & 0xFFFF0000u)),
+                                                           __float_as_uint(p1 - __uint_as_float(u1 & 0xFFFF0000u)), 0x7632);
                         }
-                        l += p0;
-                        l += p1;
-                        const uint32_t up = pack_bf16(p0, p1);
-                        w[x >> 1] = up;
-                        w[16 + (x >> 1)] = pack_bf16(p0 - bf16_lo(up), p1 - bf16_hi(up));
+                        tmem_st32(scores + c, w);
                     }
-                    tmem_st32(scores + c, w);
-                }
+                };
+                if (partly)
+                    weights(std::true_type());
+                else
+                    weights(std::false_type());
+                l = (sums[0] + sums[1]) + (sums[2] + sums[3]);
                 tmem_wait_st();
                 tc_fence_before();
-                mbar_arrive(smem_addr(&s_weights[tile & 1]));
+                mbar_arrive(smem_addr(&s_weights[now.place]));
             }
             // ---- the row's sums
-            if (tiles > 0) wait_or_report(smem_addr(&s_values), (tile - 1) & 1, alive, a.status);
+            Item after;
+            more = walk.next(sp, after);
+            if (more) ask(after);
+            if (tiles > 0) wait_or_report(smem_addr(&s_values[(tile - 1) & 1]), (tile - 1) >> 1 & 1, alive, a.status);
             tc_fence_after();
+            const bool whole = it.whole(), none = it.len - it.n + j < 0;
             const Parts<kRows, D> parts(sp, walk, it, kFixed);
             float* const part = parts.at(static_cast<int>(blockIdx.x) - parts.first);
-            const bool whole = it.whole();
             if (!whole && live) {
                 part[tid] = m * sp.scale_log2;
                 part[kRows + tid] = fminf(l, 3e38f);
             }
+            // A row that sees nothing is zeros; one whose scores are all −∞ has no value (0 · 1 / 0).
+            __nv_bfloat16* const to = a.out.data + (live ? (it.start + j) * a.out.token_stride + (it.h * sp.G + row - j * sp.G) * a.out.head_stride : 0);
+            auto put = [&](int c, const uint32_t (&v)[32], float f) {  // 32 of the row's values from column c on, times f
+#pragma unroll
+                for (int x = 0; x < 32; x += 8) {
+                    uint32_t y[4];
+#pragma unroll
+                    for (int z = 0; z < 4; ++z)
+                        y[z] = none ? 0u : pack_bf16(__uint_as_float(v[x + 2 * z]) * f, __uint_as_float(v[x + 2 * z + 1]) * f);
+                    if (c + x < a.head_dim) *reinterpret_cast<uint4*>(to + c + x) = make_uint4(y[0], y[1], y[2], y[3]);
+                }
+            };
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
                 uint32_t v[32];
-                tmem_ld32(mine + kColO + c, v);
-                if (live) {
+                tmem_ld32(mine + S::kColO + c, v);
+                if (live && !whole) {
 #pragma unroll
-                    for (int x = 0; x < 32; x += 4) {
-                        const float4 f = make_float4(__uint_as_float(v[x]), __uint_as_float(v[x + 1]), __uint_as_float(v[x + 2]), __uint_as_float(v[x + 3]));
-                        if (!whole)
-                            *reinterpret_cast<float4*>(part + 2 * kRows + tid * D + c + x) = f;
-                        else if (c + x < a.head_dim)
-                            put_row(sp, it, row, c + x, &f.x, 4, l);
-                    }
+                    for (int x = 0; x < 32; ++x) part[(2 + c + x) * kRows + tid] = __uint_as_float(v[x]);
+                } else if (live) {
+                    put(c, v, 1.f / l);
                 }
                 __syncwarp();
             }
             tc_fence_before();
             rows_sync();
-            if (!whole) parts.template finish<kSoftmaxWarps>(sp, it, s_last, rows_sync);
+            // Parts as [reference, sum, D columns][row], so that neighbouring threads' rows lie side by side.
+            if (!whole)
+                parts.finish(sp, s_last, rows_sync, [&](int k0, int n, int step, bool last) {
+                    auto at = [&](int k) { return parts.at(k0 + min(k, n - 1) * step) + tid; };
+                    float mm = -INFINITY, ll = 0.f;
+#pragma unroll 4
+                    for (int k = 0; k < n; ++k) mm = fmaxf(mm, live ? __ldcg(at(k)) : 0.f);
+                    const float rm = mm == -INFINITY ? 0.f : mm;
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 32) {
+                        uint32_t v[32];
+                        float sum = 0.f;
+#pragma unroll
+                        for (int x = 0; x < 32; ++x) v[x] = 0;
+#pragma unroll 1
+                        for (int k = 0; k < n; k += 2) {  // two parts' loads in flight
+                            const float *p = at(k), *q = at(k + 1);
+                            const bool both = k + 1 < n;
+                            float u[32], w[32];
+                            if (live) {
+#pragma unroll
+                                for (int x = 0; x < 32; ++x) u[x] = __ldcg(p + (2 + c + x) * kRows), w[x] = __ldcg(q + (2 + c + x) * kRows);
+                                const float f = ex2(__ldcg(p) - rm), g = both ? ex2(__ldcg(q) - rm) : 0.f;
+                                sum += f * __ldcg(p + kRows);
+                                sum += both ? g * __ldcg(q + kRows) : 0.f;
+#pragma unroll
+                                for (int x = 0; x < 32; ++x) {
+                                    float y = fmaf(f, u[x], __uint_as_float(v[x]));
+                                    if (both) y = fmaf(g, w[x], y);
+                                    v[x] = __float_as_uint(y);
+                                }
+                            }
+                        }
+                        ll = sum;
+                        if (live && last) put(c, v, 1.f / ll);
+                        if (live && !last)
+#pragma unroll
+                            for (int x = 0; x < 32; ++x) parts.at(k0)[(2 + c + x) * kRows + tid] = __uint_as_float(v[x]);
+                    }
+                    if (live && !last) {
+                        parts.at(k0)[tid] = mm;
+                        parts.at(k0)[kRows + tid] = fminf(ll, 3e38f);
+                    }
+                });
+            it = after;
         }
     }
     tc_fence_before();
