@@ -493,6 +493,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             // Parts as [reference, sum, D columns][row], so that neighbouring threads' rows lie side by side.
             if (!whole)
                 parts.finish(sp, s_last, rows_sync, [&](int k0, int n, int step, bool last) {
+                    // This CTA's own part is still in tensor memory (the item's, when it is a group's that is joined).
+                    const int own = step == 1 ? static_cast<int>(blockIdx.x) - parts.first - k0 : -1;
                     auto at = [&](int k) { return parts.at(k0 + min(k, n - 1) * step) + tid; };
                     float mm = -INFINITY, ll = 0.f;
 #pragma unroll 4
@@ -504,24 +506,29 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                         float sum = 0.f;
 #pragma unroll
                         for (int x = 0; x < 32; ++x) v[x] = 0;
+                        auto fetch = [&](int k, uint32_t (&u)[32]) {
+                            const float* p = at(k) + (2 + c) * kRows;
+                            if (k == own) {
+                                tmem_ld32(mine + S::kColO + c, u);
+                            } else {
+#pragma unroll
+                                for (int x = 0; x < 32; ++x) u[x] = __float_as_uint(__ldcg(p + x * kRows));
+                            }
+                        };
+                        auto add = [&](int k, const uint32_t (&u)[32]) {
+                            if (k >= n || !live) return;
+                            const float f = ex2(__ldcg(at(k)) - rm);
+                            sum += f * __ldcg(at(k) + kRows);
+#pragma unroll
+                            for (int x = 0; x < 32; ++x) v[x] = __float_as_uint(fmaf(f, __uint_as_float(u[x]), __uint_as_float(v[x])));
+                        };
 #pragma unroll 1
                         for (int k = 0; k < n; k += 2) {  // two parts' loads in flight
-                            const float *p = at(k), *q = at(k + 1);
-                            const bool both = k + 1 < n;
-                            float u[32], w[32];
-                            if (live) {
-#pragma unroll
-                                for (int x = 0; x < 32; ++x) u[x] = __ldcg(p + (2 + c + x) * kRows), w[x] = __ldcg(q + (2 + c + x) * kRows);
-                                const float f = ex2(__ldcg(p) - rm), g = both ? ex2(__ldcg(q) - rm) : 0.f;
-                                sum += f * __ldcg(p + kRows);
-                                sum += both ? g * __ldcg(q + kRows) : 0.f;
-#pragma unroll
-                                for (int x = 0; x < 32; ++x) {
-                                    float y = fmaf(f, u[x], __uint_as_float(v[x]));
-                                    if (both) y = fmaf(g, w[x], y);
-                                    v[x] = __float_as_uint(y);
-                                }
-                            }
+                            uint32_t u0[32], u1[32];
+                            fetch(k, u0);
+                            fetch(k + 1, u1);
+                            add(k, u0);
+                            add(k + 1, u1);
                         }
                         ll = sum;
                         if (live && last) put(c, v, 1.f / ll);
