@@ -128,9 +128,10 @@ struct Shape {
     static constexpr int kScaleSlots = kAhead + 1;
     static constexpr int kScales = Q8 ? kScaleSlots * kTokens * 8 : 0;
     static constexpr int kGroup = kRing + kScales;
-    static constexpr int kMerge = kWarps * 16 * (D + 2) * 4;
+    // Where the groups' sums meet: rows 8 columns apart in banks, and two numbers for each row.
+    static constexpr int kMeetRow = D + 8, kMerge = kWarps * 16 * (kMeetRow + 2) * 4;
     static constexpr int kSmem = kGroups * kGroup > kMerge ? kGroups * kGroup : kMerge;
-    static_assert(kSlots >= 3, "a slot in use, two on the way");
+    static_assert(kSlots >= 3 && (!Q8 || kSlots % 2 == 0), "a slot in use, two on the way; scales in time");
 };
 
 // Chunk c (of 16 bytes) of token row r lies at r · row + ((c ^ turn(r)) · 16):
@@ -157,12 +158,24 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
     constexpr int KS = D / 16;  // k-steps of 16
     constexpr int kRow = S::kRow, kFixed = S::kFixed;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ bool s_last;
+    __shared__ bool s_last, s_more;
+    __shared__ Walk<kTile, 16 * R, S::kFixed> s_walk;
+    __shared__ Item s_item[2];  // this item and the next: read again after the tokens, whose loop has no registers to spare
     const AttnArgs& a = sp.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
     const int group = warp / R, rw = warp % R, G = sp.G;
     Walk<kTile, 16 * R, kFixed> walk;
     if (!walk.template find<kThreads>(sp)) return;
+    bool more;
+    {
+        Item it;
+        more = walk.next(sp, it);
+        if (tid == 0) {
+            s_walk = walk;
+            s_item[0] = it;
+        }
+    }
+    __syncthreads();
 
     const uint32_t ring = smem_addr(smem) + group * S::kGroup;
     float2* scales = reinterpret_cast<float2*>(smem + group * S::kGroup + S::kRing);
@@ -171,19 +184,23 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
     constexpr int kPerPass = 32 * R / S::kChunks;  // token rows of one pass of the group's lanes
     const int load_c = (rw * 32 + lane) % S::kChunks, load_r = (rw * 32 + lane) / S::kChunks;
 
-    for (Item it; walk.next(sp, it);) {
-        const int h = it.h, row0 = it.row0, rows = it.rows, tok0 = it.tok0, tok1 = it.tok1;
+    auto query_row = [&](const Item& n, int row) {
+        const int j = sp.over_G(row);
+        return a.q.data + (n.start + j) * a.q.token_stride + (n.h * G + row - j * G) * a.q.head_stride;
+    };
+    for (int which = 0; more; which ^= 1) {
+        const int h = s_item[which].h, row0 = s_item[which].row0, rows = s_item[which].rows;
+        const int tok0 = s_item[which].tok0, tok1 = s_item[which].tok1, before = s_item[which].len - s_item[which].n;
+        const int* const table = a.table + s_item[which].b * a.table_stride;
         // Stages begin at multiples of 16 tokens, so that they lie in one page where pages are such multiples.
         const int base0 = tok0 & ~15, count = tok1 - base0 - group * S::kTokens;
         const int stages = count <= 0 ? 0 : (count + S::kGroups * S::kTokens - 1) / (S::kGroups * S::kTokens);
 
         // ---- page ids of the first stages: lane l knows token l of a stage
-        const int* table = a.table + it.b * a.table_stride;
         auto token_of = [&](int i) { return base0 + (i * S::kGroups + group) * S::kTokens + (lane & (S::kTokens - 1)); };
         auto page_of = [&](int i) {  // page id of the lane's token, −1 outside the piece
             const int tok = token_of(i);
-            if (i >= stages || tok < tok0 || tok >= tok1) return -1;
-            return __ldg(table + sp.page_index(tok));
+            return tok >= tok0 && tok < tok1 ? __ldg(table + sp.page_index(tok)) : -1;
         };
         int first[S::kAhead];
 #pragma unroll
@@ -197,9 +214,9 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
         for (int x = 0; x < 2; ++x) {
             const int r = row0 + rw * 16 + g + 8 * x, j = sp.over_G(r);
             const bool live = r < rows;
-            see_hi[x] = live ? it.len - it.n + j + 1 : 0x7fffffff;
+            see_hi[x] = live ? before + j + 1 : 0x7fffffff;
             see_lo[x] = live && a.window > 0 ? static_cast<int>(max(0ll, static_cast<long long>(see_hi[x]) - a.window)) : 0;
-            const __nv_bfloat16* src = a.q.data + (live ? (it.start + j) * a.q.token_stride + (h * G + r - j * G) * a.q.head_stride : 0);
+            const __nv_bfloat16* src = live ? query_row(s_item[which], r) : a.q.data;
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
                 if (!Q8) {
@@ -217,12 +234,15 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
         }
 
         // ---- loads
-        // Scales of a token travel by register for one iteration, then through shared memory.
-        float pend_k = 0.f, pend_v = 0.f;
-        int pend_at = -1;
-        auto put_scales = [&]() {
-            if (Q8 && pend_at >= 0 && rw == 0 && lane < S::kTokens)
-                scales[pend_at * S::kTokens + lane] = make_float2(pend_k, __log2f(pend_v < kTiny ? kTiny : pend_v));
+        // Scales of the lane's token travel by register until the stage before theirs has been used (for an iteration
+        // and a half where kSlots is even), then through shared memory.
+        struct Scales {
+            float k, v;
+        };
+        Scales found = {0.f, 0.f}, older = found;
+        auto put_scales = [&](const Scales& x, int stage) {
+            if (Q8 && stage < stages && rw == 0 && lane < S::kTokens)
+                scales[stage % S::kScaleSlots * S::kTokens + lane] = make_float2(x.k, __log2f(x.v < kTiny ? kTiny : x.v));
         };
         long long off = -1;     // of the lane's token, in the stage whose keys were asked for last; −1: none
         long long off0[S::kSub];  // of the first token of each 16
@@ -239,25 +259,23 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
                     record_status(a.status, kStatusInvalid);
             }
             if (Q8) {
-                pend_k = pend_v = 0.f;
+                found = {0.f, 0.f};
                 if (off >= 0) {
                     const long long s = (static_cast<long long>(page) * a.kv_heads + h) * a.page_size + in_page;
-                    pend_k = __bfloat162float(a.k_scales[s]);
-                    pend_v = __bfloat162float(a.v_scales[s]);
+                    found.k = __bfloat162float(a.k_scales[s]);
+                    found.v = __bfloat162float(a.v_scales[s]);
                 }
-                pend_at = i < stages ? i % S::kScaleSlots : -1;
             }
 #pragma unroll
             for (int sub = 0; sub < S::kSub; ++sub) off0[sub] = __shfl_sync(~0u, off, 16 * sub);
             const long long mine = S::kSub == 2 && (lane & 16) ? off0[S::kSub - 1] : off0[0];
             even = __all_sync(~0u, mine >= 0 && off == mine + (lane & 15) * a.token_stride) && d_chunks == S::kChunks;
         };
-        int put = 0;  // ring slot of the next copy
-        auto load = [&](auto key, bool any) {  // keys or values of the stage found last
+        auto load = [&](auto key, int slot, bool any) {  // keys or values of the stage found last
             constexpr bool KEY = decltype(key)::value;
             if (any) {
                 // place of (load_r, load_c); rows p further on keep it but for the turn of p's low bits
-                const uint32_t dst = ring + put * S::kHalf + load_r * kRow + ((load_c ^ turn<kRow, Q8, KEY>(load_r)) << 4);
+                const uint32_t dst = ring + slot * S::kHalf + load_r * kRow + ((load_c ^ turn<kRow, Q8, KEY>(load_r)) << 4);
                 const uint8_t* src = static_cast<const uint8_t*>(KEY ? a.k : a.v);
                 auto to = [&](int p) { return (dst ^ (turn<kRow, Q8, KEY>(p) << 4)) + p * kRow; };
                 if (even) {
@@ -281,35 +299,32 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
                     }
                 }
             }
-            if (++put == S::kSlots) put = 0;
             cp_async_commit();
         };
         // Copy n holds the keys (n even) or values of stage n / 2; copy n + kSlots − 1 is asked for when copy n is
-        // there, into the slot of copy n − 1.  asked: the next stage to find.
-        int asked = S::kSlots / 2;
-        auto load_next = [&](auto key, int& page, int n) {
+        // there, into the slot of copy n − 1.  So stage i + kSlots / 2 is found while stage i is worked on.
+        auto load_next = [&](auto key, int i, int slot, int& page, int n) {
             if (decltype(key)::value) {
-                find(asked, page);
-                ++asked;
-                page = page_of(asked);
+                find(i + S::kSlots / 2, page);
+                page = page_of(i + S::kSlots / 2 + 1);
             }
-            load(key, (n >> 1) < stages);
+            load(key, slot, (n >> 1) < stages);
         };
         constexpr bool kOdd = S::kSlots % 2 != 0;
         using First = std::integral_constant<bool, kOdd>;    // keys where kSlots is odd: copy 2i + kSlots − 1
         using Second = std::integral_constant<bool, !kOdd>;  // copy 2i + kSlots
+        Scales begin[S::kAhead];
 #pragma unroll
         for (int n = 0; n < S::kSlots - 1; ++n) {
             if ((n & 1) == 0) {
                 find(n >> 1, first[n >> 1]);
-                put_scales();
-                load(std::true_type(), (n >> 1) < stages);
+                begin[n >> 1] = found;
+                load(std::true_type(), n, (n >> 1) < stages);
             } else {
-                load(std::false_type(), (n >> 1) < stages);
+                load(std::false_type(), n, (n >> 1) < stages);
             }
         }
-        pend_at = -1;
-        int page_next = page_of(asked);
+        int page_next = page_of(S::kSlots / 2);
 
         float row_scale[2] = {sp.scale_log2, sp.scale_log2};  // of scores, to base 2
         if (!Q8) {
@@ -343,8 +358,23 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
         int all_hi, all_lo;
         {
             const int j0 = sp.over_G(row0 + rw * 16), j1 = sp.over_G(max(min(row0 + rw * 16 + 15, rows - 1), 0));
-            all_hi = it.len - it.n + j0 + 1;
-            all_lo = a.window > 0 ? static_cast<int>(max(0ll, static_cast<long long>(it.len) - it.n + j1 + 1 - a.window)) : 0;
+            all_hi = before + j0 + 1;
+            all_lo = a.window > 0 ? static_cast<int>(max(0ll, static_cast<long long>(before) + j1 + 1 - a.window)) : 0;
+        }
+
+        // ---- the next item, and its first page ids and its queries to L2, while this one's first bytes are on their way
+        if (warp == 0) {
+            if (lane == 0) s_more = s_walk.next(sp, s_item[which ^ 1]);
+            __syncwarp();
+            if (s_more) {
+                const Item& n = s_item[which ^ 1];
+                const int tok = n.tok0 + lane * 32;  // a line of 32 page ids, or fewer where pages hold several tokens
+                if (lane < S::kAhead * S::kGroups * S::kTokens / 32 && tok < n.tok1)
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(a.table + n.b * a.table_stride + sp.page_index(tok)));
+                for (int x = lane; x < 16 * R * 4; x += 32)
+                    if (n.row0 + (x >> 2) < n.rows && 64 * (x & 3) < a.head_dim)
+                        asm volatile("prefetch.global.L2 [%0];" ::"l"(query_row(n, n.row0 + (x >> 2)) + 64 * (x & 3)));
+            }
         }
 
         float o[NT][4];
@@ -357,13 +387,19 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
         // near 1 whatever the scales; the sum is that of the weights by the same reference.
         float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 
+#pragma unroll
+        for (int i = 0; i < S::kSlots / 2; ++i) put_scales(begin[i], i);
         int get = 0;
         for (int i = 0; i < stages; ++i) {
             cp_async_wait<S::kSlots - 2>();
-            if (!kOdd) put_scales();
+            if (!kOdd) {
+                if (i > 1) put_scales(older, i + S::kSlots / 2 - 2);
+                older = found;
+            }
             group_sync<R>(group);
-            load_next(First(), page_next, 2 * i + S::kSlots - 1);
+            load_next(First(), i, get == 0 ? S::kSlots - 1 : get - 1, page_next, 2 * i + S::kSlots - 1);
             const int base = base0 + (i * S::kGroups + group) * S::kTokens;
+            const int key_slot = get;
             const uint32_t keys = ring + get * S::kHalf;
             if (++get == S::kSlots) get = 0;
             const uint32_t vals = ring + get * S::kHalf;
@@ -392,15 +428,20 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
                 // token 8·y + g, chunk 4·kb + t4: four k-steps of two pairs
                 const uint32_t from = keys + g * kRow + ((t4 ^ turn<kRow, Q8, true>(g)) << 4);
 #pragma unroll
-                for (int kb = 0; kb < KS / 4; ++kb)
+                for (int kb = 0; kb < KS / 4; ++kb) {
+                    uint32_t w[2 * S::kSub][4];
 #pragma unroll
                     for (int y = 0; y < 2 * S::kSub; ++y) {
-                        const uint4 w = lds128((from ^ ((kb & 1) << 6)) + (kb >> 1) * 128 + y * 8 * kRow);
-                        const uint32_t u[4] = {w.x ^ 0x80808080u, w.y ^ 0x80808080u, w.z ^ 0x80808080u, w.w ^ 0x80808080u};
-#pragma unroll
-                        for (int x = 0; x < 4; ++x)
-                            mma16816<true>(s[y], q[kb * 4 + x], codes_f16(u[x], 0x4140), codes_f16(u[x], 0x4342));
+                        const uint4 v = lds128((from ^ ((kb & 1) << 6)) + (kb >> 1) * 128 + y * 8 * kRow);
+                        w[y][0] = v.x ^ 0x80808080u, w[y][1] = v.y ^ 0x80808080u, w[y][2] = v.z ^ 0x80808080u, w[y][3] = v.w ^ 0x80808080u;
                     }
+                    // (neighbouring products go to different sums)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+#pragma unroll
+                        for (int y = 0; y < 2 * S::kSub; ++y)
+                            mma16816<true>(s[y], q[kb * 4 + x], codes_f16(w[y][x], 0x4140), codes_f16(w[y][x], 0x4342));
+                }
             }
             float inv[2 * S::kSub][2];  // 1 / value scale of the lane's tokens
             if (Q8) {
@@ -469,9 +510,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
 
             // ---- values
             cp_async_wait<S::kSlots - 2>();
-            if (kOdd) put_scales();
             group_sync<R>(group);
-            load_next(Second(), page_next, 2 * i + S::kSlots);
+            load_next(Second(), i, key_slot, page_next, 2 * i + S::kSlots);
             if (!Q8) {
                 bool odd = false;  // a value that is not finite, in tokens that some rows do not see
                 if (hidden) {
@@ -587,10 +627,10 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
         }
         cp_async_wait<0>();
 
-        // ---- the groups' sums meet in shared memory: [warp][16 rows][D], then the reference and sum of each row
+        // ---- the groups' sums meet in shared memory: [warp][16 rows][kMeetRow], then the reference and sum of each row
         __syncthreads();
         float* s_o = reinterpret_cast<float*>(smem);
-        float* s_stat = s_o + kWarps * 16 * D;  // [2][warp][16]
+        float* s_stat = s_o + kWarps * 16 * S::kMeetRow;  // [2][warp][16]
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
             l[x] = quad_sum(l[x]);
@@ -600,17 +640,27 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
             }
         }
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int x = 0; x < 2; ++x) {
+            float* to = s_o + (warp * 16 + g + 8 * x) * S::kMeetRow;
+            if (!Q8) {
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const int col = !Q8 ? n * 8 + 2 * t4 + (x & 1)
-                                    : D == 64 ? (2 * t4 + (x & 1)) * 8 + n : (n >> 4) * 128 + (2 * t4 + (x & 1)) * 16 + (n & 15);
-                s_o[(warp * 16 + g + 8 * (x >> 1)) * D + col] = o[n][x];
+                for (int n = 0; n < NT; ++n) *reinterpret_cast<float2*>(to + n * 8 + 2 * t4) = make_float2(o[n][2 * x], o[n][2 * x + 1]);
+            } else {
+                constexpr int kRun = D == 64 ? 8 : 16;  // neighbouring values of a lane's column
+#pragma unroll
+                for (int n = 0; n < NT; n += 4)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        *reinterpret_cast<float4*>(to + n / kRun * 128 + (2 * t4 + e) * kRun + n % kRun) =
+                            make_float4(o[n][2 * x + e], o[n + 1][2 * x + e], o[n + 2][2 * x + e], o[n + 3][2 * x + e]);
             }
+        }
         __syncthreads();
 
+        const Item it = s_item[which];
         const bool whole = it.whole();
-        const Parts<16 * R, D> parts(sp, walk, it, kFixed);
+        more = s_more;
+        const Parts<16 * R, D> parts(sp, s_walk, it, kFixed);
         float* const part = parts.at(static_cast<int>(blockIdx.x) - parts.first);
         for (int x = tid; x < 16 * R * (D / 4); x += kThreads) {
             const int r = x / (D / 4), col = x % (D / 4) * 4, row = row0 + r;
@@ -623,7 +673,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
 #pragma unroll
             for (int k = 0; k < S::kGroups; ++k) {
                 const float f = ex2(s_stat[k * R * 16 + r] - rm);
-                const float4 w = *reinterpret_cast<const float4*>(s_o + (k * R * 16 + r) * D + col);
+                const float4 w = *reinterpret_cast<const float4*>(s_o + (k * R * 16 + r) * S::kMeetRow + col);
                 ll += f * s_stat[kWarps * 16 + k * R * 16 + r];
                 v[0] += f * w.x, v[1] += f * w.y, v[2] += f * w.z, v[3] += f * w.w;
             }
