@@ -120,8 +120,10 @@ struct Shape {
     // Three CTAs of 168 registers on an SM, where the outputs' D / 2 leave that; else two.
     static constexpr int kCtas = D == 256 ? 2 : 3;
     static constexpr int kBudget = (kCtas == 3 ? 72 : 108) * 1024;
-    static constexpr int kFit = kBudget / (kGroups * (kHalf + (Q8 ? kTokens * 8 : 0)));
-    static constexpr int kSlots = kFit > 12 ? 12 : kFit;
+    // Format 8 keeps the queries (as fp16, in the products' order) in shared memory: its decoding needs the registers.
+    static constexpr int kQueries = Q8 ? R * (D / 16) * 512 : 0;
+    static constexpr int kFit = (kBudget - kQueries) / (kGroups * (kHalf + (Q8 ? kTokens * 8 : 0)));
+    static constexpr int kSlots = kFit > 12 ? 12 : Q8 ? kFit & ~1 : kFit;
     static constexpr int kAhead = (kSlots + 1) / 2;  // stages whose keys may be under way or in use
     static constexpr int kRing = kSlots * kHalf;
     // (key scale, log2 of value scale) of each token, for the stages on the way and the one in use
@@ -130,7 +132,7 @@ struct Shape {
     static constexpr int kGroup = kRing + kScales;
     // Where the groups' sums meet: rows 8 columns apart in banks, and two numbers for each row.
     static constexpr int kMeetRow = D + 8, kMerge = kWarps * 16 * (kMeetRow + 2) * 4;
-    static constexpr int kSmem = kGroups * kGroup > kMerge ? kGroups * kGroup : kMerge;
+    static constexpr int kMain = kGroups * kGroup > kMerge ? kGroups * kGroup : kMerge, kSmem = kMain + kQueries;
     static_assert(kSlots >= 3 && (!Q8 || kSlots % 2 == 0), "a slot in use, two on the way; scales in time");
 };
 
@@ -179,6 +181,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
 
     const uint32_t ring = smem_addr(smem) + group * S::kGroup;
     float2* scales = reinterpret_cast<float2*>(smem + group * S::kGroup + S::kRing);
+    uint4* queries = reinterpret_cast<uint4*>(smem + S::kMain);
     const int d_chunks = a.head_dim * S::kElt / 16;
     // The lane's places in a slot: of its 16 bytes of a copy's pass, and of what it reads.
     constexpr int kPerPass = 32 * R / S::kChunks;  // token rows of one pass of the group's lanes
@@ -207,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
         for (int i = 0; i < S::kAhead; ++i) first[i] = page_of(i);
 
         // ---- queries of the thread's rows g and g + 8, asked for ahead of the tokens' bytes
-        uint32_t q[KS][4];
+        uint32_t q[Q8 ? 1 : KS][4];
         int see_lo[2], see_hi[2];   // tokens that a row sees
         uint2 raw[Q8 ? 2 : 1][Q8 ? KS : 1];
 #pragma unroll
@@ -223,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
                         const int k = ks * 16 + 2 * t4 + 8 * y;
-                        q[ks][x + 2 * y] = live && k < a.head_dim ? *reinterpret_cast<const uint32_t*>(src + k) : 0u;
+                        q[Q8 ? 0 : ks][x + 2 * y] = live && k < a.head_dim ? *reinterpret_cast<const uint32_t*>(src + k) : 0u;
                     }
                 } else {
                     // four values in a row for each k-step and lane, like the keys' codes below
@@ -331,9 +334,10 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-                for (int x = 0; x < 4; ++x) q[ks][x] ^= sp.flip;
+                for (int x = 0; x < 4; ++x) q[Q8 ? 0 : ks][x] ^= sp.flip;
         } else {
             // As fp16, after a division of the row by a power of two near its largest value.
+            float down[2];
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 float most = 0.f;
@@ -344,15 +348,18 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
                 }
                 most = quad_max(most);
                 const int e = min(max(static_cast<int>(__float_as_uint(most) >> 23), 7), 247) - 127;
-                const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+                down[x] = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
                 row_scale[x] *= __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+            }
+            if (group == 0)  // the other groups have the same rows
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks) {
-                    const uint2 w = raw[Q8 ? x : 0][Q8 ? ks : 0];
-                    q[ks][x] = pack_f16(bf16_lo(w.x) * down, bf16_hi(w.x) * down) ^ sp.flip;
-                    q[ks][x + 2] = pack_f16(bf16_lo(w.y) * down, bf16_hi(w.y) * down) ^ sp.flip;
+                    const uint2 u = raw[0][Q8 ? ks : 0], w = raw[Q8 ? 1 : 0][Q8 ? ks : 0];
+                    queries[(rw * KS + ks) * 32 + lane] =
+                        make_uint4(pack_f16(bf16_lo(u.x) * down[0], bf16_hi(u.x) * down[0]) ^ sp.flip, pack_f16(bf16_lo(w.x) * down[1], bf16_hi(w.x) * down[1]) ^ sp.flip,
+                                   pack_f16(bf16_lo(u.y) * down[0], bf16_hi(u.y) * down[0]) ^ sp.flip, pack_f16(bf16_lo(w.y) * down[1], bf16_hi(w.y) * down[1]) ^ sp.flip);
                 }
-            }
+            __syncthreads();
         }
         // Tokens before all_hi and from all_lo on are seen by every row of the warp.
         int all_hi, all_lo;
@@ -421,8 +428,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
                     for (int sub = 0; sub < S::kSub; ++sub) {
                         uint32_t k[4];
                         ldmatrix_x4((from ^ ((ks & 3) << 5)) + (ks >> 2) * 128 + sub * 16 * kRow, k);
-                        mma16816<false>(s[2 * sub], q[ks], k[0], k[1]);
-                        mma16816<false>(s[2 * sub + 1], q[ks], k[2], k[3]);
+                        mma16816<false>(s[2 * sub], q[Q8 ? 0 : ks], k[0], k[1]);
+                        mma16816<false>(s[2 * sub + 1], q[Q8 ? 0 : ks], k[2], k[3]);
                     }
             } else {
                 // token 8·y + g, chunk 4·kb + t4: four k-steps of two pairs
@@ -437,13 +444,15 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
                     }
                     // (neighbouring products go to different sums)
 #pragma unroll
-                    for (int x = 0; x < 4; ++x)
+                    for (int x = 0; x < 4; ++x) {
+                        const uint4 v = queries[(rw * KS + kb * 4 + x) * 32 + lane];
+                        const uint32_t f[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                         for (int y = 0; y < 2 * S::kSub; ++y)
-                            mma16816<true>(s[y], q[kb * 4 + x], codes_f16(w[y][x], 0x4140), codes_f16(w[y][x], 0x4342));
+                            mma16816<true>(s[y], f, codes_f16(w[y][x], 0x4140), codes_f16(w[y][x], 0x4342));
+                    }
                 }
             }
-            float inv[2 * S::kSub][2];  // 1 / value scale of the lane's tokens
             if (Q8) {
 #pragma unroll
                 for (int y = 0; y < 2 * S::kSub; ++y) {
@@ -452,9 +461,6 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
                     s[y][1] = fmaf(s[y][1], row_scale[0] * f.z, f.w);
                     s[y][2] = fmaf(s[y][2], row_scale[1] * f.x, f.y);
                     s[y][3] = fmaf(s[y][3], row_scale[1] * f.z, f.w);
-                    // A number even where the scale is none: a hidden token's weight of 0 makes it 0 then.
-                    inv[y][0] = fminf(ex2(-f.y), 3e38f);
-                    inv[y][1] = fminf(ex2(-f.w), 3e38f);
                 }
             }
             // Some row does not see some token of the stage; there are such tokens, too, past the end.
@@ -496,17 +502,26 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
             const float ref[2] = {m[0] == -INFINITY ? 0.f : m[0] * (Q8 ? 1.f : row_scale[0]),
                                   m[1] == -INFINITY ? 0.f : m[1] * (Q8 ? 1.f : row_scale[1])};
 #pragma unroll
-            for (int y = 0; y < 2 * S::kSub; ++y)
+            for (int y = 0; y < 2 * S::kSub; ++y) {
+                // 1 / value scale of the lane's tokens: a number even where the scale is none, since a hidden token's
+                // weight of 0 makes it 0 then.
+                float inv[2] = {1.f, 1.f};
+                if (Q8) {
+                    const float4 f = *reinterpret_cast<const float4*>(stage_scales + y * 8 + 2 * t4);
+                    inv[0] = fminf(ex2(-f.y), 3e38f);
+                    inv[1] = fminf(ex2(-f.w), 3e38f);
+                }
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
                     if (Q8) {
                         s[y][x] = ex2(s[y][x] - ref[x >> 1]);
-                        l[x >> 1] = fmaf(s[y][x], inv[y][x & 1], l[x >> 1]);
+                        l[x >> 1] = fmaf(s[y][x], inv[x & 1], l[x >> 1]);
                     } else {
                         s[y][x] = ex2(fmaf(s[y][x], row_scale[x >> 1], -ref[x >> 1]));
                         l[x >> 1] += s[y][x];
                     }
                 }
+            }
 
             // ---- values
             cp_async_wait<S::kSlots - 2>();
