@@ -169,7 +169,7 @@ struct Axes {
     uint16_t of[16];
 };
 
-constexpr int kAppendThreads = 256;
+constexpr int kManyThreads = 64, kManyTokens = 8;  // (tokens to an SM)
 constexpr int kBatch = 4;  // rows that a lane has in flight
 
 // x·c + y·s for the two values of a word, every operation rounded on its own
@@ -186,10 +186,10 @@ __device__ __forceinline__ uint32_t turn_pair(uint32_t x, uint32_t y, float2 c, 
 // shared memory, and turn and write the rows.  blockIdx.y shares a token's rows
 // among CTAs where there are few tokens.  Bound by reading and writing each row
 // once.
-template <int LPR, bool Q8>
-__global__ void __launch_bounds__(kAppendThreads, 4) kv_append_kernel(const __grid_constant__ KvAppendArgs a,
-                                                                       const __grid_constant__ Axes axes) {
-    constexpr int kGroups = kAppendThreads / LPR;
+template <int THREADS, int LPR, bool Q8>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) kv_append_kernel(const __grid_constant__ KvAppendArgs a,
+                                                                           const __grid_constant__ Axes axes) {
+    constexpr int kGroups = THREADS / LPR;
     __shared__ __align__(16) float s_cos[2][128], s_sin[2][128];
     const int c = threadIdx.x % LPR, group0 = blockIdx.y * kGroups, group = group0 + threadIdx.x / LPR;
     const int groups = gridDim.y * kGroups;
@@ -220,15 +220,15 @@ __global__ void __launch_bounds__(kAppendThreads, 4) kv_append_kernel(const __gr
             }
             if (base == group0) {
                 slot = a.slots[t];
-                if (threadIdx.x < F) {
-                    const int axis = axes.of[threadIdx.x >> 3] >> (2 * (threadIdx.x & 7)) & 3;
+                for (int i = threadIdx.x; i < F; i += THREADS) {
+                    const int axis = axes.of[i >> 3] >> (2 * (i & 7)) & 3;
                     int row = a.positions[axis * a.axis_stride + t];
                     if (row < 0 || row >= a.rows) {
                         record_status(a.status, kStatusInvalid);
                         row = 0;
                     }
-                    s_cos[turn][threadIdx.x] = a.cos[static_cast<long long>(row) * F + threadIdx.x];
-                    s_sin[turn][threadIdx.x] = a.sin[static_cast<long long>(row) * F + threadIdx.x];
+                    s_cos[turn][i] = a.cos[static_cast<long long>(row) * F + i];
+                    s_sin[turn][i] = a.sin[static_cast<long long>(row) * F + i];
                 }
                 __syncthreads();
                 if (turned && !a.paired) {
@@ -322,13 +322,23 @@ __global__ void __launch_bounds__(kAppendThreads, 4) kv_append_kernel(const __gr
     }
 }
 
-template <int LPR>
-cudaError_t append(const KvAppendArgs& a, const Axes& axes, bool q8, dim3 grid, cudaStream_t stream) {
+template <int THREADS, int LPR>
+cudaError_t append(const KvAppendArgs& a, const Axes& axes, bool q8, int64_t tokens, int sm_count, cudaStream_t stream) {
+    const int per_cta = THREADS / LPR, rows = 2 * a.kv_heads + a.q_heads;
+    // Few tokens: a CTA for every THREADS / LPR rows, so that the rows of a token are in flight at once.
+    const dim3 grid(static_cast<unsigned>(std::min(a.T, tokens)), a.T * 2 >= sm_count ? 1u : static_cast<unsigned>((rows + per_cta - 1) / per_cta));
     if (q8)
-        kv_append_kernel<LPR, true><<<grid, kAppendThreads, 0, stream>>>(a, axes);
+        kv_append_kernel<THREADS, LPR, true><<<grid, THREADS, 0, stream>>>(a, axes);
     else
-        kv_append_kernel<LPR, false><<<grid, kAppendThreads, 0, stream>>>(a, axes);
+        kv_append_kernel<THREADS, LPR, false><<<grid, THREADS, 0, stream>>>(a, axes);
     return cudaGetLastError();
+}
+
+template <int THREADS>
+cudaError_t append_dim(const KvAppendArgs& a, const Axes& axes, bool q8, int64_t tokens, int sm_count, cudaStream_t stream) {
+    if (a.head_dim <= 64) return append<THREADS, 8>(a, axes, q8, tokens, sm_count, stream);
+    if (a.head_dim <= 128) return append<THREADS, 16>(a, axes, q8, tokens, sm_count, stream);
+    return append<THREADS, 32>(a, axes, q8, tokens, sm_count, stream);
 }
 
 }  // namespace
@@ -355,16 +365,11 @@ cudaError_t launch_kv_append(KvAppendArgs a, const int32_t sections[4], bool cyc
         ++used[axis];
         if (cycled) ++turn;
     }
-    const int lpr = a.head_dim <= 64 ? 8 : a.head_dim <= 128 ? 16 : 32;
-    const int per_cta = kAppendThreads / lpr, rows = 2 * a.kv_heads + a.q_heads;
-    // Few tokens: a CTA for every 256 / LPR rows, so that the rows of a token are in flight at once.
-    const int split = a.T * 2 >= dev.sm_count ? 1 : (rows + per_cta - 1) / per_cta;
-    // Many tokens: CTAs that stay, four to an SM.
-    const int64_t tokens = std::min<int64_t>(a.T, std::max(1, 4 * dev.sm_count));
-    const dim3 grid(static_cast<unsigned>(tokens), static_cast<unsigned>(split));
-    if (lpr == 8) return append<8>(a, axes, q8, grid, stream);
-    if (lpr == 16) return append<16>(a, axes, q8, grid, stream);
-    return append<32>(a, axes, q8, grid, stream);
+    // Small CTAs wait less for one another between tokens, large ones have a token's rows in flight sooner.  56 rows
+    // of 128: 208 tokens take 3.7 µs with 256 threads and 5.9 with 64, 800 take 6.6 and 7.2, 1600 14.1 and 12.4,
+    // 5000 34 and 30, 16001 100 and 78 (81 with 128).
+    if (a.T >= kManyTokens * dev.sm_count) return append_dim<kManyThreads>(a, axes, q8, 1024 / kManyThreads * dev.sm_count, dev.sm_count, stream);
+    return append_dim<256>(a, axes, q8, 4 * dev.sm_count, dev.sm_count, stream);
 }
 
 }  // namespace w4
