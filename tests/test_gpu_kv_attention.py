@@ -262,3 +262,97 @@ def test_binding_refusals(cuda_lib):
         w4.w4_attn_decode(q, case.k, case.v, table, lens, scale=float("nan"))
     with pytest.raises(w4.W4Error):
         w4.w4_attn_decode(q, case.k, case.v, table, lens, workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
+
+
+# ---- many rows to a key-value head (the tensor-core kernel), and enough tokens for each CTA's ring to go round
+MANY = [(32, 2, 64), (16, 1, 128), (24, 2, 128), (16, 1, 256), (18, 1, 80), (64, 4, 192), (9, 1, 16)]
+
+
+@pytest.mark.parametrize("Hq,H,D", MANY)
+@pytest.mark.parametrize("order,page_size", [("token", 16), ("head", 24), ("pair", 1)])
+def test_many_rows_ragged(cuda_lib, Hq, H, D, order, page_size):
+    """Rows in all amounts on one call: none, a few, more than 128; requests without tokens among them."""
+    lens = [0, 7, 1, 13, 200, 300, 64, 0, 129, 20, 257]
+    fresh = [5, 7, 1, 13, 5, 13, 0, 0, 1, 20, 9]
+    case = AttentionCase(lens, fresh, Hq, H, D, page_size, order, seed=Hq + D)
+    finish(case, case.run(w4))
+
+
+@pytest.mark.parametrize("window", [1, 9, 100, 1000])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_many_rows_windows(cuda_lib, window, D):
+    lens, fresh = [1, 40, 500, 333, 13, 130], [1, 13, 9, 13, 13, 6]
+    case = AttentionCase(lens, fresh, 16, 2, D, 16, seed=window)
+    finish(case, case.run(w4, window=window), window=window)
+
+
+@pytest.mark.parametrize("scale,std", [(0.0, 1.0), (-0.1, 1.0), (0.3, 30.0)])
+def test_many_rows_scales(cuda_lib, scale, std):
+    case = AttentionCase([50, 300, 777], [13, 9, 13], 16, 2, 128, 16, seed=21, std=std)
+    finish(case, case.run(w4, scale=scale), scale=scale)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("window", [0, 9])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_many_rows_hidden_tokens(cuda_lib, D, window, bad):
+    """As test_a_hidden_token_changes_nothing, in the first tile of an item and in a later one."""
+    for L in (45, 300):
+        n = 13
+        case = AttentionCase([L, 200], [n, 13], 16, 2, D, 16, seed=22)
+        token = L - 8
+        page, place = int(case.table[0, token // 16]), token % 16
+        case.k[page, place, :, 5] = bad
+        case.v[page, place, :, 5] = bad
+        out = case.run(w4, window=window)
+        torch.cuda.synchronize()
+        assert w4.w4_last_device_status() == 0
+        position = np.arange(L - n, L)
+        sees = np.concatenate([(token <= position) & ((window == 0) | (token > position - window)), [False] * 13])
+        case.check(out, window=window, rows=~sees)
+        assert not np.isfinite(values(out)[sees]).all(axis=(1, 2)).any()
+
+
+def test_many_rows_values_that_are_not_finite(cuda_lib):
+    """Of the values alone: the column of the rows that see the token, and nothing else."""
+    case = AttentionCase([300], [13], 16, 1, 128, 16, seed=23)
+    page, place = int(case.table[0, 290 // 16]), 290 % 16
+    case.v[page, place, 0, 77] = float("inf")
+    out = case.run(w4)
+    torch.cuda.synchronize()
+    sees = np.arange(287, 300) >= 290
+    assert not np.isfinite(values(out)[sees][..., 77]).any()
+    case.check(out, columns=np.arange(128) != 77)
+    case.check(out, rows=~sees)
+
+
+@pytest.mark.parametrize("Hq,H,D,n,format", [(40, 8, 128, 1, 16), (40, 8, 128, 1, 8), (64, 8, 64, 5, 16), (64, 8, 128, 5, 16),
+                                             (32, 4, 256, 5, 16), (16, 4, 256, 2, 16), (16, 4, 256, 2, 8), (64, 8, 128, 5, 8)])
+def test_long_runs(cuda_lib, Hq, H, D, n, format):
+    """Many tiles for every CTA, and items that two, three and more of them share."""
+    rng = np.random.default_rng(D + n)
+    lens = [int(x) for x in rng.integers(500, 4500, 20)] + [9000, n]
+    case = AttentionCase(lens, [n] * len(lens), Hq, H, D, 16, format=format, seed=24)
+    finish(case, case.run(w4, uniform=True))
+
+
+@pytest.mark.parametrize("Hq,H", [(8, 1), (64, 1)])
+def test_one_item_shared_by_every_cta(cuda_lib, Hq, H):
+    """More parts than are joined at once: groups of them, then the groups."""
+    case = AttentionCase([60000], [1], Hq, H, 128, 16, seed=25)
+    finish(case, case.run(w4))
+
+
+def test_many_rows_same_bits_again(cuda_lib):
+    case = AttentionCase([3000, 170, 900, 13], [13] * 4, 16, 2, 128, 16, seed=26)
+    q, table, lens, starts = case.q.to(DEV), gpu(case.table), gpu(case.lens), gpu(case.starts)
+    first = w4.w4_attn_decode(q, case.k, case.v, table, lens, starts=starts)
+    finish(case, first)
+    dirty = torch.full((w4.w4_attn_decode_workspace_bytes(q, case.k, 4),), 255, dtype=torch.uint8, device=DEV)
+    out = q.clone()
+    for i in range(20):
+        if i % 5 == 0:
+            dirty.fill_(i)
+        out.copy_(q)
+        w4.w4_attn_decode(out, case.k, case.v, table, lens, starts=starts, workspace=dirty, out=out)  # in place
+        assert torch.equal(first.view(torch.int16), out.view(torch.int16))
