@@ -46,8 +46,6 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kTile = 64;       // tokens of a unit of work
-// A value scale of zero stands for this one, whose logarithm is a number.
-constexpr float kTiny = 1.17549435e-38f;
 
 // ------------------------------------------------------------- small pieces
 __device__ __forceinline__ void ldmatrix_x4(uint32_t addr, uint32_t (&r)[4]) {
@@ -245,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
         Scales found = {0.f, 0.f}, older = found;
         auto put_scales = [&](const Scales& x, int stage) {
             if (Q8 && stage < stages && rw == 0 && lane < S::kTokens)
-                scales[stage % S::kScaleSlots * S::kTokens + lane] = make_float2(x.k, __log2f(x.v < kTiny ? kTiny : x.v));
+                scales[stage % S::kScaleSlots * S::kTokens + lane] = make_float2(x.k, __log2f(x.v < kLeastScale ? kLeastScale : x.v));
         };
         long long off = -1;     // of the lane's token, in the stage whose keys were asked for last; −1: none
         long long off0[S::kSub];  // of the first token of each 16

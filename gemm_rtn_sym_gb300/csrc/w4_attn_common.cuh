@@ -17,6 +17,9 @@ constexpr int kJoinGroup = 16;          // parts of an item that are joined at o
 constexpr int kMaxLength = 0x7fff0000;  // token numbers a little past a length stay below 2³¹
 constexpr int kMaxDevices = 64;         // as many as the library knows (device_info refuses others)
 constexpr int kMaxCtas = 512;           // bounds the workspace
+// Format 8's value scales from here on (2⁻¹⁰⁰): with smaller ones, and for zero, this one stands in.  It has a
+// logarithm, its inverse can be summed over all tokens that a length can name, and the codes of a zero scale are zero.
+constexpr float kLeastScale = 7.888609052210118e-31f;
 
 // The weights' reference and their sum, ROWS of each, then ROWS rows of D values.
 __host__ __device__ constexpr size_t partial_floats(int rows, int D) { return static_cast<size_t>(rows) * (2 + D); }

@@ -356,3 +356,18 @@ def test_many_rows_same_bits_again(cuda_lib):
         out.copy_(q)
         w4.w4_attn_decode(out, case.k, case.v, table, lens, starts=starts, workspace=dirty, out=out)  # in place
         assert torch.equal(first.view(torch.int16), out.view(torch.int16))
+
+
+@pytest.mark.parametrize("zeros", [3, 60, 900])
+@pytest.mark.parametrize("n", [1, 13])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_values_of_zero_in_8_bits(cuda_lib, zeros, n, D):
+    """Tokens whose values are all zero have a value scale of zero; their weights count all the same."""
+    case = AttentionCase([1000, zeros + n], [n, n], 8, 1, D, 16, format=8, seed=zeros + D)
+    for b in range(2):
+        for token in range(zeros):
+            page, place = case.table[b, token // 16], token % 16
+            case.v[page, place] = 0
+            case.v_scales[page, :, place] = 0
+            case.vv[page, place] = 0.0
+    finish(case, case.run(w4))
