@@ -713,15 +713,27 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
 
 int dim_of(int head_dim) { return head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256; }
 
-// Whether the tensor-core kernel takes the call: more than 32 rows to a key-value head, on the average.
-bool many_rows(int32_t B, int64_t T, int G, bool q8) { return !q8 && (T + B - 1) / B * G > 32; }
+// Query rows to a key-value head of a request, on the average.
+int64_t average_rows(int32_t B, int64_t T, int G) { return (T + B - 1) / B * G; }
 
-// Warps (of 16 rows) that share a stage: what the requests' rows need on the
-// average, at most 4.
-int row_warps(int32_t B, int64_t T, int G) {
-    const int64_t rows = (T + B - 1) / B * G;
-    return rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+// Whether the tensor-core kernel takes the call.  A row tile of 16 rows is a
+// pass over the request's tokens here, one of 128 rows there.  Requests of
+// 1024 to 8192 tokens (16 of them) and of 8192 to 16384 (64), µs here and there:
+// head_dim 128, 16 rows: 56 and 67; 24: 67 and 67, 593 and 517; 32: 71 and 66,
+// 594 and 517.  head_dim 256, 32 rows: 69 and 90, 475 and 548; 52: 130 and 92.
+// head_dim 64, 32 rows: 26 and 29; 40: 35 and 29.
+bool many_rows(int32_t B, int64_t T, int G, int D, bool q8) {
+    return !q8 && average_rows(B, T, G) > (D == 128 ? 16 : 32);
 }
+
+// Warps (of 16 rows) that share a stage.  With two, 17 to 32 rows are one pass
+// over the cache instead of two: 69 and 475 µs for 76 and 932 at head_dim 256,
+// 32 rows, in the two calls above, but 243 for 301 only where 64 is the
+// head_dim (and 54 for 52 where 8 rows are all there are: fewer rings, and a
+// barrier of two warps).  Format 8 is bound by its decoding, which each row
+// tile repeats in any case: 61 µs with one and 65 with two warps at 32 rows,
+// 570 and 545 in longer requests, 107 and 108 at 64 rows.
+int row_warps(int32_t B, int64_t T, int G, bool q8) { return !q8 && average_rows(B, T, G) > 16 ? 2 : 1; }
 
 template <int D, bool Q8, int R>
 cudaError_t run(const SplitArgs& sp, const DeviceInfo& dev, cudaStream_t stream) {
@@ -751,10 +763,9 @@ cudaError_t run(const SplitArgs& sp, const DeviceInfo& dev, cudaStream_t stream)
 
 template <int D, bool Q8>
 cudaError_t run_rows(const SplitArgs& sp, const DeviceInfo& dev, cudaStream_t stream) {
-    const int R = row_warps(sp.a.B, sp.a.T, sp.G);
-    if (R == 1) return run<D, Q8, 1>(sp, dev, stream);
-    if (R == 2) return run<D, Q8, 2>(sp, dev, stream);
-    return run<D, Q8, 4>(sp, dev, stream);
+    if constexpr (!Q8 && D != 128)  // (the tensor-core kernel takes more than 16 rows of 128)
+        if (row_warps(sp.a.B, sp.a.T, sp.G, Q8) == 2) return run<D, Q8, 2>(sp, dev, stream);
+    return run<D, Q8, 1>(sp, dev, stream);
 }
 
 template <bool Q8>
@@ -768,9 +779,9 @@ cudaError_t run_dim(const SplitArgs& sp, const DeviceInfo& dev, cudaStream_t str
 }  // namespace
 
 size_t attn_decode_workspace_bytes(int32_t B, int64_t T, int32_t q_heads, int32_t kv_heads, int32_t head_dim, bool q8) {
-    const int G = q_heads / kv_heads;
-    const size_t part = B > 0 && many_rows(B, T, G, q8) ? attn_tc_partial_floats(head_dim)
-                                                        : partial_floats(16 * (B > 0 ? row_warps(B, T, G) : 1), dim_of(head_dim));
+    const int G = q_heads / kv_heads, D = dim_of(head_dim);
+    if (B <= 0) B = 1;
+    const size_t part = many_rows(B, T, G, D, q8) ? attn_tc_partial_floats(head_dim) : partial_floats(16 * row_warps(B, T, G, q8), D);
     return 2 * kMaxCtas * (sizeof(unsigned long long) + part * sizeof(float));
 }
 
@@ -787,7 +798,7 @@ cudaError_t launch_attn_decode(AttnArgs a, bool q8, void* workspace, const Devic
     // largest score is then that of the unscaled products, and hidden ones stay at −∞.
     sp.scale_log2 = std::max(std::fabs(a.scale) * 1.4426950408889634f, 1e-30f);
     sp.flip = a.scale < 0.f ? 0x80008000u : 0u;
-    if (many_rows(a.B, a.T, sp.G, q8)) return launch_attn_tc(sp, dev, stream);
+    if (many_rows(a.B, a.T, sp.G, dim_of(a.head_dim), q8)) return launch_attn_tc(sp, dev, stream);
     return q8 ? run_dim<true>(sp, dev, stream) : run_dim<false>(sp, dev, stream);
 }
 

@@ -325,7 +325,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) kv_append_kernel(cons
 template <int THREADS, int LPR>
 cudaError_t append(const KvAppendArgs& a, const Axes& axes, bool q8, int64_t tokens, int sm_count, cudaStream_t stream) {
     const int per_cta = THREADS / LPR, rows = 2 * a.kv_heads + a.q_heads;
-    // Few tokens: a CTA for every THREADS / LPR rows, so that the rows of a token are in flight at once.
+    // Few tokens: a CTA for every THREADS / LPR rows, so that the rows of a token are in flight at once.  80 rows of 128
+    // with and without: 2.5 and 3.6 µs for 1 token, 3.2 and 3.8 for 76, 5.0 and 3.9 for 152.
     const dim3 grid(static_cast<unsigned>(std::min(a.T, tokens)), a.T * 2 >= sm_count ? 1u : static_cast<unsigned>((rows + per_cta - 1) / per_cta));
     if (q8)
         kv_append_kernel<THREADS, LPR, true><<<grid, THREADS, 0, stream>>>(a, axes);
@@ -345,7 +346,8 @@ cudaError_t append_dim(const KvAppendArgs& a, const Axes& axes, bool q8, int64_t
 
 cudaError_t launch_kv_pages(KvPagesArgs a, const DeviceInfo& dev, cudaStream_t stream) {
     divide_by(a.page_size, &a.page_mul, &a.page_shift);
-    // Few requests: smaller CTAs, whose barriers cost less.
+    // Small CTAs' barriers cost less, but each thread scans one request at a time: 3.2 µs with 256 threads and 4.2 with
+    // 1024 for 64 requests (a token each), 3.6 and 4.7 for 256, 5.5 and 4.8 for 384, 9.4 and 5.6 for 1000.
     const int threads = a.B <= 256 ? 256 : kPagesThreads;
     const int64_t blocks = (a.T + threads - 1) / threads;
     const int grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(blocks, dev.sm_count * (kPagesThreads / threads))));
