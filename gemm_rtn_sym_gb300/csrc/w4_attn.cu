@@ -722,8 +722,11 @@ int64_t average_rows(int32_t B, int64_t T, int G) { return (T + B - 1) / B * G; 
 // head_dim 128, 16 rows: 56 and 67; 24: 67 and 67, 593 and 517; 32: 71 and 66,
 // 594 and 517.  head_dim 256, 32 rows: 69 and 90, 475 and 548; 52: 130 and 92.
 // head_dim 64, 32 rows: 26 and 29; 40: 35 and 29.
+// Format 8: head_dim 128, 40 rows: 84 and 96; 64: 107 and 96, 1121 and 787;
+// 104: 176 and 96.  256, 52 rows: 120 and 111.  64, 64 rows: 27 and 32, 104: 38
+// and 33.
 bool many_rows(int32_t B, int64_t T, int G, int D, bool q8) {
-    return !q8 && average_rows(B, T, G) > (D == 128 ? 16 : 32);
+    return average_rows(B, T, G) > (q8 ? 48 : D == 128 ? 16 : 32);
 }
 
 // Warps (of 16 rows) that share a stage.  With two, 17 to 32 rows are one pass
@@ -732,7 +735,7 @@ bool many_rows(int32_t B, int64_t T, int G, int D, bool q8) {
 // head_dim (and 54 for 52 where 8 rows are all there are: fewer rings, and a
 // barrier of two warps).  Format 8 is bound by its decoding, which each row
 // tile repeats in any case: 61 µs with one and 65 with two warps at 32 rows,
-// 570 and 545 in longer requests, 107 and 108 at 64 rows.
+// 570 and 545 in longer requests.
 int row_warps(int32_t B, int64_t T, int G, bool q8) { return !q8 && average_rows(B, T, G) > 16 ? 2 : 1; }
 
 template <int D, bool Q8, int R>
@@ -798,7 +801,7 @@ cudaError_t launch_attn_decode(AttnArgs a, bool q8, void* workspace, const Devic
     // largest score is then that of the unscaled products, and hidden ones stay at −∞.
     sp.scale_log2 = std::max(std::fabs(a.scale) * 1.4426950408889634f, 1e-30f);
     sp.flip = a.scale < 0.f ? 0x80008000u : 0u;
-    if (many_rows(a.B, a.T, sp.G, dim_of(a.head_dim), q8)) return launch_attn_tc(sp, dev, stream);
+    if (many_rows(a.B, a.T, sp.G, dim_of(a.head_dim), q8)) return launch_attn_tc(sp, q8, dev, stream);
     return q8 ? run_dim<true>(sp, dev, stream) : run_dim<false>(sp, dev, stream);
 }
 

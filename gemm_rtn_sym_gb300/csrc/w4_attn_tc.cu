@@ -6,7 +6,8 @@
 // of shared items joined by the CTA that finishes last.  What differs is what
 // bounds it: with R rows a byte of keys and values takes 2·R operations, and
 // the m16n8k16 MMAs of the other kernel reach a quarter of the tensor cores'
-// rate (104 rows of 128 over 16 requests: 196 µs, the cache's bytes 39 µs).
+// rate (104 rows of 128 over 16 requests of 1024 to 8192 tokens: 255 µs with
+// 16 rows to a pass, 196 with 64; here 71, of which the cache's bytes are 39).
 //
 //   S [128 rows, TT tokens] = Q [rows, D] · Kᵀ     both from shared memory
 //   O [128 rows, D]        += P [rows, tokens] · V  P from tensor memory
@@ -15,11 +16,19 @@
 // way).  Warps 0 to 3 hold a row per thread: they read S from tensor memory,
 // twice (the largest score, then the weights), so that a row's statistics need
 // no exchange between threads, and write the weights over it, as two bf16 each
-// (one alone would err as much as the result's rounding).  Warps 4 to 7 copy
-// the tokens' rows by cp.async, from pages of any size, into a ring of six
-// slots, keys and values in turn.  Warp 8 issues the products: the scores of
-// tile i + 1 while the weights of tile i are made.
+// (one alone would err as much as the result's rounding).  That takes them
+// about 3000 cycles a tile of 128 tokens, as long as its bytes take at D = 128.
+// The next warps copy the tokens' rows by cp.async, from pages of any size, into
+// a ring of slots, keys and values in turn.  The last warp issues the products:
+// the scores of tile i + 1 while the weights of tile i are made.
 // Tensor memory: S of three tiles from column 0, then O.
+//
+// Format 8: codes are exact as bf16, so the products are those of format 16,
+// with the key scales applied to the scores and the value scales to the
+// weights.  Codes arrive in slots of their own and eight warps turn them to
+// bf16 (96 µs for the call above, 99 with four; 787 and 875 for 32 rows over 64
+// requests of 8192 to 16384).  Bound by the row threads' and these warps'
+// instructions, the bytes being half of format 16's.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -39,23 +48,24 @@ namespace w4 {
 namespace {
 
 constexpr int kRows = 128;
-constexpr int kSoftmaxWarps = 4, kLoadWarps = 4;
-constexpr int kMmaWarp = kSoftmaxWarps + kLoadWarps;
-constexpr int kThreads = 32 * (kMmaWarp + 1);
-constexpr int kSlots = 6;
+constexpr int kSoftmaxWarps = 4;
 constexpr int kFixed = 2;  // an item's fixed cost in tiles
 constexpr uint32_t kTmemCols = 512;
 
-template <int D>
+template <int D, bool Q8>
 struct Shape {
+    static constexpr int kLoadWarps = Q8 ? 8 : 4, kMmaWarp = kSoftmaxWarps + kLoadWarps, kThreads = 32 * (kMmaWarp + 1);
     static constexpr int kTile = D == 256 ? 64 : 128;
     static constexpr uint32_t kColO = D == 256 ? 256 : 384;
     static constexpr int kBlocks = D / 64;            // 128-byte columns of a row
     static constexpr int kSlot = kTile * D * 2;       // keys or values of a tile
-    static constexpr int kSlotsHere = D == 256 ? 4 : kSlots;
+    static constexpr int kSlots = Q8 ? (D == 256 ? 3 : 4) : D == 256 ? 4 : 6;  // what shared memory holds
     static constexpr int kQ = kRows * D * 2;
+    // Format 8: tiles of codes on their way, in slots of their own.
+    static constexpr int kAhead = 2, kRaw = kTile * D, kRawSlots = Q8 ? kAhead + 1 : 0;
     // At least what keeps a second CTA, which would wait for tensor memory, off the SM.
-    static constexpr int kNeed = 1024 + kQ + kSlotsHere * kSlot, kSmem = kNeed > 120 * 1024 ? kNeed : 120 * 1024;
+    static constexpr int kNeed = 1024 + kQ + kSlots * kSlot + kRawSlots * kRaw;
+    static constexpr int kSmem = kNeed > 120 * 1024 ? kNeed : 120 * 1024;
 };
 
 // Byte of 16-byte chunk c of row r in a tile of ROWS rows: columns of 128 bytes, 128-byte swizzle.
@@ -104,13 +114,27 @@ struct Turn {
     }
 };
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_constant__ SplitArgs sp) {
-    using S = Shape<D>;
-    constexpr int TT = S::kTile, NS = S::kSlotsHere;
+// Four codes as bf16, exactly: 0x4300 | m is 128 + m for the lower seven bits m, and 128 or 256 goes off for the sign.
+__device__ __forceinline__ uint2 codes_bf16(uint32_t w) {
+    const uint32_t m = w & 0x7F7F7F7Fu, sign = w & 0x80808080u;
+    auto pair = [&](uint32_t sel) {
+        const uint32_t from = __byte_perm(m, 0x43434343u, sel), off = __byte_perm(sign, 0x43434343u, sel);
+        const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&from), *reinterpret_cast<const __nv_bfloat162*>(&off));
+        return *reinterpret_cast<const uint32_t*>(&v);
+    };
+    return make_uint2(pair(0x4140), pair(0x4342));
+}
+
+template <int D, bool Q8>
+__global__ void __launch_bounds__(Shape<D, Q8>::kThreads, 1) attn_tc_kernel(const __grid_constant__ SplitArgs sp) {
+    using S = Shape<D, Q8>;
+    constexpr int TT = S::kTile, NS = S::kSlots, kLoadWarps = S::kLoadWarps, kMmaWarp = S::kMmaWarp;
     extern __shared__ uint8_t smem_raw[];
     // s_values: the products of even and of odd tiles are in O; apart, since a wait may look two tiles back.
     __shared__ __align__(8) uint64_t s_full[NS], s_empty[NS], s_scores[3], s_weights[3], s_values[2], s_queries;
+    // Format 8, by the tile's score buffer: the tokens' key scales (times that of the scores) and value scales.
+    __shared__ __align__(8) uint64_t s_scaled[3];
+    __shared__ __align__(16) float s_scale[Q8 ? 3 : 1][2][Q8 ? TT : 4];
     __shared__ uint32_t s_tmem;
     __shared__ bool s_last;
     const AttnArgs& a = sp.a;
@@ -125,6 +149,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         for (int i = 0; i < 3; ++i) {
             mbar_init(smem_addr(&s_scores[i]), 1);
             mbar_init(smem_addr(&s_weights[i]), kSoftmaxWarps * 32);
+            mbar_init(smem_addr(&s_scaled[i]), kLoadWarps * 32);
         }
         mbar_init(smem_addr(&s_values[0]), 1);
         mbar_init(smem_addr(&s_values[1]), 1);
@@ -132,7 +157,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     Walk<TT, kRows, kFixed> walk;
-    if (!walk.template find<kThreads>(sp)) return;
+    if (!walk.template find<S::kThreads>(sp)) return;
     if (warp == kMmaWarp) tmem_alloc(smem_addr(&s_tmem), kTmemCols);
     tc_fence_before();
     __syncthreads();
@@ -201,12 +226,66 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     } else if (warp >= kSoftmaxWarps) {
         // -------------------------------------------------------- copies
         // A warp copies TT / 4 tokens of each tile; lane l knows token l of them.
-        constexpr int kMine = TT / kLoadWarps, kSub = kMine / 16, kChunks = D / 8;
+        // Format 8: into slots of codes, which the lane that copied them turns to bf16, kAhead half tiles later.
+        constexpr int kMine = TT / kLoadWarps, kSub = Q8 ? 1 : kMine / 16, kChunks = D * (Q8 ? 1 : 2) / 16;
         constexpr int kPerPass = 32 / kChunks;  // token rows of one pass of the warp's lanes (D ≤ 256)
-        const int my_row = (warp - kSoftmaxWarps) * kMine, d_chunks = a.head_dim / 8;
+        const int my_row = (warp - kSoftmaxWarps) * kMine, d_chunks = a.head_dim * (Q8 ? 1 : 2) / 16;
         const int load_c = lane % kChunks, load_r = lane / kChunks;
         Turn slot;
         slot.round = 1;  // the ring's first round finds its slots free
+        // Format 8.  The scales of the lane's token travel by register until its codes are there.  A tile's go where
+        // those of the third tile before were: its values' slot has been filled anew, so they have been used.
+        struct Scales {
+            float k, v;
+        };
+        Scales found = {0.f, 0.f}, older = found;
+        Turn scaled;
+        const uint32_t raw = ring + NS * S::kSlot + ((warp - kSoftmaxWarps) * kMine * kChunks + lane) * 16;
+        int asked = 0, raw_ask = 0, raw_take = 0;
+        // Asks for half a tile of codes (or, past the last, for nothing) and turns that of kAhead before.
+        auto half_tile = [&](bool key, bool any, long long off) {
+            if (any) {
+                const uint8_t* src = static_cast<const uint8_t*>(key ? a.k : a.v) + load_c * 16;
+#pragma unroll
+                for (int p = 0; p < kMine; p += kPerPass) {
+                    const long long o = __shfl_sync(~0u, off, p + load_r);
+                    const bool there = o >= 0 && load_c < d_chunks;
+                    cp_async16_zfill(raw + raw_ask * S::kRaw + p * kChunks * 16, there ? src + o : static_cast<const uint8_t*>(a.k), there ? 16 : 0);
+                }
+            }
+            cp_async_commit();
+            if (++raw_ask == S::kAhead + 1) raw_ask = 0;
+            if (asked < S::kAhead) {
+                ++asked;
+                return;
+            }
+            cp_async_wait<S::kAhead>();
+            wait_or_report(smem_addr(&s_empty[slot.place]), slot.round, alive, a.status);
+            const bool keys = S::kAhead % 2 == 0 ? key : !key;
+            const uint32_t dst = ring + slot.place * S::kSlot;
+            // A 16-byte chunk of codes makes two of values; lanes in the upper half of 128 bytes of codes write the second
+            // one first, so that eight lanes' chunks fall in different banks.
+            const int second = D > 64 && (load_c & 4) ? 1 : 0;
+#pragma unroll 4
+            for (int p = 0; p < kMine; p += kPerPass) {
+                const uint4 w = lds128(raw + raw_take * S::kRaw + p * kChunks * 16);
+                const uint2 x = codes_bf16(w.x), y = codes_bf16(w.y), z = codes_bf16(w.z), u = codes_bf16(w.w);
+                const uint4 lo = make_uint4(x.x, x.y, y.x, y.y), hi = make_uint4(z.x, z.y, u.x, u.y);
+                sts128(dst + place<TT>(my_row + p + load_r, 2 * load_c + second), second ? hi : lo);
+                sts128(dst + place<TT>(my_row + p + load_r, 2 * load_c + (second ^ 1)), second ? lo : hi);
+            }
+            if (++raw_take == S::kAhead + 1) raw_take = 0;
+            if (keys) {
+                if (lane < kMine) {
+                    s_scale[scaled.place][0][my_row + lane] = older.k * sp.scale_log2;
+                    s_scale[scaled.place][1][my_row + lane] = older.v;
+                }
+                mbar_arrive(smem_addr(&s_scaled[scaled.place]));
+                scaled.step(3);
+            }
+            mbar_arrive(smem_addr(&s_full[slot.place]));
+            slot.step(NS);
+        };
         for (Item it; walk.next(sp, it);) {
             const int base0 = it.tok0 & ~15, tiles = max(0, (it.tok1 - base0 + TT - 1) / TT);
             const int* table = a.table + it.b * a.table_stride;
@@ -225,37 +304,56 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                     else
                         record_status(a.status, kStatusInvalid);
                 }
-                long long off0[kSub];  // of the first token of each 16
+                if constexpr (Q8) {
+                    older = found;
+                    found = {0.f, 0.f};
+                    if (off >= 0) {
+                        const long long at = (static_cast<long long>(page) * a.kv_heads + it.h) * a.page_size + (tok - sp.page_index(tok) * a.page_size);
+                        found.k = __bfloat162float(a.k_scales[at]);
+                        found.v = __bfloat162float(a.v_scales[at]);
+                    }
+                    half_tile(true, true, off);
+                    half_tile(false, true, off);
+                } else {
+                    long long off0[kSub];  // of the first token of each 16
 #pragma unroll
-                for (int sub = 0; sub < kSub; ++sub) off0[sub] = __shfl_sync(~0u, off, 16 * sub);
-                const long long mine = kSub == 2 && (lane & 16) ? off0[kSub - 1] : off0[0];
-                const bool even = __all_sync(~0u, mine >= 0 && off == mine + (lane & 15) * a.token_stride) && d_chunks == kChunks;
+                    for (int sub = 0; sub < kSub; ++sub) off0[sub] = __shfl_sync(~0u, off, 16 * sub);
+                    const long long mine = kSub == 2 && (lane & 16) ? off0[kSub - 1] : off0[0];
+                    const bool even = __all_sync(~0u, mine >= 0 && off == mine + (lane & 15) * a.token_stride) && d_chunks == kChunks;
 #pragma unroll
-                for (int key = 1; key >= 0; --key) {
-                    wait_or_report(smem_addr(&s_empty[slot.place]), slot.round, alive, a.status);
-                    const uint32_t dst = ring + slot.place * S::kSlot;
-                    const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(key ? a.k : a.v);
-                    if (even) {
+                    for (int key = 1; key >= 0; --key) {
+                        wait_or_report(smem_addr(&s_empty[slot.place]), slot.round, alive, a.status);
+                        const uint32_t dst = ring + slot.place * S::kSlot;
+                        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(key ? a.k : a.v);
+                        if (even) {
 #pragma unroll
-                        for (int sub = 0; sub < kSub; ++sub) {
-                            const __nv_bfloat16* from = src + off0[sub] + load_r * a.token_stride + load_c * 8;
+                            for (int sub = 0; sub < kSub; ++sub) {
+                                const __nv_bfloat16* from = src + off0[sub] + load_r * a.token_stride + load_c * 8;
 #pragma unroll
-                            for (int p = 0; p < 16; p += kPerPass) {
-                                cp_async16(dst + place<TT>(my_row + sub * 16 + p + load_r, load_c), from);
-                                from += kPerPass * a.token_stride;
+                                for (int p = 0; p < 16; p += kPerPass) {
+                                    cp_async16(dst + place<TT>(my_row + sub * 16 + p + load_r, load_c), from);
+                                    from += kPerPass * a.token_stride;
+                                }
+                            }
+                        } else {
+#pragma unroll 4
+                            for (int p = 0; p < kMine; p += kPerPass) {
+                                const long long o = __shfl_sync(~0u, off, p + load_r);
+                                const bool there = o >= 0 && load_c < d_chunks;
+                                cp_async16_zfill(dst + place<TT>(my_row + p + load_r, load_c), src + (there ? o + load_c * 8 : 0), there ? 16 : 0);
                             }
                         }
-                    } else {
-#pragma unroll 4
-                        for (int p = 0; p < kMine; p += kPerPass) {
-                            const long long o = __shfl_sync(~0u, off, p + load_r);
-                            const bool there = o >= 0 && load_c < d_chunks;
-                            cp_async16_zfill(dst + place<TT>(my_row + p + load_r, load_c), src + (there ? o + load_c * 8 : 0), there ? 16 : 0);
-                        }
+                        cp_async_arrive(smem_addr(&s_full[slot.place]));
+                        slot.step(NS);
                     }
-                    cp_async_arrive(smem_addr(&s_full[slot.place]));
-                    slot.step(NS);
                 }
+            }
+        }
+        if constexpr (Q8) {
+            if (asked > 0) {
+                older = found;
+#pragma unroll 1
+                for (int i = 0; i < S::kAhead; ++i) half_tile(i % 2 == 0, false, 0);
             }
         }
         cp_async_wait_all();
@@ -303,7 +401,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                 tc_fence_before();
                 mbar_arrive(smem_addr(&s_queries));
             }
-            float m = -INFINITY, l = 0.f;  // reference score, unscaled; sum of the weights
+            float m = -INFINITY, l = 0.f;  // reference score, unscaled (format 8: to base 2); sum of the weights
+            const float unit = Q8 ? 1.f : sp.scale_log2;
             for (int i = 0; i < tiles; ++i, ++tile, now.step(3), slot.step(NS), slot.step(NS)) {
                 const int base = base0 + i * TT;
                 const bool hidden = min(base + TT, it.tok1) > all_hi || max(base, it.tok0) < all_lo;
@@ -314,6 +413,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                 const uint32_t scores = mine + now.place * TT;
                 wait_or_report(smem_addr(&s_scores[now.place]), now.round, alive, a.status);
                 tc_fence_after();
+                const float(*const scale)[Q8 ? TT : 4] = s_scale[Q8 ? now.place : 0];
+                // v times the key scales from column c on
+                auto scale_scores = [&](uint32_t(&v)[32], int c) {
+                    if (Q8)
+#pragma unroll
+                        for (int x = 0; x < 32; x += 4) {
+                            const float4 f = *reinterpret_cast<const float4*>(&scale[0][c + x]);
+                            v[x] = __float_as_uint(__uint_as_float(v[x]) * f.x);
+                            v[x + 1] = __float_as_uint(__uint_as_float(v[x + 1]) * f.y);
+                            v[x + 2] = __float_as_uint(__uint_as_float(v[x + 2]) * f.z);
+                            v[x + 3] = __float_as_uint(__uint_as_float(v[x + 3]) * f.w);
+                        }
+                };
+                if (Q8) wait_or_report(smem_addr(&s_scaled[now.place]), now.round, alive, a.status);
                 // ---- reference
                 float grown = m;
                 auto largest = [&](auto some) {  // of the scores that the row sees: all of the tile's, or some
@@ -321,6 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                     for (int c = 0; c < TT; c += 32) {
                         uint32_t v[32];
                         tmem_ld32(scores + c, v);
+                        scale_scores(v, c);
 #pragma unroll
                         for (int x = 0; x < 32; ++x) {
                             const float f = __uint_as_float(v[x]);
@@ -336,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                     if (i > 0) wait_or_report(smem_addr(&s_values[(tile - 1) & 1]), (tile - 1) >> 1 & 1, alive, a.status);
                     tc_fence_after();
                 };
-                const float by = (grown - m) * sp.scale_log2;
+                const float by = (grown - m) * unit;
                 if (__any_sync(~0u, by > 8.f)) {
                     const float keep = m == -INFINITY ? 0.f : ex2(-by);
                     if (i > 0) {
@@ -354,11 +468,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                     l *= keep;
                     m = grown;
                 }
-                const float ref = m == -INFINITY ? 0.f : m * sp.scale_log2;
+                const float ref = m == -INFINITY ? 0.f : m * unit;
 
                 // ---- values that are not finite, of tokens that some rows do not see: 0 · ∞ would spoil those rows.
                 // They are made 0 for the product and added here to the rows that see them.
-                if (hidden) {
+                if (!Q8 && hidden) {
                     const uint32_t vals = ring + slot.place * S::kSlot;
                     wait_or_report(smem_addr(&s_full[slot.place]), slot.round, alive, a.status);
                     bool odd = false;
@@ -422,16 +536,21 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                     for (int c = 0; c < TT; c += 32) {
                         uint32_t v[32], w[32];
                         tmem_ld32(scores + c, v);
+                        scale_scores(v, c);
 #pragma unroll
                         for (int x = 0; x < 32; x += 2) {
                             float s0 = __uint_as_float(v[x]), s1 = __uint_as_float(v[x + 1]);
-                            if (decltype(some)::value) {
-                                s0 = sees(c + x) ? s0 : -INFINITY;
-                                s1 = sees(c + x + 1) ? s1 : -INFINITY;
-                            }
-                            const float p0 = ex2(fmaf(s0, sp.scale_log2, -ref)), p1 = ex2(fmaf(s1, sp.scale_log2, -ref));
+                            const bool see0 = !decltype(some)::value || sees(c + x), see1 = !decltype(some)::value || sees(c + x + 1);
+                            s0 = see0 ? s0 : -INFINITY;
+                            s1 = see1 ? s1 : -INFINITY;
+                            float p0 = ex2(Q8 ? s0 - ref : fmaf(s0, unit, -ref)), p1 = ex2(Q8 ? s1 - ref : fmaf(s1, unit, -ref));
                             sums[x & 2] += p0;
                             sums[(x & 2) + 1] += p1;
+                            if (Q8) {  // (a hidden token's scale may be anything)
+                                const float2 f = *reinterpret_cast<const float2*>(&scale[1][c + x]);
+                                p0 = see0 ? p0 * f.x : 0.f;
+                                p1 = see1 ? p1 * f.y : 0.f;
+                            }
                             // Upper halves cut off, not rounded: the lower ones take what is left, to 16 bits in all
                             // (roundings to bf16 would share the exponentials' slow pipe).
                             const uint32_t u0 = __float_as_uint(p0), u1 = __float_as_uint(p1);
@@ -461,7 +580,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             const Parts<kRows, D> parts(sp, walk, it, kFixed);
             float* const part = parts.at(static_cast<int>(blockIdx.x) - parts.first);
             if (!whole && live) {
-                part[tid] = m * sp.scale_log2;
+                part[tid] = m * unit;
                 part[kRows + tid] = fminf(l, 3e38f);
             }
             // A row that sees nothing is zeros; one whose scores are all −∞ has no value (0 · 1 / 0).
@@ -552,19 +671,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     }
 }
 
-template <int D>
+template <int D, bool Q8>
 cudaError_t run(const SplitArgs& sp, int grid, cudaStream_t stream) {
-    using S = Shape<D>;
+    using S = Shape<D, Q8>;
     static std::atomic<bool> ready[kMaxDevices];  // the kernel may use its shared memory on this device
     int device = 0;
     cudaError_t err = cudaGetDevice(&device);
     if (err != cudaSuccess) return err;
     if (!ready[device & (kMaxDevices - 1)].load(std::memory_order_relaxed)) {
-        err = cudaFuncSetAttribute(attn_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+        err = cudaFuncSetAttribute(attn_tc_kernel<D, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
         if (err != cudaSuccess) return err;
         ready[device & (kMaxDevices - 1)].store(true, std::memory_order_relaxed);
     }
-    attn_tc_kernel<D><<<grid, kThreads, S::kSmem, stream>>>(sp);
+    attn_tc_kernel<D, Q8><<<grid, S::kThreads, S::kSmem, stream>>>(sp);
     return cudaGetLastError();
 }
 
@@ -572,16 +691,16 @@ cudaError_t run(const SplitArgs& sp, int grid, cudaStream_t stream) {
 
 size_t attn_tc_partial_floats(int head_dim) { return partial_floats(kRows, head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256); }
 
-cudaError_t launch_attn_tc(const SplitArgs& sp, const DeviceInfo& dev, cudaStream_t stream) {
+cudaError_t launch_attn_tc(const SplitArgs& sp, bool q8, const DeviceInfo& dev, cudaStream_t stream) {
     const AttnArgs& a = sp.a;
     const int tile = a.head_dim <= 128 ? 128 : 64;
     // At least as many units as the batch can have: a CTA for each, where they are few.
     const double reach = std::min(static_cast<double>(a.width) * a.page_size, a.window > 0 ? static_cast<double>(a.window) + a.T : 1e18);
     const double most = static_cast<double>(a.kv_heads) * (a.B + static_cast<double>(a.T) * sp.G / kRows) * (reach / tile + 2 + kFixed);
     const int grid = static_cast<int>(std::min<double>(std::min(dev.sm_count, kMaxCtas), most));
-    if (a.head_dim <= 64) return run<64>(sp, grid, stream);
-    if (a.head_dim <= 128) return run<128>(sp, grid, stream);
-    return run<256>(sp, grid, stream);
+    if (a.head_dim <= 64) return q8 ? run<64, true>(sp, grid, stream) : run<64, false>(sp, grid, stream);
+    if (a.head_dim <= 128) return q8 ? run<128, true>(sp, grid, stream) : run<128, false>(sp, grid, stream);
+    return q8 ? run<256, true>(sp, grid, stream) : run<256, false>(sp, grid, stream);
 }
 
 }  // namespace w4

@@ -11,6 +11,6 @@ namespace w4 {
 
 // Floats of a part of a shared item.
 size_t attn_tc_partial_floats(int head_dim);
-cudaError_t launch_attn_tc(const SplitArgs& sp, const DeviceInfo& dev, cudaStream_t stream);
+cudaError_t launch_attn_tc(const SplitArgs& sp, bool q8, const DeviceInfo& dev, cudaStream_t stream);
 
 }  // namespace w4

@@ -382,7 +382,8 @@ int w4_gemm_grouped_noalloc(int32_t count, const w4_gemm_problem* problems, void
  * head_dim] and [pages, kv_heads, page_size, head_dim] memory serve.
  *   format 16: bf16 rows.
  *   format 8 : int8 codes c and one bf16 scale d per row, [pages, kv_heads,
- *              page_size]; the row stands for d·c.
+ *              page_size]; the row stands for d·c, d ≥ 0.  w4_attn_decode
+ *              may take value scales below 2⁻¹⁰⁰ as 2⁻¹⁰⁰.
  * head_dim: a multiple of 16, at most 256.  k and v 16-byte aligned, strides
  * multiples of 16 bytes, rows apart from each other; scales 2-byte aligned.
  *
@@ -514,14 +515,16 @@ int w4_kv_append(const w4_kv_cache* cache, const w4_rope* rope, int64_t T, int32
  * Row j of a request with n rows and length L stands at position p = L − n + j
  * and sees the tokens t with max(0, p − window + 1) ≤ t ≤ p:
  *   out = Σ_t softmax_t(scale · q·k_t) · v_t,
- * scores, maxima, sums and products in fp32, rounded once to bf16.  A row that
+ * scores, maxima, sums and products in fp32, rounded once to bf16; a weight
+ * enters its products with 16 bits (11 in format 8).  A row that
  * sees no token (p < 0) is zeros.  What the masked and unused places of the
  * cache hold, NaN and infinities included, changes nothing.  Rows past
  * starts[B] are not written.
  * Out of range: a length past width · page_size (or 2³¹ − 2¹⁶) counts as that; starts that
  * fall or pass T are cut; a page id outside [0, pages) reads as rows of zeros.
  * workspace: w4_attn_decode_workspace_bytes(...) bytes, 256-byte aligned,
- * contents unspecified before and after.  Deterministic.  out may be q.
+ * contents unspecified before and after, and not that of another call that may
+ * run at the same time.  Deterministic.  out may be q.
  */
 size_t w4_attn_decode_workspace_bytes(const w4_kv_cache* cache, int32_t B, int64_t T, int32_t q_heads);
 int w4_attn_decode(const w4_kv_cache* cache, int32_t B, int64_t T, int32_t q_heads, const w4_rows* q,

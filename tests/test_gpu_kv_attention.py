@@ -371,3 +371,71 @@ def test_values_of_zero_in_8_bits(cuda_lib, zeros, n, D):
             case.v_scales[page, :, place] = 0
             case.vv[page, place] = 0.0
     finish(case, case.run(w4))
+
+
+# ---- many rows over a cache in 8 bits
+@pytest.mark.parametrize("Hq,H,D", MANY)
+@pytest.mark.parametrize("order,page_size", [("token", 16), ("head", 24), ("token", 1)])
+def test_many_rows_in_8_bits(cuda_lib, Hq, H, D, order, page_size):
+    lens = [0, 7, 1, 13, 200, 300, 64, 0, 129, 20, 257]
+    fresh = [5, 7, 1, 13, 5, 13, 0, 0, 1, 20, 9]
+    case = AttentionCase(lens, fresh, Hq, H, D, page_size, order, format=8, seed=Hq + D)
+    finish(case, case.run(w4))
+
+
+@pytest.mark.parametrize("window", [1, 9, 100, 1000])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_many_rows_windows_in_8_bits(cuda_lib, window, D):
+    lens, fresh = [1, 40, 500, 333, 13, 130], [1, 13, 9, 13, 13, 6]
+    case = AttentionCase(lens, fresh, 16, 2, D, 16, format=8, seed=window)
+    finish(case, case.run(w4, window=window), window=window)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.1])
+def test_many_rows_scales_in_8_bits(cuda_lib, scale):
+    case = AttentionCase([50, 300, 777], [13, 9, 13], 16, 2, 128, 16, format=8, seed=21)
+    finish(case, case.run(w4, scale=scale), scale=scale)
+
+
+@pytest.mark.parametrize("n", [1, 13])
+@pytest.mark.parametrize("scale,std", [(1.0, 8.0), (-0.3, 30.0)])
+def test_sharp_scores_in_8_bits(cuda_lib, scale, std, n):
+    """One token outweighs the others by far.  Its values have no codes of zero, under which a column would hold nothing
+    but weights that underflow."""
+    case = AttentionCase([50, 300, 777], [n] * 3, 16, 2, 128, 16, format=8, seed=21, std=std)
+    step = np.where(case.vv == 0, values(case.v_scales.transpose(1, 2))[..., None], 0.0)
+    case.vv = case.vv + np.where(np.isfinite(step), step, 0.0)
+    case.v[case.v == 0] = 1
+    finish(case, case.run(w4, scale=scale), scale=scale)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("window", [0, 9])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_many_rows_hidden_tokens_in_8_bits(cuda_lib, D, window, bad):
+    for L in (45, 300):
+        n = 13
+        case = AttentionCase([L, 200], [n, 13], 16, 2, D, 16, format=8, seed=22)
+        token = L - 8
+        page, place = int(case.table[0, token // 16]), token % 16
+        case.k_scales[page, :, place] = bad
+        case.v_scales[page, :, place] = bad
+        out = case.run(w4, window=window)
+        torch.cuda.synchronize()
+        assert w4.w4_last_device_status() == 0
+        position = np.arange(L - n, L)
+        sees = np.concatenate([(token <= position) & ((window == 0) | (token > position - window)), [False] * 13])
+        case.check(out, window=window, rows=~sees)
+        assert not np.isfinite(values(out)[sees]).all(axis=(1, 2)).any()
+
+
+@pytest.mark.parametrize("Hq,H,D,n", [(64, 8, 64, 13), (64, 8, 128, 13), (40, 8, 128, 13), (32, 4, 256, 5), (16, 1, 192, 20)])
+def test_long_runs_of_many_rows_in_8_bits(cuda_lib, Hq, H, D, n):
+    """Many tiles for every CTA: each ring goes round, and a cache page may end inside a tile."""
+    rng = np.random.default_rng(D + n)
+    lens = [int(x) for x in rng.integers(300, 2500, 8)] + [6000, n]
+    case = AttentionCase(lens, [n] * len(lens), Hq, H, D, 24, format=8, seed=24)
+    out = case.run(w4, uniform=True)
+    finish(case, out)
+    for _ in range(3):
+        assert torch.equal(out.view(torch.int16), case.run(w4, uniform=True).view(torch.int16))
