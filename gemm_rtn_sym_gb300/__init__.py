@@ -489,17 +489,19 @@ def _device_index(t: torch.Tensor, name: str) -> int:
 
 
 def _typed(t: torch.Tensor, name: str, dtype: torch.dtype, index: int) -> None:
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index:
+        return
     if not isinstance(t, torch.Tensor) or t.get_device() < 0:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.get_device() != index:
-        raise ValueError(f"{name} must be on cuda:{index}")
+    raise ValueError(f"{name} must be on cuda:{index}")
 
 
 def _vector(t: torch.Tensor, name: str, dtype: torch.dtype, n: int, index: int) -> int:
     """Address of a contiguous tensor of n values."""
-    _typed(t, name, dtype, index)
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != index:
+        _typed(t, name, dtype, index)
     if t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous tensor of {n} values")
     return t.data_ptr()
@@ -507,7 +509,8 @@ def _vector(t: torch.Tensor, name: str, dtype: torch.dtype, n: int, index: int) 
 
 def _strides(t: torch.Tensor, name: str, dtype: torch.dtype, ndim: int, index: int):
     """Strides of a tensor with unit stride in its last dimension."""
-    _typed(t, name, dtype, index)
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != index:
+        _typed(t, name, dtype, index)
     strides = t.stride()
     if len(strides) != ndim or (strides[-1] != 1 and t.shape[-1] > 1):
         raise ValueError(f"{name} must be a {ndim}-D tensor with unit stride in its last dimension")
@@ -547,12 +550,14 @@ def _kv_cache(k_cache, v_cache, k_scales, v_scales, index) -> _KvCache:
 
 # The address of a device's current stream (what torch.cuda.current_stream(i).cuda_stream gives, without the objects).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
+# (where a tensor is on the GPU, CUDA has been set up)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _call(name: str, index: int, *args) -> None:
     """Runs a library function on the current stream of the device."""
     fn = getattr(_lib or load(), name)
-    if torch.cuda.current_device() == index:
+    if _current_device() == index:
         status = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(index):
