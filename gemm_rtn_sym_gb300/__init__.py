@@ -552,6 +552,9 @@ def _kv_cache(k_cache, v_cache, k_scales, v_scales, index) -> _KvCache:
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
 # (where a tensor is on the GPU, CUDA has been set up)
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+# Memory of the caching allocator without a tensor around it, for the time of a call (a tensor costs 2 µs more).
+_raw_alloc = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_alloc", None)
+_raw_delete = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_delete", None)
 
 
 def _call(name: str, index: int, *args) -> None:
@@ -664,15 +667,21 @@ def w4_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     if out is None:
         out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
     rows_q, rows_out = _rows(q, "q", shape, index), _rows(out, "out", shape, index)
-    if workspace is None:
-        size = (_lib or load()).w4_attn_decode_workspace_bytes(cache, B, T, q_heads)
-        workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
-        scratch = workspace.data_ptr()
-    else:
+    args = (cache, B, T, q_heads, rows_q, rows_out, block_table.data_ptr(), stride, width,
+            _vector(lens, "lens", torch.int32, B, index),
+            None if starts is None else _vector(starts, "starts", torch.int32, B + 1, index),
+            dim ** -0.5 if scale is None else scale, window)
+    if workspace is not None:
         size = workspace.numel()
-        scratch = _vector(workspace, "workspace", torch.uint8, size, index)
-    _call("w4_attn_decode", index, cache, B, T, q_heads, rows_q, rows_out, block_table.data_ptr(), stride, width,
-          _vector(lens, "lens", torch.int32, B, index),
-          None if starts is None else _vector(starts, "starts", torch.int32, B + 1, index),
-          dim ** -0.5 if scale is None else scale, window, scratch, size)
+        _call("w4_attn_decode", index, *args, _vector(workspace, "workspace", torch.uint8, size, index), size)
+        return out
+    size = (_lib or load()).w4_attn_decode_workspace_bytes(cache, B, T, q_heads)
+    if size and _raw_alloc and _raw_delete and _current_device() == index:
+        scratch = _raw_alloc(size, _raw_stream(index))
+        try:
+            _call("w4_attn_decode", index, *args, scratch, size)
+        finally:
+            _raw_delete(scratch)  # the stream's next allocations may have it
+    else:
+        _call("w4_attn_decode", index, *args, torch.empty(size, dtype=torch.uint8, device=q.device).data_ptr(), size)
     return out

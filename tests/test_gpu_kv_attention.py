@@ -439,3 +439,25 @@ def test_long_runs_of_many_rows_in_8_bits(cuda_lib, Hq, H, D, n):
     finish(case, out)
     for _ in range(3):
         assert torch.equal(out.view(torch.int16), case.run(w4, uniform=True).view(torch.int16))
+
+
+def test_calls_without_a_workspace_in_a_graph_and_among_other_allocations(cuda_lib):
+    """The workspace of a call goes back to the allocator with it: what is allocated next on the stream may lie there."""
+    case = AttentionCase([3000, 170, 900, 13], [1] * 4, 16, 2, 128, 16, seed=27)
+    q, table, lens = case.q.to(DEV), gpu(case.table), gpu(case.lens)
+    first = w4.w4_attn_decode(q, case.k, case.v, table, lens)
+    finish(case, first)
+    size = w4.w4_attn_decode_workspace_bytes(q, case.k, 4)
+    outs = []
+    for i in range(10):
+        outs.append(w4.w4_attn_decode(q, case.k, case.v, table, lens))
+        torch.empty(size, dtype=torch.uint8, device=DEV).fill_(i)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for i in range(3):
+            outs.append(w4.w4_attn_decode(q, case.k, case.v, table, lens))
+            torch.empty(size, dtype=torch.uint8, device=DEV).fill_(i)
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(first.view(torch.int16), x.view(torch.int16)) for x in outs)
