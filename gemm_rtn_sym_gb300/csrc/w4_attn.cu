@@ -28,7 +28,7 @@
 //
 // One request of 131071 tokens, 64 query and 8 key-value heads of 128: 100 µs
 // (5.4 TB/s); 64 requests of up to 16384, 40 heads: 114 µs (5.6), in 8 bits
-// 80 µs (4.1: bound by decoding); 96 requests that see 1024 tokens, 16 and 4
+// 74 µs (4.4: bound by decoding); 96 requests that see 1024 tokens, 16 and 4
 // heads of 256: 43 µs (3.4: half of it starts and ends of items).
 #include <algorithm>
 #include <atomic>
@@ -244,14 +244,18 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
 
         // ---- loads
         // Scales of the lane's token travel by register until the stage before theirs has been used (for an iteration
-        // and a half where kSlots is even), then through shared memory.
+        // and a half where kSlots is even), then through shared memory.  As they come: a conversion right behind the
+        // load would wait for it in every stage (80 µs for 74 at 64 ragged requests).
         struct Scales {
-            float k, v;
+            __nv_bfloat16 k, v;
         };
-        Scales found = {0.f, 0.f}, older = found;
+        const Scales none = {__ushort_as_bfloat16(0), __ushort_as_bfloat16(0)};
+        Scales found = none, older = none;
         auto put_scales = [&](const Scales& x, int stage) {
-            if (Q8 && stage < stages && rw == 0 && lane < S::kTokens)
-                scales[stage % S::kScaleSlots * S::kTokens + lane] = make_float2(x.k, __log2f(x.v < kLeastScale ? kLeastScale : x.v));
+            if (Q8 && stage < stages && rw == 0 && lane < S::kTokens) {
+                const float v = __bfloat162float(x.v);
+                scales[stage % S::kScaleSlots * S::kTokens + lane] = make_float2(__bfloat162float(x.k), __log2f(v < kLeastScale ? kLeastScale : v));
+            }
         };
         long long off = -1;     // of the lane's token, in the stage whose keys were asked for last; −1: none
         long long off0[S::kSub];  // of the first token of each 16
@@ -268,11 +272,11 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
                     record_status(a.status, kStatusInvalid);
             }
             if (Q8) {
-                found = {0.f, 0.f};
+                found = none;
                 if (off >= 0) {
                     const long long s = (static_cast<long long>(page) * a.kv_heads + h) * a.page_size + in_page;
-                    found.k = __bfloat162float(a.k_scales[s]);
-                    found.v = __bfloat162float(a.v_scales[s]);
+                    found.k = a.k_scales[s];
+                    found.v = a.v_scales[s];
                 }
             }
 #pragma unroll
@@ -730,9 +734,9 @@ int64_t average_rows(int32_t B, int64_t T, int G) { return (T + B - 1) / B * G; 
 // head_dim 128, 16 rows: 56 and 67; 24: 67 and 67, 593 and 517; 32: 71 and 66,
 // 594 and 517.  head_dim 256, 32 rows: 69 and 90, 475 and 548; 52: 130 and 92.
 // head_dim 64, 32 rows: 26 and 29; 40: 35 and 29.
-// Format 8: head_dim 128, 40 rows: 84 and 96; 64: 107 and 96, 1121 and 787;
-// 104: 176 and 96.  256, 52 rows: 120 and 111.  64, 64 rows: 27 and 32, 104: 38
-// and 33.
+// Format 8: head_dim 128, 40 rows: 81 and 94; 64: 103 and 94, 1060 and 785;
+// 104: 166 and 97.  256, 52 rows: 110 and 112.  64, 64 rows: 27 and 33, 104: 39
+// and 34.
 bool many_rows(int32_t B, int64_t T, int G, int D, bool q8) {
     return average_rows(B, T, G) > (q8 ? 48 : D == 128 ? 16 : 32);
 }

@@ -236,9 +236,10 @@ __global__ void __launch_bounds__(Shape<D, Q8>::kThreads, 1) attn_tc_kernel(cons
         // Format 8.  The scales of the lane's token travel by register until its codes are there.  A tile's go where
         // those of the third tile before were: its values' slot has been filled anew, so they have been used.
         struct Scales {
-            float k, v;
+            __nv_bfloat16 k, v;
         };
-        Scales found = {0.f, 0.f}, older = found;
+        const Scales none = {__ushort_as_bfloat16(0), __ushort_as_bfloat16(0)};
+        Scales found = none, older = none;
         Turn scaled;
         const uint32_t raw = ring + NS * S::kSlot + ((warp - kSoftmaxWarps) * kMine * kChunks + lane) * 16;
         int asked = 0, raw_ask = 0, raw_take = 0;
@@ -277,8 +278,8 @@ __global__ void __launch_bounds__(Shape<D, Q8>::kThreads, 1) attn_tc_kernel(cons
             if (++raw_take == S::kAhead + 1) raw_take = 0;
             if (keys) {
                 if (lane < kMine) {
-                    s_scale[scaled.place][0][my_row + lane] = older.k * sp.scale_log2;
-                    s_scale[scaled.place][1][my_row + lane] = older.v;
+                    s_scale[scaled.place][0][my_row + lane] = __bfloat162float(older.k) * sp.scale_log2;
+                    s_scale[scaled.place][1][my_row + lane] = __bfloat162float(older.v);
                 }
                 mbar_arrive(smem_addr(&s_scaled[scaled.place]));
                 scaled.step(3);
@@ -306,11 +307,11 @@ __global__ void __launch_bounds__(Shape<D, Q8>::kThreads, 1) attn_tc_kernel(cons
                 }
                 if constexpr (Q8) {
                     older = found;
-                    found = {0.f, 0.f};
+                    found = none;
                     if (off >= 0) {
                         const long long at = (static_cast<long long>(page) * a.kv_heads + it.h) * a.page_size + (tok - sp.page_index(tok) * a.page_size);
-                        found.k = __bfloat162float(a.k_scales[at]);
-                        found.v = __bfloat162float(a.v_scales[at]);
+                        found.k = a.k_scales[at];
+                        found.v = a.v_scales[at];
                     }
                     half_tile(true, true, off);
                     half_tile(false, true, off);
