@@ -728,17 +728,23 @@ int dim_of(int head_dim) { return head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 
 // Query rows to a key-value head of a request, on the average.
 int64_t average_rows(int32_t B, int64_t T, int G) { return (T + B - 1) / B * G; }
 
-// Whether the tensor-core kernel takes the call.  A row tile of 16 rows is a
-// pass over the request's tokens here, one of 128 rows there.  Requests of
-// 1024 to 8192 tokens (16 of them) and of 8192 to 16384 (64), µs here and there:
-// head_dim 128, 16 rows: 56 and 67; 24: 67 and 67, 593 and 517; 32: 71 and 66,
-// 594 and 517.  head_dim 256, 32 rows: 69 and 90, 475 and 548; 52: 130 and 92.
-// head_dim 64, 32 rows: 26 and 29; 40: 35 and 29.
-// Format 8: head_dim 128, 40 rows: 81 and 94; 64: 103 and 94, 1060 and 785;
-// 104: 166 and 97.  256, 52 rows: 110 and 112.  64, 64 rows: 27 and 33, 104: 39
-// and 34.
-bool many_rows(int32_t B, int64_t T, int G, int D, bool q8) {
-    return average_rows(B, T, G) > (q8 ? 48 : D == 128 ? 16 : 32);
+// Whether the tensor-core kernel takes the call.  A row tile of 16 or 32 rows
+// is a pass over the request's tokens here, one of 128 rows there, but a piece
+// of work starts and joins in less time here.  µs here and there, requests of
+// 1024 to 8192 tokens (16 of them) where nothing else is said:
+// head_dim 128, 16 rows: 56 and 67; 24: 67 and 67, and 21 and 28 for 64 requests
+// of 128 tokens; 32: 71 and 66; 40: 108 and 68.  64, 32 rows: 26 and 29; 40: 35
+// and 29.  256, 32 rows: 69 and 90; 52, for 64 requests of 512 tokens: 66 and 56.
+// Format 8: head_dim 128, 40 rows: 81 and 94; 64: 103 and 94; 104: 166 and 97.
+// 256, 52 rows: 110 and 112.  64, 64 rows: 27 and 33; 104: 39 and 34.
+// Where requests × heads leave half of the 152 SMs without an item of their own,
+// that kernel joins many large parts: head_dim 256, 52 rows, 4 heads, 4 requests
+// of 512 tokens 28 and 44, of 2048 tokens 34 and 62; in format 8 22 and 48, 31
+// and 67; 64, 104 rows, 2 heads, 4 requests of 2048 tokens in format 8: 14 and 25.
+bool many_rows(int32_t B, int64_t T, int G, int32_t kv_heads, int D, bool q8) {
+    const int limit = q8 ? (D == 64 ? 64 : 48) : D == 128 ? 24 : 32;
+    const bool few = static_cast<int64_t>(B) * kv_heads < 76 && (q8 || D == 256);
+    return average_rows(B, T, G) > (few ? 2 * limit : limit);
 }
 
 // Warps (of 16 rows) that share a stage.  With two, 17 to 32 rows are one pass
@@ -778,7 +784,7 @@ cudaError_t run(const SplitArgs& sp, const DeviceInfo& dev, cudaStream_t stream)
 
 template <int D, bool Q8>
 cudaError_t run_rows(const SplitArgs& sp, const DeviceInfo& dev, cudaStream_t stream) {
-    if constexpr (!Q8 && D != 128)  // (the tensor-core kernel takes more than 16 rows of 128)
+    if constexpr (!Q8)
         if (row_warps(sp.a.B, sp.a.T, sp.G, Q8) == 2) return run<D, Q8, 2>(sp, dev, stream);
     return run<D, Q8, 1>(sp, dev, stream);
 }
@@ -796,7 +802,7 @@ cudaError_t run_dim(const SplitArgs& sp, const DeviceInfo& dev, cudaStream_t str
 size_t attn_decode_workspace_bytes(int32_t B, int64_t T, int32_t q_heads, int32_t kv_heads, int32_t head_dim, bool q8) {
     const int G = q_heads / kv_heads, D = dim_of(head_dim);
     if (B <= 0) B = 1;
-    const size_t part = many_rows(B, T, G, D, q8) ? attn_tc_partial_floats(head_dim) : partial_floats(16 * row_warps(B, T, G, q8), D);
+    const size_t part = many_rows(B, T, G, kv_heads, D, q8) ? attn_tc_partial_floats(head_dim) : partial_floats(16 * row_warps(B, T, G, q8), D);
     return 2 * kMaxCtas * (sizeof(unsigned long long) + part * sizeof(float));
 }
 
@@ -813,7 +819,7 @@ cudaError_t launch_attn_decode(AttnArgs a, bool q8, void* workspace, const Devic
     // largest score is then that of the unscaled products, and hidden ones stay at −∞.
     sp.scale_log2 = std::max(std::fabs(a.scale) * 1.4426950408889634f, 1e-30f);
     sp.flip = a.scale < 0.f ? 0x80008000u : 0u;
-    if (many_rows(a.B, a.T, sp.G, dim_of(a.head_dim), q8)) return launch_attn_tc(sp, q8, dev, stream);
+    if (many_rows(a.B, a.T, sp.G, a.kv_heads, dim_of(a.head_dim), q8)) return launch_attn_tc(sp, q8, dev, stream);
     return q8 ? run_dim<true>(sp, dev, stream) : run_dim<false>(sp, dev, stream);
 }
 
