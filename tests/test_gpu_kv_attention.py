@@ -461,3 +461,24 @@ def test_calls_without_a_workspace_in_a_graph_and_among_other_allocations(cuda_l
         graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(first.view(torch.int16), x.view(torch.int16)) for x in outs)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("window", [0, 1, 9, 100])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_more_than_128_rows_in_8_bits(cuda_lib, D, window, bad):
+    """208 rows to a key-value head: two row tiles of the tensor-core kernel, whatever the head_dim, with a hidden token."""
+    for L in (45, 300):
+        n = 13
+        case = AttentionCase([L, 200, 13], [n, 13, 13], 32, 2, D, 16, format=8, seed=28)
+        token = L - 8
+        page, place = int(case.table[0, token // 16]), token % 16
+        case.k_scales[page, :, place] = bad
+        case.v_scales[page, :, place] = bad
+        out = case.run(w4, window=window)
+        torch.cuda.synchronize()
+        assert w4.w4_last_device_status() == 0
+        position = np.arange(L - n, L)
+        sees = np.concatenate([(token <= position) & ((window == 0) | (token > position - window)), [False] * 26])
+        case.check(out, window=window, rows=~sees)
+        assert not np.isfinite(values(out)[sees]).all(axis=(1, 2)).any()
