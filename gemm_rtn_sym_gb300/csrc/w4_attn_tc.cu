@@ -93,6 +93,12 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
+// Tiles that an item's tokens fall in, from the sixteen on that its first lies in: none in a request without tokens.
+template <int TT>
+__device__ __forceinline__ int tiles_of(const Item& it) {
+    return max(0, (it.tok1 - (it.tok0 & ~15) + TT - 1) / TT);
+}
+
 // Waits, as a warp, for a phase; where the wait runs out, reports it, gives what is in
 // flight once more as long, and lets the caller go on without waiting.
 __device__ __forceinline__ void wait_or_report(uint32_t bar, uint32_t parity, bool& alive, unsigned* status) {
@@ -173,7 +179,7 @@ __global__ void __launch_bounds__(Shape<D, Q8>::kThreads, 1) attn_tc_kernel(cons
         Turn next, now;       // score buffers of the tile to be scored next and of the one whose values are next
         uint32_t tile = 0, items = 0;
         for (Item it; walk.next(sp, it);) {
-            const int tiles = max(0, (it.tok1 - (it.tok0 & ~15) + TT - 1) / TT);
+            const int tiles = tiles_of<TT>(it);
             if (tiles == 0) continue;
             wait_or_report(smem_addr(&s_queries), items++ & 1, alive, a.status);
             auto scores = [&]() {  // of the tile whose keys come next
@@ -288,7 +294,7 @@ __global__ void __launch_bounds__(Shape<D, Q8>::kThreads, 1) attn_tc_kernel(cons
             slot.step(NS);
         };
         for (Item it; walk.next(sp, it);) {
-            const int base0 = it.tok0 & ~15, tiles = max(0, (it.tok1 - base0 + TT - 1) / TT);
+            const int base0 = it.tok0 & ~15, tiles = tiles_of<TT>(it);
             const int* table = a.table + it.b * a.table_stride;
             auto page_of = [&](int i) {  // page id of the lane's token, −1 outside the piece
                 const int tok = base0 + i * TT + my_row + (lane & (kMine - 1));
@@ -365,8 +371,11 @@ __global__ void __launch_bounds__(Shape<D, Q8>::kThreads, 1) attn_tc_kernel(cons
         slot.step(NS);
         uint32_t tile = 0;
         Turn now;  // of the tile's scores
-        // The queries of an item are asked for before the sums of the one before it go out: a row by D / 8 lanes.
+        // The queries of an item are asked for before the sums of the one before it go out: a row by D / 8 lanes.  Not those
+        // of an item without tokens: nothing reads or waits for them, and the next item's copies to the same places would
+        // be under way together with them, in no order.
         auto ask = [&](const Item& n) {
+            if (tiles_of<TT>(n) == 0) return;
             constexpr int kChunks = D / 8, kPerPass = kSoftmaxWarps * 32 / kChunks;
             const int c = tid % kChunks;
 #pragma unroll 4
@@ -381,7 +390,7 @@ __global__ void __launch_bounds__(Shape<D, Q8>::kThreads, 1) attn_tc_kernel(cons
         bool more = walk.next(sp, it);
         if (more) ask(it);
         while (more) {
-            const int base0 = it.tok0 & ~15, tiles = max(0, (it.tok1 - base0 + TT - 1) / TT);
+            const int base0 = it.tok0 & ~15, tiles = tiles_of<TT>(it);
             const int row = it.row0 + tid, j = sp.over_G(row);
             const bool live = row < it.rows;
             const int see_hi = live ? it.len - it.n + j + 1 : 0x7fffffff;  // tokens that the row sees
