@@ -683,5 +683,6 @@ def w4_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
         finally:
             _raw_delete(scratch)  # the stream's next allocations may have it
     else:
-        _call("w4_attn_decode", index, *args, torch.empty(size, dtype=torch.uint8, device=q.device).data_ptr(), size)
+        scratch = torch.empty(size, dtype=torch.uint8, device=q.device)  # (a name keeps it until the launch)
+        _call("w4_attn_decode", index, *args, scratch.data_ptr(), size)
     return out
