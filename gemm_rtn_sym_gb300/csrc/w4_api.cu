@@ -525,6 +525,11 @@ int w4_gemm_grouped_noalloc(int32_t count, const w4_gemm_problem* problems, void
 
 namespace {
 
+// The cache's kernels count requests, tokens and rows in 32 bits, and a loop's
+// last step may go past them by less than 2¹⁶ (a block of threads, a grid, a
+// tile of rows).
+constexpr int64_t kMostCounted = 0x7fff0000;
+
 // Memory of strided rows: `bytes` in all; where period > 0, rows of `inner`
 // bytes (at most period) that repeat every `period` bytes.
 struct Region {
@@ -626,7 +631,7 @@ int w4_kv_pages(const int32_t* lens, const int32_t* target, int32_t B, int32_t p
                 int64_t T, int32_t* new_lens, int32_t* starts, int64_t* slots, int32_t* positions,
                 int64_t* free_range_out, void* stream) {
     if (B < 0 || T < 0 || page_size < 1 || pages < 1 || width < 1) return W4_ERR_INVALID_ARG;
-    if (T > INT32_MAX || pages > INT32_MAX) return W4_ERR_UNSUPPORTED;
+    if (B > kMostCounted || T > INT32_MAX || pages > INT32_MAX) return W4_ERR_UNSUPPORTED;
     if (!free_pages || !free_range || !starts || !free_range_out) return W4_ERR_INVALID_ARG;
     if (B > 0 && (!lens || !target || !block_table || !new_lens)) return W4_ERR_INVALID_ARG;
     if (T > 0 && (!slots || !positions)) return W4_ERR_INVALID_ARG;
@@ -656,7 +661,7 @@ int w4_kv_append(const w4_kv_cache* cache, const w4_rope* rope, int64_t T, int32
     if (T < 0 || q_heads < 0 || !rope) return W4_ERR_INVALID_ARG;
     Region outs[5], ins[7];
     if (const int s = cache_regions(cache, *reinterpret_cast<Region(*)[4]>(&outs[1]))) return s;
-    if (T > INT32_MAX || q_heads > 65536 || cache->kv_heads > 65536) return W4_ERR_UNSUPPORTED;
+    if (T > kMostCounted || q_heads > 65536 || cache->kv_heads > 65536) return W4_ERR_UNSUPPORTED;
     const w4_rope& r = *rope;
     if (r.rotary < 0 || r.rotary > cache->head_dim) return W4_ERR_INVALID_ARG;
     if (r.rotary % 16 != 0) return W4_ERR_UNSUPPORTED;
@@ -740,7 +745,7 @@ int w4_attn_decode(const w4_kv_cache* cache, int32_t B, int64_t T, int32_t q_hea
     Region outs[2], ins[8];
     if (const int s = cache_regions(cache, *reinterpret_cast<Region(*)[4]>(&ins[1]))) return s;
     if (q_heads % cache->kv_heads != 0) return W4_ERR_INVALID_ARG;
-    if (q_heads > 65536 || T > INT32_MAX / q_heads) return W4_ERR_UNSUPPORTED;
+    if (q_heads > 65536 || B > kMostCounted || T > kMostCounted / q_heads) return W4_ERR_UNSUPPORTED;
     if (B > 0 && !starts && T % B != 0) return W4_ERR_INVALID_ARG;
     if (B == 0 || T == 0) return W4_OK;
     if (!block_table || !lens || !workspace) return W4_ERR_INVALID_ARG;

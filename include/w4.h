@@ -386,6 +386,8 @@ int w4_gemm_grouped_noalloc(int32_t count, const w4_gemm_problem* problems, void
  *              may take value scales below 2⁻¹⁰⁰ as 2⁻¹⁰⁰.
  * head_dim: a multiple of 16, at most 256.  k and v 16-byte aligned, strides
  * multiples of 16 bytes, rows apart from each other; scales 2-byte aligned.
+ * Requests, new tokens (w4_kv_append) and query rows (T · q_heads): at most
+ * 2³¹ − 2¹⁶.
  *
  * Numbers that the kernels read from device memory (lengths, positions, page
  * ids, slots) are checked there: one out of range records W4_ERR_INVALID_ARG

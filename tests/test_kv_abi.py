@@ -126,3 +126,13 @@ def test_workspace_bytes(lib):
     assert lib.w4_attn_decode_workspace_bytes(c, 3, 6, 7) == 0
     assert lib.w4_attn_decode_workspace_bytes(c, -1, 6, 8) == 0
     assert lib.w4_attn_decode_workspace_bytes(cache(head_dim=300), 3, 6, 8) == 0
+
+
+@pytest.mark.parametrize("size", [2 ** 31 - 1, 2 ** 31 - 2 ** 16 + 1])
+def test_sizes_whose_loops_would_pass_2_to_the_31(lib, size):
+    """Kernels count requests, tokens and rows in 32 bits and step past the last by less than 2¹⁶."""
+    assert pages(lib, B=size) == w4.W4_ERR_UNSUPPORTED
+    assert append(lib, T=size, rope=dict(rotary=0)) == w4.W4_ERR_UNSUPPORTED
+    assert attend(lib, B=size, T=0) == w4.W4_ERR_UNSUPPORTED
+    assert attend(lib, c=cache(kv_heads=1), B=1, T=size, q_heads=1) == w4.W4_ERR_UNSUPPORTED
+    assert attend(lib, B=1, T=size // 8 + 1, q_heads=8) == w4.W4_ERR_UNSUPPORTED
