@@ -53,6 +53,9 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kTile = 64;       // tokens of a unit of work
+// Format 8's weights (times value scales) are at most 2⁸ of the reference and enter their products as fp16, below 65504
+// and with 11 bits down to 2⁻¹⁴ only: they are taken 2⁷ times as large, and the outputs back at an item's end.
+constexpr float kLift = 7.f, kLower = 0.0078125f;
 
 // ------------------------------------------------------------- small pieces
 __device__ __forceinline__ void ldmatrix_x4(uint32_t addr, uint32_t (&r)[4]) {
@@ -401,7 +404,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
             for (int x = 0; x < 4; ++x) o[i][x] = 0.f;
         // Format 16: the reference score, unscaled, and the sum of the weights 2^(row_scale · (s − m)).
         // Format 8: the reference of score + log2(value scale), to base 2: the weights times their value scales are
-        // near 1 whatever the scales; the sum is that of the weights by the same reference.
+        // near 2⁷ whatever the scales (the reference is taken 7 lower); the sum is that of the weights by the same
+        // reference, over 2⁷.
         float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 
 #pragma unroll
@@ -495,10 +499,12 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
             grown[0] = quad_max(grown[0]);
             grown[1] = quad_max(grown[1]);
             const float by0 = (grown[0] - m[0]) * (Q8 ? 1.f : row_scale[0]), by1 = (grown[1] - m[1]) * (Q8 ? 1.f : row_scale[1]);
-            if (__any_sync(~0u, by0 > 8.f || by1 > 8.f)) {
+            constexpr float kFar = Q8 ? kLift + 8.f : 8.f;
+            if (__any_sync(~0u, by0 > kFar || by1 > kFar)) {
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    const float keep = m[x] == -INFINITY ? 0.f : ex2(x ? -by1 : -by0);
+                    if (Q8) grown[x] = fmaxf(m[x], grown[x] - kLift);
+                    const float keep = m[x] == -INFINITY ? 0.f : ex2(Q8 ? m[x] - grown[x] : x ? -by1 : -by0);
                     l[x] = fminf(l[x], 3e38f) * keep;
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
@@ -513,13 +519,13 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
                                   m[1] == -INFINITY ? 0.f : m[1] * (Q8 ? 1.f : row_scale[1])};
 #pragma unroll
             for (int y = 0; y < 2 * S::kSub; ++y) {
-                // 1 / value scale of the lane's tokens: a number even where the scale is none, since a hidden token's
-                // weight of 0 makes it 0 then.
+                // 1 / value scale of the lane's tokens, over 2⁷: a number even where the scale is none, since a hidden
+                // token's weight of 0 makes it 0 then.
                 float inv[2] = {1.f, 1.f};
                 if (Q8) {
                     const float4 f = *reinterpret_cast<const float4*>(stage_scales + y * 8 + 2 * t4);
-                    inv[0] = fminf(ex2(-f.y), 3e38f);
-                    inv[1] = fminf(ex2(-f.w), 3e38f);
+                    inv[0] = fminf(ex2(-f.y), 3e38f) * kLower;
+                    inv[1] = fminf(ex2(-f.w), 3e38f) * kLower;
                 }
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
@@ -605,7 +611,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
                         }
                 }
             } else {
-                // Weights times value scales as fp16 (2⁻¹¹): an eighth of the result's rounding.
+                // Weights times value scales as fp16 (2⁻¹¹): an eighth of the result's rounding.  Below 2⁻²¹ of the
+                // reference they err by 2⁻³² of it, which shows only where the tokens above have codes of zero.
 #pragma unroll
                 for (int sub = 0; sub < S::kSub; ++sub) {
                     uint32_t p[4];
@@ -699,8 +706,9 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
             for (int k = 0; k < S::kGroups; ++k) {
                 const float f = ex2(s_stat[k * R * 16 + r] - rm);
                 const float4 w = *reinterpret_cast<const float4*>(s_o + (k * R * 16 + r) * S::kMeetRow + col);
+                const float fv = Q8 ? f * kLower : f;
                 ll += f * s_stat[kWarps * 16 + k * R * 16 + r];
-                v[0] += f * w.x, v[1] += f * w.y, v[2] += f * w.z, v[3] += f * w.w;
+                v[0] += fv * w.x, v[1] += fv * w.y, v[2] += fv * w.z, v[3] += fv * w.w;
             }
             if (whole) {
                 put_row(sp, it, row, col, v, 4, ll);

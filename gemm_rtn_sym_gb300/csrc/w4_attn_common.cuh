@@ -18,7 +18,8 @@ constexpr int kMaxLength = 0x7fff0000;  // token numbers a little past a length 
 constexpr int kMaxDevices = 64;         // as many as the library knows (device_info refuses others)
 constexpr int kMaxCtas = 512;           // bounds the workspace
 // Format 8's value scales from here on (2⁻¹⁰⁰): with smaller ones, and for zero, this one stands in.  It has a
-// logarithm, its inverse can be summed over all tokens that a length can name, and the codes of a zero scale are zero.
+// logarithm, the codes of a zero scale are zero, and its inverse times weights of at most 2⁸ can be summed over 2²⁰
+// tokens of one warp's stream (tokens of larger scales, where there are any, put the reference up).
 constexpr float kLeastScale = 7.888609052210118e-31f;
 
 // The weights' reference and their sum, ROWS of each, then ROWS rows of D values.

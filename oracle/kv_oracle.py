@@ -137,3 +137,33 @@ def attention_bound(out, spread, largest, dim, longest, format=16):
     """
     u = 2.0 ** -24
     return 2.0 ** -8 * np.abs(out) + (2 * (dim + 2) * u * largest + longest * u + (2.0 ** -15 if format == 16 else 2.0 ** -11)) * spread
+
+
+def attention8_floor(q, k, codes, d, table, lens, starts, scale, window=0):
+    """What format 8's weights may add to attention_bound, for codes [pages, page_size, heads, dim] and value scales d
+    [pages, page_size, heads].
+
+    A token's weight times its value scale is one fp16 number in units of (at least 2⁻⁷ of) the largest such product M
+    that its row has met: 11 bits down to 2⁻¹⁴ of the unit, and an error of at most 2⁻²⁵ of it below, 2⁻³² of M.  Each
+    token's codes take that much: 2⁻³² · M · Σ|c|.
+    """
+    T, Hq, D = q.shape
+    P, H = k.shape[1], k.shape[2]
+    G = Hq // H
+    out = np.zeros((T, Hq, D))
+    for b, L in enumerate(lens):
+        n = int(starts[b + 1] - starts[b])
+        used = table[b, :-(-int(L) // P)]
+        kb, db, cb = k[used].reshape(-1, H, D), d[used].reshape(-1, H), np.abs(codes[used]).reshape(-1, H, D)
+        for j in range(n):
+            p = int(L) - n + j
+            if p < 0:
+                continue
+            low = max(0, p - window + 1) if window else 0
+            for h in range(H):
+                row = (starts[b] + j, slice(h * G, (h + 1) * G))
+                s = scale * (q[row] @ kb[low:p + 1, h].T)
+                w = np.exp(s - s.max(-1, keepdims=True))
+                w /= w.sum(-1, keepdims=True)
+                out[row] = 2.0 ** -32 * (w * db[low:p + 1, h]).max(-1, keepdims=True) * cb[low:p + 1, h].sum(0)
+    return out

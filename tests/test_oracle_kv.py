@@ -69,3 +69,14 @@ def test_attention_rows_before_the_first_token_are_zeros():
     q, k, v = rng.normal(size=(3, 2, 4)), rng.normal(size=(2, 4, 1, 4)), rng.normal(size=(2, 4, 1, 4))
     out, _, _ = KO.attention(q, k, v, np.array([[1]]), [2], [0, 3], 0.5)
     assert (out[0] == 0).all() and np.allclose(out[1], v[1, 0, 0])
+
+
+def test_floor_of_format_8_hand_worked():
+    q = np.array([[[1.0, 0.0]], [[1.0, 0.0]]])
+    k = np.array([[[[0.0, 3.0]], [[np.log(3.0), 5.0]]]])
+    codes, d = np.array([[[[2.0, -2.0]], [[6.0, 10.0]]]]), np.array([[[8.0], [4.0]]])
+    # weights 1, and 1/4 and 3/4: products 8, and 2 and 3
+    got = KO.attention8_floor(q, k, codes, d, np.array([[0]]), [2], [0, 2], 1.0)
+    assert np.allclose(got * 2.0 ** 32, [[[16, 16]], [[24, 36]]])
+    last = KO.attention8_floor(q[1:], k, codes, d, np.array([[0]]), [2], [0, 1], 1.0, window=1)
+    assert np.allclose(last * 2.0 ** 32, [[[24, 40]]])
