@@ -349,8 +349,10 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
 #pragma unroll
                 for (int x = 0; x < 4; ++x) q[Q8 ? 0 : ks][x] ^= sp.flip;
         } else {
-            // As fp16, after a division of the row by a power of two near its largest value.
-            float down[2];
+            // As fp16, after a multiplication of the row by a power of two that takes its largest value to 2¹⁴ and more:
+            // values down to 2⁻³¹ of it keep all bits, smaller ones err by 2⁻³⁹ of it (by nothing where the row is below
+            // 2⁻⁹⁵: a bf16 is a multiple of 2⁻¹³³).
+            float to16[2];
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 float most = 0.f;
@@ -360,17 +362,17 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
                     most = fmaxf(most, fmaxf(fmaxf(fabsf(bf16_lo(w.x)), fabsf(bf16_hi(w.x))), fmaxf(fabsf(bf16_lo(w.y)), fabsf(bf16_hi(w.y)))));
                 }
                 most = quad_max(most);
-                const int e = min(max(static_cast<int>(__float_as_uint(most) >> 23), 7), 247) - 127;
-                down[x] = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-                row_scale[x] *= __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+                const int e = min(max(static_cast<int>(__float_as_uint(most) >> 23), 32), 254) - 127;
+                to16[x] = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
+                row_scale[x] *= __uint_as_float(static_cast<uint32_t>(127 - 14 + e) << 23);
             }
             if (group == 0)  // the other groups have the same rows
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks) {
                     const uint2 u = raw[0][Q8 ? ks : 0], w = raw[Q8 ? 1 : 0][Q8 ? ks : 0];
                     queries[(rw * KS + ks) * 32 + lane] =
-                        make_uint4(pack_f16(bf16_lo(u.x) * down[0], bf16_hi(u.x) * down[0]) ^ sp.flip, pack_f16(bf16_lo(w.x) * down[1], bf16_hi(w.x) * down[1]) ^ sp.flip,
-                                   pack_f16(bf16_lo(u.y) * down[0], bf16_hi(u.y) * down[0]) ^ sp.flip, pack_f16(bf16_lo(w.y) * down[1], bf16_hi(w.y) * down[1]) ^ sp.flip);
+                        make_uint4(pack_f16(bf16_lo(u.x) * to16[0], bf16_hi(u.x) * to16[0]) ^ sp.flip, pack_f16(bf16_lo(w.x) * to16[1], bf16_hi(w.x) * to16[1]) ^ sp.flip,
+                                   pack_f16(bf16_lo(u.y) * to16[0], bf16_hi(u.y) * to16[0]) ^ sp.flip, pack_f16(bf16_lo(w.y) * to16[1], bf16_hi(w.y) * to16[1]) ^ sp.flip);
                 }
             __syncthreads();
         }

@@ -520,8 +520,8 @@ int w4_kv_append(const w4_kv_cache* cache, const w4_rope* rope, int64_t T, int32
  * scores, maxima, sums and products in fp32, rounded once to bf16; a weight
  * enters its products with 16 bits.  In format 8 a weight times its value scale
  * may enter with 11 bits, and with an error of 2⁻³² of the row's largest such
- * product where that is more.  A row that
- * sees no token (p < 0) is zeros.  What the masked and unused places of the
+ * product where that is more, and a query value with an error of 2⁻³⁹ of its
+ * row's largest.  A row that sees no token (p < 0) is zeros.  What the masked and unused places of the
  * cache hold, NaN and infinities included, changes nothing.  Rows past
  * starts[B] are not written.
  * Out of range: a length past width · page_size (or 2³¹ − 2¹⁶) counts as that; starts that

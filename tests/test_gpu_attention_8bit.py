@@ -1,4 +1,5 @@
-"""w4_attn_decode over a cache in 8 bits, where its fp16 operands are short of range: weights far below the largest."""
+"""w4_attn_decode over a cache in 8 bits, where its fp16 operands are short of range: weights and query values far below
+the largest."""
 import numpy as np
 import pytest
 import torch
@@ -20,7 +21,10 @@ def check(case, out, scale, window=0):
     d = values(case.v_scales.transpose(1, 2))
     codes = case.v.cpu().numpy().astype(np.float64)
     floor = KO.attention8_floor(*args[:2], codes, np.where(np.isfinite(d), d, 0.0), *args[3:])
-    bound = KO.attention_bound(ref, spread, largest, case.q.shape[2], max(case.lens), 8) + floor
+    # a query value errs by 2⁻³⁹ of its row's largest, which moves weights by twice that times the keys' sum
+    keys = np.where(np.isfinite(case.kv), np.abs(case.kv), 0.0).sum(-1).max()
+    moved = 2 * abs(scale) * 2.0 ** -39 * np.abs(args[0]).max(-1, keepdims=True) * keys
+    bound = KO.attention_bound(ref, spread, largest, case.q.shape[2], max(case.lens), 8) + floor + moved * spread
     got = values(out)
     assert np.isfinite(got).all()
     worst = (np.abs(got - ref) / np.maximum(bound, 1e-300)).max()
@@ -58,3 +62,25 @@ def test_sharp_scores_with_any_codes(cuda_lib, scale, std, n):
     """One token outweighs the others by far; columns where its code is zero are left to weights that may underflow."""
     case = AttentionCase([50, 300, 777], [n] * 3, 8, 2, 128, 16, format=8, seed=21, std=std)
     check(case, case.run(w4, scale=scale), scale)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("exponent", [10, 20, 24])
+def test_queries_with_one_large_value(cuda_lib, D, exponent):
+    """A query value that meets keys of zero, next to others 2^exponent times smaller that make the scores."""
+    case = AttentionCase([300, 17], [1, 2], 8, 2, D, 16, format=8, seed=exponent)
+    case.q[..., 3] = 2.0 ** exponent
+    case.k[..., 3] = 0
+    case.kv[..., 3] = 0
+    check(case, case.run(w4), D ** -0.5)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("exponent", [100, -100, -118])
+def test_large_and_small_queries(cuda_lib, D, exponent):
+    """Queries times 2^exponent on keys times 2^-exponent: the same scores."""
+    case = AttentionCase([300, 17], [1, 2], 8, 2, D, 16, format=8, seed=-exponent if exponent < 0 else exponent)
+    case.q *= 2.0 ** exponent
+    case.k_scales *= 2.0 ** -exponent
+    case.kv *= 2.0 ** -exponent
+    check(case, case.run(w4), D ** -0.5)
