@@ -530,23 +530,50 @@ namespace {
 // tile of rows).
 constexpr int64_t kMostCounted = 0x7fff0000;
 
-// Memory of strided rows: `bytes` in all; where period > 0, rows of `inner`
-// bytes (at most period) that repeat every `period` bytes.
+// Memory of strided rows: `bytes` in all.  Level 0, the outermost, has count[0]
+// blocks of inner[0] ≤ stride[0] bytes, stride[0] bytes apart; level 1 says the
+// same of each such block, and so on.  A block of the last level is solid.
 struct Region {
     const void* p = nullptr;
-    size_t bytes = 0, period = 0, inner = 0;
+    int64_t bytes = 0;
+    int levels = 0;
+    int64_t count[3] = {}, stride[3] = {}, inner[3] = {};
 };
 
-Region plain(const void* p, size_t bytes) { return {p, p ? bytes : 0, 0, 0}; }
+Region plain(const void* p, size_t bytes) {
+    Region r;
+    r.p = p;
+    r.bytes = p ? static_cast<int64_t>(std::min(bytes, size_t{1} << 62)) : 0;
+    return r;
+}
 
-// Whether two regions share a byte.  Regions of one period (slices of a fused
-// projection's output, keys and values side by side in one page) may interleave.
+// Whether a block of `a` (of `a_bytes`, of level la on) and one of `b` that
+// starts `off` bytes after it share a byte.  Blocks that repeat at one stride
+// (slices of a fused projection's output, keys and values side by side in a
+// page, a token or a row) may interleave; blocks wider than the stride of what
+// they lie among count as meeting it.
+bool blocks_meet(const Region& a, int la, int64_t a_bytes, const Region& b, int lb, int64_t b_bytes, int64_t off) {
+    if (off >= a_bytes || -off >= b_bytes) return false;
+    const int64_t sa = la < a.levels ? a.stride[la] : 0, sb = lb < b.levels ? b.stride[lb] : 0, s = std::max(sa, sb);
+    if (s == 0) return true;
+    const bool in_a = sa == s, in_b = sb == s;
+    const int64_t na = in_a ? a.count[la] : 1, nb = in_b ? b.count[lb] : 1;
+    const int64_t ea = in_a ? a.inner[la] : a_bytes, eb = in_b ? b.inner[lb] : b_bytes;
+    if (ea > s || eb > s) return true;
+    // Block j of b lies off + (j − i)·s after block i of a: only the two k = j − i around −off / s can meet.
+    const int64_t at = (off % s + s) % s;
+    for (const int64_t d : {at, at - s}) {
+        const int64_t k = (d - off) / s;
+        if (k > -na && k < nb && blocks_meet(a, la + in_a, ea, b, lb + in_b, eb, d)) return true;
+    }
+    return false;
+}
+
+// Whether two regions share a byte.
 bool meets(const Region& a, const Region& b) {
-    if (!overlaps(a.p, a.bytes, b.p, b.bytes)) return false;
-    if (a.period == 0 || a.period != b.period) return true;
-    const size_t T = a.period;
-    const size_t at = (reinterpret_cast<uintptr_t>(b.p) % T + T - reinterpret_cast<uintptr_t>(a.p) % T) % T;
-    return at < a.inner || at + b.inner > T;
+    if (!overlaps(a.p, static_cast<size_t>(a.bytes), b.p, static_cast<size_t>(b.bytes))) return false;
+    const uintptr_t off = reinterpret_cast<uintptr_t>(b.p) - reinterpret_cast<uintptr_t>(a.p);
+    return blocks_meet(a, 0, a.bytes, b, 0, b.bytes, static_cast<int64_t>(off));
 }
 
 struct Dim {
@@ -559,18 +586,23 @@ struct Dim {
 // not start on 16 bytes.
 int strided(const void* p, Dim* dims, int count, int64_t row, int64_t size, Region* out) {
     std::sort(dims, dims + count, [](const Dim& a, const Dim& b) { return a.stride < b.stride; });
-    int64_t extent = row, inner = 0, period = 0;
+    Region r;
+    int64_t extent = row;
     for (int i = 0; i < count; ++i) {
         const Dim& d = dims[i];
         if (d.n <= 1) continue;
         if (d.stride < extent || d.stride > ((int64_t{1} << 59) - extent) / (d.n - 1)) return W4_ERR_INVALID_ARG;
         if (d.stride * size % 16 != 0) return W4_ERR_MISALIGNED;
-        inner = extent;
-        period = d.stride;
+        for (int l = r.levels++; l > 0; --l) r.count[l] = r.count[l - 1], r.stride[l] = r.stride[l - 1], r.inner[l] = r.inner[l - 1];
+        r.count[0] = d.n;
+        r.stride[0] = d.stride * size;
+        r.inner[0] = extent * size;
         extent += (d.n - 1) * d.stride;
     }
     if (!aligned(p, 16)) return W4_ERR_MISALIGNED;
-    *out = {p, static_cast<size_t>(extent * size), static_cast<size_t>(period * size), static_cast<size_t>(inner * size)};
+    r.p = p;
+    r.bytes = extent * size;
+    *out = r;
     return W4_OK;
 }
 

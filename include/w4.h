@@ -385,7 +385,8 @@ int w4_gemm_grouped_noalloc(int32_t count, const w4_gemm_problem* problems, void
  *              page_size]; the row stands for d·c, d ≥ 0.  w4_attn_decode
  *              may take value scales below 2⁻¹⁰⁰ as 2⁻¹⁰⁰.
  * head_dim: a multiple of 16, at most 256.  k and v 16-byte aligned, strides
- * multiples of 16 bytes, rows apart from each other; scales 2-byte aligned.
+ * multiples of 16 bytes, rows apart from each other (keys and values may lie
+ * side by side in a page, a token or a row); scales 2-byte aligned.
  * Requests, new tokens (w4_kv_append) and query rows (T · q_heads): at most
  * 2³¹ − 2¹⁶.
  *

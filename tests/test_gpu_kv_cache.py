@@ -332,3 +332,26 @@ def test_binding_refusals(cuda_lib):
     same = gpu([1])
     with pytest.raises(w4.W4Error):
         w4.w4_kv_pages(same, gpu([3]), gpu([[0]]), gpu([2, 3]), gpu([0, 2], torch.int64), 16, 2, new_lens=same)
+
+
+@pytest.mark.parametrize("where", ["token", "head", "page of heads"])
+@pytest.mark.parametrize("format", [16, 8])
+def test_append_and_attend_with_keys_and_values_side_by_side(cuda_lib, where, format):
+    """One pool whose keys and values interleave below the page: in each token, in each row, or by head in each page."""
+    case = AppendCase(33, 8, 2, 128, 64, (10, 11, 11), format=format, seed=3)
+    shape = {"token": (case.pages, 16, 2, 2, 128), "head": (case.pages, 16, 2, 256),
+             "page of heads": (case.pages, 2, 2, 16, 128)}[where]
+    both = torch.zeros(shape, dtype=case.k_cache.dtype, device=DEV)
+    if where == "token":
+        case.k_cache, case.v_cache = both[:, :, 0], both[:, :, 1]
+    elif where == "head":
+        case.k_cache, case.v_cache = both[..., :128], both[..., 128:]
+    else:
+        case.k_cache, case.v_cache = both[:, 0].transpose(1, 2), both[:, 1].transpose(1, 2)
+    case.before = [values(case.k_cache), values(case.v_cache)]
+    case.check(case.run())
+    lens, table = gpu([20, 13]), gpu([[0, 1], [2, 3]])
+    q, scales = case.q[:2].to(DEV), dict(k_scales=case.k_scales, v_scales=case.v_scales)
+    apart = w4.w4_attn_decode(q, case.k_cache.contiguous(), case.v_cache.contiguous(), table, lens, **scales)
+    out = w4.w4_attn_decode(q, case.k_cache, case.v_cache, table, lens, **scales)
+    assert torch.equal(out.view(torch.int16), apart.view(torch.int16)) and w4.w4_last_device_status() == 0

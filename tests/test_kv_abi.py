@@ -1,8 +1,10 @@
 """Refusals of the paged key-value cache's entry points: each is made on the host, before any launch (the addresses are
 never read)."""
 import os
+import random
 
 import pytest
+import torch
 
 import gemm_rtn_sym_gb300 as w4
 from gemm_rtn_sym_gb300 import build as b
@@ -136,3 +138,96 @@ def test_sizes_whose_loops_would_pass_2_to_the_31(lib, size):
     assert attend(lib, B=size, T=0) == w4.W4_ERR_UNSUPPORTED
     assert attend(lib, c=cache(kv_heads=1), B=1, T=size, q_heads=1) == w4.W4_ERR_UNSUPPORTED
     assert attend(lib, B=1, T=size // 8 + 1, q_heads=8) == w4.W4_ERR_UNSUPPORTED
+
+
+# ---- keys and values (and the rows of a projection) side by side in one piece of memory: places that share no byte
+#      pass, and those that do are refused.  Units: elements of bf16, 2 heads of 128.
+SIDE_BY_SIDE = {  # strides of page, token, head; where the values start
+    "page": (8192, 256, 128, 4096),         # [pages, 2, 16, heads, dim]
+    "token": (8192, 512, 128, 256),         # [pages, 16, 2, heads, dim]
+    "head": (8192, 512, 256, 128),          # [pages, 16, heads, 2, dim]
+    "head, page of heads": (8192, 256, 4096, 128),  # [pages, heads, 16, 2, dim]
+    "page of heads": (8192, 128, 4096, 2048),       # [pages, heads, 2, 16, dim]
+    "pool": (4096, 256, 128, 4 * 4096),     # [2, pages, 16, heads, dim]
+}
+
+
+def side_by_side(where, shift=0):
+    page, token, head, v = SIDE_BY_SIDE[where]
+    return cache(k=A, v=A + 2 * (v + shift), page_stride=page, token_stride=token, head_stride=head)
+
+
+def far_rows(i, token_stride=1024, head_stride=128):
+    return rows(0x1000000 + i * 0x10000, token_stride, head_stride)
+
+
+def append_far(lib, c, **kw):
+    a = dict(q=far_rows(0), out=far_rows(1), k=far_rows(2), v=far_rows(3), slots=0x1000000 + 20 * A,
+             rope=dict(positions=0x1000000 + 11 * A, cos=0x1000000 + 12 * A, sin=0x1000000 + 13 * A))
+    return append(lib, c=c, **{**a, **kw})
+
+
+needs_no_gpu = pytest.mark.skipif(torch.cuda.is_available(), reason="the addresses are not memory: only without a device")
+
+
+@needs_no_gpu
+@pytest.mark.parametrize("where", SIDE_BY_SIDE)
+def test_keys_and_values_side_by_side_pass(lib, where):
+    assert append_far(lib, side_by_side(where)) == w4.W4_ERR_CUDA  # (no device here)
+
+
+@pytest.mark.parametrize("shift", [-120, -8, 8, 120])
+@pytest.mark.parametrize("where", [w for w in SIDE_BY_SIDE if w != "pool"])
+def test_keys_and_values_that_share_bytes_are_refused(lib, where, shift):
+    assert append_far(lib, side_by_side(where, shift)) == w4.W4_ERR_INVALID_ARG
+
+
+@needs_no_gpu
+def test_rows_of_a_projection_with_the_heads_side_by_side_pass(lib):
+    """[T, heads, 3, dim]: query, key and value of each head in turn, the queries turned in place."""
+    q, k, v = (rows(0x1000000 + 2 * 128 * i, 2 * 384, 384) for i in range(3))
+    assert append_far(lib, cache(), q_heads=2, q=q, out=q, k=k, v=v) == w4.W4_ERR_CUDA
+
+
+def test_rows_of_a_projection_that_share_bytes_are_refused(lib):
+    q, k, v = (rows(0x1000000 + 2 * 128 * i, 2 * 384, 384) for i in range(3))
+    assert append_far(lib, cache(), q_heads=2, q=q, out=k, k=k, v=v) == w4.W4_ERR_INVALID_ARG
+    k = rows(0x1000000 + 2 * 120, 2 * 384, 384)
+    assert append_far(lib, cache(), q_heads=2, q=q, out=q, k=k, v=v) == w4.W4_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_rows_meet_where_they_share_a_byte(lib, seed):
+    """Against a count of the bytes: queries out over keys, at any offset and with any nested strides."""
+    r = random.Random(seed)
+    for _ in range(50):
+        T, Hq = r.randint(1, 4), 2 * r.randint(1, 3)
+        dim, kind = 16, r.random()
+        inner = r.choice([16, 32, 48, 64])
+        def strides(heads):
+            if r.random() < 0.5:
+                return (inner * heads + 16 * r.randint(0, 4), inner)
+            return (inner, inner * T + 16 * r.randint(0, 4))
+        so, sk = strides(Hq), strides(2)
+        if kind < 0.5:
+            sk = so
+        at = 8 * r.randint(-60, 60)
+        c = cache(head_dim=dim, page_stride=4096, token_stride=256, head_stride=128)
+        out, k = rows(0x4000000, *so), rows(0x4000000 + 2 * at, *sk)
+
+        def taken(base, s, heads):
+            return {base + t * s[0] + h * s[1] + i for t in range(T) for h in range(heads) for i in range(dim)}
+        nested = all(s[0] >= (heads - 1) * s[1] + dim if s[0] >= s[1] else s[1] >= (T - 1) * s[0] + dim or heads == 1
+                     for s, heads in ((so, Hq), (sk, 2)))
+        share = bool(taken(0, so, Hq) & taken(at, sk, 2))
+        if not nested or (not share and torch.cuda.is_available()):
+            continue
+        rope = dict(rotary=0)
+        got = append(lib, c=c, rope=rope, T=T, q_heads=Hq, q=rows(0x6000000, 4096, 64), out=out, k=k, v=far_rows(3),
+                     slots=0x1000000 + 20 * A)
+        if share:
+            assert got == w4.W4_ERR_INVALID_ARG
+        elif so == sk:
+            assert got == w4.W4_ERR_CUDA
+        else:  # strides that differ may be refused without need
+            assert got in (w4.W4_ERR_CUDA, w4.W4_ERR_INVALID_ARG)
