@@ -43,6 +43,9 @@ __device__ __forceinline__ int last_at_most(const long long* v, int n, long long
     return lo;
 }
 
+// A sum of new tokens as the int32 of `starts`: those past 2³¹ − 1 have no rows, and must not come out as rows of others.
+__device__ __forceinline__ int row_number(long long sum) { return static_cast<int>(min(sum, 0x7fffffffll)); }
+
 // Every CTA scans all requests' sums, one per thread at a time, and writes
 // every gridDim.x-th block of tokens and of returned pages; CTA 0 writes what
 // there is one of for each request.  Reading the lengths again in every CTA
@@ -109,7 +112,7 @@ __global__ void __launch_bounds__(kPagesThreads) kv_pages_kernel(KvPagesArgs a) 
         s_want[tid] = want;
         if (blockIdx.x == 0) {
             if (tid < n) {
-                a.starts[base + tid] = static_cast<int>(sum.grow - own.grow);
+                a.starts[base + tid] = row_number(sum.grow - own.grow);
                 a.new_lens[base + tid] = granted ? target : len;
             }
             // The sums grow, so the last granted request's sum is the most that is used.
@@ -158,7 +161,7 @@ __global__ void __launch_bounds__(kPagesThreads) kv_pages_kernel(KvPagesArgs a) 
         a.positions[t] = 0;
     }
     if (blockIdx.x == 0 && tid == 0) {
-        a.starts[a.B] = static_cast<int>(carry.grow);
+        a.starts[a.B] = row_number(carry.grow);
         a.range_out[0] = head + used;
         a.range_out[1] = tail + carry.back;
     }

@@ -431,6 +431,7 @@ typedef struct w4_rows {
  *   T              in : rows of slots and positions (all requests' new tokens)
  *   new_lens       out: int32 [B]
  *   starts         out: int32 [B + 1], a request's first row among the tokens
+ *                       (2³¹ − 1 where it is past that)
  *   slots          out: int64 [T], −1: no slot (not granted, or past the last
  *                       new token)
  *   positions      out: int32 [T] (0 past the last new token)

@@ -355,3 +355,15 @@ def test_append_and_attend_with_keys_and_values_side_by_side(cuda_lib, where, fo
     apart = w4.w4_attn_decode(q, case.k_cache.contiguous(), case.v_cache.contiguous(), table, lens, **scales)
     out = w4.w4_attn_decode(q, case.k_cache, case.v_cache, table, lens, **scales)
     assert torch.equal(out.view(torch.int16), apart.view(torch.int16)) and w4.w4_last_device_status() == 0
+
+
+def test_targets_whose_tokens_pass_2_to_the_31(cuda_lib):
+    """Targets far out of range: the requests behind them start past every row, not at rows that others have."""
+    lens, target = [0, 0, 0, 0], [4, 2 ** 31 - 1, 2 ** 31 - 1, 5]
+    new_lens, starts, slots, positions, left = w4.w4_kv_pages(gpu(lens), gpu(target), gpu(np.full((4, 3), -1)),
+                                                              gpu(np.arange(9)), gpu([0, 9], torch.int64), 16, 9)
+    torch.cuda.synchronize()
+    assert w4.w4_last_device_status() == w4.W4_ERR_INVALID_ARG
+    assert starts.tolist() == [0, 4] + [2 ** 31 - 1] * 3
+    assert new_lens.tolist() == [4, 0, 0, 0] and left.tolist() == [1, 9]
+    assert slots.tolist() == [0, 1, 2, 3] + [-1] * 5 and positions.tolist() == [0, 1, 2, 3, 0, 1, 2, 3, 4]
