@@ -44,12 +44,16 @@ class AttentionBlock:
         self.sections = sections
         rotary = 2 * sum(sections)
         frequency = 1e6 ** (-torch.arange(rotary // 2, dtype=torch.float64, device=device) * 2 / rotary)
-        angle = torch.arange(longest, dtype=torch.float64, device=device)[:, None] * frequency
+        # A row for every position that the table's pages hold: a request may fill its last page.
+        held = self.table.shape[1] * page_size
+        angle = torch.arange(held, dtype=torch.float64, device=device)[:, None] * frequency
         self.cos, self.sin = angle.cos().float(), angle.sin().float()
 
     def step(self, x: torch.Tensor, target: torch.Tensor) -> torch.Tensor:
         """x bf16 [new tokens, hidden], request after request; target int32 [requests].  Returns bf16 [new tokens,
-        hidden].  Requests may also shrink (rejected drafts) or end (target 0); those have no rows in x."""
+        hidden].  Requests may also shrink (rejected drafts) or end (target 0); those have no rows in x.  A request whose
+        pages the pool does not have keeps its length (self.lens then differs from target), and its rows of the result
+        mean nothing."""
         T = x.shape[0]
         self.lens, starts, slots, positions, self.free_range = w4_kv_pages(
             self.lens, target, self.table, self.free_pages, self.free_range, self.page_size, T)

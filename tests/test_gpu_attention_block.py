@@ -80,3 +80,21 @@ def dequantised(packed, scales):
 def test_command(cuda_lib):
     assert attention_block.main(["--requests", "4", "--drafts", "3", "--steps", "2"]) == 0
     assert attention_block.main(["--requests", "3", "--drafts", "12", "--steps", "1", "--format", "8"]) == 0
+
+
+def test_a_request_fills_its_last_page(cuda_lib):
+    """`longest` need not be a multiple of the page: every position that the pages hold has its cosines and sines."""
+    block = attention_block.AttentionBlock(512, 8, 2, 128, 60, 16, 2, 300, seed=3)
+    block.step(wl.random_bf16((303, 512), 1.0, seed=1, device=DEV), gpu([303, 0]))
+    x = wl.random_bf16((1, 512), 1.0, seed=2, device=DEV)
+    block.step(x, gpu([304, 0]))
+    torch.cuda.synchronize()
+    assert w4.w4_last_device_status() == 0 and block.lens.tolist() == [304, 0]
+    # the key of position 303, turned by its angles
+    key = values(w4.w4_gemm(x, *block.qkv))[:, 8 * 128:10 * 128].reshape(1, 2, 128)
+    frequency = 1e6 ** (-np.arange(64) * 2 / 128)
+    angle = np.arange(304)[:, None] * frequency
+    turned = KO.rotate(key, np.full((3, 1), 303), np.cos(angle), np.sin(angle), block.sections)[0]
+    got = values(block.k)[int(block.table[0, 18]), 303 % 16]
+    # one rounding to bf16, and the fp32 angles' cosines and sines (2⁻²⁴ of each) and products
+    assert (np.abs(got - turned) <= 2.0 ** -8 * np.abs(turned) + 2.0 ** -21 * np.abs(key).max()).all()
