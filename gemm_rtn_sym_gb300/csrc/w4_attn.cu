@@ -812,8 +812,9 @@ cudaError_t run_dim(const SplitArgs& sp, const DeviceInfo& dev, cudaStream_t str
 size_t attn_decode_workspace_bytes(int32_t B, int64_t T, int32_t q_heads, int32_t kv_heads, int32_t head_dim, bool q8) {
     const int G = q_heads / kv_heads, D = dim_of(head_dim);
     if (B <= 0) B = 1;
-    const size_t part = many_rows(B, T, G, kv_heads, D, q8) ? attn_tc_partial_floats(head_dim) : partial_floats(16 * row_warps(B, T, G, q8), D);
-    return 2 * kMaxCtas * (sizeof(unsigned long long) + part * sizeof(float));
+    const bool many = many_rows(B, T, G, kv_heads, D, q8);
+    const size_t part = many ? attn_tc_partial_floats(head_dim) : partial_floats(16 * row_warps(B, T, G, q8), D);
+    return 2 * (kMaxCtas * sizeof(unsigned long long) + (many ? kMaxTcCtas : kMaxCtas) * part * sizeof(float));
 }
 
 cudaError_t launch_attn_decode(AttnArgs a, bool q8, void* workspace, const DeviceInfo& dev, cudaStream_t stream) {

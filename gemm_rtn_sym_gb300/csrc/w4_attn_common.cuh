@@ -16,7 +16,8 @@ namespace w4 {
 constexpr int kJoinGroup = 16;          // parts of an item that are joined at once
 constexpr int kMaxLength = 0x7fff0000;  // token numbers a little past a length stay below 2³¹
 constexpr int kMaxDevices = 64;         // as many as the library knows (device_info refuses others)
-constexpr int kMaxCtas = 512;           // bounds the workspace
+constexpr int kMaxCtas = 512;           // bounds the workspace,
+constexpr int kMaxTcCtas = 160;         // and that of the tensor-core kernel, which has one CTA on an SM (of 152)
 // Format 8's value scales from here on (2⁻¹⁰⁰): with smaller ones, and for zero, this one stands in.  It has a
 // logarithm, the codes of a zero scale are zero, and its inverse times weights of at most 2⁸ can be summed over 2²⁰
 // tokens of one warp's stream (tokens of larger scales, where there are any, put the reference up).
@@ -28,7 +29,7 @@ __host__ __device__ constexpr size_t partial_floats(int rows, int D) { return st
 struct SplitArgs {
     AttnArgs a;
     unsigned long long* arrived;  // [2][kMaxCtas] parts there of a group, groups there of an item
-    float* partial;               // [kMaxCtas][2][partial_floats]
+    float* partial;               // [kMaxCtas or kMaxTcCtas][2][partial_floats]
     int G;                        // query heads per key-value head
     uint32_t G_mul;               // divide_by(G)
     int G_shift;

@@ -707,7 +707,7 @@ cudaError_t launch_attn_tc(const SplitArgs& sp, bool q8, const DeviceInfo& dev, 
     // At least as many units as the batch can have: a CTA for each, where they are few.
     const double reach = std::min(static_cast<double>(a.width) * a.page_size, a.window > 0 ? static_cast<double>(a.window) + a.T : 1e18);
     const double most = static_cast<double>(a.kv_heads) * (a.B + static_cast<double>(a.T) * sp.G / kRows) * (reach / tile + 2 + kFixed);
-    const int grid = static_cast<int>(std::min<double>(std::min(dev.sm_count, kMaxCtas), most));
+    const int grid = static_cast<int>(std::min<double>(std::min(dev.sm_count, kMaxTcCtas), most));
     if (a.head_dim <= 64) return q8 ? run<64, true>(sp, grid, stream) : run<64, false>(sp, grid, stream);
     if (a.head_dim <= 128) return q8 ? run<128, true>(sp, grid, stream) : run<128, false>(sp, grid, stream);
     return q8 ? run<256, true>(sp, grid, stream) : run<256, false>(sp, grid, stream);

@@ -231,3 +231,12 @@ def test_rows_meet_where_they_share_a_byte(lib, seed):
             assert got == w4.W4_ERR_CUDA
         else:  # strides that differ may be refused without need
             assert got in (w4.W4_ERR_CUDA, w4.W4_ERR_INVALID_ARG)
+
+
+@pytest.mark.parametrize("format", [16, 8])
+@pytest.mark.parametrize("head_dim,D", [(64, 64), (128, 128), (256, 256), (16, 64), (80, 128), (192, 256)])
+def test_workspace_of_many_rows(lib, head_dim, D, format):
+    """208 rows to each of 8 heads: parts of 128 rows, two for each CTA of a grid of one on an SM (152 of them)."""
+    size = lib.w4_attn_decode_workspace_bytes(cache(kv_heads=8, head_dim=head_dim, format=format), 16, 208, 128)
+    parts = 2 * 152 * 128 * (2 + D) * 4
+    assert parts <= size <= 1.1 * parts
