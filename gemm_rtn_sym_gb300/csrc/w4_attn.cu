@@ -28,7 +28,7 @@
 //
 // One request of 131071 tokens, 64 query and 8 key-value heads of 128: 100 µs
 // (5.4 TB/s); 64 requests of up to 16384, 40 heads: 114 µs (5.6), in 8 bits
-// 74 µs (4.4: bound by decoding); 96 requests that see 1024 tokens, 16 and 4
+// 75 µs (4.4: bound by decoding, for 16 rows of which 5 exist); 96 requests that see 1024 tokens, 16 and 4
 // heads of 256: 43 µs (3.4: half of it starts and ends of items).
 #include <algorithm>
 #include <atomic>

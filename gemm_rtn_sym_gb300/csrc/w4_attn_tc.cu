@@ -561,8 +561,9 @@ __global__ void __launch_bounds__(Shape<D, Q8>::kThreads, 1) attn_tc_kernel(cons
                                 p0 = see0 ? p0 * f.x : 0.f;
                                 p1 = see1 ? p1 * f.y : 0.f;
                             }
-                            // Upper halves cut off, not rounded: the lower ones take what is left, to 16 bits in all
-                            // (roundings to bf16 would share the exponentials' slow pipe).
+                            // Both halves cut off, not rounded (roundings to bf16 would share the exponentials' slow
+                            // pipe): the lower ones take what the upper ones leave, to 16 bits in all, at most 2⁻¹⁵ and
+                            // on the average 2⁻¹⁷ of the weight too low.
                             const uint32_t u0 = __float_as_uint(p0), u1 = __float_as_uint(p1);
                             w[x >> 1] = __byte_perm(u0, u1, 0x7632);
                             w[16 + (x >> 1)] = __byte_perm(__float_as_uint(p0 - __uint_as_float(u0 & 0xFFFF0000u)),

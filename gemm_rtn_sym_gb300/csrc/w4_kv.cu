@@ -190,7 +190,8 @@ __device__ __forceinline__ uint32_t turn_pair(uint32_t x, uint32_t y, float2 c, 
 // shared memory, and turn and write the rows.  blockIdx.y shares a token's rows
 // among CTAs where there are few tokens.  Bound by reading and writing each row
 // once: 16001 tokens, 40 query and 8 key-value heads of 128, in 79 µs (5.9 TB/s,
-// 0.89 of a copy's rate); one token in 2.6 µs.
+// 0.89 of a copy's rate); one token in 2.6 µs.  Into a cache in 8 bits, whose rows' maxima and divisions come on top: 104
+// and 3.2 µs (bytes 65).
 template <int THREADS, int LPR, bool Q8>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS) kv_append_kernel(const __grid_constant__ KvAppendArgs a,
                                                                            const __grid_constant__ Axes axes) {

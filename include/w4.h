@@ -497,7 +497,7 @@ typedef struct w4_rope {
  * d = bf16_rne(fp32(max|x| / 127)) over the (rotated, bf16) row, c =
  * clamp(round_half_even(fp32(x / d)), −128, 127), c = 0 where d = 0; a row
  * with an infinity or NaN is stored as c = 0 with d = NaN.
- * Two tokens with one slot leave either's row, not a defined one.  Out of
+ * Two tokens with one slot leave any mixture of their rows there.  Out of
  * range: a slot outside [−1, pages · page_size) is not stored; a position
  * outside [0, rows) turns as position 0.
  */
@@ -524,7 +524,8 @@ int w4_kv_append(const w4_kv_cache* cache, const w4_rope* rope, int64_t T, int32
  * may enter with 11 bits, and with an error of 2⁻³² of the row's largest such
  * product where that is more, and a query value with an error of 2⁻³⁹ of its
  * row's largest.  A row that sees no token (p < 0) is zeros.  What the masked and unused places of the
- * cache hold, NaN and infinities included, changes nothing.  Rows past
+ * cache hold, NaN and infinities included, changes nothing; an infinite value
+ * that a row sees may leave NaN in its column (format 8: in the row).  Rows past
  * starts[B] are not written.
  * Out of range: a length past width · page_size (or 2³¹ − 2¹⁶) counts as that; starts that
  * fall or pass T are cut; a page id outside [0, pages) reads as rows of zeros.
