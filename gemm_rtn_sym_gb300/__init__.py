@@ -25,6 +25,8 @@ __all__ = [
     "w4_status_string", "W4_PATH_AUTO", "W4_PATH_SMALL_M", "W4_PATH_TENSOR", "GROUP",
     "GroupedPlan", "w4_grouped_plan", "w4_gemm_grouped", "w4_gemm_grouped_noalloc",
     "w4_kv_pages", "w4_kv_append", "w4_attn_decode", "w4_attn_decode_workspace_bytes",
+    "w4_kv_append_norm", "w4_kv_fork", "w4_kv_copy", "w4_kv_compact",
+    "w4_attn_decode_shared", "w4_attn_decode_shared_workspace_bytes",
 ]
 
 GROUP = 128
@@ -97,7 +99,25 @@ class _Rope(ctypes.Structure):
                 ("rotary", _i32), ("axes", _i32), ("sections", _i32 * 4), ("cycled", _i32), ("paired", _i32)]
 
 
+class _Norm(ctypes.Structure):
+    """w4_norm of include/w4.h."""
+    _fields_ = [("q_weight", _vp), ("k_weight", _vp), ("format", _i32), ("eps", ctypes.c_float), ("unit_offset", _i32)]
+
+
 _SIGNATURES.update({
+    "w4_kv_pages_held": (ctypes.c_int, [_vp, _vp, _i32, _i32, _vp, _i64, _vp, _vp, _i64, _i32, _i64, _vp, _vp, _vp, _vp,
+                                        _vp, _vp, _vp]),
+    "w4_kv_fork": (ctypes.c_int, [_vp, _vp, _vp, _i32, _i32, _vp, _i64, _i32, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _vp]),
+    "w4_kv_compact": (ctypes.c_int, [_vp, _i32, _i32, _vp, _i64, _i32, _vp, _i64, _vp, _vp, _i64, _vp, _vp, _vp, _vp,
+                                     _vp]),
+    "w4_kv_copy": (ctypes.c_int, [ctypes.POINTER(_KvCache), _vp, _i32, _vp]),
+    "w4_kv_append_norm": (ctypes.c_int, [ctypes.POINTER(_KvCache), ctypes.POINTER(_Rope), ctypes.POINTER(_Norm), _i64,
+                                         _i32, ctypes.POINTER(_Rows), ctypes.POINTER(_Rows), ctypes.POINTER(_Rows),
+                                         ctypes.POINTER(_Rows), _vp, _vp]),
+    "w4_attn_decode_shared_workspace_bytes": (_sz, [ctypes.POINTER(_KvCache), _i32, _i64, _i32, _i32]),
+    "w4_attn_decode_shared": (ctypes.c_int, [ctypes.POINTER(_KvCache), _i32, _i64, _i32, ctypes.POINTER(_Rows),
+                                             ctypes.POINTER(_Rows), _vp, _i64, _i32, _vp, _vp, _i32, _vp, _vp, _i64,
+                                             _i32, _vp, ctypes.c_float, _vp, _sz, _vp]),
     "w4_kv_pages": (ctypes.c_int, [_vp, _vp, _i32, _i32, _vp, _i64, _vp, _vp, _i64, _i32, _i64, _vp, _vp, _vp, _vp,
                                    _vp, _vp]),
     "w4_kv_append": (ctypes.c_int, [ctypes.POINTER(_KvCache), ctypes.POINTER(_Rope), _i64, _i32, ctypes.POINTER(_Rows),
@@ -572,11 +592,14 @@ def _call(name: str, index: int, *args) -> None:
 def w4_kv_pages(lens: torch.Tensor, target: torch.Tensor, block_table: torch.Tensor, free_pages: torch.Tensor,
                 free_range: torch.Tensor, page_size: int, tokens: int, new_lens: torch.Tensor | None = None,
                 starts: torch.Tensor | None = None, slots: torch.Tensor | None = None,
-                positions: torch.Tensor | None = None, free_range_out: torch.Tensor | None = None):
+                positions: torch.Tensor | None = None, free_range_out: torch.Tensor | None = None,
+                holders: torch.Tensor | None = None):
     """Moves requests from `lens` to `target` tokens (int32 [B]): takes pages from, and gives them back to, the
     ring free_pages (int32 [pages]; entries free_range[0] to free_range[1], int64 [2]), updates block_table (int32
     [B, width]) and returns (new_lens int32 [B], starts int32 [B + 1], slots int64 [tokens], positions int32
-    [tokens], free_range_out int64 [2]).  `tokens`: the new tokens of all requests together."""
+    [tokens], free_range_out int64 [2]).  `tokens`: the new tokens of all requests together.  holders (int32 [pages],
+    in and out): the table entries that each page stands in, where requests share pages (w4_kv_fork); a page goes back to
+    the ring when its last holder lets go."""
     index = _device_index(block_table, "block_table")
     stride = _strides(block_table, "block_table", torch.int32, 2, index)[0]
     B, width = block_table.shape
@@ -592,21 +615,87 @@ def w4_kv_pages(lens: torch.Tensor, target: torch.Tensor, block_table: torch.Ten
             addresses.append(_vector(t, name, dtype, n, index))
         outs.append(t)
     pages = free_pages.numel()
-    _call("w4_kv_pages", index, _vector(lens, "lens", i32, B, index), _vector(target, "target", i32, B, index), B,
-          page_size, _vector(free_pages, "free_pages", i32, pages, index), pages,
-          _vector(free_range, "free_range", i64, 2, index), block_table.data_ptr(), stride, width, tokens, *addresses)
+    args = (_vector(lens, "lens", i32, B, index), _vector(target, "target", i32, B, index), B, page_size,
+            _vector(free_pages, "free_pages", i32, pages, index), pages, _vector(free_range, "free_range", i64, 2, index),
+            block_table.data_ptr(), stride, width, tokens)
+    if holders is None:
+        _call("w4_kv_pages", index, *args, *addresses)
+    else:
+        _call("w4_kv_pages_held", index, *args, _vector(holders, "holders", i32, pages, index), *addresses)
     return tuple(outs)
 
 
-def w4_kv_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor | None,
-                 cos: torch.Tensor | None, sin: torch.Tensor | None, k_cache: torch.Tensor, v_cache: torch.Tensor,
-                 slots: torch.Tensor, sections=None, cycled: bool = False, paired: bool = False,
-                 k_scales: torch.Tensor | None = None, v_scales: torch.Tensor | None = None,
-                 q_out: torch.Tensor | None = None) -> torch.Tensor | None:
-    """Rotates q (bf16 [T, q_heads, head_dim]) and k ([T, kv_heads, head_dim]) by the rows of cos and sin (fp32
-    [rows, rotary / 2]) at positions (int32 [T], or [axes, T] with `sections` frequencies per axis) and writes k
-    and v to their slots (int64 [T], −1: none) of the cache.  Returns the rotated queries (q_out; may be q).
-    cos None: no rotation; q None: keys and values only."""
+def _outputs(outs, index: int, dev):
+    """Tensors and addresses of outputs (tensor or None, name, dtype, shape): contiguous, made where they are None."""
+    tensors, addresses = [], []
+    for t, name, dtype, shape in outs:
+        if t is None:
+            t = torch.empty(shape, dtype=dtype, device=dev)
+        elif not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != index:
+            _typed(t, name, dtype, index)
+        if t.shape != shape or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous tensor of shape {shape}")
+        tensors.append(t)
+        addresses.append(t.data_ptr())
+    return tensors, addresses
+
+
+def w4_kv_fork(lens: torch.Tensor, source: torch.Tensor, keep: torch.Tensor, block_table: torch.Tensor,
+               holders: torch.Tensor, free_pages: torch.Tensor, free_range: torch.Tensor, page_size: int,
+               new_lens: torch.Tensor | None = None, copies: torch.Tensor | None = None,
+               free_range_out: torch.Tensor | None = None):
+    """Lets requests of length 0 begin as the first keep[b] tokens of request source[b] (int32 [B]; −1: none): full pages
+    are shared, with one more holder (int32 [pages]) each; a page filled in part gets a page of its own from the ring,
+    to be copied.  Updates block_table (int32 [B, width]) and holders, and returns (new_lens int32 [B], copies int32
+    [3, B] for w4_kv_copy, free_range_out int64 [2])."""
+    index = _device_index(block_table, "block_table")
+    stride = _strides(block_table, "block_table", torch.int32, 2, index)[0]
+    B, width = block_table.shape
+    i32, i64 = torch.int32, torch.int64
+    outs, addresses = _outputs(((new_lens, "new_lens", i32, (B,)), (copies, "copies", i32, (3, B)),
+                                (free_range_out, "free_range_out", i64, (2,))), index, block_table.device)
+    pages = free_pages.numel()
+    _call("w4_kv_fork", index, _vector(lens, "lens", i32, B, index), _vector(source, "source", i32, B, index),
+          _vector(keep, "keep", i32, B, index), B, page_size, block_table.data_ptr(), stride, width,
+          _vector(holders, "holders", i32, pages, index), _vector(free_pages, "free_pages", i32, pages, index), pages,
+          _vector(free_range, "free_range", i64, 2, index), *addresses)
+    return tuple(outs)
+
+
+def w4_kv_compact(lens: torch.Tensor, block_table: torch.Tensor, holders: torch.Tensor, free_range: torch.Tensor,
+                  page_size: int, new_table: torch.Tensor | None = None, new_holders: torch.Tensor | None = None,
+                  free_pages: torch.Tensor | None = None, free_range_out: torch.Tensor | None = None,
+                  copies: torch.Tensor | None = None):
+    """Moves the pages in use (holders above 0) to the lowest ids.  Returns (new_table int32 [B, width], new_holders and
+    the ring free_pages int32 [pages], free_range_out int64 [2], copies int32 [3, pages // 2] for w4_kv_copy)."""
+    index = _device_index(block_table, "block_table")
+    stride = _strides(block_table, "block_table", torch.int32, 2, index)[0]
+    B, width = block_table.shape
+    i32, i64 = torch.int32, torch.int64
+    pages = holders.numel()
+    outs, addresses = _outputs(((new_table, "new_table", i32, (B, width)), (new_holders, "new_holders", i32, (pages,)),
+                                (free_pages, "free_pages", i32, (pages,)), (free_range_out, "free_range_out", i64, (2,)),
+                                (copies, "copies", i32, (3, pages // 2))), index, block_table.device)
+    _call("w4_kv_compact", index, _vector(lens, "lens", i32, B, index), B, page_size, block_table.data_ptr(), stride, width,
+          _vector(holders, "holders", i32, pages, index), pages, _vector(free_range, "free_range", i64, 2, index),
+          addresses[0], width, *addresses[1:])
+    return tuple(outs)
+
+
+def w4_kv_copy(k_cache: torch.Tensor, v_cache: torch.Tensor, copies: torch.Tensor, k_scales: torch.Tensor | None = None,
+               v_scales: torch.Tensor | None = None) -> None:
+    """Copies the first copies[2][i] tokens of page copies[0][i] to page copies[1][i] (int32 [3, n]; −1, −1: nothing), keys,
+    values and scales."""
+    index = _device_index(k_cache, "k_cache")
+    cache = _kv_cache(k_cache, v_cache, k_scales, v_scales, index)
+    _typed(copies, "copies", torch.int32, index)
+    if copies.dim() != 2 or copies.shape[0] != 3 or not copies.is_contiguous():
+        raise ValueError("copies must be a contiguous [3, n] tensor")
+    _call("w4_kv_copy", index, cache, copies.data_ptr(), copies.shape[1])
+
+
+def _append(name, q, k, v, positions, cos, sin, k_cache, v_cache, slots, sections, cycled, paired, k_scales, v_scales, q_out,
+            norm=None):
     index = _device_index(k, "k")
     cache = _kv_cache(k_cache, v_cache, k_scales, v_scales, index)
     T = k.shape[0]
@@ -637,9 +726,46 @@ def w4_kv_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, posit
         if q_out is None:
             q_out = torch.empty(shape, dtype=torch.bfloat16, device=k.device)
         rows_q, rows_out = _rows(q, "q", shape, index), _rows(q_out, "q_out", shape, index)
-    _call("w4_kv_append", index, cache, rope, T, q_heads, rows_q, rows_out, _rows(k, "k", kv_shape, index),
-          _rows(v, "v", kv_shape, index), _vector(slots, "slots", torch.int64, T, index))
+    args = (T, q_heads, rows_q, rows_out, _rows(k, "k", kv_shape, index), _rows(v, "v", kv_shape, index),
+            _vector(slots, "slots", torch.int64, T, index))
+    if norm is None:
+        _call(name, index, cache, rope, *args)
+    else:
+        q_weight, k_weight, eps, unit_offset = norm
+        dtype = k_weight.dtype if isinstance(k_weight, torch.Tensor) else None
+        if dtype is not torch.bfloat16 and dtype is not torch.float32:
+            raise TypeError("k_weight must be a bfloat16 or float32 CUDA tensor")
+        weights = _Norm(None if q is None else _vector(q_weight, "q_weight", dtype, dim, index),
+                        _vector(k_weight, "k_weight", dtype, dim, index), 16 if dtype is torch.bfloat16 else 32, eps,
+                        unit_offset)
+        _call(name, index, cache, rope, weights, *args)
     return q_out
+
+
+def w4_kv_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor | None,
+                 cos: torch.Tensor | None, sin: torch.Tensor | None, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                 slots: torch.Tensor, sections=None, cycled: bool = False, paired: bool = False,
+                 k_scales: torch.Tensor | None = None, v_scales: torch.Tensor | None = None,
+                 q_out: torch.Tensor | None = None) -> torch.Tensor | None:
+    """Rotates q (bf16 [T, q_heads, head_dim]) and k ([T, kv_heads, head_dim]) by the rows of cos and sin (fp32
+    [rows, rotary / 2]) at positions (int32 [T], or [axes, T] with `sections` frequencies per axis) and writes k
+    and v to their slots (int64 [T], −1: none) of the cache.  Returns the rotated queries (q_out; may be q).
+    cos None: no rotation; q None: keys and values only."""
+    return _append("w4_kv_append", q, k, v, positions, cos, sin, k_cache, v_cache, slots, sections, cycled, paired,
+                   k_scales, v_scales, q_out)
+
+
+def w4_kv_append_norm(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, q_weight: torch.Tensor | None,
+                      k_weight: torch.Tensor, positions: torch.Tensor | None, cos: torch.Tensor | None,
+                      sin: torch.Tensor | None, k_cache: torch.Tensor, v_cache: torch.Tensor, slots: torch.Tensor,
+                      eps: float = 1e-6, unit_offset: bool = False, sections=None, cycled: bool = False,
+                      paired: bool = False, k_scales: torch.Tensor | None = None, v_scales: torch.Tensor | None = None,
+                      q_out: torch.Tensor | None = None) -> torch.Tensor | None:
+    """w4_kv_append of queries and keys normalised head by head before they turn: x · (mean(x²) + eps)^−½ · w over each
+    row's head_dim values, with q_weight and k_weight (bf16 or fp32 [head_dim]; unit_offset: w = 1 + weight) for all
+    heads; one rounding in all."""
+    return _append("w4_kv_append_norm", q, k, v, positions, cos, sin, k_cache, v_cache, slots, sections, cycled, paired,
+                   k_scales, v_scales, q_out, (q_weight, k_weight, eps, unit_offset))
 
 
 def w4_attn_decode_workspace_bytes(q: torch.Tensor, k_cache: torch.Tensor, requests: int) -> int:
@@ -671,18 +797,64 @@ def w4_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
             _vector(lens, "lens", torch.int32, B, index),
             None if starts is None else _vector(starts, "starts", torch.int32, B + 1, index),
             dim ** -0.5 if scale is None else scale, window)
+    _attend("w4_attn_decode", index, args, workspace, q.device,
+            lambda: (_lib or load()).w4_attn_decode_workspace_bytes(cache, B, T, q_heads))
+    return out
+
+
+def _attend(name: str, index: int, args, workspace, dev, bytes_needed) -> None:
+    """Runs a library function with the caller's workspace, or one for the time of the call."""
     if workspace is not None:
         size = workspace.numel()
-        _call("w4_attn_decode", index, *args, _vector(workspace, "workspace", torch.uint8, size, index), size)
-        return out
-    size = (_lib or load()).w4_attn_decode_workspace_bytes(cache, B, T, q_heads)
+        _call(name, index, *args, _vector(workspace, "workspace", torch.uint8, size, index), size)
+        return
+    size = bytes_needed()
     if size and _raw_alloc and _raw_delete and _current_device() == index:
         scratch = _raw_alloc(size, _raw_stream(index))
         try:
-            _call("w4_attn_decode", index, *args, scratch, size)
+            _call(name, index, *args, scratch, size)
         finally:
             _raw_delete(scratch)  # the stream's next allocations may have it
     else:
-        scratch = torch.empty(size, dtype=torch.uint8, device=q.device)  # (a name keeps it until the launch)
-        _call("w4_attn_decode", index, *args, scratch.data_ptr(), size)
+        scratch = torch.empty(size, dtype=torch.uint8, device=dev)  # (a name keeps it until the launch)
+        _call(name, index, *args, scratch.data_ptr(), size)
+
+
+def w4_attn_decode_shared_workspace_bytes(q: torch.Tensor, k_cache: torch.Tensor, requests: int, groups: int) -> int:
+    """Bytes of workspace of w4_attn_decode_shared for these queries, cache pages and numbers of requests and groups."""
+    cache = _KvCache(kv_heads=k_cache.shape[2], head_dim=k_cache.shape[3], format=8 if k_cache.dtype == torch.int8 else 16)
+    return load().w4_attn_decode_shared_workspace_bytes(cache, requests, q.shape[0], q.shape[1], groups)
+
+
+def w4_attn_decode_shared(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
+                          lens: torch.Tensor, group_starts: torch.Tensor, prefix_table: torch.Tensor,
+                          prefix_lens: torch.Tensor, starts: torch.Tensor | None = None,
+                          k_scales: torch.Tensor | None = None, v_scales: torch.Tensor | None = None,
+                          scale: float | None = None, out: torch.Tensor | None = None,
+                          workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """w4_attn_decode of requests that share prefixes.  Requests group_starts[g] to group_starts[g + 1] − 1 (int32
+    [groups + 1]) begin with the prefix_lens[g] tokens (int32 [groups]) in the pages prefix_table[g] (int32 [groups,
+    width]), which are read once for all of them; what follows is in their own pages, at the places that block_table has
+    for it.  lens counts the prefix.  Requests outside of the groups, and those whose new tokens do not all lie behind the
+    prefix, are attended over their own pages."""
+    index = _device_index(q, "q")
+    cache = _kv_cache(k_cache, v_cache, k_scales, v_scales, index)
+    stride = _strides(block_table, "block_table", torch.int32, 2, index)[0]
+    prefix_stride = _strides(prefix_table, "prefix_table", torch.int32, 2, index)[0]
+    B, width = block_table.shape
+    groups, prefix_width = prefix_table.shape
+    if q.dim() != 3:
+        raise ValueError("q must be a 3-D tensor")
+    T, q_heads, dim = q.shape
+    shape = (T, q_heads, cache.head_dim)
+    if out is None:
+        out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
+    rows_q, rows_out = _rows(q, "q", shape, index), _rows(out, "out", shape, index)
+    i32 = torch.int32
+    args = (cache, B, T, q_heads, rows_q, rows_out, block_table.data_ptr(), stride, width, _vector(lens, "lens", i32, B, index),
+            None if starts is None else _vector(starts, "starts", i32, B + 1, index), groups,
+            _vector(group_starts, "group_starts", i32, groups + 1, index), prefix_table.data_ptr(), prefix_stride,
+            prefix_width, _vector(prefix_lens, "prefix_lens", i32, groups, index), dim ** -0.5 if scale is None else scale)
+    _attend("w4_attn_decode_shared", index, args, workspace, q.device,
+            lambda: (_lib or load()).w4_attn_decode_shared_workspace_bytes(cache, B, T, q_heads, groups))
     return out

@@ -656,42 +656,46 @@ int usable_device(const DeviceInfo** dev) {
     return (*dev)->cc_major < 10 ? W4_ERR_UNSUPPORTED : W4_OK;
 }
 
-}  // namespace
+bool table_fits(int32_t B, int64_t stride, int32_t width) { return B <= 1 || (stride >= width && stride <= (int64_t{1} << 59) / B); }
 
-int w4_kv_pages(const int32_t* lens, const int32_t* target, int32_t B, int32_t page_size, int32_t* free_pages,
-                int64_t pages, const int64_t* free_range, int32_t* block_table, int64_t table_stride, int32_t width,
-                int64_t T, int32_t* new_lens, int32_t* starts, int64_t* slots, int32_t* positions,
-                int64_t* free_range_out, void* stream) {
+size_t table_bytes(int32_t B, int64_t stride, int32_t width) {
+    return B > 0 ? (static_cast<size_t>(B - 1) * static_cast<size_t>(B > 1 ? stride : 0) + width) * 4 : 0;
+}
+
+int kv_pages(const int32_t* lens, const int32_t* target, int32_t B, int32_t page_size, int32_t* free_pages,
+             int64_t pages, const int64_t* free_range, int32_t* block_table, int64_t table_stride, int32_t width,
+             int64_t T, bool held, int32_t* holders, int32_t* new_lens, int32_t* starts, int64_t* slots,
+             int32_t* positions, int64_t* free_range_out, void* stream) {
     if (B < 0 || T < 0 || page_size < 1 || pages < 1 || width < 1) return W4_ERR_INVALID_ARG;
     if (B > kMostCounted || T > INT32_MAX || pages > INT32_MAX) return W4_ERR_UNSUPPORTED;
-    if (!free_pages || !free_range || !starts || !free_range_out) return W4_ERR_INVALID_ARG;
+    if (!free_pages || !free_range || !starts || !free_range_out || (held && !holders)) return W4_ERR_INVALID_ARG;
     if (B > 0 && (!lens || !target || !block_table || !new_lens)) return W4_ERR_INVALID_ARG;
     if (T > 0 && (!slots || !positions)) return W4_ERR_INVALID_ARG;
-    if (B > 1 && (table_stride < width || table_stride > (int64_t{1} << 59) / B)) return W4_ERR_INVALID_ARG;
-    const void* fours[] = {lens, target, free_pages, block_table, new_lens, starts, positions};
+    if (!table_fits(B, table_stride, width)) return W4_ERR_INVALID_ARG;
+    const void* fours[] = {lens, target, free_pages, block_table, new_lens, starts, positions, holders};
     const void* eights[] = {free_range, slots, free_range_out};
     for (const void* p : fours)
         if (!aligned(p, 4)) return W4_ERR_MISALIGNED;
     for (const void* p : eights)
         if (!aligned(p, 8)) return W4_ERR_MISALIGNED;
     const size_t b4 = static_cast<size_t>(B) * 4, t4 = static_cast<size_t>(T) * 4;
-    const size_t table_bytes = B > 0 ? (static_cast<size_t>(B - 1) * static_cast<size_t>(B > 1 ? table_stride : 0) + width) * 4 : 0;
-    const Region outs[] = {plain(block_table, table_bytes), plain(free_pages, static_cast<size_t>(pages) * 4),
+    const Region outs[] = {plain(block_table, table_bytes(B, table_stride, width)), plain(free_pages, static_cast<size_t>(pages) * 4),
                            plain(new_lens, b4), plain(starts, b4 + 4), plain(slots, 2 * t4), plain(positions, t4),
-                           plain(free_range_out, 16)};
+                           plain(free_range_out, 16), plain(holders, static_cast<size_t>(pages) * 4)};
     const Region ins[] = {plain(lens, b4), plain(target, b4), plain(free_range, 16)};
-    if (any_meet(outs, 7, ins, 3)) return W4_ERR_INVALID_ARG;
+    if (any_meet(outs, 8, ins, 3)) return W4_ERR_INVALID_ARG;
     const DeviceInfo* dev;
     if (const int s = usable_device(&dev)) return s;
     const KvPagesArgs a = {lens, target, B, page_size, free_pages, pages, free_range, block_table, table_stride, width,
-                           T, new_lens, starts, slots, positions, free_range_out, dev->status, 0, 0};
+                           T, holders, new_lens, starts, slots, positions, free_range_out, dev->status, 0, 0};
     return to_status(launch_kv_pages(a, *dev, static_cast<cudaStream_t>(stream)));
 }
 
-int w4_kv_append(const w4_kv_cache* cache, const w4_rope* rope, int64_t T, int32_t q_heads, const w4_rows* q,
-                 const w4_rows* q_out, const w4_rows* k, const w4_rows* v, const int64_t* slots, void* stream) {
+// norm: nullptr for rows that enter as they are.
+int kv_append(const w4_kv_cache* cache, const w4_rope* rope, const w4_norm* norm, int64_t T, int32_t q_heads, const w4_rows* q,
+              const w4_rows* q_out, const w4_rows* k, const w4_rows* v, const int64_t* slots, void* stream) {
     if (T < 0 || q_heads < 0 || !rope) return W4_ERR_INVALID_ARG;
-    Region outs[5], ins[7];
+    Region outs[5], ins[9];
     if (const int s = cache_regions(cache, *reinterpret_cast<Region(*)[4]>(&outs[1]))) return s;
     if (T > kMostCounted || q_heads > 65536 || cache->kv_heads > 65536) return W4_ERR_UNSUPPORTED;
     const w4_rope& r = *rope;
@@ -708,8 +712,19 @@ int w4_kv_append(const w4_kv_cache* cache, const w4_rope* rope, int64_t T, int32
             (r.axis_stride > 0 && r.axis_stride < T) || r.axis_stride > (int64_t{1} << 59))
             return W4_ERR_INVALID_ARG;
     }
+    if (norm) {
+        if (norm->format != 16 && norm->format != 32) return W4_ERR_UNSUPPORTED;
+        if (!(norm->eps >= 1e-20f && norm->eps <= 3e38f)) return W4_ERR_INVALID_ARG;
+    }
     if (T == 0) return W4_OK;
     if (!slots || (r.rotary > 0 && (!r.positions || !r.cos || !r.sin))) return W4_ERR_INVALID_ARG;
+    if (norm) {
+        if (!norm->k_weight || (q_heads > 0 && !norm->q_weight)) return W4_ERR_INVALID_ARG;
+        const size_t size = norm->format / 8;
+        if (!aligned(norm->k_weight, size) || (q_heads > 0 && !aligned(norm->q_weight, size))) return W4_ERR_MISALIGNED;
+        ins[7] = plain(norm->k_weight, size * cache->head_dim);
+        ins[8] = plain(q_heads > 0 ? norm->q_weight : nullptr, size * cache->head_dim);
+    }
     if (!aligned(slots, 8)) return W4_ERR_MISALIGNED;
     if (r.rotary > 0 && (!aligned(r.positions, 4) || !aligned(r.cos, 16) || !aligned(r.sin, 16)))
         return W4_ERR_MISALIGNED;
@@ -725,7 +740,7 @@ int w4_kv_append(const w4_kv_cache* cache, const w4_rope* rope, int64_t T, int32
         if (const int s = rows_region(q, T, q_heads, d, &ins[6])) return s;
         if (const int s = rows_region(q_out, T, q_heads, d, &outs[0])) return s;
     }
-    if (any_meet(outs, 5, ins, 7, q_heads > 0 && same_rows(q, q_out) ? 6 : -1)) return W4_ERR_INVALID_ARG;
+    if (any_meet(outs, 5, ins, 9, q_heads > 0 && same_rows(q, q_out) ? 6 : -1)) return W4_ERR_INVALID_ARG;
     const DeviceInfo* dev;
     if (const int s = usable_device(&dev)) return s;
     KvAppendArgs a = {};
@@ -758,40 +773,51 @@ int w4_kv_append(const w4_kv_cache* cache, const w4_rope* rope, int64_t T, int32
     a.page_size = cache->page_size;
     a.slots = slots;
     a.status = dev->status;
-    return to_status(launch_kv_append(a, r.sections, r.cycled != 0, cache->format == 8, *dev,
-                                      static_cast<cudaStream_t>(stream)));
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (!norm) return to_status(launch_kv_append(a, r.sections, r.cycled != 0, cache->format == 8, *dev, st));
+    const KvNorm n = {q_heads > 0 ? norm->q_weight : nullptr, norm->k_weight, norm->format == 16,
+                      norm->unit_offset ? 1.f : 0.f, norm->eps, 1.f / static_cast<float>(d)};
+    return to_status(launch_kv_append_norm(a, n, r.sections, r.cycled != 0, cache->format == 8, *dev, st));
 }
 
-size_t w4_attn_decode_workspace_bytes(const w4_kv_cache* cache, int32_t B, int64_t T, int32_t q_heads) {
-    if (!cache || B < 0 || T < 0 || q_heads < 1 || cache->kv_heads < 1 || cache->head_dim < 1 ||
-        cache->head_dim > 256 || cache->head_dim % 16 != 0 || q_heads % cache->kv_heads != 0)
-        return 0;
-    return attn_decode_workspace_bytes(B, T, q_heads, cache->kv_heads, cache->head_dim, cache->format == 8);
-}
-
-int w4_attn_decode(const w4_kv_cache* cache, int32_t B, int64_t T, int32_t q_heads, const w4_rows* q,
-                   const w4_rows* out, const int32_t* block_table, int64_t table_stride, int32_t width,
-                   const int32_t* lens, const int32_t* starts, float scale, int64_t window, void* workspace,
-                   size_t workspace_bytes, void* stream) {
+// shared: nullptr for requests on their own.
+int attn_decode(const w4_kv_cache* cache, int32_t B, int64_t T, int32_t q_heads, const w4_rows* q,
+                const w4_rows* out, const int32_t* block_table, int64_t table_stride, int32_t width,
+                const int32_t* lens, const int32_t* starts, const SharedArgs* shared, float scale, int64_t window,
+                void* workspace, size_t workspace_bytes, void* stream) {
     if (B < 0 || T < 0 || q_heads < 1 || width < 1 || window < 0 || !(scale - scale == 0.f)) return W4_ERR_INVALID_ARG;
-    Region outs[2], ins[8];
+    if (shared && (shared->groups < 0 || shared->width < 1)) return W4_ERR_INVALID_ARG;
+    Region outs[2], ins[11];
     if (const int s = cache_regions(cache, *reinterpret_cast<Region(*)[4]>(&ins[1]))) return s;
     if (q_heads % cache->kv_heads != 0) return W4_ERR_INVALID_ARG;
     if (q_heads > 65536 || B > kMostCounted || T > kMostCounted / q_heads) return W4_ERR_UNSUPPORTED;
+    if (shared && (shared->groups > kMostCounted || T > kMostShared)) return W4_ERR_UNSUPPORTED;
     if (B > 0 && !starts && T % B != 0) return W4_ERR_INVALID_ARG;
     if (B == 0 || T == 0) return W4_OK;
-    if (!block_table || !lens || !workspace) return W4_ERR_INVALID_ARG;
-    if (B > 1 && (table_stride < width || table_stride > (int64_t{1} << 59) / B)) return W4_ERR_INVALID_ARG;
-    if (!aligned(block_table, 4) || !aligned(lens, 4) || !aligned(starts, 4) || !aligned(workspace, 256))
+    const bool groups = shared && shared->groups > 0;
+    if (!block_table || !lens || !workspace || (groups && (!shared->starts || !shared->table || !shared->lens))) return W4_ERR_INVALID_ARG;
+    if (!table_fits(B, table_stride, width) || (groups && !table_fits(shared->groups, shared->table_stride, shared->width)))
+        return W4_ERR_INVALID_ARG;
+    if (!aligned(block_table, 4) || !aligned(lens, 4) || !aligned(starts, 4) || !aligned(workspace, 256) ||
+        (groups && (!aligned(shared->starts, 4) || !aligned(shared->table, 4) || !aligned(shared->lens, 4))))
         return W4_ERR_MISALIGNED;
-    if (workspace_bytes < w4_attn_decode_workspace_bytes(cache, B, T, q_heads)) return W4_ERR_INVALID_ARG;
-    if (const int s = rows_region(q, T, q_heads, cache->head_dim, &ins[0])) return s;
-    if (const int s = rows_region(out, T, q_heads, cache->head_dim, &outs[0])) return s;
+    const int32_t H = cache->kv_heads, d = cache->head_dim;
+    const bool q8 = cache->format == 8;
+    const size_t need = groups ? attn_shared_workspace_bytes(B, T, q_heads, H, d, q8, shared->groups)
+                               : attn_decode_workspace_bytes(B, T, q_heads, H, d, q8);
+    if (workspace_bytes < need) return W4_ERR_INVALID_ARG;
+    if (const int s = rows_region(q, T, q_heads, d, &ins[0])) return s;
+    if (const int s = rows_region(out, T, q_heads, d, &outs[0])) return s;
     outs[1] = plain(workspace, workspace_bytes);
-    ins[5] = plain(block_table, (static_cast<size_t>(B - 1) * static_cast<size_t>(B > 1 ? table_stride : 0) + width) * 4);
+    ins[5] = plain(block_table, table_bytes(B, table_stride, width));
     ins[6] = plain(lens, static_cast<size_t>(B) * 4);
     ins[7] = plain(starts, static_cast<size_t>(B) * 4 + 4);
-    if (any_meet(outs, 2, ins, 8, same_rows(q, out) ? 0 : -1)) return W4_ERR_INVALID_ARG;
+    if (groups) {
+        ins[8] = plain(shared->starts, static_cast<size_t>(shared->groups) * 4 + 4);
+        ins[9] = plain(shared->table, table_bytes(shared->groups, shared->table_stride, shared->width));
+        ins[10] = plain(shared->lens, static_cast<size_t>(shared->groups) * 4);
+    }
+    if (any_meet(outs, 2, ins, 11, same_rows(q, out) ? 0 : -1)) return W4_ERR_INVALID_ARG;
     const DeviceInfo* dev;
     if (const int s = usable_device(&dev)) return s;
     AttnArgs a = {};
@@ -800,8 +826,8 @@ int w4_attn_decode(const w4_kv_cache* cache, int32_t B, int64_t T, int32_t q_hea
     a.B = B;
     a.T = T;
     a.q_heads = q_heads;
-    a.kv_heads = cache->kv_heads;
-    a.head_dim = cache->head_dim;
+    a.kv_heads = H;
+    a.head_dim = d;
     a.k = cache->k;
     a.v = cache->v;
     a.k_scales = static_cast<const __nv_bfloat16*>(cache->k_scales);
@@ -819,7 +845,161 @@ int w4_attn_decode(const w4_kv_cache* cache, int32_t B, int64_t T, int32_t q_hea
     a.scale = scale;
     a.window = window;
     a.status = dev->status;
-    return to_status(launch_attn_decode(a, cache->format == 8, workspace, *dev, static_cast<cudaStream_t>(stream)));
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return to_status(groups ? launch_attn_shared(a, *shared, q8, workspace, *dev, st) : launch_attn_decode(a, q8, workspace, *dev, st));
+}
+
+bool attn_workspace_known(const w4_kv_cache* cache, int32_t B, int64_t T, int32_t q_heads) {
+    return cache && B >= 0 && T >= 0 && q_heads >= 1 && cache->kv_heads >= 1 && cache->head_dim >= 1 &&
+           cache->head_dim <= 256 && cache->head_dim % 16 == 0 && q_heads % cache->kv_heads == 0;
+}
+
+}  // namespace
+
+int w4_kv_pages(const int32_t* lens, const int32_t* target, int32_t B, int32_t page_size, int32_t* free_pages,
+                int64_t pages, const int64_t* free_range, int32_t* block_table, int64_t table_stride, int32_t width,
+                int64_t T, int32_t* new_lens, int32_t* starts, int64_t* slots, int32_t* positions,
+                int64_t* free_range_out, void* stream) {
+    return kv_pages(lens, target, B, page_size, free_pages, pages, free_range, block_table, table_stride, width, T, false,
+                    nullptr, new_lens, starts, slots, positions, free_range_out, stream);
+}
+
+int w4_kv_pages_held(const int32_t* lens, const int32_t* target, int32_t B, int32_t page_size, int32_t* free_pages,
+                     int64_t pages, const int64_t* free_range, int32_t* block_table, int64_t table_stride,
+                     int32_t width, int64_t T, int32_t* holders, int32_t* new_lens, int32_t* starts, int64_t* slots,
+                     int32_t* positions, int64_t* free_range_out, void* stream) {
+    return kv_pages(lens, target, B, page_size, free_pages, pages, free_range, block_table, table_stride, width, T, true,
+                    holders, new_lens, starts, slots, positions, free_range_out, stream);
+}
+
+int w4_kv_append(const w4_kv_cache* cache, const w4_rope* rope, int64_t T, int32_t q_heads, const w4_rows* q,
+                 const w4_rows* q_out, const w4_rows* k, const w4_rows* v, const int64_t* slots, void* stream) {
+    return kv_append(cache, rope, nullptr, T, q_heads, q, q_out, k, v, slots, stream);
+}
+
+int w4_kv_append_norm(const w4_kv_cache* cache, const w4_rope* rope, const w4_norm* norm, int64_t T, int32_t q_heads,
+                      const w4_rows* q, const w4_rows* q_out, const w4_rows* k, const w4_rows* v,
+                      const int64_t* slots, void* stream) {
+    if (!norm) return W4_ERR_INVALID_ARG;
+    return kv_append(cache, rope, norm, T, q_heads, q, q_out, k, v, slots, stream);
+}
+
+int w4_kv_fork(const int32_t* lens, const int32_t* source, const int32_t* keep, int32_t B, int32_t page_size,
+               int32_t* block_table, int64_t table_stride, int32_t width, int32_t* holders, const int32_t* free_pages,
+               int64_t pages, const int64_t* free_range, int32_t* new_lens, int32_t* copies, int64_t* free_range_out,
+               void* stream) {
+    if (B < 0 || page_size < 1 || pages < 1 || width < 1) return W4_ERR_INVALID_ARG;
+    if (B > kMostCounted || pages > INT32_MAX) return W4_ERR_UNSUPPORTED;
+    if (!free_pages || !free_range || !free_range_out || !holders) return W4_ERR_INVALID_ARG;
+    if (B > 0 && (!lens || !source || !keep || !block_table || !new_lens || !copies)) return W4_ERR_INVALID_ARG;
+    if (!table_fits(B, table_stride, width)) return W4_ERR_INVALID_ARG;
+    const void* fours[] = {lens, source, keep, block_table, holders, free_pages, new_lens, copies};
+    const void* eights[] = {free_range, free_range_out};
+    for (const void* p : fours)
+        if (!aligned(p, 4)) return W4_ERR_MISALIGNED;
+    for (const void* p : eights)
+        if (!aligned(p, 8)) return W4_ERR_MISALIGNED;
+    const size_t b4 = static_cast<size_t>(B) * 4, p4 = static_cast<size_t>(pages) * 4;
+    const Region outs[] = {plain(block_table, table_bytes(B, table_stride, width)), plain(holders, p4), plain(new_lens, b4),
+                           plain(copies, 3 * b4), plain(free_range_out, 16)};
+    const Region ins[] = {plain(lens, b4), plain(source, b4), plain(keep, b4), plain(free_pages, p4), plain(free_range, 16)};
+    if (any_meet(outs, 5, ins, 5)) return W4_ERR_INVALID_ARG;
+    const DeviceInfo* dev;
+    if (const int s = usable_device(&dev)) return s;
+    const KvForkArgs a = {lens, source, keep, B, page_size, block_table, table_stride, width, holders, free_pages, pages,
+                          free_range, new_lens, copies, free_range_out, dev->status, 0, 0};
+    return to_status(launch_kv_fork(a, *dev, static_cast<cudaStream_t>(stream)));
+}
+
+int w4_kv_compact(const int32_t* lens, int32_t B, int32_t page_size, const int32_t* block_table, int64_t table_stride,
+                  int32_t width, const int32_t* holders, int64_t pages, const int64_t* free_range, int32_t* new_table,
+                  int64_t new_stride, int32_t* new_holders, int32_t* free_pages, int64_t* free_range_out,
+                  int32_t* copies, void* stream) {
+    if (B < 0 || page_size < 1 || pages < 1 || width < 1) return W4_ERR_INVALID_ARG;
+    if (B > kMostCounted || pages > kMostCompacted) return W4_ERR_UNSUPPORTED;
+    if (!holders || !free_range || !new_holders || !free_pages || !free_range_out || (pages > 1 && !copies)) return W4_ERR_INVALID_ARG;
+    if (B > 0 && (!lens || !block_table || !new_table)) return W4_ERR_INVALID_ARG;
+    if (!table_fits(B, table_stride, width) || !table_fits(B, new_stride, width)) return W4_ERR_INVALID_ARG;
+    const void* fours[] = {lens, block_table, holders, new_table, new_holders, free_pages, copies};
+    const void* eights[] = {free_range, free_range_out};
+    for (const void* p : fours)
+        if (!aligned(p, 4)) return W4_ERR_MISALIGNED;
+    for (const void* p : eights)
+        if (!aligned(p, 8)) return W4_ERR_MISALIGNED;
+    const size_t p4 = static_cast<size_t>(pages) * 4;
+    const Region outs[] = {plain(new_table, table_bytes(B, new_stride, width)), plain(new_holders, p4), plain(free_pages, p4),
+                           plain(free_range_out, 16), plain(copies, static_cast<size_t>(pages / 2) * 12)};
+    const Region ins[] = {plain(lens, static_cast<size_t>(B) * 4), plain(block_table, table_bytes(B, table_stride, width)),
+                          plain(holders, p4), plain(free_range, 16)};
+    if (any_meet(outs, 5, ins, 4)) return W4_ERR_INVALID_ARG;
+    const DeviceInfo* dev;
+    if (const int s = usable_device(&dev)) return s;
+    const KvCompactArgs a = {lens, B, page_size, block_table, table_stride, width, holders, pages, free_range, new_table,
+                             new_stride, new_holders, free_pages, free_range_out, copies, dev->status, 0, 0};
+    return to_status(launch_kv_compact(a, *dev, static_cast<cudaStream_t>(stream)));
+}
+
+int w4_kv_copy(const w4_kv_cache* cache, const int32_t* copies, int32_t n, void* stream) {
+    if (n < 0) return W4_ERR_INVALID_ARG;
+    Region outs[4];
+    if (const int s = cache_regions(cache, outs)) return s;
+    const int64_t size = cache->format == 8 ? 1 : 2, chunks = cache->head_dim * size / 16;
+    if (n > kMostCounted || cache->page_size > kMostCopied / chunks / cache->kv_heads) return W4_ERR_UNSUPPORTED;
+    if (n == 0) return W4_OK;
+    if (!copies) return W4_ERR_INVALID_ARG;
+    if (!aligned(copies, 4)) return W4_ERR_MISALIGNED;
+    const Region in = plain(copies, static_cast<size_t>(n) * 12);
+    if (any_meet(outs, 4, &in, 1)) return W4_ERR_INVALID_ARG;
+    const DeviceInfo* dev;
+    if (const int s = usable_device(&dev)) return s;
+    KvCopyArgs a = {};
+    a.k = cache->k;
+    a.v = cache->v;
+    a.k_scales = cache->format == 8 ? static_cast<__nv_bfloat16*>(cache->k_scales) : nullptr;
+    a.v_scales = cache->format == 8 ? static_cast<__nv_bfloat16*>(cache->v_scales) : nullptr;
+    a.pages = cache->pages;
+    a.page_stride = cache->page_stride * size;
+    a.token_stride = cache->token_stride * size;
+    a.head_stride = cache->head_stride * size;
+    a.page_size = cache->page_size;
+    a.kv_heads = cache->kv_heads;
+    a.chunks = static_cast<int32_t>(chunks);
+    a.copies = copies;
+    a.n = n;
+    a.status = dev->status;
+    return to_status(launch_kv_copy(a, *dev, static_cast<cudaStream_t>(stream)));
+}
+
+size_t w4_attn_decode_workspace_bytes(const w4_kv_cache* cache, int32_t B, int64_t T, int32_t q_heads) {
+    if (!attn_workspace_known(cache, B, T, q_heads)) return 0;
+    return attn_decode_workspace_bytes(B, T, q_heads, cache->kv_heads, cache->head_dim, cache->format == 8);
+}
+
+int w4_attn_decode(const w4_kv_cache* cache, int32_t B, int64_t T, int32_t q_heads, const w4_rows* q,
+                   const w4_rows* out, const int32_t* block_table, int64_t table_stride, int32_t width,
+                   const int32_t* lens, const int32_t* starts, float scale, int64_t window, void* workspace,
+                   size_t workspace_bytes, void* stream) {
+    return attn_decode(cache, B, T, q_heads, q, out, block_table, table_stride, width, lens, starts, nullptr, scale, window,
+                       workspace, workspace_bytes, stream);
+}
+
+size_t w4_attn_decode_shared_workspace_bytes(const w4_kv_cache* cache, int32_t B, int64_t T, int32_t q_heads,
+                                             int32_t groups) {
+    if (!attn_workspace_known(cache, B, T, q_heads) || groups < 0 || T > kMostShared) return 0;
+    const bool q8 = cache->format == 8;
+    return groups > 0 ? attn_shared_workspace_bytes(B, T, q_heads, cache->kv_heads, cache->head_dim, q8, groups)
+                      : attn_decode_workspace_bytes(B, T, q_heads, cache->kv_heads, cache->head_dim, q8);
+}
+
+int w4_attn_decode_shared(const w4_kv_cache* cache, int32_t B, int64_t T, int32_t q_heads, const w4_rows* q,
+                          const w4_rows* out, const int32_t* block_table, int64_t table_stride, int32_t width,
+                          const int32_t* lens, const int32_t* starts, int32_t groups, const int32_t* group_starts,
+                          const int32_t* prefix_table, int64_t prefix_stride, int32_t prefix_width,
+                          const int32_t* prefix_lens, float scale, void* workspace, size_t workspace_bytes,
+                          void* stream) {
+    const SharedArgs shared = {groups, group_starts, prefix_table, prefix_stride, prefix_width, prefix_lens};
+    return attn_decode(cache, B, T, q_heads, q, out, block_table, table_stride, width, lens, starts, &shared, scale, 0,
+                       workspace, workspace_bytes, stream);
 }
 
 int w4_last_device_status(void* stream) {

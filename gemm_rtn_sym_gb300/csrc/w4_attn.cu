@@ -175,6 +175,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
     const AttnArgs& a = sp.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
     const int group = warp / R, rw = warp % R, G = sp.G;
+    if (a.pass == kPrefixes) find_low(sp);
     Walk<kTile, 16 * R, kFixed> walk;
     if (!walk.template find<kThreads>(sp)) return;
     bool more;
@@ -202,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
     };
     for (int which = 0; more; which ^= 1) {
         const int h = s_item[which].h, row0 = s_item[which].row0, rows = s_item[which].rows;
-        const int tok0 = s_item[which].tok0, tok1 = s_item[which].tok1, before = s_item[which].len - s_item[which].n;
+        const int tok0 = s_item[which].tok0, tok1 = s_item[which].tok1, before = s_item[which].before;
         const int* const table = a.table + s_item[which].b * a.table_stride;
         // Stages begin at multiples of 16 tokens, so that they lie in one page where pages are such multiples.
         const int base0 = tok0 & ~15, count = tok1 - base0 - group * S::kTokens;
@@ -713,7 +714,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
                 v[0] += fv * w.x, v[1] += fv * w.y, v[2] += fv * w.z, v[3] += fv * w.w;
             }
             if (whole) {
-                put_row(sp, it, row, col, v, 4, ll);
+                put_row(sp, it, row, col, v, 4, mm, ll);
             } else {
                 if (col == 0) {
                     part[r] = mm;
@@ -825,13 +826,57 @@ cudaError_t launch_attn_decode(AttnArgs a, bool q8, void* workspace, const Devic
     sp.partial = reinterpret_cast<float*>(sp.arrived + 2 * kMaxCtas);
     sp.G = a.q_heads / a.kv_heads;
     divide_by(sp.G, &sp.G_mul, &sp.G_shift);
-    sp.rows_each = static_cast<int>(a.T / a.B);
+    sp.rows_each = static_cast<int>(a.T / (a.pass == kPrefixes ? a.requests : a.B));
     // A factor below zero turns the queries' signs over, and one of zero is one so small that every weight is 1: the
     // largest score is then that of the unscaled products, and hidden ones stay at −∞.
     sp.scale_log2 = std::max(std::fabs(a.scale) * 1.4426950408889634f, 1e-30f);
     sp.flip = a.scale < 0.f ? 0x80008000u : 0u;
     if (many_rows(a.B, a.T, sp.G, a.kv_heads, dim_of(a.head_dim), q8)) return launch_attn_tc(sp, q8, dev, stream);
+    sp.lift = q8 ? kLift : 0.f;
     return q8 ? run_dim<true>(sp, dev, stream) : run_dim<false>(sp, dev, stream);
+}
+
+namespace {
+size_t padded(size_t bytes) { return (bytes + 255) / 256 * 256; }
+}  // namespace
+
+// Workspaces of the two passes, first own tokens, and the rows' sums over the prefixes.
+size_t attn_shared_workspace_bytes(int32_t B, int64_t T, int32_t q_heads, int32_t kv_heads, int32_t head_dim, bool q8,
+                                   int32_t groups) {
+    const size_t rows = static_cast<size_t>(T) * q_heads;
+    return padded(attn_decode_workspace_bytes(groups, T, q_heads, kv_heads, head_dim, q8)) +
+           padded(attn_decode_workspace_bytes(B, T, q_heads, kv_heads, head_dim, q8)) + padded(static_cast<size_t>(B) * 4) +
+           padded(rows * sizeof(float2)) + rows * head_dim * sizeof(float);
+}
+
+cudaError_t launch_attn_shared(AttnArgs a, const SharedArgs& shared, bool q8, void* workspace, const DeviceInfo& dev,
+                               cudaStream_t stream) {
+    uint8_t* at = static_cast<uint8_t*>(workspace);
+    auto take = [&](size_t bytes) {
+        void* const p = at;
+        at += padded(bytes);
+        return p;
+    };
+    void* const first = take(attn_decode_workspace_bytes(shared.groups, a.T, a.q_heads, a.kv_heads, a.head_dim, q8));
+    void* const second = take(attn_decode_workspace_bytes(a.B, a.T, a.q_heads, a.kv_heads, a.head_dim, q8));
+    const size_t rows = static_cast<size_t>(a.T) * a.q_heads;
+    a.low = static_cast<int32_t*>(take(static_cast<size_t>(a.B) * 4));
+    a.prefix_stats = static_cast<float2*>(take(rows * sizeof(float2)));
+    a.prefix_values = static_cast<float*>(take(rows * a.head_dim * sizeof(float)));
+    AttnArgs p = a;
+    p.pass = kPrefixes;
+    p.requests = a.B;
+    p.own_lens = a.lens;
+    p.B = shared.groups;
+    p.group_starts = shared.starts;
+    p.table = shared.table;
+    p.table_stride = shared.table_stride;
+    p.width = shared.width;
+    p.lens = shared.lens;
+    const cudaError_t err = launch_attn_decode(p, q8, first, dev, stream);
+    if (err != cudaSuccess) return err;
+    a.pass = kOwn;
+    return launch_attn_decode(a, q8, second, dev, stream);
 }
 
 }  // namespace w4

@@ -35,6 +35,7 @@ struct SplitArgs {
     int G_shift;
     int rows_each;                // rows of each request, where starts is null
     float scale_log2;             // |scale| · log2(e)
+    float lift;                   // what a row's sums lie below its reference, to base 2
     uint32_t flip;                // sign bits of a pair of queries to turn over: scale < 0
 
     __device__ __forceinline__ int over_G(int r) const { return static_cast<int>((static_cast<uint64_t>(r) * G_mul) >> G_shift); }
@@ -62,6 +63,7 @@ struct Request {
     int start, n;     // token rows
     int len;          // tokens in the cache
     int low;          // first token that any row sees
+    int before;       // position of the first row: it sees the tokens up to there
     int tiles;        // tiles of TILE tokens from the one of `low`
     int row_tiles;    // of ROWS rows (new tokens × query heads per key-value head)
 };
@@ -71,7 +73,12 @@ __device__ __forceinline__ Request request(const SplitArgs& sp, int b) {
     const AttnArgs& a = sp.a;
     Request r;
     const int len = a.lens[b];
-    if (a.starts) {
+    if (a.pass == kPrefixes) {
+        const int first = min(max(a.group_starts[b], 0), a.requests), end = min(max(a.group_starts[b + 1], first), a.requests);
+        const int T = static_cast<int>(a.T);
+        r.start = a.starts ? min(max(a.starts[first], 0), T) : first * sp.rows_each;
+        r.n = a.starts ? min(max(a.starts[end], r.start), T) - r.start : (end - first) * sp.rows_each;
+    } else if (a.starts) {
         const int T = static_cast<int>(a.T);
         r.start = min(max(a.starts[b], 0), T);
         r.n = min(max(a.starts[b + 1], r.start), T) - r.start;
@@ -79,11 +86,16 @@ __device__ __forceinline__ Request request(const SplitArgs& sp, int b) {
         r.n = sp.rows_each;
         r.start = b * r.n;
     }
-    const int most = static_cast<int>(min(static_cast<long long>(a.width) * a.page_size, static_cast<long long>(kMaxLength)));
+    const int most = static_cast<int>(min(static_cast<long long>(a.width) * a.page_size,
+                                          static_cast<long long>(a.pass == kPrefixes ? kMostShared : kMaxLength)));
     if (len < 0 || len > most) record_status(a.status, kStatusInvalid);
     r.len = min(max(len, 0), most);
     const long long low = a.window > 0 ? static_cast<long long>(r.len) - r.n - a.window + 1 : 0;
     r.low = static_cast<int>(max(low, 0ll));
+    if (a.pass == kPrefixes && r.len == 0) r.n = 0;
+    if (a.pass == kOwn) r.low = a.low[b];
+    // Every row sees all of a prefix.
+    r.before = a.pass == kPrefixes ? r.len : r.len - r.n;
     // A request without tokens still has its rows of zeros to write: one tile.
     r.tiles = max(1, (r.len + TILE - 1) / TILE - r.low / TILE);
     r.row_tiles = (r.n * sp.G + ROWS - 1) / ROWS;
@@ -100,6 +112,35 @@ __device__ __forceinline__ long long units(const AttnArgs& a, const Request& r) 
 __device__ __forceinline__ long long quotient(long long x, int y) {
     return x >> 32 ? static_cast<long long>(static_cast<unsigned long long>(x) / static_cast<unsigned>(y))
                    : static_cast<long long>(static_cast<unsigned>(x) / static_cast<unsigned>(y));
+}
+
+// kPrefixes: the first token that each request of the batch reads by itself.  That is its group's prefix length, where
+// all of its rows stand behind the prefix; any other request reads all of its tokens.
+__device__ __forceinline__ void find_low(const SplitArgs& sp) {
+    const AttnArgs& a = sp.a;
+    const int T = static_cast<int>(a.T);
+    const long long most = min(static_cast<long long>(a.width) * a.page_size, static_cast<long long>(kMostShared));
+    for (int b = blockIdx.x * blockDim.x + threadIdx.x; b < a.requests; b += gridDim.x * blockDim.x) {
+        int lo = 0, hi = a.B;  // the last group that begins at b or before (or the first)
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (a.group_starts[mid] <= b)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        int low = 0;
+        if (a.group_starts[lo] <= b && b < a.group_starts[lo + 1]) {
+            int n = sp.rows_each;
+            if (a.starts) {
+                const int start = min(max(a.starts[b], 0), T);
+                n = min(max(a.starts[b + 1], start), T) - start;
+            }
+            const int prefix = static_cast<int>(min(static_cast<long long>(max(a.lens[lo], 0)), most));
+            if (static_cast<long long>(a.own_lens[b]) - n >= prefix) low = prefix;
+        }
+        a.low[b] = low;
+    }
 }
 
 // How `total` units are cut into n pieces: the first `longer` of them have one
@@ -123,7 +164,8 @@ struct Cut {
 // `tiles`, for the rows from row0 on (of `rows`) of head h of request b.
 struct Item {
     int b, h, row0, rows;
-    int start, n, len;
+    int start, n, before;
+    bool shared;     // the rows' sums over a shared prefix join
     int tok0, tok1;
     int tile0, tile1, tiles;
     long long unit;  // the item's first
@@ -211,7 +253,8 @@ struct Walk {
             s.rows = rq.n * sp.G;
             s.start = rq.start;
             s.n = rq.n;
-            s.len = rq.len;
+            s.before = rq.before;
+            s.shared = sp.a.pass == kOwn && rq.low > 0;
             s.tiles = rq.tiles;
             const int low_tile = rq.low / TILE;
             s.tok0 = max(rq.low, (low_tile + s.tile0) * TILE);
@@ -223,14 +266,45 @@ struct Walk {
 };
 
 // ------------------------------------------------------------------- output
-// n values of a row's output from column col on: `v` times 1 / `l`.  A row that
-// sees nothing is zeros; one whose scores are all −∞ has no value (0 / 0).
-__device__ __forceinline__ void put_row(const SplitArgs& sp, const Item& it, int row, int col, const float* v, int n, float l) {
-    const int j = sp.over_G(row);
-    const bool none = it.len - it.n + j < 0;
+// Sums over a row's prefix and over its own tokens on one reference.
+struct Joined {
+    float own, prefix;  // factors of the two
+    float sum;          // of the weights
+
+    __device__ __forceinline__ Joined(const SplitArgs& sp, size_t row, float m, float l) {
+        const float2 p = __ldcg(sp.a.prefix_stats + row);
+        const float top = fmaxf(m, p.x), ref = top == -INFINITY ? 0.f : top;
+        own = ex2(m - ref);
+        prefix = ex2(p.x - ref);
+        sum = l * own + p.y * prefix;
+    }
+};
+
+// n values of a row's output from column col on: `v` over `l`, weights of
+// reference m.  A row that sees nothing is zeros; one whose scores are all −∞
+// has no value (0 / 0).
+__device__ __forceinline__ void put_row(const SplitArgs& sp, const Item& it, int row, int col, const float* v, int n, float m, float l) {
+    const int j = sp.over_G(row), head = it.h * sp.G + row - j * sp.G;
+    if (sp.a.pass == kPrefixes || it.shared) {
+        const size_t at = static_cast<size_t>(it.start + j) * sp.a.q_heads + head;
+        float* const values = sp.a.prefix_values + at * sp.a.head_dim + col;
+        if (sp.a.pass == kPrefixes) {
+            if (col == 0) sp.a.prefix_stats[at] = make_float2(m + sp.lift, fminf(l, 3e38f));
+            for (int x = 0; x < n; x += 2) *reinterpret_cast<float2*>(values + x) = make_float2(v[x], v[x + 1]);
+            return;
+        }
+        const Joined both(sp, at, m + sp.lift, l);
+        const float f = 1.f / both.sum;
+        __nv_bfloat16* to = sp.a.out.data + (it.start + j) * sp.a.out.token_stride + head * sp.a.out.head_stride + col;
+        for (int x = 0; x < n; x += 2) {
+            const float2 p = __ldcg(reinterpret_cast<const float2*>(values + x));
+            *reinterpret_cast<uint32_t*>(to + x) = pack_bf16((v[x] * both.own + p.x * both.prefix) * f, (v[x + 1] * both.own + p.y * both.prefix) * f);
+        }
+        return;
+    }
+    const bool none = it.before + j < 0;
     const float f = 1.f / l;
-    __nv_bfloat16* to = sp.a.out.data + (it.start + j) * sp.a.out.token_stride +
-                        (it.h * sp.G + row - j * sp.G) * sp.a.out.head_stride + col;
+    __nv_bfloat16* to = sp.a.out.data + (it.start + j) * sp.a.out.token_stride + head * sp.a.out.head_stride + col;
     for (int x = 0; x < n; x += 2) *reinterpret_cast<uint32_t*>(to + x) = none ? 0u : pack_bf16(v[x] * f, v[x + 1] * f);
 }
 
@@ -339,7 +413,7 @@ struct Parts {
                 const float l_row = __shfl_sync(~0u, ll, y * NP), m_row = __shfl_sync(~0u, mm, y * NP);
                 if (it.row0 + r + y >= it.rows) continue;
                 if (last) {
-                    if (lane * V < sp.a.head_dim) put_row(sp, it, it.row0 + r + y, lane * V, v[y], V, l_row);
+                    if (lane * V < sp.a.head_dim) put_row(sp, it, it.row0 + r + y, lane * V, v[y], V, m_row, l_row);
                 } else {
                     float* to = at(k0);
                     if (lane == 0) to[r + y] = m_row, to[ROWS + r + y] = fminf(l_row, 3e38f);

@@ -162,6 +162,7 @@ __global__ void __launch_bounds__(Shape<D, Q8>::kThreads, 1) attn_tc_kernel(cons
         mbar_init(smem_addr(&s_queries), kSoftmaxWarps * 32);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    if (a.pass == kPrefixes) find_low(sp);
     Walk<TT, kRows, kFixed> walk;
     if (!walk.template find<S::kThreads>(sp)) return;
     if (warp == kMmaWarp) tmem_alloc(smem_addr(&s_tmem), kTmemCols);
@@ -393,11 +394,11 @@ __global__ void __launch_bounds__(Shape<D, Q8>::kThreads, 1) attn_tc_kernel(cons
             const int base0 = it.tok0 & ~15, tiles = tiles_of<TT>(it);
             const int row = it.row0 + tid, j = sp.over_G(row);
             const bool live = row < it.rows;
-            const int see_hi = live ? it.len - it.n + j + 1 : 0x7fffffff;  // tokens that the row sees
+            const int see_hi = live ? it.before + j + 1 : 0x7fffffff;  // tokens that the row sees
             const int see_lo = live && a.window > 0 ? static_cast<int>(max(0ll, static_cast<long long>(see_hi) - a.window)) : 0;
             // Tokens before all_hi and from all_lo on are seen by every row of the item.
-            const int all_hi = it.len - it.n + sp.over_G(it.row0) + 1;
-            const int all_lo = a.window > 0 ? static_cast<int>(max(0ll, static_cast<long long>(it.len) - it.n +
+            const int all_hi = it.before + sp.over_G(it.row0) + 1;
+            const int all_lo = a.window > 0 ? static_cast<int>(max(0ll, static_cast<long long>(it.before) +
                                                                           sp.over_G(min(it.row0 + kRows, it.rows) - 1) + 1 - a.window)) : 0;
             if (tiles > 0) {
                 cp_async_wait_all();
@@ -587,7 +588,7 @@ __global__ void __launch_bounds__(Shape<D, Q8>::kThreads, 1) attn_tc_kernel(cons
             if (more) ask(after);
             if (tiles > 0) wait_or_report(smem_addr(&s_values[(tile - 1) & 1]), (tile - 1) >> 1 & 1, alive, a.status);
             tc_fence_after();
-            const bool whole = it.whole(), none = it.len - it.n + j < 0;
+            const bool whole = it.whole(), none = it.before + j < 0;
             const Parts<kRows, D> parts(sp, walk, it, kFixed);
             float* const part = parts.at(static_cast<int>(blockIdx.x) - parts.first);
             if (!whole && live) {
@@ -596,7 +597,31 @@ __global__ void __launch_bounds__(Shape<D, Q8>::kThreads, 1) attn_tc_kernel(cons
             }
             // A row that sees nothing is zeros; one whose scores are all −∞ has no value (0 · 1 / 0).
             __nv_bfloat16* const to = a.out.data + (live ? (it.start + j) * a.out.token_stride + (it.h * sp.G + row - j * sp.G) * a.out.head_stride : 0);
-            auto put = [&](int c, const uint32_t (&v)[32], float f) {  // 32 of the row's values from column c on, times f
+            const size_t in_prefix = static_cast<size_t>(it.start + j) * a.q_heads + it.h * sp.G + row - j * sp.G;
+            // 32 of the row's values from column c on, weights of reference top with the sum `total`
+            auto put = [&](int c, uint32_t (&v)[32], float top, float total) {
+                if (a.pass == kPrefixes || it.shared) {
+                    float* const values = a.prefix_values + in_prefix * a.head_dim + c;
+                    if (a.pass == kPrefixes) {
+                        if (c == 0) a.prefix_stats[in_prefix] = make_float2(top, fminf(total, 3e38f));
+#pragma unroll
+                        for (int x = 0; x < 32; x += 4)
+                            if (c + x < a.head_dim) *reinterpret_cast<uint4*>(values + x) = make_uint4(v[x], v[x + 1], v[x + 2], v[x + 3]);
+                        return;
+                    }
+                    const Joined both(sp, in_prefix, top, total);
+#pragma unroll
+                    for (int x = 0; x < 32; x += 4)
+                        if (c + x < a.head_dim) {
+                            const float4 p = __ldcg(reinterpret_cast<const float4*>(values + x));
+                            v[x] = __float_as_uint(__uint_as_float(v[x]) * both.own + p.x * both.prefix);
+                            v[x + 1] = __float_as_uint(__uint_as_float(v[x + 1]) * both.own + p.y * both.prefix);
+                            v[x + 2] = __float_as_uint(__uint_as_float(v[x + 2]) * both.own + p.z * both.prefix);
+                            v[x + 3] = __float_as_uint(__uint_as_float(v[x + 3]) * both.own + p.w * both.prefix);
+                        }
+                    total = both.sum;
+                }
+                const float f = 1.f / total;
 #pragma unroll
                 for (int x = 0; x < 32; x += 8) {
                     uint32_t y[4];
@@ -614,7 +639,7 @@ __global__ void __launch_bounds__(Shape<D, Q8>::kThreads, 1) attn_tc_kernel(cons
 #pragma unroll
                     for (int x = 0; x < 32; ++x) part[(2 + c + x) * kRows + tid] = __uint_as_float(v[x]);
                 } else if (live) {
-                    put(c, v, 1.f / l);
+                    put(c, v, m * unit, l);
                 }
                 __syncwarp();
             }
@@ -661,7 +686,7 @@ __global__ void __launch_bounds__(Shape<D, Q8>::kThreads, 1) attn_tc_kernel(cons
                             add(k + 1, u1);
                         }
                         ll = sum;
-                        if (live && last) put(c, v, 1.f / ll);
+                        if (live && last) put(c, v, mm, ll);
                         if (live && !last)
 #pragma unroll
                             for (int x = 0; x < 32; ++x) parts.at(k0)[(2 + c + x) * kRows + tid] = __uint_as_float(v[x]);

@@ -53,6 +53,11 @@ __device__ __forceinline__ int row_number(long long sum) { return static_cast<in
 // chain of latencies (two loads, two barriers, a search) at every size that
 // fits a cache: 3.5 µs for a decode step of 64 requests, 7.0 for 1000 requests
 // between verify passes, 5.3 for prompts of 37 requests.
+//
+// HELD: pages have holders.  A page that is taken has one; those that requests
+// let go of are the next kernel's work, since every CTA looks at the holders
+// that pages have before the call.
+template <bool HELD>
 __global__ void __launch_bounds__(kPagesThreads) kv_pages_kernel(KvPagesArgs a) {
     __shared__ long long s_start[kPagesThreads], s_back[kPagesThreads], s_first[kPagesThreads];
     __shared__ int s_len[kPagesThreads], s_have[kPagesThreads], s_want[kPagesThreads];
@@ -86,8 +91,13 @@ __global__ void __launch_bounds__(kPagesThreads) kv_pages_kernel(KvPagesArgs a) 
             valid = len >= 0 && target >= 0 && len <= most;
             if (!valid) record_status(a.status, kStatusInvalid);
         }
-        const bool fits = valid && target <= most;
         const int have = valid && len > 0 ? page_index(len - 1) + 1 : 0;
+        bool fits = valid && target <= most;
+        if (HELD && fits && target > len && len > 0 && len < static_cast<long long>(have) * a.page_size) {
+            // The request's own tokens would go on in a page that others read.
+            const int page = a.table[(base + tid) * a.table_stride + have - 1];
+            if (page >= 0 && page < a.pages && a.holders[page] > 1) fits = false;
+        }
         const int want = valid && target > 0 ? page_index(target - 1) + 1 : 0;
         const Sums own = {valid ? max(target - len, 0) : 0, fits ? max(want - have, 0) : 0, max(have - want, 0)};
         Sums sum = warp_scan(own, lane);
@@ -139,6 +149,7 @@ __global__ void __launch_bounds__(kPagesThreads) kv_pages_kernel(KvPagesArgs a) 
                 // request that grows past its last page has one such token in
                 // each new page, since its own last page is full by then.
                 if (fresh >= 0 && place == 0) *entry = page;
+                if (HELD && fresh >= 0 && place == 0 && page >= 0 && page < a.pages) a.holders[page] = 1;
                 if (page >= 0 && page < a.pages)
                     slot = static_cast<long long>(page) * a.page_size + place;
                 else
@@ -147,7 +158,7 @@ __global__ void __launch_bounds__(kPagesThreads) kv_pages_kernel(KvPagesArgs a) 
             a.slots[t] = slot;
             a.positions[t] = pos;
         }
-        for (long long r = carry.back + static_cast<long long>(blockIdx.x) * threads + tid; r < total.back; r += step) {
+        for (long long r = carry.back + static_cast<long long>(blockIdx.x) * threads + tid; !HELD && r < total.back; r += step) {
             const int i = last_at_most(s_back, n, r);
             // The table may claim more pages than the pool has; each entry of the ring is then written again.
             *ring(tail_at, r < a.pages ? r : r % a.pages) = a.table[(base + i) * a.table_stride + s_want[i] + (r - s_back[i])];
@@ -163,16 +174,11 @@ __global__ void __launch_bounds__(kPagesThreads) kv_pages_kernel(KvPagesArgs a) 
     if (blockIdx.x == 0 && tid == 0) {
         a.starts[a.B] = row_number(carry.grow);
         a.range_out[0] = head + used;
-        a.range_out[1] = tail + carry.back;
+        if (!HELD) a.range_out[1] = tail + carry.back;
     }
 }
 
 // ------------------------------------------------------------------ append
-// Axis of each frequency (rotary ≤ 256), two bits each, eight to a word.
-struct Axes {
-    uint16_t of[16];
-};
-
 constexpr int kManyThreads = 64, kManyTokens = 8;  // (tokens to an SM)
 constexpr int kBatch = 4;  // rows that a lane has in flight
 
@@ -357,22 +363,19 @@ cudaError_t launch_kv_pages(KvPagesArgs a, const DeviceInfo& dev, cudaStream_t s
     const int threads = a.B <= 256 ? 256 : kPagesThreads;
     const int64_t blocks = (a.T + threads - 1) / threads;
     const int grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(blocks, dev.sm_count * (kPagesThreads / threads))));
-    kv_pages_kernel<<<grid, threads, 0, stream>>>(a);
-    return cudaGetLastError();
+    if (!a.holders) {
+        kv_pages_kernel<false><<<grid, threads, 0, stream>>>(a);
+        return cudaGetLastError();
+    }
+    kv_pages_kernel<true><<<grid, threads, 0, stream>>>(a);
+    const cudaError_t err = cudaGetLastError();
+    return err != cudaSuccess ? err : launch_kv_release(a, stream);
 }
 
 cudaError_t launch_kv_append(KvAppendArgs a, const int32_t sections[4], bool cycled, bool q8, const DeviceInfo& dev,
                              cudaStream_t stream) {
     divide_by(a.page_size, &a.page_mul, &a.page_shift);
-    Axes axes = {};
-    int used[4] = {0, 0, 0, 0};
-    for (int i = 0, turn = 0; i < a.rotary / 2; ++i) {
-        while (used[turn % a.axes] == sections[turn % a.axes]) ++turn;
-        const int axis = turn % a.axes;
-        axes.of[i >> 3] |= static_cast<uint16_t>(axis << (2 * (i & 7)));
-        ++used[axis];
-        if (cycled) ++turn;
-    }
+    const Axes axes = axes_of(a.rotary / 2, a.axes, sections, cycled);
     // Small CTAs wait less for one another between tokens, large ones have a token's rows in flight sooner.  56 rows
     // of 128: 208 tokens take 3.7 µs with 256 threads and 5.9 with 64, 800 take 6.6 and 7.2, 1600 14.1 and 12.4,
     // 5000 34 and 30, 16001 100 and 78 (81 with 128).

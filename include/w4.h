@@ -457,6 +457,90 @@ int w4_kv_pages(const int32_t* lens, const int32_t* target, int32_t B, int32_t p
                 int64_t* free_range_out, void* stream);
 
 /*
+ * w4_kv_pages_held — w4_kv_pages for pages that several requests may hold
+ * (w4_kv_fork).
+ *   holders  in/out: int32 [pages], the table entries that a page stands in
+ *                 (within the pages of a request's length); 0: free
+ * A page that is taken has one holder then.  A request that gives a page back
+ * lets go of it; it goes to the ring when nobody holds it any more, in the
+ * order of the entries that let go last.  A request whose last page is not
+ * full and has other holders as well does not grow into it: it is not granted
+ * and asks for no pages.  (Holders as they were before the call.)
+ * Out of range: a page that a request lets go of and nobody holds stays as it
+ * is.  Two launches; the rest as for w4_kv_pages.
+ */
+int w4_kv_pages_held(const int32_t* lens, const int32_t* target, int32_t B, int32_t page_size, int32_t* free_pages,
+                     int64_t pages, const int64_t* free_range, int32_t* block_table, int64_t table_stride,
+                     int32_t width, int64_t T, int32_t* holders, int32_t* new_lens, int32_t* starts, int64_t* slots,
+                     int32_t* positions, int64_t* free_range_out, void* stream);
+
+/*
+ * w4_kv_fork — requests that begin as the first tokens of others.
+ *   lens           in : int32 [B]
+ *   source         in : int32 [B], the request whose tokens request b takes
+ *                       over; −1: none.  Request b has length 0 then.
+ *   keep           in : int32 [B], how many tokens, at most lens[source[b]]
+ *   block_table    in/out: int32 [B, width], row stride table_stride
+ *   holders        in/out: int32 [pages], as for w4_kv_pages_held
+ *   free_pages, free_range  in : as for w4_kv_pages
+ *   new_lens       out: int32 [B]
+ *   copies         out: int32 [3, B] for w4_kv_copy: page, its copy, tokens;
+ *                       −1, −1, 0 where nothing is copied
+ *   free_range_out out: int64 [2]
+ * The pages that keep[b] tokens fill are shared: one more holder each.  Of a
+ * page that they fill in part, request b gets a page of its own from the ring,
+ * in request order, and the tokens are to be copied (in the cache of every
+ * layer).  A request whose page the ring does not have is not granted: it keeps
+ * its length of 0.
+ * Out of range: a source that is no request, a request that has tokens already,
+ * tokens that the source does not have, or a length past the table: not
+ * granted.  A page id outside [0, pages) is taken over as it is, and not
+ * copied.  Deterministic; one launch.
+ */
+int w4_kv_fork(const int32_t* lens, const int32_t* source, const int32_t* keep, int32_t B, int32_t page_size,
+               int32_t* block_table, int64_t table_stride, int32_t width, int32_t* holders, const int32_t* free_pages,
+               int64_t pages, const int64_t* free_range, int32_t* new_lens, int32_t* copies, int64_t* free_range_out,
+               void* stream);
+
+/*
+ * w4_kv_compact — moves the pages in use (holders above 0), U of them, to the
+ * ids 0 to U − 1: the k-th page in use at U or past it goes to the k-th free
+ * one before U; the others stay.  A pool of which only the first part is in
+ * use can be cut off there.
+ *   lens           in : int32 [B]
+ *   block_table    in : int32 [B, width], row stride table_stride
+ *   holders        in : int32 [pages], pages at most 2²⁰
+ *   free_range     in : int64 [2]
+ *   new_table      out: int32 [B, width], row stride new_stride: the table, with
+ *                       the new ids in the entries of each request's length
+ *   new_holders    out: int32 [pages]
+ *   free_pages     out: int32 [pages], the ring: pages U, U + 1, ... from entry
+ *                       free_range[0] on; −1 in the other entries
+ *   free_range_out out: int64 [2]
+ *   copies         out: int32 [3, pages / 2] for w4_kv_copy, moves in order,
+ *                       then −1, −1, 0
+ * Out of range: a length past the table counts as 0; a page id outside
+ * [0, pages), or of a page without holders, stays as it is.  No output
+ * overlaps an input.  Deterministic; one launch.
+ */
+int w4_kv_compact(const int32_t* lens, int32_t B, int32_t page_size, const int32_t* block_table, int64_t table_stride,
+                  int32_t width, const int32_t* holders, int64_t pages, const int64_t* free_range, int32_t* new_table,
+                  int64_t new_stride, int32_t* new_holders, int32_t* free_pages, int64_t* free_range_out,
+                  int32_t* copies, void* stream);
+
+/*
+ * w4_kv_copy — copies tokens of pages to other pages: keys, values and (format
+ * 8) scales.
+ *   copies  in : int32 [3, n]: page copies[0][i], its first copies[2][i] tokens
+ *                (at most page_size) to the same places of page copies[1][i];
+ *                −1 in both: nothing
+ * A page that is copied to and is also copied from, or copied to twice, may
+ * hold any mixture of the rows.  Out of range: page ids outside [0, pages) or a
+ * number of tokens outside [0, page_size]: not copied.
+ */
+int w4_kv_copy(const w4_kv_cache* cache, const int32_t* copies, int32_t n, void* stream);
+
+/*
  * Rotary positions with several axes (time, height, width, ...): frequency i
  * of a token turns by the table row of its position on axis(i).
  *   positions  int32 [axes, T], axis_stride elements apart (0: one position
@@ -504,6 +588,31 @@ typedef struct w4_rope {
 int w4_kv_append(const w4_kv_cache* cache, const w4_rope* rope, int64_t T, int32_t q_heads, const w4_rows* q,
                  const w4_rows* q_out, const w4_rows* k, const w4_rows* v, const int64_t* slots, void* stream);
 
+/* Norm of queries and keys, head by head: y = x · (mean(x²) + eps)^−½ · w over
+ * the head_dim values of a row, with the same w for every head.
+ *   q_weight, k_weight  [head_dim] (q_weight unused where q_heads = 0)
+ *   format              16: bf16 weights, 32: fp32
+ *   eps                 at least 1e-20
+ *   unit_offset         1: the weights count from 1 (w = 1 + weight) */
+typedef struct w4_norm {
+    const void* q_weight;
+    const void* k_weight;
+    int32_t format;
+    float eps;
+    int32_t unit_offset;
+} w4_norm;
+
+/*
+ * w4_kv_append_norm — w4_kv_append of queries and keys that are normalised
+ * before they turn, in the same pass.  Everything up to the result is fp32: the
+ * sum of squares, the normalised values and the turn; one rounding to bf16, or
+ * (format 8, keys) to the row's codes: d and c of the fp32 values by
+ * w4_kv_append's rule.  Values enter the cache as they are.
+ */
+int w4_kv_append_norm(const w4_kv_cache* cache, const w4_rope* rope, const w4_norm* norm, int64_t T, int32_t q_heads,
+                      const w4_rows* q, const w4_rows* q_out, const w4_rows* k, const w4_rows* v,
+                      const int64_t* slots, void* stream);
+
 /*
  * w4_attn_decode — attention of the newest tokens of B requests over their
  * pages: one row per request in decode, K+1 in a verify pass.
@@ -538,6 +647,38 @@ int w4_attn_decode(const w4_kv_cache* cache, int32_t B, int64_t T, int32_t q_hea
                    const w4_rows* out, const int32_t* block_table, int64_t table_stride, int32_t width,
                    const int32_t* lens, const int32_t* starts, float scale, int64_t window, void* workspace,
                    size_t workspace_bytes, void* stream);
+
+/*
+ * w4_attn_decode_shared — w4_attn_decode (without a window) of requests that
+ * share prefixes: the keys and values of a prefix are read once for all of the
+ * rows that stand behind it.
+ *   groups        0: w4_attn_decode
+ *   group_starts  int32 [groups + 1], the requests of a group: group_starts[g]
+ *                 .. group_starts[g+1] − 1; requests before the first group and
+ *                 after the last are on their own
+ *   prefix_table  int32 [groups, prefix_width], row stride prefix_stride: the
+ *                 pages of a group's prefix
+ *   prefix_lens   int32 [groups], its tokens (any number, a page may be filled
+ *                 in part)
+ * The first prefix_lens[g] tokens of a request of group g are those of
+ * prefix_table[g], and lens counts them; its further tokens are in its own
+ * pages, at the places that block_table has for them.  A request whose new
+ * tokens do not all lie behind the prefix (length − rows < prefix_lens) is
+ * attended over its own pages alone, which then need all of its tokens.
+ * Out of range: group_starts that fall or pass B are cut (and rows that two
+ * groups then claim have no meaning); a prefix length past prefix_width ·
+ * page_size (or 2³⁰) counts as that.  T: at most 2³⁰.
+ * workspace: w4_attn_decode_shared_workspace_bytes(...) bytes; the rest as for
+ * w4_attn_decode.  Deterministic.  Two launches.
+ */
+size_t w4_attn_decode_shared_workspace_bytes(const w4_kv_cache* cache, int32_t B, int64_t T, int32_t q_heads,
+                                             int32_t groups);
+int w4_attn_decode_shared(const w4_kv_cache* cache, int32_t B, int64_t T, int32_t q_heads, const w4_rows* q,
+                          const w4_rows* out, const int32_t* block_table, int64_t table_stride, int32_t width,
+                          const int32_t* lens, const int32_t* starts, int32_t groups, const int32_t* group_starts,
+                          const int32_t* prefix_table, int64_t prefix_stride, int32_t prefix_width,
+                          const int32_t* prefix_lens, float scale, void* workspace, size_t workspace_bytes,
+                          void* stream);
 
 /*
  * Every wait inside the library's kernels (mbarrier phases, TMA completion)
