@@ -532,7 +532,7 @@ def _strides(t: torch.Tensor, name: str, dtype: torch.dtype, ndim: int, index: i
     if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != index:
         _typed(t, name, dtype, index)
     strides = t.stride()
-    if len(strides) != ndim or (strides[-1] != 1 and t.shape[-1] > 1):
+    if len(strides) != ndim or (strides[-1] != 1 and t.shape[-1] > 1 and t.numel() > 0):
         raise ValueError(f"{name} must be a {ndim}-D tensor with unit stride in its last dimension")
     return strides
 
