@@ -734,6 +734,9 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
     }
 }
 
+// The parts in a pass's workspace, behind its counters.
+float* partials(void* workspace) { return reinterpret_cast<float*>(static_cast<unsigned long long*>(workspace) + 2 * kMaxCtas); }
+
 int dim_of(int head_dim) { return head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256; }
 
 // Query rows to a key-value head of a request, on the average.
@@ -818,12 +821,18 @@ size_t attn_decode_workspace_bytes(int32_t B, int64_t T, int32_t q_heads, int32_
     return 2 * (kMaxCtas * sizeof(unsigned long long) + (many ? kMaxTcCtas : kMaxCtas) * part * sizeof(float));
 }
 
+// Whether the pass leaves parts of its items for the join.
+static bool in_parts(const AttnArgs& a, bool q8) {
+    const int G = a.q_heads / a.kv_heads;
+    return a.pass == kPrefixes && a.head_dim <= 128 && many_rows(a.B, a.T, G, a.kv_heads, dim_of(a.head_dim), q8);
+}
+
 cudaError_t launch_attn_decode(AttnArgs a, bool q8, void* workspace, const DeviceInfo& dev, cudaStream_t stream) {
     divide_by(a.page_size, &a.page_mul, &a.page_shift);
     SplitArgs sp = {};
     sp.a = a;
     sp.arrived = static_cast<unsigned long long*>(workspace);
-    sp.partial = reinterpret_cast<float*>(sp.arrived + 2 * kMaxCtas);
+    sp.partial = partials(workspace);
     sp.G = a.q_heads / a.kv_heads;
     divide_by(sp.G, &sp.G_mul, &sp.G_shift);
     sp.rows_each = static_cast<int>(a.T / (a.pass == kPrefixes ? a.requests : a.B));
@@ -831,7 +840,8 @@ cudaError_t launch_attn_decode(AttnArgs a, bool q8, void* workspace, const Devic
     // largest score is then that of the unscaled products, and hidden ones stay at −∞.
     sp.scale_log2 = std::max(std::fabs(a.scale) * 1.4426950408889634f, 1e-30f);
     sp.flip = a.scale < 0.f ? 0x80008000u : 0u;
-    if (many_rows(a.B, a.T, sp.G, a.kv_heads, dim_of(a.head_dim), q8)) return launch_attn_tc(sp, q8, dev, stream);
+    if (many_rows(a.B, a.T, sp.G, a.kv_heads, dim_of(a.head_dim), q8))
+        return in_parts(a, q8) ? launch_attn_prefix(sp, q8, dev, stream) : launch_attn_tc(sp, q8, dev, stream);
     sp.lift = q8 ? kLift : 0.f;
     return q8 ? run_dim<true>(sp, dev, stream) : run_dim<false>(sp, dev, stream);
 }
@@ -840,13 +850,13 @@ namespace {
 size_t padded(size_t bytes) { return (bytes + 255) / 256 * 256; }
 }  // namespace
 
-// Workspaces of the two passes, first own tokens, and the rows' sums over the prefixes.
+// Workspaces of the two passes, first own tokens, and the rows' sums of both.
 size_t attn_shared_workspace_bytes(int32_t B, int64_t T, int32_t q_heads, int32_t kv_heads, int32_t head_dim, bool q8,
                                    int32_t groups) {
     const size_t rows = static_cast<size_t>(T) * q_heads;
     return padded(attn_decode_workspace_bytes(groups, T, q_heads, kv_heads, head_dim, q8)) +
            padded(attn_decode_workspace_bytes(B, T, q_heads, kv_heads, head_dim, q8)) + padded(static_cast<size_t>(B) * 4) +
-           padded(rows * sizeof(float2)) + rows * head_dim * sizeof(float);
+           2 * padded(rows * sizeof(float4)) + 2 * padded(rows * head_dim * sizeof(float));
 }
 
 cudaError_t launch_attn_shared(AttnArgs a, const SharedArgs& shared, bool q8, void* workspace, const DeviceInfo& dev,
@@ -861,8 +871,6 @@ cudaError_t launch_attn_shared(AttnArgs a, const SharedArgs& shared, bool q8, vo
     void* const second = take(attn_decode_workspace_bytes(a.B, a.T, a.q_heads, a.kv_heads, a.head_dim, q8));
     const size_t rows = static_cast<size_t>(a.T) * a.q_heads;
     a.low = static_cast<int32_t*>(take(static_cast<size_t>(a.B) * 4));
-    a.prefix_stats = static_cast<float2*>(take(rows * sizeof(float2)));
-    a.prefix_values = static_cast<float*>(take(rows * a.head_dim * sizeof(float)));
     AttnArgs p = a;
     p.pass = kPrefixes;
     p.requests = a.B;
@@ -873,10 +881,28 @@ cudaError_t launch_attn_shared(AttnArgs a, const SharedArgs& shared, bool q8, vo
     p.table_stride = shared.table_stride;
     p.width = shared.width;
     p.lens = shared.lens;
-    const cudaError_t err = launch_attn_decode(p, q8, first, dev, stream);
-    if (err != cudaSuccess) return err;
+    p.sums = static_cast<float4*>(take(rows * sizeof(float4)));
+    p.sum_values = static_cast<float*>(take(rows * a.head_dim * sizeof(float)));
     a.pass = kOwn;
-    return launch_attn_decode(a, q8, second, dev, stream);
+    a.sums = static_cast<float4*>(take(rows * sizeof(float4)));
+    a.sum_values = static_cast<float*>(take(rows * a.head_dim * sizeof(float)));
+    cudaError_t err = launch_attn_decode(p, q8, first, dev, stream);
+    if (err == cudaSuccess) err = launch_attn_decode(a, q8, second, dev, stream);
+    if (err != cudaSuccess) return err;
+    JoinArgs j = {};
+    j.out = a.out;
+    j.B = a.B;
+    j.T = static_cast<int32_t>(a.T);
+    j.q_heads = a.q_heads;
+    j.head_dim = a.head_dim;
+    j.starts = a.starts;
+    j.own = a.sums;
+    j.prefix = p.sums;
+    j.own_values = a.sum_values;
+    j.prefix_values = p.sum_values;
+    j.partial = partials(first);
+    j.pieces = in_parts(p, q8) ? kMaxTcCtas : 0;
+    return launch_attn_join(j, stream);
 }
 
 }  // namespace w4

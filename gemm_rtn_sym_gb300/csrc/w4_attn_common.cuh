@@ -266,43 +266,25 @@ struct Walk {
 };
 
 // ------------------------------------------------------------------- output
-// Sums over a row's prefix and over its own tokens on one reference.
-struct Joined {
-    float own, prefix;  // factors of the two
-    float sum;          // of the weights
-
-    __device__ __forceinline__ Joined(const SplitArgs& sp, size_t row, float m, float l) {
-        const float2 p = __ldcg(sp.a.prefix_stats + row);
-        const float top = fmaxf(m, p.x), ref = top == -INFINITY ? 0.f : top;
-        own = ex2(m - ref);
-        prefix = ex2(p.x - ref);
-        sum = l * own + p.y * prefix;
-    }
-};
+// What a pass of a call with shared prefixes leaves of a row.
+__device__ __forceinline__ float4 row_sums(const SplitArgs& sp, const Item& it, bool none, float m, float l) {
+    const int kind = sp.a.pass == kPrefixes ? 0 : none ? kRowEmpty : it.shared ? kRowShared : kRowAlone;
+    return make_float4(m + sp.lift, fminf(l, 3e38f), __int_as_float(kind), 0.f);
+}
 
 // n values of a row's output from column col on: `v` over `l`, weights of
 // reference m.  A row that sees nothing is zeros; one whose scores are all −∞
 // has no value (0 / 0).
 __device__ __forceinline__ void put_row(const SplitArgs& sp, const Item& it, int row, int col, const float* v, int n, float m, float l) {
     const int j = sp.over_G(row), head = it.h * sp.G + row - j * sp.G;
-    if (sp.a.pass == kPrefixes || it.shared) {
+    const bool none = it.before + j < 0;
+    if (sp.a.pass != kAlone) {
         const size_t at = static_cast<size_t>(it.start + j) * sp.a.q_heads + head;
-        float* const values = sp.a.prefix_values + at * sp.a.head_dim + col;
-        if (sp.a.pass == kPrefixes) {
-            if (col == 0) sp.a.prefix_stats[at] = make_float2(m + sp.lift, fminf(l, 3e38f));
-            for (int x = 0; x < n; x += 2) *reinterpret_cast<float2*>(values + x) = make_float2(v[x], v[x + 1]);
-            return;
-        }
-        const Joined both(sp, at, m + sp.lift, l);
-        const float f = 1.f / both.sum;
-        __nv_bfloat16* to = sp.a.out.data + (it.start + j) * sp.a.out.token_stride + head * sp.a.out.head_stride + col;
-        for (int x = 0; x < n; x += 2) {
-            const float2 p = __ldcg(reinterpret_cast<const float2*>(values + x));
-            *reinterpret_cast<uint32_t*>(to + x) = pack_bf16((v[x] * both.own + p.x * both.prefix) * f, (v[x + 1] * both.own + p.y * both.prefix) * f);
-        }
+        if (col == 0) sp.a.sums[at] = row_sums(sp, it, none, m, l);
+        float* const to = sp.a.sum_values + at * sp.a.head_dim + col;
+        for (int x = 0; x < n; x += 2) *reinterpret_cast<float2*>(to + x) = make_float2(v[x], v[x + 1]);
         return;
     }
-    const bool none = it.before + j < 0;
     const float f = 1.f / l;
     __nv_bfloat16* to = sp.a.out.data + (it.start + j) * sp.a.out.token_stride + head * sp.a.out.head_stride + col;
     for (int x = 0; x < n; x += 2) *reinterpret_cast<uint32_t*>(to + x) = none ? 0u : pack_bf16(v[x] * f, v[x + 1] * f);

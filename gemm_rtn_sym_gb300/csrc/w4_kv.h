@@ -164,18 +164,21 @@ struct AttnArgs {
     unsigned* status;
     uint32_t page_mul;  // divide_by(page_size)
     int32_t page_shift;
-    // Prefixes that groups of requests share take two passes: kPrefixes, whose "requests" are the groups (B, table and
-    // lens are theirs), leaves each row's sums over the prefix behind, and kOwn, over each request's tokens from low[b]
-    // on, joins them to its own.
+    // Prefixes that groups of requests share take two passes, each of which leaves its rows' sums behind, and a kernel that
+    // joins them: kPrefixes, whose "requests" are the groups (B, table and lens are theirs), and kOwn, over each request's
+    // tokens from low[b] on.
     int32_t pass;
     int32_t requests;             // kPrefixes: of the batch
     const int32_t* group_starts;  // kPrefixes: [B + 1], requests of each group
     const int32_t* own_lens;      // kPrefixes: lens of the batch
     int32_t* low;                 // [requests], written by kPrefixes; 0: nothing shared
-    float2* prefix_stats;         // [T · q_heads] reference and sum of the weights
-    float* prefix_values;         // [T · q_heads, head_dim]
+    // [T · q_heads]: reference and sum of the weights.  kOwn: what the row is, a RowKind.  kPrefixes: parts that the sums
+    // are still in (0: none), and where the first of them is.
+    float4* sums;
+    float* sum_values;  // [T · q_heads, head_dim]
 };
 enum : int32_t { kAlone = 0, kPrefixes = 1, kOwn = 2 };
+enum RowKind : int32_t { kRowAlone = 0, kRowShared = 1, kRowEmpty = 2 };
 // Tokens of a prefix, and rows of a batch that shares them: their sum stays below 2³¹.
 constexpr int32_t kMostShared = 1 << 30;
 
