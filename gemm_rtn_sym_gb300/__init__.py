@@ -2,7 +2,8 @@
 for NVIDIA GB300 (sm_103a).
 
 A thin ctypes binding over the C ABI in include/w4.h (libw4.so, built in-tree by
-``gemm_rtn_sym_gb300.build``).  The functions here only check and marshal
+``gemm_rtn_sym_gb300.build``; calls whose kernels last microseconds go through a
+compiled module, csrc/binding.cpp, where their tensors are what they should be).  The functions here only check and marshal
 arguments: torch tensors provide device memory and the current CUDA stream;
 every step of the computation runs in the library's CUDA kernels.  There is no
 CPU fallback: if libw4.so is missing or a CUDA device is absent, calls raise.
@@ -10,6 +11,7 @@ CPU fallback: if libw4.so is missing or a CUDA device is absent, calls raise.
 from __future__ import annotations
 
 import ctypes
+import importlib
 import os
 import threading
 
@@ -36,6 +38,7 @@ W4_PATH_AUTO, W4_PATH_SMALL_M, W4_PATH_TENSOR = 0, 1, 2
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _lib = None
+_fast = None
 _lock = threading.Lock()
 
 _i64, _i32, _vp, _sz = ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p, ctypes.c_size_t
@@ -140,8 +143,8 @@ def library_path() -> str:
 
 
 def load() -> ctypes.CDLL:
-    """Load libw4.so (built by gemm_rtn_sym_gb300.build); raises if absent."""
-    global _lib
+    """Load libw4.so (built by gemm_rtn_sym_gb300.build) and the compiled module beside it; raises if absent."""
+    global _lib, _fast
     with _lock:
         if _lib is None:
             path = library_path()
@@ -153,6 +156,10 @@ def load() -> ctypes.CDLL:
             for name, (res, args) in _SIGNATURES.items():
                 fn = getattr(lib, name)
                 fn.restype, fn.argtypes = res, args
+            try:
+                _fast = importlib.import_module("._binding", __name__)
+            except ImportError as e:
+                raise RuntimeError(f"{_PKG}/_binding.so cannot be loaded: build it with `python -m gemm_rtn_sym_gb300.build`") from e
             _lib = lib
     return _lib
 
@@ -589,6 +596,13 @@ def _call(name: str, index: int, *args) -> None:
         raise W4Error(status, name)
 
 
+def _compiled():
+    """The compiled module: its functions return NotImplemented where a call is not the usual one."""
+    if _fast is None:
+        load()
+    return _fast
+
+
 def w4_kv_pages(lens: torch.Tensor, target: torch.Tensor, block_table: torch.Tensor, free_pages: torch.Tensor,
                 free_range: torch.Tensor, page_size: int, tokens: int, new_lens: torch.Tensor | None = None,
                 starts: torch.Tensor | None = None, slots: torch.Tensor | None = None,
@@ -600,6 +614,11 @@ def w4_kv_pages(lens: torch.Tensor, target: torch.Tensor, block_table: torch.Ten
     [tokens], free_range_out int64 [2]).  `tokens`: the new tokens of all requests together.  holders (int32 [pages],
     in and out): the table entries that each page stands in, where requests share pages (w4_kv_fork); a page goes back to
     the ring when its last holder lets go."""
+    if holders is not None:
+        done = _compiled().kv_pages_held(lens, target, block_table, free_pages, free_range, page_size, tokens, holders,
+                                        new_lens, starts, slots, positions, free_range_out)
+        if done is not NotImplemented:
+            return done
     index = _device_index(block_table, "block_table")
     stride = _strides(block_table, "block_table", torch.int32, 2, index)[0]
     B, width = block_table.shape
@@ -648,6 +667,10 @@ def w4_kv_fork(lens: torch.Tensor, source: torch.Tensor, keep: torch.Tensor, blo
     are shared, with one more holder (int32 [pages]) each; a page filled in part gets a page of its own from the ring,
     to be copied.  Updates block_table (int32 [B, width]) and holders, and returns (new_lens int32 [B], copies int32
     [3, B] for w4_kv_copy, free_range_out int64 [2])."""
+    done = _compiled().kv_fork(lens, source, keep, block_table, holders, free_pages, free_range, page_size, new_lens, copies,
+                              free_range_out)
+    if done is not NotImplemented:
+        return done
     index = _device_index(block_table, "block_table")
     stride = _strides(block_table, "block_table", torch.int32, 2, index)[0]
     B, width = block_table.shape
@@ -668,6 +691,10 @@ def w4_kv_compact(lens: torch.Tensor, block_table: torch.Tensor, holders: torch.
                   copies: torch.Tensor | None = None):
     """Moves the pages in use (holders above 0) to the lowest ids.  Returns (new_table int32 [B, width], new_holders and
     the ring free_pages int32 [pages], free_range_out int64 [2], copies int32 [3, pages // 2] for w4_kv_copy)."""
+    done = _compiled().kv_compact(lens, block_table, holders, free_range, page_size, new_table, new_holders, free_pages,
+                                 free_range_out, copies)
+    if done is not NotImplemented:
+        return done
     index = _device_index(block_table, "block_table")
     stride = _strides(block_table, "block_table", torch.int32, 2, index)[0]
     B, width = block_table.shape
@@ -686,6 +713,8 @@ def w4_kv_copy(k_cache: torch.Tensor, v_cache: torch.Tensor, copies: torch.Tenso
                v_scales: torch.Tensor | None = None) -> None:
     """Copies the first copies[2][i] tokens of page copies[0][i] to page copies[1][i] (int32 [3, n]; −1, −1: nothing), keys,
     values and scales."""
+    if _compiled().kv_copy(k_cache, v_cache, copies, k_scales, v_scales) is None:
+        return
     index = _device_index(k_cache, "k_cache")
     cache = _kv_cache(k_cache, v_cache, k_scales, v_scales, index)
     _typed(copies, "copies", torch.int32, index)
@@ -764,6 +793,10 @@ def w4_kv_append_norm(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, 
     """w4_kv_append of queries and keys normalised head by head before they turn: x · (mean(x²) + eps)^−½ · w over each
     row's head_dim values, with q_weight and k_weight (bf16 or fp32 [head_dim]; unit_offset: w = 1 + weight) for all
     heads; one rounding in all."""
+    done = _compiled().kv_append_norm(q, k, v, q_weight, k_weight, positions, cos, sin, k_cache, v_cache, slots, eps,
+                                     unit_offset, sections, cycled, paired, k_scales, v_scales, q_out)
+    if done is not NotImplemented:
+        return done[0]
     return _append("w4_kv_append_norm", q, k, v, positions, cos, sin, k_cache, v_cache, slots, sections, cycled, paired,
                    k_scales, v_scales, q_out, (q_weight, k_weight, eps, unit_offset))
 
@@ -837,6 +870,11 @@ def w4_attn_decode_shared(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
     width]), which are read once for all of them; what follows is in their own pages, at the places that block_table has
     for it.  lens counts the prefix.  Requests outside of the groups, and those whose new tokens do not all lie behind the
     prefix, are attended over their own pages."""
+    if workspace is None:
+        done = _compiled().attn_decode_shared(q, k_cache, v_cache, block_table, lens, group_starts, prefix_table, prefix_lens,
+                                             starts, k_scales, v_scales, scale, out)
+        if done is not NotImplemented:
+            return done[0]
     index = _device_index(q, "q")
     cache = _kv_cache(k_cache, v_cache, k_scales, v_scales, index)
     stride = _strides(block_table, "block_table", torch.int32, 2, index)[0]

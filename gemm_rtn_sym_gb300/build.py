@@ -1,7 +1,8 @@
 """Builds libw4.so (the C-ABI library) in-tree with nvcc for sm_103a.
 
 Each .cu file under csrc/ is compiled in parallel to an object under _build/,
-then linked into gemm_rtn_sym_gb300/libw4.so.  IEEE division and no
+then linked into gemm_rtn_sym_gb300/libw4.so.  csrc/binding.cpp becomes the
+extension module gemm_rtn_sym_gb300/_binding.so, which calls the library.  IEEE division and no
 flush-to-zero are required by the quantiser, so no fast-math flags are used.
 """
 from __future__ import annotations
@@ -10,12 +11,14 @@ import concurrent.futures as cf
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libw4.so")
+BINDING = os.path.join(PKG, "_binding.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + [
@@ -45,18 +48,50 @@ def _compile(src: str, extra: list[str]) -> str:
     return obj
 
 
+def _compile_binding() -> str:
+    """Object of the extension module (host code against torch's headers)."""
+    import torch
+
+    obj = os.path.join(BUILD, "binding.o")
+    home = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    top = os.path.join(os.path.dirname(torch.__file__), "include")
+    includes = [os.path.join(ROOT, "include"), top, os.path.join(top, "torch", "csrc", "api", "include"),
+                os.path.join(home, "include"), sysconfig.get_paths()["include"]]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-c", os.path.join(CSRC, "binding.cpp"), "-o", obj,
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"] + [x for i in includes for x in ("-isystem", i)]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for binding.cpp:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _link_binding(obj: str) -> None:
+    import torch
+
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BINDING + ".tmp"
+    cmd = ["g++", "-shared", "-o", tmp, obj, "-L", PKG, "-l:libw4.so", "-Wl,-rpath,$ORIGIN", "-L", libs, "-ltorch_python",
+           "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda", f"-Wl,-rpath,{libs}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+
+
 def build(verbose: bool = False, extra: list[str] | None = None) -> str:
     """Compile and link libw4.so; returns its path."""
     os.makedirs(BUILD, exist_ok=True)
     srcs = sources()
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(12, len(srcs) + 1)) as ex:
+        binding = ex.submit(_compile_binding)
         objs = list(ex.map(lambda s: _compile(s, list(extra or [])), srcs))
     tmp = LIB + ".tmp"
-    cmd = [nvcc()] + ARCH + ["-shared", "-cudart", "shared", "-o", tmp] + objs
+    cmd = [nvcc()] + ARCH + ["-shared", "-cudart", "shared", "-Xlinker", "-soname=libw4.so", "-o", tmp] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _link_binding(binding.result())
     if verbose:
         print(f"built {LIB}")
     return LIB

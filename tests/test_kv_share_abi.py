@@ -173,3 +173,24 @@ def test_binding_checks_before_a_call():
         w4.w4_kv_fork(t, t, t, torch.zeros(3, 2, dtype=torch.int32), t, t, torch.zeros(2, dtype=torch.int64), 16)
     with pytest.raises(TypeError):
         w4.w4_kv_copy(torch.zeros(2, 16, 2, 128, dtype=torch.bfloat16), torch.zeros(2, 16, 2, 128, dtype=torch.bfloat16), t)
+
+
+def test_the_compiled_module_leaves_unusual_calls_alone():
+    """Tensors on the host, of other types or numbers of dimensions, no tensors at all, a wrong number of arguments."""
+    w4.load()
+    fast = w4._fast
+    t, table, r = torch.zeros(3, dtype=torch.int32), torch.zeros((3, 2), dtype=torch.int32), torch.zeros(2, dtype=torch.int64)
+    k = torch.zeros((2, 16, 2, 128), dtype=torch.bfloat16)
+    q = torch.zeros((3, 2, 128), dtype=torch.bfloat16)
+    calls = {"kv_fork": [t, t, t, table, t, t, r, 16, None, None, None], "kv_copy": [k, k, table, None, None],
+             "kv_compact": [t, table, t, r, 16, None, None, None, None, None],
+             "kv_pages_held": [t, t, table, t, r, 16, 4, t, None, None, None, None, None],
+             "kv_append_norm": [q, q, q, q, q, t, k, k, k, k, r, 1e-6, False, None, False, False, None, None, None],
+             "attn_decode_shared": [q, k, k, table, t, t, table, t, None, None, None, None, None]}
+    for name, args in calls.items():
+        fn = getattr(fast, name)
+        assert fn(*args) is NotImplemented
+        assert fn(*args[:-1]) is NotImplemented and fn(*args, None) is NotImplemented and fn() is NotImplemented
+        for i in range(len(args)):
+            for other in (None, 3, "x", torch.zeros(0), object()):
+                assert fn(*args[:i], other, *args[i + 1:]) is NotImplemented
