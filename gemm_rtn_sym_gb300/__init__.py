@@ -108,8 +108,9 @@ class _Norm(ctypes.Structure):
 
 
 _SIGNATURES.update({
+    "w4_kv_pages_held_workspace_bytes": (_sz, [_i32, _i32, _i64]),
     "w4_kv_pages_held": (ctypes.c_int, [_vp, _vp, _i32, _i32, _vp, _i64, _vp, _vp, _i64, _i32, _i64, _vp, _vp, _vp, _vp,
-                                        _vp, _vp, _vp]),
+                                        _vp, _vp, _vp, _sz, _vp]),
     "w4_kv_fork": (ctypes.c_int, [_vp, _vp, _vp, _i32, _i32, _vp, _i64, _i32, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _vp]),
     "w4_kv_compact": (ctypes.c_int, [_vp, _i32, _i32, _vp, _i64, _i32, _vp, _i64, _vp, _vp, _i64, _vp, _vp, _vp, _vp,
                                      _vp]),
@@ -640,7 +641,10 @@ def w4_kv_pages(lens: torch.Tensor, target: torch.Tensor, block_table: torch.Ten
     if holders is None:
         _call("w4_kv_pages", index, *args, *addresses)
     else:
-        _call("w4_kv_pages_held", index, *args, _vector(holders, "holders", i32, pages, index), *addresses)
+        size = load().w4_kv_pages_held_workspace_bytes(B, width, pages)
+        scratch = torch.empty(size, dtype=torch.uint8, device=dev)
+        _call("w4_kv_pages_held", index, *args, _vector(holders, "holders", i32, pages, index), *addresses,
+              scratch.data_ptr(), size)
     return tuple(outs)
 
 

@@ -144,6 +144,18 @@ struct Outputs {
     }
 };
 
+// Memory for the time of a call: the stream's next allocations may have it afterwards.
+struct Scratch {
+    size_t size;
+    void* p;
+    Scratch(size_t bytes, void* stream)
+        : size(bytes), p(bytes ? c10::cuda::CUDACachingAllocator::raw_alloc_with_stream(bytes, static_cast<cudaStream_t>(stream)) : nullptr) {}
+    Scratch(const Scratch&) = delete;
+    ~Scratch() {
+        if (p) c10::cuda::CUDACachingAllocator::raw_delete(p);
+    }
+};
+
 // Runs a library call without the interpreter's lock.
 template <class F>
 int run(F f) {
@@ -246,10 +258,11 @@ PyObject* kv_pages_held(PyObject*, PyObject* const* args, Py_ssize_t n) {
         int32_t* const positions = out.next<int32_t>(11, kInt, {T});
         int64_t* const left = out.next<int64_t>(12, kLong, {2});
         if (!c.ok) Py_RETURN_NOTIMPLEMENTED;
+        const Scratch scratch(w4_kv_pages_held_workspace_bytes(static_cast<int32_t>(B), static_cast<int32_t>(width), pages), c.stream);
         return out.done(run([&] {
             return w4_kv_pages_held(lens, target, static_cast<int32_t>(B), static_cast<int32_t>(page_size), static_cast<int32_t*>(ring->data_ptr()), pages, range,
                                     static_cast<int32_t*>(table->data_ptr()), table->stride(0), static_cast<int32_t>(width), T, holders, new_lens, starts, slots,
-                                    positions, left, c.stream);
+                                    positions, left, scratch.p, scratch.size, c.stream);
         }));
     });
 }
@@ -349,15 +362,13 @@ PyObject* attn_decode_shared(PyObject*, PyObject* const* args, Py_ssize_t n) {
         if (!c.ok) Py_RETURN_NOTIMPLEMENTED;
         const size_t size = w4_attn_decode_shared_workspace_bytes(&cache, static_cast<int32_t>(B), T, static_cast<int32_t>(heads), static_cast<int32_t>(groups));
         if (size == 0) Py_RETURN_NOTIMPLEMENTED;
-        void* const scratch = c10::cuda::CUDACachingAllocator::raw_alloc_with_stream(size, static_cast<cudaStream_t>(c.stream));
-        const int status = run([&] {
+        const Scratch scratch(size, c.stream);
+        return out.done(run([&] {
             return w4_attn_decode_shared(&cache, static_cast<int32_t>(B), T, static_cast<int32_t>(heads), &q_rows, &out_rows, static_cast<const int32_t*>(table->data_ptr()),
                                          table->stride(0), static_cast<int32_t>(width), lens, starts, static_cast<int32_t>(groups), group_starts,
                                          static_cast<const int32_t*>(prefix->data_ptr()), prefix->stride(0), static_cast<int32_t>(prefix_width), prefix_lens,
-                                         static_cast<float>(scale), scratch, size, c.stream);
-        });
-        c10::cuda::CUDACachingAllocator::raw_delete(scratch);  // the stream's next allocations may have it
-        return out.done(status);
+                                         static_cast<float>(scale), scratch.p, size, c.stream);
+        }));
     });
 }
 

@@ -665,10 +665,13 @@ size_t table_bytes(int32_t B, int64_t stride, int32_t width) {
 int kv_pages(const int32_t* lens, const int32_t* target, int32_t B, int32_t page_size, int32_t* free_pages,
              int64_t pages, const int64_t* free_range, int32_t* block_table, int64_t table_stride, int32_t width,
              int64_t T, bool held, int32_t* holders, int32_t* new_lens, int32_t* starts, int64_t* slots,
-             int32_t* positions, int64_t* free_range_out, void* stream) {
+             int32_t* positions, int64_t* free_range_out, void* workspace, size_t workspace_bytes, void* stream) {
     if (B < 0 || T < 0 || page_size < 1 || pages < 1 || width < 1) return W4_ERR_INVALID_ARG;
-    if (B > kMostCounted || T > INT32_MAX || pages > INT32_MAX) return W4_ERR_UNSUPPORTED;
+    if (B > kMostCounted || T > INT32_MAX || pages > INT32_MAX || (held && static_cast<int64_t>(B) * width > kMostCounted)) return W4_ERR_UNSUPPORTED;
     if (!free_pages || !free_range || !starts || !free_range_out || (held && !holders)) return W4_ERR_INVALID_ARG;
+    const size_t need = held ? kv_held_workspace_bytes(B, width, pages) : 0;
+    if (need > 0 && (!workspace || workspace_bytes < need)) return W4_ERR_INVALID_ARG;
+    if (need > 0 && !aligned(workspace, 256)) return W4_ERR_MISALIGNED;
     if (B > 0 && (!lens || !target || !block_table || !new_lens)) return W4_ERR_INVALID_ARG;
     if (T > 0 && (!slots || !positions)) return W4_ERR_INVALID_ARG;
     if (!table_fits(B, table_stride, width)) return W4_ERR_INVALID_ARG;
@@ -681,13 +684,15 @@ int kv_pages(const int32_t* lens, const int32_t* target, int32_t B, int32_t page
     const size_t b4 = static_cast<size_t>(B) * 4, t4 = static_cast<size_t>(T) * 4;
     const Region outs[] = {plain(block_table, table_bytes(B, table_stride, width)), plain(free_pages, static_cast<size_t>(pages) * 4),
                            plain(new_lens, b4), plain(starts, b4 + 4), plain(slots, 2 * t4), plain(positions, t4),
-                           plain(free_range_out, 16), plain(holders, static_cast<size_t>(pages) * 4)};
+                           plain(free_range_out, 16), plain(holders, static_cast<size_t>(pages) * 4),
+                           plain(need > 0 ? workspace : nullptr, workspace_bytes)};
     const Region ins[] = {plain(lens, b4), plain(target, b4), plain(free_range, 16)};
-    if (any_meet(outs, 8, ins, 3)) return W4_ERR_INVALID_ARG;
+    if (any_meet(outs, 9, ins, 3)) return W4_ERR_INVALID_ARG;
     const DeviceInfo* dev;
     if (const int s = usable_device(&dev)) return s;
+    unsigned* const words = need > 0 ? static_cast<unsigned*>(workspace) : nullptr;
     const KvPagesArgs a = {lens, target, B, page_size, free_pages, pages, free_range, block_table, table_stride, width,
-                           T, holders, new_lens, starts, slots, positions, free_range_out, dev->status, 0, 0};
+                           T, holders, words, words ? words + pages : nullptr, new_lens, starts, slots, positions, free_range_out, dev->status, 0, 0};
     return to_status(launch_kv_pages(a, *dev, static_cast<cudaStream_t>(stream)));
 }
 
@@ -861,15 +866,20 @@ int w4_kv_pages(const int32_t* lens, const int32_t* target, int32_t B, int32_t p
                 int64_t T, int32_t* new_lens, int32_t* starts, int64_t* slots, int32_t* positions,
                 int64_t* free_range_out, void* stream) {
     return kv_pages(lens, target, B, page_size, free_pages, pages, free_range, block_table, table_stride, width, T, false,
-                    nullptr, new_lens, starts, slots, positions, free_range_out, stream);
+                    nullptr, new_lens, starts, slots, positions, free_range_out, nullptr, 0, stream);
+}
+
+size_t w4_kv_pages_held_workspace_bytes(int32_t B, int32_t width, int64_t pages) {
+    return B < 0 || width < 1 || pages < 1 || pages > INT32_MAX || static_cast<int64_t>(B) * width > kMostCounted
+               ? 0 : kv_held_workspace_bytes(B, width, pages);
 }
 
 int w4_kv_pages_held(const int32_t* lens, const int32_t* target, int32_t B, int32_t page_size, int32_t* free_pages,
                      int64_t pages, const int64_t* free_range, int32_t* block_table, int64_t table_stride,
                      int32_t width, int64_t T, int32_t* holders, int32_t* new_lens, int32_t* starts, int64_t* slots,
-                     int32_t* positions, int64_t* free_range_out, void* stream) {
+                     int32_t* positions, int64_t* free_range_out, void* workspace, size_t workspace_bytes, void* stream) {
     return kv_pages(lens, target, B, page_size, free_pages, pages, free_range, block_table, table_stride, width, T, true,
-                    holders, new_lens, starts, slots, positions, free_range_out, stream);
+                    holders, new_lens, starts, slots, positions, free_range_out, workspace, workspace_bytes, stream);
 }
 
 int w4_kv_append(const w4_kv_cache* cache, const w4_rope* rope, int64_t T, int32_t q_heads, const w4_rows* q,

@@ -8,6 +8,7 @@
 
 #include "w4_device.cuh"
 #include "w4_kv.h"
+#include "w4_kv_release.cuh"
 
 namespace w4 {
 namespace {
@@ -30,19 +31,6 @@ __device__ __forceinline__ Sums warp_scan(Sums v, int lane) {
 
 constexpr int kPagesThreads = 1024;
 
-// Last of the n ascending values that is at most x (the first is).
-__device__ __forceinline__ int last_at_most(const long long* v, int n, long long x) {
-    int lo = 0, hi = n;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (v[mid] <= x)
-            lo = mid;
-        else
-            hi = mid;
-    }
-    return lo;
-}
-
 // A sum of new tokens as the int32 of `starts`: those past 2³¹ − 1 have no rows, and must not come out as rows of others.
 __device__ __forceinline__ int row_number(long long sum) { return static_cast<int>(min(sum, 0x7fffffffll)); }
 
@@ -56,7 +44,7 @@ __device__ __forceinline__ int row_number(long long sum) { return static_cast<in
 //
 // HELD: pages have holders.  A page that is taken has one; those that requests
 // let go of are the next kernel's work, since every CTA looks at the holders
-// that pages have before the call.
+// that pages have before the call, or this one's, where it is alone.
 template <bool HELD>
 __global__ void __launch_bounds__(kPagesThreads) kv_pages_kernel(KvPagesArgs a) {
     __shared__ long long s_start[kPagesThreads], s_back[kPagesThreads], s_first[kPagesThreads];
@@ -175,6 +163,14 @@ __global__ void __launch_bounds__(kPagesThreads) kv_pages_kernel(KvPagesArgs a) 
         a.starts[a.B] = row_number(carry.grow);
         a.range_out[0] = head + used;
         if (!HELD) a.range_out[1] = tail + carry.back;
+    }
+    if (HELD && a.last) {
+        const long long step = static_cast<long long>(gridDim.x) * threads, words = (static_cast<long long>(a.B) * a.width + 31) / 32;
+        for (long long i = static_cast<long long>(blockIdx.x) * threads + tid; i < a.pages; i += step) a.last[i] = 0;
+        for (long long i = static_cast<long long>(blockIdx.x) * threads + tid; i < words; i += step) a.marks[i] = 0;
+    } else if (HELD && gridDim.x == 1) {
+        __syncthreads();
+        release_pages(a);
     }
 }
 
@@ -369,7 +365,7 @@ cudaError_t launch_kv_pages(KvPagesArgs a, const DeviceInfo& dev, cudaStream_t s
     }
     kv_pages_kernel<true><<<grid, threads, 0, stream>>>(a);
     const cudaError_t err = cudaGetLastError();
-    return err != cudaSuccess ? err : launch_kv_release(a, stream);
+    return err != cudaSuccess || (grid == 1 && !a.last) ? err : launch_kv_release(a, dev, stream);
 }
 
 cudaError_t launch_kv_append(KvAppendArgs a, const int32_t sections[4], bool cycled, bool q8, const DeviceInfo& dev,

@@ -25,6 +25,8 @@ struct KvPagesArgs {
     int32_t width;
     int64_t T;
     int32_t* holders;  // nullptr: every page has one
+    unsigned* last;    // nullptr where the table has few entries; else a word for each page,
+    unsigned* marks;   // and a bit for each entry
     int32_t* new_lens;
     int32_t* starts;
     int64_t* slots;
@@ -222,7 +224,8 @@ cudaError_t launch_kv_append(KvAppendArgs a, const int32_t sections[4], bool cyc
 cudaError_t launch_kv_append_norm(KvAppendArgs a, const KvNorm& norm, const int32_t sections[4], bool cycled, bool q8,
                                   const DeviceInfo& dev, cudaStream_t stream);
 // Adds to the launch of w4_kv_pages the pages that requests let go of (their holders are a.holders).
-cudaError_t launch_kv_release(const KvPagesArgs& a, cudaStream_t stream);
+cudaError_t launch_kv_release(const KvPagesArgs& a, const DeviceInfo& dev, cudaStream_t stream);
+size_t kv_held_workspace_bytes(int32_t B, int32_t width, int64_t pages);
 cudaError_t launch_kv_fork(KvForkArgs a, const DeviceInfo& dev, cudaStream_t stream);
 cudaError_t launch_kv_compact(KvCompactArgs a, const DeviceInfo& dev, cudaStream_t stream);
 cudaError_t launch_kv_copy(const KvCopyArgs& a, const DeviceInfo& dev, cudaStream_t stream);

@@ -13,152 +13,109 @@
 
 #include "w4_device.cuh"
 #include "w4_kv.h"
+#include "w4_kv_release.cuh"
 
 namespace w4 {
 namespace {
 
 constexpr int kThreads = 1024;
 
-__device__ __forceinline__ long long warp_sum_to(long long v, int lane) {  // of the lanes up to this one
-    for (int d = 1; d < 32; d <<= 1) {
-        const long long u = __shfl_up_sync(~0u, v, d);
-        if (lane >= d) v += u;
-    }
-    return v;
-}
+__global__ void __launch_bounds__(kThreads) kv_release_kernel(KvPagesArgs a) { release_pages(a); }
 
-// Sums of v over the threads before this one, and `total` over all of them.  Ends behind a barrier that leaves s_warp
-// (33 of them) free once more threads pass the caller's next one.
-__device__ __forceinline__ long long block_sum_before(long long v, long long* s_warp, long long& total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    const long long sum = warp_sum_to(v, lane);
-    if (lane == 31) s_warp[warp] = sum;
-    __syncthreads();
-    if (warp == 0) {
-        const long long w = lane < warps ? s_warp[lane] : 0, to = warp_sum_to(w, lane);
-        s_warp[lane] = to - w;
-        if (lane == 31) s_warp[32] = to;
-    }
-    __syncthreads();
-    total = s_warp[32];
-    return s_warp[warp] + sum - v;
-}
-
-// Last of the n ascending values that is at most x (the first is).
-__device__ __forceinline__ int last_at_most(const long long* v, int n, long long x) {
-    int lo = 0, hi = n;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (v[mid] <= x)
-            lo = mid;
-        else
-            hi = mid;
-    }
-    return lo;
-}
-
-struct Divide {
-    uint32_t mul;
-    int shift;
-    __device__ __forceinline__ int operator()(int x) const { return static_cast<int>((static_cast<uint64_t>(x) * mul) >> shift); }
-};
-
-// ----------------------------------------------------------------- release
-constexpr int kEach = 4;  // entries that a thread takes at a time
-
-// The entries that requests let go of, in their order, 4096 at a time: each
-// counts its page's holders down; of a page that then has none, the last entry
-// gives it back.  Which entry that is, the count itself tells: the entries of
-// one page that find it at zero leave the largest of their numbers in it,
-// below zero, and that one puts the zero back.  One CTA: a step lets go of
-// few pages, and a request of 131071 tokens that ends, of 8192.
-__global__ void __launch_bounds__(kThreads) kv_release_kernel(KvPagesArgs a) {
+// ------------------------------------------------------- release, many pages
+// Entries by all CTAs at once.  Each leaves its number in its page's word if
+// that is the largest so far, and then counts the page's holders down: whoever
+// finds the last of them finds the number of the last entry there as well, and
+// marks that entry.
+__global__ void __launch_bounds__(kThreads) kv_let_go_kernel(KvPagesArgs a) {
     __shared__ long long s_first[kThreads], s_warp[33];
     __shared__ int s_want[kThreads];
-    __shared__ int s_gone[kEach * 32];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const long long tail = a.range[1], most = static_cast<long long>(a.width) * a.page_size;
-    const Divide pages_of = {a.page_mul, a.page_shift};
-    const long long tail_at = static_cast<long long>(static_cast<uint64_t>(tail) % static_cast<uint64_t>(a.pages));
-    long long given = 0;
+    const int tid = threadIdx.x;
+    long long before = 0;
     for (int base = 0; base < a.B; base += kThreads) {
         const int n = min(a.B - base, kThreads);
-        int have = 0, want = 0;
-        if (tid < n) {
-            const int len = a.lens[base + tid], target = a.target[base + tid];
-            if (len >= 0 && target >= 0 && len <= most) {
-                have = len > 0 ? pages_of(len - 1) + 1 : 0;
-                want = target > 0 ? pages_of(target - 1) + 1 : 0;
+        const long long total = scan_given(a, base, n, s_first, s_want, s_warp);
+        for (long long r = static_cast<long long>(blockIdx.x) * kThreads + tid; r < total; r += static_cast<long long>(gridDim.x) * kThreads) {
+            const int i = last_at_most(s_first, n, r);
+            const int page = a.table[(base + i) * a.table_stride + s_want[i] + (r - s_first[i])];
+            if (page < 0 || page >= a.pages) {
+                record_status(a.status, kStatusInvalid);
+                continue;
+            }
+            atomicMax(a.last + page, static_cast<unsigned>(before + r) + 1);
+            __threadfence();
+            const int held = atomicSub(a.holders + page, 1);
+            if (held <= 0) {
+                record_status(a.status, kStatusInvalid);
+                atomicAdd(a.holders + page, 1);
+            } else if (held == 1) {
+                __threadfence();
+                const unsigned last = __ldcg(a.last + page) - 1;
+                atomicOr(a.marks + (last >> 5), 1u << (last & 31));
             }
         }
-        long long total;
-        const long long first = block_sum_before(max(have - want, 0), s_warp, total);
-        s_first[tid] = first;
-        s_want[tid] = want;
-        __syncthreads();
-        for (long long r0 = 0; r0 < total; r0 += kEach * kThreads) {
-            int page[kEach];
-            bool gone[kEach];
-#pragma unroll
-            for (int j = 0; j < kEach; ++j) {
-                const long long r = r0 + j * kThreads + tid;
-                page[j] = -1;
-                if (r < total) {
-                    const int i = last_at_most(s_first, n, r);
-                    page[j] = a.table[(base + i) * a.table_stride + s_want[i] + (r - s_first[i])];
-                    if (page[j] < 0 || page[j] >= a.pages) {
-                        record_status(a.status, kStatusInvalid);
-                        page[j] = -1;
-                    }
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < kEach; ++j)
-                if (page[j] >= 0 && atomicSub(a.holders + page[j], 1) <= 0) {
-                    // Nobody holds the page: more entries than its count says.
-                    record_status(a.status, kStatusInvalid);
-                    atomicAdd(a.holders + page[j], 1);
-                    page[j] = -1;
-                }
-            __syncthreads();
-#pragma unroll
-            for (int j = 0; j < kEach; ++j) gone[j] = page[j] >= 0 && __ldcg(a.holders + page[j]) == 0;
-            __syncthreads();
-#pragma unroll
-            for (int j = 0; j < kEach; ++j)
-                if (gone[j]) atomicMin(a.holders + page[j], -1 - (j * kThreads + tid));
-            __syncthreads();
-#pragma unroll
-            for (int j = 0; j < kEach; ++j) {
-                gone[j] = gone[j] && __ldcg(a.holders + page[j]) == -1 - (j * kThreads + tid);
-                const unsigned votes = __ballot_sync(~0u, gone[j]);
-                if (lane == 0) s_gone[j * 32 + warp] = __popc(votes);
-            }
-            __syncthreads();
-            int before[kEach], count = 0;  // (each warp sums for itself)
-#pragma unroll
-            for (int j = 0; j < kEach; ++j) {
-                const int w = s_gone[j * 32 + lane];
-                const int to = static_cast<int>(warp_sum_to(w, lane));
-                before[j] = count + __shfl_sync(~0u, to - w, warp);
-                count += __shfl_sync(~0u, to, 31);
-            }
-#pragma unroll
-            for (int j = 0; j < kEach; ++j) {
-                const unsigned votes = __ballot_sync(~0u, gone[j]);
-                if (gone[j]) {
-                    a.holders[page[j]] = 0;
-                    long long at = tail_at + (given + before[j] + __popc(votes & ((1u << lane) - 1))) % a.pages;
-                    if (at >= a.pages) at -= a.pages;
-                    a.ring[at] = page[j];
-                }
-            }
-            given += count;
-            __syncthreads();
-        }
+        before += total;
         __syncthreads();
     }
-    if (tid == 0) a.range_out[1] = tail + given;
+}
+
+constexpr int kMarkWords = 256, kMarked = kMarkWords * 32, kMarkEach = kMarked / kThreads;  // words and entries that a CTA takes at a time
+
+// The marked entries' pages go to the ring, in the order of the entries.  A CTA counts the marks before its own.
+__global__ void __launch_bounds__(kThreads) kv_give_back_kernel(KvPagesArgs a) {
+    __shared__ long long s_first[kThreads], s_warp[33];
+    __shared__ int s_want[kThreads], s_before[kMarkWords];
+    __shared__ unsigned s_words[kMarkWords];
+    const int tid = threadIdx.x;
+    const long long tail = a.range[1];
+    const long long tail_at = static_cast<long long>(static_cast<uint64_t>(tail) % static_cast<uint64_t>(a.pages));
+    // (of all entries, marked or not)
+    long long entries = 0;
+    for (int base = 0; base < a.B; base += kThreads) {
+        entries += scan_given(a, base, min(a.B - base, kThreads), s_first, s_want, s_warp);
+        __syncthreads();
+    }
+    const long long words = (entries + 31) / 32;
+    auto marks = [&](long long from, long long to) {  // in words from .. to − 1
+        long long n = 0, total;
+        for (long long w = from + tid; w < to; w += kThreads) n += __popc(a.marks[w]);
+        block_sum_before(n, s_warp, total);
+        __syncthreads();
+        return total;
+    };
+    if (blockIdx.x == 0) {
+        const long long given = marks(0, words);
+        if (tid == 0) a.range_out[1] = tail + given;
+    }
+    for (long long w0 = static_cast<long long>(blockIdx.x) * kMarkWords; w0 < words; w0 += static_cast<long long>(gridDim.x) * kMarkWords) {
+        const long long given = marks(0, w0);
+        const unsigned word = tid < kMarkWords && w0 + tid < words ? a.marks[w0 + tid] : 0;
+        long long total;
+        const long long before = block_sum_before(__popc(word), s_warp, total);
+        if (tid < kMarkWords) {
+            s_words[tid] = word;
+            s_before[tid] = static_cast<int>(before);
+        }
+        __syncthreads();
+        long long done = 0;  // entries of the requests before `base`
+        for (int base = 0; base < a.B; base += kThreads) {
+            const int n = min(a.B - base, kThreads);
+            const long long mine = scan_given(a, base, n, s_first, s_want, s_warp);
+#pragma unroll
+            for (int j = 0; j < kMarkEach; ++j) {
+                const int e = j * kThreads + tid;
+                const long long r = w0 * 32 + e - done;
+                if (r >= 0 && r < mine && s_words[e >> 5] >> (e & 31) & 1) {
+                    const int i = last_at_most(s_first, n, r);
+                    long long at = tail_at + (given + s_before[e >> 5] + __popc(s_words[e >> 5] & ((1u << (e & 31)) - 1))) % a.pages;
+                    if (at >= a.pages) at -= a.pages;
+                    a.ring[at] = a.table[(base + i) * a.table_stride + s_want[i] + (r - s_first[i])];
+                }
+            }
+            done += mine;
+            __syncthreads();
+        }
+    }
 }
 
 // -------------------------------------------------------------------- fork
@@ -473,9 +430,24 @@ __global__ void __launch_bounds__(kCopyThreads) kv_copy_kernel(const __grid_cons
 
 }  // namespace
 
-cudaError_t launch_kv_release(const KvPagesArgs& a, cudaStream_t stream) {
-    kv_release_kernel<<<1, kThreads, 0, stream>>>(a);
+cudaError_t launch_kv_release(const KvPagesArgs& a, const DeviceInfo& dev, cudaStream_t stream) {
+    const int64_t entries = static_cast<int64_t>(a.B) * a.width;
+    if (!a.last) {
+        kv_release_kernel<<<1, kThreads, 0, stream>>>(a);
+        return cudaGetLastError();
+    }
+    auto ctas = [&](int64_t each) { return static_cast<unsigned>(std::min<int64_t>((entries + each - 1) / each, dev.sm_count)); };
+    kv_let_go_kernel<<<ctas(kThreads), kThreads, 0, stream>>>(a);
+    const cudaError_t err = cudaGetLastError();
+    if (err != cudaSuccess) return err;
+    kv_give_back_kernel<<<ctas(kMarked), kThreads, 0, stream>>>(a);
     return cudaGetLastError();
+}
+
+// Words for each page and a bit for each entry of the table, where more pages may go back than one CTA should see to.
+size_t kv_held_workspace_bytes(int32_t B, int32_t width, int64_t pages) {
+    const int64_t entries = static_cast<int64_t>(B) * width;
+    return entries <= kFewEntries ? 0 : static_cast<size_t>(pages + (entries + 31) / 32) * 4;
 }
 
 cudaError_t launch_kv_fork(KvForkArgs a, const DeviceInfo& dev, cudaStream_t stream) {

@@ -467,12 +467,18 @@ int w4_kv_pages(const int32_t* lens, const int32_t* target, int32_t B, int32_t p
  * full and has other holders as well does not grow into it: it is not granted
  * and asks for no pages.  (Holders as they were before the call.)
  * Out of range: a page that a request lets go of and nobody holds stays as it
- * is.  Two launches; the rest as for w4_kv_pages.
+ * is.  B · width: at most 2³¹ − 2¹⁶.
+ * workspace: w4_kv_pages_held_workspace_bytes(...) bytes (none for a table of
+ * few entries), 256-byte aligned, contents unspecified before and after, and not
+ * that of another call that may run at the same time.  One launch for few
+ * requests and tokens, three for many; the rest as for w4_kv_pages.
  */
+size_t w4_kv_pages_held_workspace_bytes(int32_t B, int32_t width, int64_t pages);
 int w4_kv_pages_held(const int32_t* lens, const int32_t* target, int32_t B, int32_t page_size, int32_t* free_pages,
                      int64_t pages, const int64_t* free_range, int32_t* block_table, int64_t table_stride,
                      int32_t width, int64_t T, int32_t* holders, int32_t* new_lens, int32_t* starts, int64_t* slots,
-                     int32_t* positions, int64_t* free_range_out, void* stream);
+                     int32_t* positions, int64_t* free_range_out, void* workspace, size_t workspace_bytes,
+                     void* stream);
 
 /*
  * w4_kv_fork — requests that begin as the first tokens of others.

@@ -133,12 +133,14 @@ def test_many_requests(cuda_lib, B):
     pool.consistent()
 
 
-def test_many_pages_let_go_at_once(cuda_lib):
-    """More entries than the kernel takes at a time, each page let go of several times."""
-    pool = Pool(7, 3000, 3300, 4, seed=2)
-    pool.step([11990, 0, 0, 0, 0, 0, 100])
-    pool.fork([-1, 0, 0, 0, 0, 0, -1], [0, 11990, 11988, 6000, 11988, 3, 0])
-    pool.step([0, 0, 11988, 17, 0, 0, 99])
+@pytest.mark.parametrize("width", [2300, 3000, 40000])
+def test_many_pages_let_go_at_once(cuda_lib, width):
+    """More entries than a CTA takes at a time, each page let go of several times: by one CTA and by many."""
+    n = 4 * width - 10
+    pool = Pool(7, width, width + 300, 4, seed=2)
+    pool.step([n, 0, 0, 0, 0, 0, 100])
+    pool.fork([-1, 0, 0, 0, 0, 0, -1], [0, n, n - 2, n // 2, n - 2, 3, 0])
+    pool.step([0, 0, n - 2, 17, 0, 0, 99])
     pool.consistent()
     pool.step([0, 0, 0, 0, 0, 0, 0])
     pool.consistent()
@@ -213,8 +215,9 @@ def test_a_length_past_the_table_is_left_alone(cuda_lib):
     pool.compact(status=w4.W4_ERR_INVALID_ARG)
 
 
-def test_pages_that_nobody_holds_are_not_given_back(cuda_lib):
-    pool = Pool(3, 4, 12, 16)
+@pytest.mark.parametrize("width", [4, 6000])
+def test_pages_that_nobody_holds_are_not_given_back(cuda_lib, width):
+    pool = Pool(3, width, 12, 16)
     pool.step([30, 20, 0])
     pool.holders[pool.table[0, 0]] = 0
     pool.holders[pool.table[1, 1]] = -5

@@ -30,7 +30,7 @@ def rows(at, token_stride=1024, head_stride=128):
 
 def held(lib, **kw):
     a = dict(lens=A, target=2 * A, B=4, page_size=16, ring=3 * A, pages=8, free=4 * A, table=5 * A, stride=6, width=6, T=10,
-             holders=11 * A, new=6 * A, starts=7 * A, slots=8 * A, positions=9 * A, left=10 * A)
+             holders=11 * A, new=6 * A, starts=7 * A, slots=8 * A, positions=9 * A, left=10 * A, workspace=None, size=0)
     a.update(kw)
     return lib.w4_kv_pages_held(*a.values(), None)
 
@@ -42,6 +42,21 @@ def held(lib, **kw):
 ])
 def test_held_pages_refusals(lib, kw, expect):
     assert held(lib, **kw) == getattr(w4, "W4_ERR_" + expect)
+
+
+def test_workspace_of_held_pages(lib):
+    """None for few entries; then a word for each page and a bit for each entry."""
+    assert lib.w4_kv_pages_held_workspace_bytes(64, 256, 5000) == 0
+    assert lib.w4_kv_pages_held_workspace_bytes(1000, 300, 5000) >= 4 * 5000 + 1000 * 300 // 8
+    for bad in ((-1, 4, 8), (4, 0, 8), (4, 4, 0), (4, 4, 1 << 31), (1 << 16, 1 << 16, 8)):
+        assert lib.w4_kv_pages_held_workspace_bytes(*bad) == 0
+    far = dict(lens=1 << 32, target=2 << 32, new=3 << 32, starts=4 << 32, table=5 << 32, B=1000, width=300, stride=300, pages=8)
+    need = lib.w4_kv_pages_held_workspace_bytes(1000, 300, 8)
+    assert held(lib, **far) == w4.W4_ERR_INVALID_ARG
+    assert held(lib, **far, workspace=20 * A, size=need - 1) == w4.W4_ERR_INVALID_ARG
+    assert held(lib, **far, workspace=20 * A + 64, size=need) == w4.W4_ERR_MISALIGNED
+    assert held(lib, **far, workspace=3 << 32, size=need) == w4.W4_ERR_INVALID_ARG  # over the new lengths
+    assert held(lib, **{**far, "B": 1 << 16, "width": 1 << 16, "stride": 1 << 16}) == w4.W4_ERR_UNSUPPORTED
 
 
 def fork(lib, **kw):
