@@ -23,8 +23,8 @@ namespace {
 constexpr int kManyThreads = 64, kManyTokens = 8;  // (tokens to an SM)
 constexpr int kBatch = 4;  // rows that a lane has in flight
 
-__device__ __forceinline__ uint32_t pair_bf16(float lo, float hi) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+__device__ __forceinline__ uint32_t pair_bf16(uint64_t x) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(first_of(x), second_of(x));
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
@@ -32,13 +32,13 @@ __device__ __forceinline__ uint32_t pair_bf16(float lo, float hi) {
 // takes the largest near 1.  A row with an infinity keeps its sum (every finite value then becomes 0), and so does one
 // with a NaN.
 template <int LPR>
-__device__ __forceinline__ float far_root(const float (&v)[8], float sum, const KvNorm& norm) {
+__device__ __forceinline__ float far_root(const uint64_t (&v)[4], float sum, const KvNorm& norm) {
     float most = 0.f;
     bool finite = true;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        most = fmaxf(most, fabsf(v[i]));
-        finite = finite && isfinite(v[i]);
+    for (int i = 0; i < 4; ++i) {
+        most = fmaxf(most, fmaxf(fabsf(first_of(v[i])), fabsf(second_of(v[i]))));
+        finite = finite && isfinite(first_of(v[i])) && isfinite(second_of(v[i]));
     }
     if (!finite) most = INFINITY;
 #pragma unroll
@@ -47,185 +47,236 @@ __device__ __forceinline__ float far_root(const float (&v)[8], float sum, const 
     const float s = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
     float scaled = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) scaled = fmaf(v[i] * s, v[i] * s, scaled);
+    for (int i = 0; i < 4; ++i) scaled = fmaf(first_of(v[i]) * s, first_of(v[i]) * s, fmaf(second_of(v[i]) * s, second_of(v[i]) * s, scaled));
 #pragma unroll
     for (int m = LPR / 2; m > 0; m >>= 1) scaled += __shfl_xor_sync(~0u, scaled, m);
     return isfinite(most) && !(sum < 1e37f) ? s * rsqrtf(fmaf(scaled, norm.inv_dim, norm.eps * s * s))
                                             : rsqrtf(fmaf(sum, norm.inv_dim, norm.eps));
 }
 
-// LPR lanes work on a row.  Lane c has eight of its values, in two runs of four
-// that begin at columns `one` and `two`: where halves turn with one another,
-// values 4c.. of the first and of the second half, so that no value has to
-// come from another lane; else values 8c and 8c + 4.  A CTA takes every
-// gridDim.x-th token: its threads ask for the token's rows (keys, values,
-// queries), fetch its cosines and sines once for all of them, and normalise,
-// turn and write.  blockIdx.y shares a token's rows among CTAs where there are
-// few tokens.
-template <int THREADS, int LPR, bool Q8>
-__global__ void __launch_bounds__(THREADS, 1024 / THREADS) kv_append_norm_kernel(const __grid_constant__ KvAppendArgs a,
-                                                                                const __grid_constant__ KvNorm norm,
-                                                                                const __grid_constant__ Axes axes) {
-    constexpr int kGroups = THREADS / LPR;
-    __shared__ __align__(16) float s_cos[2][128], s_sin[2][128];
-    const int c = threadIdx.x % LPR, group0 = blockIdx.y * kGroups, group = group0 + threadIdx.x / LPR;
-    const int groups = gridDim.y * kGroups;
-    const int d = a.head_dim, H = a.kv_heads, F = a.rotary / 2;
-    const bool live = 8 * c < d, turned = 8 * c < a.rotary;
-    const int one = turned && !a.paired ? 4 * c : 8 * c, two = turned && !a.paired ? F + 4 * c : 8 * c + 4;
-    const int rows = 2 * H + a.q_heads;
-    // Rows r of a token: keys from 0, values from H, queries from 2H, so that r · head_stride counts from there.
-    const __nv_bfloat16* const k_from = a.k.data;
-    const __nv_bfloat16* const v_from = a.v.data - H * a.v.head_stride;
-    const __nv_bfloat16* const q_from = a.q.data - 2 * H * a.q.head_stride;
+enum Kind { kKey, kValue, kQuery };
 
-    float wq[8], wk[8];
+// What a thread knows of the rows that it works on: LPR lanes to a row.  Lane c has eight of its values, in two runs of
+// four that begin at columns `one` and `other`: where halves turn with one another, values 4c.. of the first and of the
+// second half, so that no value has to come from another lane; else values 8c and 8c + 4.
+struct Lane {
+    int one, other;
+    bool live, turned, paired;
+};
+
+// The turn of a token: cosines and sines of the lane's four frequencies.
+struct Turned {
+    uint64_t C[2], S[2], minus[2];
+};
+
+__device__ __forceinline__ void turn_values(uint64_t (&v)[4], const Turned& t, bool paired) {
+    if (paired) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int col = (i < 4 ? one : two) + (i & 3);
-        auto weight = [&](const void* w) {
-            if (!live || !w) return 0.f;
-            return (norm.bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(w)[col]) : static_cast<const float*>(w)[col]) + norm.offset;
-        };
-        wq[i] = weight(norm.q_weight);
-        wk[i] = weight(norm.k_weight);
+        for (int y = 0; y < 4; ++y) {  // the two of a pair, by one cosine and sine
+            const float cos = y & 1 ? second_of(t.C[y >> 1]) : first_of(t.C[y >> 1]), sin = y & 1 ? second_of(t.S[y >> 1]) : first_of(t.S[y >> 1]);
+            v[y] = fma2(two(second_of(v[y]), first_of(v[y])), two(-sin, sin), mul2(v[y], two(cos, cos)));
+        }
+    } else {
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+            const uint64_t was = v[y];
+            v[y] = fma2(v[y + 2], t.minus[y], mul2(was, t.C[y]));
+            v[y + 2] = fma2(was, t.S[y], mul2(v[y + 2], t.C[y]));
+        }
     }
+}
 
-    for (int t = blockIdx.x, turn = 0; t < a.T; t += gridDim.x, turn ^= 1) {
-        long long slot = 0, at = 0, scale_at = 0;
-        bool stored = false;
-        float C[4] = {}, S[4] = {};
-        for (int r0 = group, base = group0; base < rows; r0 += kBatch * groups, base += kBatch * groups) {
-            uint2 x[kBatch][2];
+// Row's codes and scale by RTN at 8 bits of its fp32 values, over its LPR lanes (idle ones hold zeros).
+template <int LPR>
+__device__ __forceinline__ void put_codes(const uint64_t (&v)[4], const Lane& lane, bool store, int8_t* to, __nv_bfloat16* scale_to) {
+    float most = 0.f;
+    bool finite = true;
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                const int r = r0 + i * groups;
-                x[i][0] = x[i][1] = make_uint2(0, 0);
-                if (live && r < rows) {
-                    const __nv_bfloat16* src = r < H       ? k_from + t * a.k.token_stride + r * a.k.head_stride
-                                               : r < 2 * H ? v_from + t * a.v.token_stride + r * a.v.head_stride
-                                                           : q_from + t * a.q.token_stride + r * a.q.head_stride;
-                    x[i][0] = *reinterpret_cast<const uint2*>(src + one);
-                    x[i][1] = *reinterpret_cast<const uint2*>(src + two);
+    for (int y = 0; y < 4; ++y) {
+        most = fmaxf(most, fmaxf(fabsf(first_of(v[y])), fabsf(second_of(v[y]))));
+        finite = finite && isfinite(first_of(v[y])) && isfinite(second_of(v[y]));
+    }
+    if (!finite && lane.live) most = INFINITY;
+#pragma unroll
+    for (int m = LPR / 2; m > 0; m >>= 1) most = fmaxf(most, __shfl_xor_sync(~0u, most, m));
+    if (!store) return;
+    const bool bad = isinf(most);
+    const __nv_bfloat16 scale = __float2bfloat16_rn(bad ? NAN : __fdiv_rn(most, 127.f));
+    const float s = __bfloat162float(scale);
+    uint32_t code[2] = {0, 0};
+    if (!bad && s > 0.f)
+#pragma unroll
+        for (int y = 0; y < 8; ++y) {
+            const int q = __float2int_rn(fminf(fmaxf(rintf(__fdiv_rn(y & 1 ? second_of(v[y >> 1]) : first_of(v[y >> 1]), s)), -128.f), 127.f));
+            code[y / 4] |= (q & 0xFFu) << (8 * (y & 3));
+        }
+    *reinterpret_cast<uint32_t*>(to + lane.one) = code[0];
+    *reinterpret_cast<uint32_t*>(to + lane.other) = code[1];
+    if (threadIdx.x % LPR == 0) *scale_to = scale;
+}
+
+// A token's rows of one kind: `rows` of them, every groups-th of which, from `group` on, is this thread's; `first` is the
+// same for the whole CTA.
+struct Part {
+    const __nv_bfloat16* from;
+    int64_t stride;
+    int rows, first, group, groups;
+};
+
+// A thread's next rows of a part, all loads at once; src moves behind them.
+__device__ __forceinline__ void load_rows(const Part& p, const Lane& lane, const __nv_bfloat16*& src, int r, uint2 (&x)[kBatch][2]) {
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i, src += p.groups * p.stride) {
+        x[i][0] = x[i][1] = make_uint2(0, 0);
+        if (lane.live && r + i * p.groups < p.rows) {
+            x[i][0] = *reinterpret_cast<const uint2*>(src + lane.one);
+            x[i][1] = *reinterpret_cast<const uint2*>(src + lane.other);
+        }
+    }
+}
+
+// weight: fp32 [head_dim] in shared memory.  x: the first rows, where they are loaded already.
+template <int KIND, int LPR, bool Q8>
+__device__ __forceinline__ void put_rows(const KvNorm& norm, const Lane& lane, const Turned& turned, const float* weight, const Part& p, bool loaded,
+                                         uint2 (&x)[kBatch][2], void* to, int64_t to_stride, __nv_bfloat16* scales, int64_t scale_stride) {
+    constexpr bool kCodes = Q8 && KIND != kQuery;
+    uint64_t w[4] = {};
+    if (KIND != kValue && lane.live) {
+        const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(weight + lane.one), b = *reinterpret_cast<const ulonglong2*>(weight + lane.other);
+        w[0] = a.x, w[1] = a.y, w[2] = b.x, w[3] = b.y;
+    }
+    const int rows = p.rows, groups = p.groups;
+    const __nv_bfloat16* src = p.from + p.group * p.stride;
+    const int64_t to_step = groups * to_stride;
+    int64_t at = p.group * to_stride;
+    for (int r = p.group, base = p.first; base < rows; base += kBatch * groups) {
+        if (!loaded)
+            load_rows(p, lane, src, r, x);
+        else
+            src += kBatch * groups * p.stride;
+        loaded = false;
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i, r += groups, at += to_step) {
+            if (base + i * groups >= rows) break;  // the same for the whole CTA
+            const bool store = lane.live && r < rows;
+            if (KIND == kValue && !kCodes) {  // (as they are, NaN's bits among them)
+                if (store) {
+                    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(to) + at + lane.one) = x[i][0];
+                    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(to) + at + lane.other) = x[i][1];
                 }
+                continue;
             }
-            if (base == group0) {
-                slot = a.slots[t];
-                for (int i = threadIdx.x; i < F; i += THREADS) {
-                    const int axis = axes.of[i >> 3] >> (2 * (i & 7)) & 3;
-                    int row = a.positions[axis * a.axis_stride + t];
-                    if (row < 0 || row >= a.rows) {
-                        record_status(a.status, kStatusInvalid);
-                        row = 0;
-                    }
-                    s_cos[turn][i] = a.cos[static_cast<long long>(row) * F + i];
-                    s_sin[turn][i] = a.sin[static_cast<long long>(row) * F + i];
-                }
-                __syncthreads();
-                if (turned) {
-                    const float4 u = *reinterpret_cast<const float4*>(&s_cos[turn][4 * c]);
-                    const float4 w = *reinterpret_cast<const float4*>(&s_sin[turn][4 * c]);
-                    C[0] = u.x, C[1] = u.y, C[2] = u.z, C[3] = u.w;
-                    S[0] = w.x, S[1] = w.y, S[2] = w.z, S[3] = w.w;
-                }
-                stored = slot >= 0 && slot < a.pages * a.page_size;
-                if (!stored && slot != -1) record_status(a.status, kStatusInvalid);
-                if (stored) {
-                    const long long page = slot <= 0x7fffffff
-                                               ? static_cast<long long>((static_cast<uint64_t>(slot) * a.page_mul) >> a.page_shift)
-                                               : slot / a.page_size;
-                    const long long place = slot - page * a.page_size;
-                    at = page * a.page_stride + place * a.cache_token_stride;
-                    scale_at = page * H * a.page_size + place;
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                if (base + i * groups >= rows) break;  // the same for the whole CTA
-                const int r = r0 + i * groups;
-                const bool is_q = r >= 2 * H, is_v = !is_q && r >= H;
-                const bool work = live && r < rows && (is_q || stored);
-                float v[8] = {bf16_lo(x[i][0].x), bf16_hi(x[i][0].x), bf16_lo(x[i][0].y), bf16_hi(x[i][0].y),
-                              bf16_lo(x[i][1].x), bf16_hi(x[i][1].x), bf16_lo(x[i][1].y), bf16_hi(x[i][1].y)};
-                float sum = 0.f;
-#pragma unroll
-                for (int y = 0; y < 8; ++y) sum = fmaf(v[y], v[y], sum);
+            uint64_t v[4] = {two(bf16_lo(x[i][0].x), bf16_hi(x[i][0].x)), two(bf16_lo(x[i][0].y), bf16_hi(x[i][0].y)),
+                             two(bf16_lo(x[i][1].x), bf16_hi(x[i][1].x)), two(bf16_lo(x[i][1].y), bf16_hi(x[i][1].y))};
+            if (KIND != kValue) {
+                uint64_t squares = fma2(v[1], v[1], mul2(v[0], v[0]));
+                squares = add2(squares, fma2(v[3], v[3], mul2(v[2], v[2])));
+                float sum = first_of(squares) + second_of(squares);
 #pragma unroll
                 for (int m = LPR / 2; m > 0; m >>= 1) sum += __shfl_xor_sync(~0u, sum, m);
                 float root = rsqrtf(fmaf(sum, norm.inv_dim, norm.eps));
                 if (__any_sync(~0u, !(sum < 1e37f))) root = far_root<LPR>(v, sum, norm);
-                if (!is_v) {
+                const uint64_t by = two(root, root);
 #pragma unroll
-                    for (int y = 0; y < 8; ++y) v[y] *= root * (is_q ? wq[y] : wk[y]);
-                    if (turned && a.paired) {
-#pragma unroll
-                        for (int y = 0; y < 4; ++y) {
-                            const float one_was = v[2 * y];
-                            v[2 * y] = one_was * C[y] - v[2 * y + 1] * S[y];
-                            v[2 * y + 1] = v[2 * y + 1] * C[y] + one_was * S[y];
-                        }
-                    } else if (turned) {
-#pragma unroll
-                        for (int y = 0; y < 4; ++y) {
-                            const float one_was = v[y];
-                            v[y] = one_was * C[y] - v[y + 4] * S[y];
-                            v[y + 4] = v[y + 4] * C[y] + one_was * S[y];
-                        }
-                    }
-                }
-                if (Q8 && base + i * groups < 2 * H) {
-                    // RTN at 8 bits over the row's LPR lanes (idle lanes hold zeros); query rows go along unused.
-                    float most = 0.f;
-                    bool finite = true;
-#pragma unroll
-                    for (int y = 0; y < 8; ++y) {
-                        most = fmaxf(most, fabsf(v[y]));
-                        finite = finite && isfinite(v[y]);
-                    }
-                    if (!finite && live) most = INFINITY;
-#pragma unroll
-                    for (int m = LPR / 2; m > 0; m >>= 1) most = fmaxf(most, __shfl_xor_sync(~0u, most, m));
-                    if (work && !is_q) {
-                        const bool bad = isinf(most);
-                        const __nv_bfloat16 scale = __float2bfloat16_rn(bad ? NAN : __fdiv_rn(most, 127.f));
-                        const float s = __bfloat162float(scale);
-                        uint32_t code[2] = {0, 0};
-                        if (!bad && s > 0.f)
-#pragma unroll
-                            for (int y = 0; y < 8; ++y) {
-                                const int q = __float2int_rn(fminf(fmaxf(rintf(__fdiv_rn(v[y], s)), -128.f), 127.f));
-                                code[y / 4] |= (q & 0xFFu) << (8 * (y & 3));
-                            }
-                        const int h = is_v ? r - H : r;
-                        int8_t* dst = static_cast<int8_t*>(is_v ? a.v_cache : a.k_cache) + at + h * a.cache_head_stride;
-                        *reinterpret_cast<uint32_t*>(dst + one) = code[0];
-                        *reinterpret_cast<uint32_t*>(dst + two) = code[1];
-                        if (c == 0) (is_v ? a.v_scales : a.k_scales)[scale_at + static_cast<long long>(h) * a.page_size] = scale;
-                    }
-                }
-                if (work && (is_q || !Q8)) {
-                    __nv_bfloat16* dst;
-                    if (is_q)
-                        dst = a.q_out.data + t * a.q_out.token_stride + (r - 2 * H) * a.q_out.head_stride;
-                    else
-                        dst = static_cast<__nv_bfloat16*>(is_v ? a.v_cache : a.k_cache) + at + (is_v ? r - H : r) * a.cache_head_stride;
-                    if (is_v) {  // (as they are, NaN's bits among them)
-                        *reinterpret_cast<uint2*>(dst + one) = x[i][0];
-                        *reinterpret_cast<uint2*>(dst + two) = x[i][1];
-                    } else {
-                        *reinterpret_cast<uint2*>(dst + one) = make_uint2(pair_bf16(v[0], v[1]), pair_bf16(v[2], v[3]));
-                        *reinterpret_cast<uint2*>(dst + two) = make_uint2(pair_bf16(v[4], v[5]), pair_bf16(v[6], v[7]));
-                    }
-                }
+                for (int y = 0; y < 4; ++y) v[y] = mul2(mul2(v[y], by), w[y]);
+                if (lane.turned) turn_values(v, turned, lane.paired);
+            }
+            if (kCodes) {
+                put_codes<LPR>(v, lane, store, static_cast<int8_t*>(to) + at, scales + r * scale_stride);
+            } else if (store) {
+                *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(to) + at + lane.one) = make_uint2(pair_bf16(v[0]), pair_bf16(v[1]));
+                *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(to) + at + lane.other) = make_uint2(pair_bf16(v[2]), pair_bf16(v[3]));
             }
         }
     }
 }
 
+// A CTA takes every gridDim.x-th token: its threads fetch the token's cosines and
+// sines once for all of its rows, and then read, normalise, turn and write
+// keys, values and queries, kind by kind, so that a row takes few instructions
+// beside its own (one loop over all kinds of rows took 190 to two rows of 128,
+// and was bound by them: 104 µs for the prompt below).  blockIdx.y shares a
+// token's rows among CTAs where there are few tokens.
+template <int THREADS, int LPR, bool Q8>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) kv_append_norm_kernel(const __grid_constant__ KvAppendArgs a,
+                                                                                const __grid_constant__ KvNorm norm,
+                                                                                const __grid_constant__ Axes axes) {
+    constexpr int kGroups = THREADS / LPR;
+    __shared__ __align__(16) float s_cos[2][128], s_sin[2][128], s_weight[2][256];
+    const int c = threadIdx.x % LPR, own = threadIdx.x / LPR;
+    const int d = a.head_dim, H = a.kv_heads, F = a.rotary / 2;
+    // All kinds' rows are this CTA's, or, where there are few tokens, some of one kind.
+    auto slice = [&](const Rows& from, int rows, int y, int of) { return Part{from.data, from.head_stride, rows, y * kGroups, y * kGroups + own, of * kGroups}; };
+    const bool all = gridDim.y == 1;
+    const int q_slices = all ? 1 : (a.q_heads + kGroups - 1) / kGroups, kv_slices = all ? 1 : (H + kGroups - 1) / kGroups, y = blockIdx.y;
+    const bool keys = all || (y >= q_slices && y < q_slices + kv_slices), values = all || y >= q_slices + kv_slices;
+    const bool queries = (all || y < q_slices) && a.q_heads > 0;
+    const Part q_part = slice(a.q, a.q_heads, all ? 0 : y, q_slices), k_part = slice(a.k, H, all ? 0 : y - q_slices, kv_slices),
+               v_part = slice(a.v, H, all ? 0 : y - q_slices - kv_slices, kv_slices);
+    Lane lane;
+    lane.live = 8 * c < d;
+    lane.turned = 8 * c < a.rotary;
+    lane.paired = a.paired;
+    lane.one = lane.turned && !a.paired ? 4 * c : 8 * c;
+    lane.other = lane.turned && !a.paired ? F + 4 * c : 8 * c + 4;
+    for (int i = threadIdx.x; i < 2 * d; i += THREADS) {  // (read behind the first token's barrier)
+        const int which = i >= d, col = i - which * d;
+        const void* const w = which ? norm.q_weight : norm.k_weight;
+        s_weight[which][col] = !w ? 0.f : norm.offset + (norm.bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(w)[col]) : static_cast<const float*>(w)[col]);
+    }
+    for (int t = blockIdx.x, turn = 0; t < a.T; t += gridDim.x, turn ^= 1) {
+        const long long slot = a.slots[t];
+        Part qp = q_part, kp = k_part, vp = v_part;
+        qp.from += t * a.q.token_stride, kp.from += t * a.k.token_stride, vp.from += t * a.v.token_stride;
+        uint2 x[kBatch][2];  // the first rows' loads are under way while the token's turn is fetched
+        {
+            const Part p = queries ? qp : keys ? kp : vp;
+            const __nv_bfloat16* src = p.from + p.group * p.stride;
+            load_rows(p, lane, src, p.group, x);
+        }
+        for (int i = threadIdx.x; i < F; i += THREADS) {
+            const int axis = axes.of[i >> 3] >> (2 * (i & 7)) & 3;
+            int row = a.positions[axis * a.axis_stride + t];
+            if (row < 0 || row >= a.rows) {
+                record_status(a.status, kStatusInvalid);
+                row = 0;
+            }
+            s_cos[turn][i] = a.cos[static_cast<long long>(row) * F + i];
+            s_sin[turn][i] = a.sin[static_cast<long long>(row) * F + i];
+        }
+        __syncthreads();
+        Turned turned = {};
+        if (lane.turned) {
+            const float4 u = *reinterpret_cast<const float4*>(&s_cos[turn][4 * c]);
+            const float4 w = *reinterpret_cast<const float4*>(&s_sin[turn][4 * c]);
+            turned.C[0] = two(u.x, u.y), turned.C[1] = two(u.z, u.w);
+            turned.S[0] = two(w.x, w.y), turned.S[1] = two(w.z, w.w);
+            turned.minus[0] = two(-w.x, -w.y), turned.minus[1] = two(-w.z, -w.w);
+        }
+        if (queries)
+            put_rows<kQuery, LPR, Q8>(norm, lane, turned, s_weight[1], qp, true, x, a.q_out.data + t * a.q_out.token_stride, a.q_out.head_stride, nullptr, 0);
+        const bool stored = slot >= 0 && slot < a.pages * a.page_size;
+        if (!stored && slot != -1) record_status(a.status, kStatusInvalid);
+        if (!stored) continue;  // the same for the whole CTA
+        const long long page = slot <= 0x7fffffff ? static_cast<long long>((static_cast<uint64_t>(slot) * a.page_mul) >> a.page_shift)
+                                                  : slot / a.page_size;
+        const long long place = slot - page * a.page_size, at = page * a.page_stride + place * a.cache_token_stride;
+        const long long scale_at = page * H * a.page_size + place;
+        constexpr int kSize = Q8 ? 1 : 2;
+        if (keys)
+            put_rows<kKey, LPR, Q8>(norm, lane, turned, s_weight[0], kp, !queries, x, static_cast<uint8_t*>(a.k_cache) + at * kSize, a.cache_head_stride,
+                                    a.k_scales + scale_at, a.page_size);
+        if (values)
+            put_rows<kValue, LPR, Q8>(norm, lane, turned, nullptr, vp, !queries && !keys, x, static_cast<uint8_t*>(a.v_cache) + at * kSize, a.cache_head_stride,
+                                      a.v_scales + scale_at, a.page_size);
+    }
+}
+
 template <int THREADS, int LPR>
 cudaError_t append(const KvAppendArgs& a, const KvNorm& norm, const Axes& axes, bool q8, int64_t tokens, int sm_count, cudaStream_t stream) {
-    const int per_cta = THREADS / LPR, rows = 2 * a.kv_heads + a.q_heads;
-    const dim3 grid(static_cast<unsigned>(std::min(a.T, tokens)), a.T * 2 >= sm_count ? 1u : static_cast<unsigned>((rows + per_cta - 1) / per_cta));
+    const int per_cta = THREADS / LPR;
+    auto slices = [&](int rows) { return static_cast<unsigned>((rows + per_cta - 1) / per_cta); };
+    const dim3 grid(static_cast<unsigned>(std::min(a.T, tokens)), a.T * 2 >= sm_count ? 1u : slices(a.q_heads) + 2 * slices(a.kv_heads));
     if (q8)
         kv_append_norm_kernel<THREADS, LPR, true><<<grid, THREADS, 0, stream>>>(a, norm, axes);
     else
