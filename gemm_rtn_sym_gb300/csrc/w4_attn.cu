@@ -175,9 +175,12 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
     const AttnArgs& a = sp.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
     const int group = warp / R, rw = warp % R, G = sp.G;
-    if (a.pass == kPrefixes) find_low(sp);
+    let_next_start(a);
     Walk<kTile, 16 * R, kFixed> walk;
-    if (!walk.template find<kThreads>(sp)) return;
+    if (!walk.template find<kThreads>(sp)) {
+        end_after_the_one_before(a);
+        return;
+    }
     bool more;
     {
         Item it;
@@ -732,6 +735,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
                     parts.template join_rows<kWarps, 16>(sp, it, warp, lane, k0, n, step, last);
             });
     }
+    end_after_the_one_before(a);
 }
 
 // The parts in a pass's workspace, behind its counters.
@@ -792,8 +796,7 @@ cudaError_t run(const SplitArgs& sp, const DeviceInfo& dev, cudaStream_t stream)
     const double reach = std::min(static_cast<double>(a.width) * a.page_size, a.window > 0 ? static_cast<double>(a.window) + a.T : 1e18);
     const double most = static_cast<double>(a.kv_heads) * (a.B + static_cast<double>(a.T) * sp.G / (16 * R)) * (reach / kTile + 2 + S::kFixed);
     const int grid = static_cast<int>(std::min<double>(std::min(per_sm * dev.sm_count, kMaxCtas), most));
-    attn_split_kernel<D, Q8, R><<<grid, kThreads, S::kSmem, stream>>>(sp);
-    return cudaGetLastError();
+    return launch_pass(attn_split_kernel<D, Q8, R>, grid, kThreads, S::kSmem, stream, sp.a.pass == kOwn, sp);
 }
 
 template <int D, bool Q8>
@@ -850,13 +853,12 @@ namespace {
 size_t padded(size_t bytes) { return (bytes + 255) / 256 * 256; }
 }  // namespace
 
-// Workspaces of the two passes, first own tokens, and the rows' sums of both.
+// Workspaces of the two passes, and the rows' sums of both.
 size_t attn_shared_workspace_bytes(int32_t B, int64_t T, int32_t q_heads, int32_t kv_heads, int32_t head_dim, bool q8,
                                    int32_t groups) {
     const size_t rows = static_cast<size_t>(T) * q_heads;
     return padded(attn_decode_workspace_bytes(groups, T, q_heads, kv_heads, head_dim, q8)) +
-           padded(attn_decode_workspace_bytes(B, T, q_heads, kv_heads, head_dim, q8)) + padded(static_cast<size_t>(B) * 4) +
-           2 * padded(rows * sizeof(float4)) + 2 * padded(rows * head_dim * sizeof(float));
+           padded(attn_decode_workspace_bytes(B, T, q_heads, kv_heads, head_dim, q8)) + 2 * padded(rows * sizeof(float4)) + 2 * padded(rows * head_dim * sizeof(float));
 }
 
 cudaError_t launch_attn_shared(AttnArgs a, const SharedArgs& shared, bool q8, void* workspace, const DeviceInfo& dev,
@@ -870,11 +872,9 @@ cudaError_t launch_attn_shared(AttnArgs a, const SharedArgs& shared, bool q8, vo
     void* const first = take(attn_decode_workspace_bytes(shared.groups, a.T, a.q_heads, a.kv_heads, a.head_dim, q8));
     void* const second = take(attn_decode_workspace_bytes(a.B, a.T, a.q_heads, a.kv_heads, a.head_dim, q8));
     const size_t rows = static_cast<size_t>(a.T) * a.q_heads;
-    a.low = static_cast<int32_t*>(take(static_cast<size_t>(a.B) * 4));
     AttnArgs p = a;
     p.pass = kPrefixes;
     p.requests = a.B;
-    p.own_lens = a.lens;
     p.B = shared.groups;
     p.group_starts = shared.starts;
     p.table = shared.table;
@@ -884,6 +884,10 @@ cudaError_t launch_attn_shared(AttnArgs a, const SharedArgs& shared, bool q8, vo
     p.sums = static_cast<float4*>(take(rows * sizeof(float4)));
     p.sum_values = static_cast<float*>(take(rows * a.head_dim * sizeof(float)));
     a.pass = kOwn;
+    a.groups = shared.groups;
+    a.group_starts = shared.starts;
+    a.prefix_lens = shared.lens;
+    a.most_prefix = std::min<long long>(static_cast<long long>(shared.width) * a.page_size, kMostShared);
     a.sums = static_cast<float4*>(take(rows * sizeof(float4)));
     a.sum_values = static_cast<float*>(take(rows * a.head_dim * sizeof(float)));
     cudaError_t err = launch_attn_decode(p, q8, first, dev, stream);

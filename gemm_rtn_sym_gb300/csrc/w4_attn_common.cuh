@@ -57,6 +57,16 @@ __device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, 
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 
+// The three kernels of a call with shared prefixes follow one another closely: each lets the next one start as soon as
+// there is room, and the one over the requests' own tokens, which needs nothing from the one before, ends after it, so
+// that the join, which waits for its end, has both.
+__device__ __forceinline__ void let_next_start(const AttnArgs& a) {
+    if (a.pass != kAlone) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void end_after_the_one_before(const AttnArgs& a) {
+    if (a.pass == kOwn) asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // --------------------------------------------------------------- work list
 // A request's part of the work: rows and tokens, clipped to what is there.
 struct Request {
@@ -67,6 +77,21 @@ struct Request {
     int tiles;        // tiles of TILE tokens from the one of `low`
     int row_tiles;    // of ROWS rows (new tokens × query heads per key-value head)
 };
+
+// kOwn: the first token that request b, with n rows, reads by itself.  That is its group's prefix length, where all of
+// its rows stand behind the prefix; any other request reads all of its tokens.
+__device__ __forceinline__ int first_own(const AttnArgs& a, int b, int len, int n) {
+    int lo = 0, hi = a.groups;  // the last group that begins at b or before (or the first)
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (a.group_starts[mid] <= b)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    const int prefix = static_cast<int>(min(static_cast<long long>(max(a.prefix_lens[lo], 0)), a.most_prefix));
+    return a.group_starts[lo] <= b && b < a.group_starts[lo + 1] && static_cast<long long>(len) - n >= prefix ? prefix : 0;
+}
 
 template <int TILE, int ROWS>
 __device__ __forceinline__ Request request(const SplitArgs& sp, int b) {
@@ -93,7 +118,7 @@ __device__ __forceinline__ Request request(const SplitArgs& sp, int b) {
     const long long low = a.window > 0 ? static_cast<long long>(r.len) - r.n - a.window + 1 : 0;
     r.low = static_cast<int>(max(low, 0ll));
     if (a.pass == kPrefixes && r.len == 0) r.n = 0;
-    if (a.pass == kOwn) r.low = a.low[b];
+    if (a.pass == kOwn) r.low = min(first_own(a, b, len, r.n), r.len);
     // Every row sees all of a prefix.
     r.before = a.pass == kPrefixes ? r.len : r.len - r.n;
     // A request without tokens still has its rows of zeros to write: one tile.
@@ -112,35 +137,6 @@ __device__ __forceinline__ long long units(const AttnArgs& a, const Request& r) 
 __device__ __forceinline__ long long quotient(long long x, int y) {
     return x >> 32 ? static_cast<long long>(static_cast<unsigned long long>(x) / static_cast<unsigned>(y))
                    : static_cast<long long>(static_cast<unsigned>(x) / static_cast<unsigned>(y));
-}
-
-// kPrefixes: the first token that each request of the batch reads by itself.  That is its group's prefix length, where
-// all of its rows stand behind the prefix; any other request reads all of its tokens.
-__device__ __forceinline__ void find_low(const SplitArgs& sp) {
-    const AttnArgs& a = sp.a;
-    const int T = static_cast<int>(a.T);
-    const long long most = min(static_cast<long long>(a.width) * a.page_size, static_cast<long long>(kMostShared));
-    for (int b = blockIdx.x * blockDim.x + threadIdx.x; b < a.requests; b += gridDim.x * blockDim.x) {
-        int lo = 0, hi = a.B;  // the last group that begins at b or before (or the first)
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (a.group_starts[mid] <= b)
-                lo = mid;
-            else
-                hi = mid;
-        }
-        int low = 0;
-        if (a.group_starts[lo] <= b && b < a.group_starts[lo + 1]) {
-            int n = sp.rows_each;
-            if (a.starts) {
-                const int start = min(max(a.starts[b], 0), T);
-                n = min(max(a.starts[b + 1], start), T) - start;
-            }
-            const int prefix = static_cast<int>(min(static_cast<long long>(max(a.lens[lo], 0)), most));
-            if (static_cast<long long>(a.own_lens[b]) - n >= prefix) low = prefix;
-        }
-        a.low[b] = low;
-    }
 }
 
 // How `total` units are cut into n pieces: the first `longer` of them have one

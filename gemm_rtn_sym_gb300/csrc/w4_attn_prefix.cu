@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(Shape<D, Q8>::kThreads, 1) attn_prefix_kernel(
         mbar_init(smem_addr(&s_queries), kRowThreads);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    find_low(sp);
+    let_next_start(a);
     Walk<TT, kRows, kFixed> walk;
     if (!walk.template find<S::kThreads>(sp)) return;
     if (warp == kMmaWarp) tmem_alloc(smem_addr(&s_tmem), kTmemCols);
@@ -658,6 +658,7 @@ constexpr int kJoinWarps = 4, kJoinBatch = 8;
 // 19 of 66 KB where one prefix's 8 heads are shared by 152 SMs.)
 template <int V>  // float4 of a lane: head_dim ≤ 128 · V
 __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const __grid_constant__ JoinArgs a) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int lane = threadIdx.x & 31;
     const long long first = a.starts ? min(max(a.starts[0], 0), a.T) : 0, end = a.starts ? min(max(a.starts[a.B], 0), a.T) : a.T;
     const long long row = (first * a.q_heads) + static_cast<long long>(blockIdx.x) * kJoinWarps + (threadIdx.x >> 5);
@@ -734,11 +735,7 @@ cudaError_t launch_attn_join(JoinArgs a, cudaStream_t stream) {
     a.part_floats = partial_floats(kRows, a.D);
     const long long rows = static_cast<long long>(a.T) * a.q_heads;
     const unsigned grid = static_cast<unsigned>((rows + kJoinWarps - 1) / kJoinWarps);
-    if (a.head_dim <= 128)
-        attn_join_kernel<1><<<grid, 32 * kJoinWarps, 0, stream>>>(a);
-    else
-        attn_join_kernel<2><<<grid, 32 * kJoinWarps, 0, stream>>>(a);
-    return cudaGetLastError();
+    return launch_pass(a.head_dim <= 128 ? attn_join_kernel<1> : attn_join_kernel<2>, static_cast<int>(grid), 32 * kJoinWarps, 0, stream, true, a);
 }
 
 cudaError_t launch_attn_prefix(const SplitArgs& sp, bool q8, const DeviceInfo& dev, cudaStream_t stream) {

@@ -102,9 +102,12 @@ __global__ void __launch_bounds__(Shape<D, Q8>::kThreads, 1) attn_tc_kernel(cons
         mbar_init(smem_addr(&s_queries), kSoftmaxWarps * 32);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (a.pass == kPrefixes) find_low(sp);
+    let_next_start(a);
     Walk<TT, kRows, kFixed> walk;
-    if (!walk.template find<S::kThreads>(sp)) return;
+    if (!walk.template find<S::kThreads>(sp)) {
+        end_after_the_one_before(a);
+        return;
+    }
     if (warp == kMmaWarp) tmem_alloc(smem_addr(&s_tmem), kTmemCols);
     tc_fence_before();
     __syncthreads();
@@ -631,6 +634,7 @@ __global__ void __launch_bounds__(Shape<D, Q8>::kThreads, 1) attn_tc_kernel(cons
         tc_fence_after();
         tmem_dealloc(tmem, kTmemCols);
     }
+    end_after_the_one_before(a);
 }
 
 template <int D, bool Q8>
@@ -645,8 +649,7 @@ cudaError_t run(const SplitArgs& sp, int grid, cudaStream_t stream) {
         if (err != cudaSuccess) return err;
         ready[device & (kMaxDevices - 1)].store(true, std::memory_order_relaxed);
     }
-    attn_tc_kernel<D, Q8><<<grid, S::kThreads, S::kSmem, stream>>>(sp);
-    return cudaGetLastError();
+    return launch_pass(attn_tc_kernel<D, Q8>, grid, S::kThreads, S::kSmem, stream, sp.a.pass == kOwn, sp);
 }
 
 }  // namespace

@@ -168,12 +168,13 @@ struct AttnArgs {
     int32_t page_shift;
     // Prefixes that groups of requests share take two passes, each of which leaves its rows' sums behind, and a kernel that
     // joins them: kPrefixes, whose "requests" are the groups (B, table and lens are theirs), and kOwn, over each request's
-    // tokens from low[b] on.
+    // tokens behind its prefix.
     int32_t pass;
     int32_t requests;             // kPrefixes: of the batch
-    const int32_t* group_starts;  // kPrefixes: [B + 1], requests of each group
-    const int32_t* own_lens;      // kPrefixes: lens of the batch
-    int32_t* low;                 // [requests], written by kPrefixes; 0: nothing shared
+    int32_t groups;               // kOwn
+    const int32_t* group_starts;  // [groups + 1], requests of each group
+    const int32_t* prefix_lens;   // kOwn: [groups]
+    long long most_prefix;        // kOwn: tokens that a row of the prefixes' table holds
     // [T · q_heads]: reference and sum of the weights.  kOwn: what the row is, a RowKind.  kPrefixes: parts that the sums
     // are still in (0: none), and where the first of them is.
     float4* sums;
