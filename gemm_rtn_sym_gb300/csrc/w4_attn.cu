@@ -796,7 +796,7 @@ cudaError_t run(const SplitArgs& sp, const DeviceInfo& dev, cudaStream_t stream)
     const double reach = std::min(static_cast<double>(a.width) * a.page_size, a.window > 0 ? static_cast<double>(a.window) + a.T : 1e18);
     const double most = static_cast<double>(a.kv_heads) * (a.B + static_cast<double>(a.T) * sp.G / (16 * R)) * (reach / kTile + 2 + S::kFixed);
     const int grid = static_cast<int>(std::min<double>(std::min(per_sm * dev.sm_count, kMaxCtas), most));
-    return launch_pass(attn_split_kernel<D, Q8, R>, grid, kThreads, S::kSmem, stream, sp.a.pass == kOwn, sp);
+    return launch_pass(attn_split_kernel<D, Q8, R>, grid, kThreads, S::kSmem, stream, sp.a.pass != kAlone, sp);
 }
 
 template <int D, bool Q8>

@@ -57,10 +57,11 @@ __device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, 
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 
-// The three kernels of a call with shared prefixes follow one another closely: each lets the next one start as soon as
-// there is room, and the one over the requests' own tokens, which needs nothing from the one before, ends after it, so
-// that the join, which waits for its end, has both.
+// The three kernels of a call with shared prefixes follow one another closely.  The first waits for what the stream did
+// before the call; each then lets the next one start as soon as there is room; the one over the requests' own tokens,
+// which needs nothing from the one before, ends after it, so that the join, which waits for its end, has both.
 __device__ __forceinline__ void let_next_start(const AttnArgs& a) {
+    if (a.pass == kPrefixes) asm volatile("griddepcontrol.wait;" ::: "memory");
     if (a.pass != kAlone) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 __device__ __forceinline__ void end_after_the_one_before(const AttnArgs& a) {

@@ -128,6 +128,7 @@ __global__ void __launch_bounds__(Shape<D, Q8>::kThreads, 1) attn_prefix_kernel(
     Walk<TT, kRows, kFixed> walk;
     if (!walk.template find<S::kThreads>(sp)) return;
     if (warp == kMmaWarp) tmem_alloc(smem_addr(&s_tmem), kTmemCols);
+    if (warp == kRowWarps && lane < 2 && boxes.tokens > 0) asm volatile("prefetch.tensormap [%0];" ::"l"(lane ? &boxes.v : &boxes.k));
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -391,7 +392,7 @@ __global__ void __launch_bounds__(Shape<D, Q8>::kThreads, 1) attn_prefix_kernel(
         const int group = warp >> 2, own_row = tid & (kRows - 1);
         const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16), scores = lanes + group * TT, out = lanes + kColO + group * D;
         uint32_t tile = 0, four = 0, items = 0;  // tiles of the group so far; of both; items
-        // The queries of an item are asked for before the sums of the one before it go out: a row by D / 8 lanes.
+        // The queries of an item: a row by D / 8 lanes.
         auto ask = [&](const Item& n) {
             constexpr int kChunks = D / 8, kPerPass = kRowThreads / kChunks;
             const int c = tid % kChunks;
@@ -404,14 +405,12 @@ __global__ void __launch_bounds__(Shape<D, Q8>::kThreads, 1) attn_prefix_kernel(
             }
         };
         Item it;
-        bool more = walk.next(sp, it);
+        bool more = walk.next(sp, it), first = true;
         if (more) ask(it);
         while (more) {
             const int tiles = tiles_of<TT>(it);
             const int row = it.row0 + own_row, j = sp.over_G(row);
             const bool live = row < it.rows;
-            cp_async_wait_all();
-            fence_async_smem();
             {
                 uint32_t zero[32];
 #pragma unroll
@@ -420,16 +419,24 @@ __global__ void __launch_bounds__(Shape<D, Q8>::kThreads, 1) attn_prefix_kernel(
                 for (int c = 0; c < D; c += 32) tmem_st32(out + c, zero);
                 tmem_wait_st();
             }
-            tc_fence_before();
-            mbar_arrive(smem_addr(&s_queries));
+            auto queries_there = [&] {
+                cp_async_wait_all();
+                fence_async_smem();
+                tc_fence_before();
+                mbar_arrive(smem_addr(&s_queries));
+            };
+            if (!first) queries_there();
             float m = -INFINITY, l = 0.f;  // reference score, unscaled (format 8: to base 2); sum of the weights
             const float unit = Q8 ? 1.f : sp.scale_log2;
-            for (int i = group; i < tiles; i += 2, ++tile) {
+            // The first of a CTA's tiles has one before it that leaves nothing behind: its instructions, which are in no cache
+            // yet, arrive while queries and tokens do.
+            for (int i = first ? group - 2 : group; i < tiles; i += 2) {
+                const bool real = i >= 0;
                 const int there = it.tok1 - it.tok0 - i * TT;  // columns that are tokens
-                wait_or_report(smem_addr(&s_scores[group]), tile & 1, alive, a.status);
+                if (real) wait_or_report(smem_addr(&s_scores[group]), tile & 1, alive, a.status);
                 tc_fence_after();
                 const uint32_t buffer = (four + i) & 3;
-                if (Q8) wait_or_report(smem_addr(&s_scaled[buffer]), (four + i) >> 2 & 1, alive, a.status);
+                if (Q8 && real) wait_or_report(smem_addr(&s_scaled[buffer]), (four + i) >> 2 & 1, alive, a.status);
                 const float(*const scale)[Q8 ? TT : 4] = s_scale[Q8 ? buffer : 0];
                 // Format 16 holds the 128 scores, format 8 (which has less room) reads them twice.
                 constexpr int kHeld = Q8 ? 1 : TT / 32;
@@ -515,7 +522,7 @@ __global__ void __launch_bounds__(Shape<D, Q8>::kThreads, 1) attn_prefix_kernel(
                         w[x >> 1] = __byte_perm(u0, u1, 0x7632);
                         w[16 + (x >> 1)] = __byte_perm(__float_as_uint(first_of(left)), __float_as_uint(second_of(left)), 0x7632);
                     }
-                    tmem_st32(scores + 32 * c, w);
+                    if (real) tmem_st32(scores + 32 * c, w);
                 };
                 if constexpr (!Q8) {
 #pragma unroll
@@ -529,10 +536,17 @@ __global__ void __launch_bounds__(Shape<D, Q8>::kThreads, 1) attn_prefix_kernel(
                     }
                 }
                 l = (first_of(sums[0]) + second_of(sums[0])) + (first_of(sums[1]) + second_of(sums[1]));
+                if (!real) {
+                    m = -INFINITY, l = 0.f;
+                    queries_there();
+                    continue;
+                }
                 tmem_wait_st();
                 tc_fence_before();
                 mbar_arrive(smem_addr(&s_weights[group]));
+                ++tile;
             }
+            first = false;
             four += tiles;
             // ---- the two groups' sums
             wait_or_report(smem_addr(&s_values), items++ & 1, alive, a.status);
@@ -541,9 +555,6 @@ __global__ void __launch_bounds__(Shape<D, Q8>::kThreads, 1) attn_prefix_kernel(
             if (group == 1) s_stats[own_row] = make_float2(m * unit, l);
             rows_sync();
             tc_fence_after();
-            Item after;
-            more = walk.next(sp, after);
-            if (more) ask(after);
             float top = 0.f, sum = 0.f, by_even, by_odd;  // (top and sum: of the even group's threads)
             if (group == 0) {
                 const float2 odd = s_stats[own_row];
@@ -567,41 +578,46 @@ __global__ void __launch_bounds__(Shape<D, Q8>::kThreads, 1) attn_prefix_kernel(
                 if (!whole) reinterpret_cast<float2*>(part)[own_row] = make_float2(top, fminf(sum, 3e38f));
                 if (k == 0) a.sums[at_row] = make_float4(top, fminf(sum, 3e38f), __int_as_float(whole ? 0 : parts.count), __int_as_float(parts.first << 8 | own_row));
             }
-            // Eight lanes turn eight chunks of four columns of their rows round, so that each row's go out as 128 bytes.
+            // A warp's 32 rows go out through its part of the queries' place, some columns at a time, so that a row's lie side
+            // by side (16-byte chunks of eight rows in different banks).
+            constexpr int kCols = D / 4, kPieces = kCols / 4, kRowsAtOnce = 32 / kPieces;
             float* const to = whole ? a.sum_values + at_row * a.head_dim : part + 2 * kRows + own_row * D;
+            const uint32_t corner = q_smem + warp * 32 * kCols * 4;
+            auto chunk = [&](int r, int q) { return corner + (r * kPieces + (q ^ (r & (kPieces - 1)))) * 16; };
 #pragma unroll 1
-            for (int c = group * (D / 2); c < (group + 1) * (D / 2); c += 32) {
-                uint32_t u[32];
-                float v[32];
-                tmem_ld32(lanes + kColO + c, u);
+            for (int c = group * (D / 2); c < (group + 1) * (D / 2); c += kCols) {
+                uint32_t u[kCols / 16][16], v[kCols / 16][16];
 #pragma unroll
-                for (int x = 0; x < 32; ++x) v[x] = __uint_as_float(u[x]) * by_even;
-                tmem_ld32(lanes + kColO + D + c, u);
-#pragma unroll
-                for (int x = 0; x < 32; ++x) v[x] = fmaf(__uint_as_float(u[x]), by_odd, v[x]);
-#pragma unroll
-                for (int s = 4; s > 0; s >>= 1)
-#pragma unroll
-                    for (int q = 0; q < 8; ++q)
-                        if (!(q & s))
-#pragma unroll
-                            for (int y = 0; y < 4; ++y) {
-                                const bool upper = lane & s;
-                                const float got = __shfl_xor_sync(~0u, upper ? v[4 * q + y] : v[4 * (q + s) + y], s);
-                                (upper ? v[4 * q + y] : v[4 * (q + s) + y]) = got;
-                            }
-                const int col = c + 4 * (lane & 7);
-#pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    const int from = (lane & 24) + q;
-                    float* const row_to = reinterpret_cast<float*>(__shfl_sync(~0u, reinterpret_cast<unsigned long long>(to), from));
-                    if (it.row0 + (own_row & ~31) + from < it.rows && col < a.head_dim)
-                        *reinterpret_cast<float4*>(row_to + col) = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+                for (int y = 0; y < kCols / 16; ++y) {
+                    tmem_ld16_async(lanes + kColO + c + 16 * y, u[y]);
+                    tmem_ld16_async(lanes + kColO + D + c + 16 * y, v[y]);
                 }
+                tmem_wait_ld();
+#pragma unroll
+                for (int y = 0; y < kCols / 16; ++y) {
+                    reg_fence16(u[y]);
+                    reg_fence16(v[y]);
+                    auto joined = [&](int x) { return __float_as_uint(fmaf(__uint_as_float(v[y][x]), by_odd, __uint_as_float(u[y][x]) * by_even)); };
+#pragma unroll
+                    for (int x = 0; x < 16; x += 4) sts128(chunk(lane, 4 * y + x / 4), make_uint4(joined(x), joined(x + 1), joined(x + 2), joined(x + 3)));
+                }
+                __syncwarp();
+                const int q = lane % kPieces, col = c + 4 * q;
+#pragma unroll
+                for (int r = 0; r < 32; r += kRowsAtOnce) {
+                    const int from = r + lane / kPieces;
+                    float* const row_to = reinterpret_cast<float*>(__shfl_sync(~0u, reinterpret_cast<unsigned long long>(to), from));
+                    const uint4 w = lds128(chunk(from, q));
+                    if (it.row0 + (own_row & ~31) + from < it.rows && col < a.head_dim) *reinterpret_cast<uint4*>(row_to + col) = w;
+                }
+                __syncwarp();
             }
             tc_fence_before();
             rows_sync();  // the sums are read: the next item's may begin
             tc_fence_after();
+            Item after;
+            more = walk.next(sp, after);
+            if (more) ask(after);
             it = after;
         }
     }
@@ -645,8 +661,7 @@ cudaError_t run(const SplitArgs& sp, int grid, cudaStream_t stream) {
         if (err != cudaSuccess) return err;
         ready[device & (kMaxDevices - 1)].store(true, std::memory_order_relaxed);
     }
-    attn_prefix_kernel<D, Q8><<<grid, S::kThreads, S::kSmem, stream>>>(sp, Q8 ? Boxes{} : boxes_of(sp.a));
-    return cudaGetLastError();
+    return launch_pass(attn_prefix_kernel<D, Q8>, grid, S::kThreads, S::kSmem, stream, true, sp, Q8 ? Boxes{} : boxes_of(sp.a));
 }
 
 // -------------------------------------------------------------------- join

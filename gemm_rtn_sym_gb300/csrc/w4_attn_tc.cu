@@ -649,7 +649,7 @@ cudaError_t run(const SplitArgs& sp, int grid, cudaStream_t stream) {
         if (err != cudaSuccess) return err;
         ready[device & (kMaxDevices - 1)].store(true, std::memory_order_relaxed);
     }
-    return launch_pass(attn_tc_kernel<D, Q8>, grid, S::kThreads, S::kSmem, stream, sp.a.pass == kOwn, sp);
+    return launch_pass(attn_tc_kernel<D, Q8>, grid, S::kThreads, S::kSmem, stream, sp.a.pass != kAlone, sp);
 }
 
 }  // namespace

@@ -11,22 +11,6 @@ namespace w4 {
 
 // Floats of a part of a shared item.
 size_t attn_tc_partial_floats(int head_dim);
-// `early`: the kernel may start before the one ahead of it has ended, and waits itself where it has to.
-template <class... Args>
-cudaError_t launch_pass(void (*kernel)(Args...), int grid, int threads, size_t smem, cudaStream_t stream, bool early, Args... args) {
-    cudaLaunchAttribute attr = {};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(grid));
-    cfg.blockDim = dim3(static_cast<unsigned>(threads));
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cfg.attrs = &attr;
-    cfg.numAttrs = early ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 // The rows' sums of the two passes of a call with shared prefixes.
 struct JoinArgs {
     Rows out;

@@ -20,6 +20,30 @@ struct DeviceInfo {
 // Returns nullptr (and sets *err) when the current device cannot be queried.
 const DeviceInfo* device_info(cudaError_t* err);
 
+// (arguments convert to what the kernel takes)
+template <class T>
+struct SameType {
+    using type = T;
+};
+template <class T>
+using Same = typename SameType<T>::type;
+
+// `early`: the kernel may start before the one ahead of it has ended, and waits itself where it has to.
+template <class... Args>
+cudaError_t launch_pass(void (*kernel)(Args...), dim3 grid, int threads, size_t smem, cudaStream_t stream, bool early, Same<Args>... args) {
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = early ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<Args>(args)...);
+}
+
 // Launchers.  Arguments are already validated by the C ABI layer.
 // group 32/64/128; zeros == nullptr: symmetric, else asymmetric (int8 z − 8 per
 // group).  s != nullptr (group 128, symmetric only): RTN of bf16_rne(fp32(w·s_k)).

@@ -51,6 +51,7 @@ __global__ void __launch_bounds__(kPagesThreads) kv_pages_kernel(KvPagesArgs a) 
     __shared__ int s_len[kPagesThreads], s_have[kPagesThreads], s_want[kPagesThreads];
     __shared__ Sums s_warp[32];
     __shared__ long long s_used[32];
+    if (HELD) pdl_start();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x;
     const long long head = a.range[0], tail = a.range[1];
     const long long most = static_cast<long long>(a.width) * a.page_size;
@@ -363,8 +364,7 @@ cudaError_t launch_kv_pages(KvPagesArgs a, const DeviceInfo& dev, cudaStream_t s
         kv_pages_kernel<false><<<grid, threads, 0, stream>>>(a);
         return cudaGetLastError();
     }
-    kv_pages_kernel<true><<<grid, threads, 0, stream>>>(a);
-    const cudaError_t err = cudaGetLastError();
+    const cudaError_t err = launch_pass(kv_pages_kernel<true>, grid, threads, 0, stream, true, a);
     return err != cudaSuccess || (grid == 1 && !a.last) ? err : launch_kv_release(a, dev, stream);
 }
 

@@ -219,6 +219,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) kv_append_norm_kernel
     lane.paired = a.paired;
     lane.one = lane.turned && !a.paired ? 4 * c : 8 * c;
     lane.other = lane.turned && !a.paired ? F + 4 * c : 8 * c + 4;
+    pdl_start();
     for (int i = threadIdx.x; i < 2 * d; i += THREADS) {  // (read behind the first token's barrier)
         const int which = i >= d, col = i - which * d;
         const void* const w = which ? norm.q_weight : norm.k_weight;
@@ -275,13 +276,12 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) kv_append_norm_kernel
 template <int THREADS, int LPR>
 cudaError_t append(const KvAppendArgs& a, const KvNorm& norm, const Axes& axes, bool q8, int64_t tokens, int sm_count, cudaStream_t stream) {
     const int per_cta = THREADS / LPR;
-    auto slices = [&](int rows) { return static_cast<unsigned>((rows + per_cta - 1) / per_cta); };
-    const dim3 grid(static_cast<unsigned>(std::min(a.T, tokens)), a.T * 2 >= sm_count ? 1u : slices(a.q_heads) + 2 * slices(a.kv_heads));
-    if (q8)
-        kv_append_norm_kernel<THREADS, LPR, true><<<grid, THREADS, 0, stream>>>(a, norm, axes);
-    else
-        kv_append_norm_kernel<THREADS, LPR, false><<<grid, THREADS, 0, stream>>>(a, norm, axes);
-    return cudaGetLastError();
+    auto slices = [&](int rows) { return (rows + per_cta - 1) / per_cta; };
+    const int y = a.T * 2 >= sm_count ? 1 : slices(a.q_heads) + 2 * slices(a.kv_heads);
+    // A few CTAs may start before the kernel ahead of them ends (3.3 to 3.0 µs for one token, one call after another);
+    // many would take its SMs' room (5.5 to 7.0 for 208 tokens, 87 to 91 for 16001).
+    const dim3 grid(static_cast<unsigned>(std::min(a.T, tokens)), static_cast<unsigned>(y));
+    return launch_pass(q8 ? kv_append_norm_kernel<THREADS, LPR, true> : kv_append_norm_kernel<THREADS, LPR, false>, grid, THREADS, 0, stream, y > 1, a, norm, axes);
 }
 
 template <int THREADS>

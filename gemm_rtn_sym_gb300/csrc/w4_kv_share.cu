@@ -20,7 +20,10 @@ namespace {
 
 constexpr int kThreads = 1024;
 
-__global__ void __launch_bounds__(kThreads) kv_release_kernel(KvPagesArgs a) { release_pages(a); }
+__global__ void __launch_bounds__(kThreads) kv_release_kernel(KvPagesArgs a) {
+    pdl_start();
+    release_pages(a);
+}
 
 // ------------------------------------------------------- release, many pages
 // Entries by all CTAs at once.  Each leaves its number in its page's word if
@@ -30,6 +33,7 @@ __global__ void __launch_bounds__(kThreads) kv_release_kernel(KvPagesArgs a) { r
 __global__ void __launch_bounds__(kThreads) kv_let_go_kernel(KvPagesArgs a) {
     __shared__ long long s_first[kThreads], s_warp[33];
     __shared__ int s_want[kThreads];
+    pdl_start();
     const int tid = threadIdx.x;
     long long before = 0;
     for (int base = 0; base < a.B; base += kThreads) {
@@ -66,6 +70,7 @@ __global__ void __launch_bounds__(kThreads) kv_give_back_kernel(KvPagesArgs a) {
     __shared__ long long s_first[kThreads], s_warp[33];
     __shared__ int s_want[kThreads], s_before[kMarkWords];
     __shared__ unsigned s_words[kMarkWords];
+    pdl_start();
     const int tid = threadIdx.x;
     const long long tail = a.range[1];
     const long long tail_at = static_cast<long long>(static_cast<uint64_t>(tail) % static_cast<uint64_t>(a.pages));
@@ -127,6 +132,7 @@ __global__ void __launch_bounds__(kThreads) kv_give_back_kernel(KvPagesArgs a) {
 __global__ void __launch_bounds__(kThreads) kv_fork_kernel(KvForkArgs a) {
     __shared__ long long s_first[kThreads], s_warp[33], s_need[33];
     __shared__ int s_full[kThreads], s_source[kThreads], s_page[kThreads];
+    pdl_start();
     const int tid = threadIdx.x;
     const long long head = a.range[0], tail = a.range[1], most = static_cast<long long>(a.width) * a.page_size;
     const long long free = min(max(tail - head, 0ll), static_cast<long long>(a.pages));
@@ -256,6 +262,7 @@ struct Bits {
 __global__ void __launch_bounds__(kThreads, 1) kv_compact_kernel(KvCompactArgs a) {
     extern __shared__ uint32_t s_words[];
     __shared__ long long s_warp[33];
+    pdl_start();
     const int tid = threadIdx.x, lane = tid & 31;
     const int pages = static_cast<int>(a.pages), blocks = (pages + kBlockPages - 1) / kBlockPages;
     int* const s_before = reinterpret_cast<int*>(s_words + 4 * blocks);
@@ -341,6 +348,7 @@ struct CopyShape {
 __global__ void __launch_bounds__(kCopyThreads) kv_copy_kernel(const __grid_constant__ CopyShape s) {
     __shared__ int s_from[kList], s_to[kList], s_tokens[kList];
     __shared__ int s_warp[kCopyThreads / 32];
+    pdl_start();
     const KvCopyArgs& a = s.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const Divide over_chunks = {s.chunk_mul, s.chunk_shift}, over_inner = {s.inner_mul, s.inner_shift}, over_pieces = {s.piece_mul, s.piece_shift};
@@ -433,15 +441,11 @@ __global__ void __launch_bounds__(kCopyThreads) kv_copy_kernel(const __grid_cons
 cudaError_t launch_kv_release(const KvPagesArgs& a, const DeviceInfo& dev, cudaStream_t stream) {
     const int64_t entries = static_cast<int64_t>(a.B) * a.width;
     if (!a.last) {
-        kv_release_kernel<<<1, kThreads, 0, stream>>>(a);
-        return cudaGetLastError();
+        return launch_pass(kv_release_kernel, 1, kThreads, 0, stream, true, a);
     }
-    auto ctas = [&](int64_t each) { return static_cast<unsigned>(std::min<int64_t>((entries + each - 1) / each, dev.sm_count)); };
-    kv_let_go_kernel<<<ctas(kThreads), kThreads, 0, stream>>>(a);
-    const cudaError_t err = cudaGetLastError();
-    if (err != cudaSuccess) return err;
-    kv_give_back_kernel<<<ctas(kMarked), kThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+    auto ctas = [&](int64_t each) { return static_cast<int>(std::min<int64_t>((entries + each - 1) / each, dev.sm_count)); };
+    const cudaError_t err = launch_pass(kv_let_go_kernel, ctas(kThreads), kThreads, 0, stream, true, a);
+    return err != cudaSuccess ? err : launch_pass(kv_give_back_kernel, ctas(kMarked), kThreads, 0, stream, true, a);
 }
 
 // Words for each page and a bit for each entry of the table, where more pages may go back than one CTA should see to.
@@ -453,8 +457,7 @@ size_t kv_held_workspace_bytes(int32_t B, int32_t width, int64_t pages) {
 cudaError_t launch_kv_fork(KvForkArgs a, const DeviceInfo& dev, cudaStream_t stream) {
     divide_by(a.page_size, &a.page_mul, &a.page_shift);
     const int64_t blocks = (static_cast<int64_t>(a.B) * a.width + 4 * kThreads - 1) / (4 * kThreads);
-    kv_fork_kernel<<<static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(blocks, dev.sm_count))), kThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+    return launch_pass(kv_fork_kernel, static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(blocks, dev.sm_count))), kThreads, 0, stream, true, a);
 }
 
 cudaError_t launch_kv_compact(KvCompactArgs a, const DeviceInfo& dev, cudaStream_t stream) {
@@ -467,8 +470,7 @@ cudaError_t launch_kv_compact(KvCompactArgs a, const DeviceInfo& dev, cudaStream
     }
     const int64_t work = std::max<int64_t>(a.pages, static_cast<int64_t>(a.B) * a.width);
     const int64_t grid = std::max<int64_t>(1, std::min<int64_t>((work + kThreads - 1) / kThreads, dev.sm_count));
-    kv_compact_kernel<<<static_cast<unsigned>(grid), kThreads, smem, stream>>>(a);
-    return cudaGetLastError();
+    return launch_pass(kv_compact_kernel, static_cast<int>(grid), kThreads, smem, stream, true, a);
 }
 
 cudaError_t launch_kv_copy(const KvCopyArgs& a, const DeviceInfo& dev, cudaStream_t stream) {
@@ -483,8 +485,7 @@ cudaError_t launch_kv_copy(const KvCopyArgs& a, const DeviceInfo& dev, cudaStrea
     divide_by(per_copy, &s.piece_mul, &s.piece_shift);
     const int64_t most = static_cast<int64_t>(a.n) * per_copy;
     const int grid = static_cast<int>(std::min<int64_t>(most, 8 * dev.sm_count));
-    kv_copy_kernel<<<grid, kCopyThreads, 0, stream>>>(s);
-    return cudaGetLastError();
+    return launch_pass(kv_copy_kernel, grid, kCopyThreads, 0, stream, true, s);
 }
 
 }  // namespace w4
