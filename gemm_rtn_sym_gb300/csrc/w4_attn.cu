@@ -162,8 +162,8 @@ __device__ __forceinline__ void group_sync(int group) {
         asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(R * 32) : "memory");
 }
 
-template <int D, bool Q8, int R>
-__global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_kernel(const __grid_constant__ SplitArgs sp) {
+template <int D, bool Q8, int R, class SP>
+__global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_kernel(const __grid_constant__ SP sp) {
     using S = Shape<D, Q8, R>;
     constexpr int NT = D / 8;   // output tiles of 8 columns
     constexpr int KS = D / 16;  // k-steps of 16
@@ -175,10 +175,10 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
     const AttnArgs& a = sp.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
     const int group = warp / R, rw = warp % R, G = sp.G;
-    let_next_start(a);
+    let_next_start(sp);
     Walk<kTile, 16 * R, kFixed> walk;
     if (!walk.template find<kThreads>(sp)) {
-        end_after_the_one_before(a);
+        end_after_the_one_before(sp);
         return;
     }
     bool more;
@@ -735,7 +735,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, Q8, R>::kCtas) attn_split_k
                     parts.template join_rows<kWarps, 16>(sp, it, warp, lane, k0, n, step, last);
             });
     }
-    end_after_the_one_before(a);
+    end_after_the_one_before(sp);
 }
 
 // The parts in a pass's workspace, behind its counters.
@@ -774,8 +774,8 @@ bool many_rows(int32_t B, int64_t T, int G, int32_t kv_heads, int D, bool q8) {
 // 570 and 545 in longer requests.
 int row_warps(int32_t B, int64_t T, int G, bool q8) { return !q8 && average_rows(B, T, G) > 16 ? 2 : 1; }
 
-template <int D, bool Q8, int R>
-cudaError_t run(const SplitArgs& sp, const DeviceInfo& dev, cudaStream_t stream) {
+template <int D, bool Q8, int R, class SP>
+cudaError_t run(const SP& sp, const DeviceInfo& dev, cudaStream_t stream) {
     using S = Shape<D, Q8, R>;
     // CTAs that an SM holds, asked once per device.
     static std::atomic<int> known[kMaxDevices];
@@ -784,9 +784,9 @@ cudaError_t run(const SplitArgs& sp, const DeviceInfo& dev, cudaStream_t stream)
     if (err != cudaSuccess) return err;
     int per_sm = known[device & (kMaxDevices - 1)].load(std::memory_order_relaxed);
     if (per_sm == 0) {
-        err = cudaFuncSetAttribute(attn_split_kernel<D, Q8, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+        err = cudaFuncSetAttribute(attn_split_kernel<D, Q8, R, SP>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
         if (err != cudaSuccess) return err;
-        err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, attn_split_kernel<D, Q8, R>, kThreads, S::kSmem);
+        err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, attn_split_kernel<D, Q8, R, SP>, kThreads, S::kSmem);
         if (err != cudaSuccess) return err;
         if (per_sm < 1) return cudaErrorInvalidConfiguration;
         known[device & (kMaxDevices - 1)].store(per_sm, std::memory_order_relaxed);
@@ -796,18 +796,18 @@ cudaError_t run(const SplitArgs& sp, const DeviceInfo& dev, cudaStream_t stream)
     const double reach = std::min(static_cast<double>(a.width) * a.page_size, a.window > 0 ? static_cast<double>(a.window) + a.T : 1e18);
     const double most = static_cast<double>(a.kv_heads) * (a.B + static_cast<double>(a.T) * sp.G / (16 * R)) * (reach / kTile + 2 + S::kFixed);
     const int grid = static_cast<int>(std::min<double>(std::min(per_sm * dev.sm_count, kMaxCtas), most));
-    return launch_pass(attn_split_kernel<D, Q8, R>, grid, kThreads, S::kSmem, stream, sp.a.pass != kAlone, sp);
+    return launch_pass(attn_split_kernel<D, Q8, R, SP>, grid, kThreads, S::kSmem, stream, !std::is_same<SP, SplitArgs>::value, sp);
 }
 
-template <int D, bool Q8>
-cudaError_t run_rows(const SplitArgs& sp, const DeviceInfo& dev, cudaStream_t stream) {
+template <int D, bool Q8, class SP>
+cudaError_t run_rows(const SP& sp, const DeviceInfo& dev, cudaStream_t stream) {
     if constexpr (!Q8)
         if (row_warps(sp.a.B, sp.a.T, sp.G, Q8) == 2) return run<D, Q8, 2>(sp, dev, stream);
     return run<D, Q8, 1>(sp, dev, stream);
 }
 
-template <bool Q8>
-cudaError_t run_dim(const SplitArgs& sp, const DeviceInfo& dev, cudaStream_t stream) {
+template <bool Q8, class SP>
+cudaError_t run_dim(const SP& sp, const DeviceInfo& dev, cudaStream_t stream) {
     const int D = dim_of(sp.a.head_dim);
     if (D == 64) return run_rows<64, Q8>(sp, dev, stream);
     if (D == 128) return run_rows<128, Q8>(sp, dev, stream);
@@ -844,9 +844,11 @@ cudaError_t launch_attn_decode(AttnArgs a, bool q8, void* workspace, const Devic
     sp.scale_log2 = std::max(std::fabs(a.scale) * 1.4426950408889634f, 1e-30f);
     sp.flip = a.scale < 0.f ? 0x80008000u : 0u;
     if (many_rows(a.B, a.T, sp.G, a.kv_heads, dim_of(a.head_dim), q8))
-        return in_parts(a, q8) ? launch_attn_prefix(sp, q8, dev, stream) : launch_attn_tc(sp, q8, dev, stream);
+        return in_parts(a, q8) ? launch_attn_prefix(sp, q8, dev, stream) : launch_attn_tc(sp, a.pass != kAlone, q8, dev, stream);
     sp.lift = q8 ? kLift : 0.f;
-    return q8 ? run_dim<true>(sp, dev, stream) : run_dim<false>(sp, dev, stream);
+    if (a.pass == kAlone) return q8 ? run_dim<true>(sp, dev, stream) : run_dim<false>(sp, dev, stream);
+    const PassArgs pass = {sp};
+    return q8 ? run_dim<true>(pass, dev, stream) : run_dim<false>(pass, dev, stream);
 }
 
 namespace {

@@ -38,10 +38,21 @@ struct SplitArgs {
     float lift;                   // what a row's sums lie below its reference, to base 2
     uint32_t flip;                // sign bits of a pair of queries to turn over: scale < 0
 
+    // What the kernel is a pass of, known where it is one type's: attention of requests on their own keeps no trace of the
+    // others' choices (they cost it 0 to 3 %).
+    __device__ static constexpr int pass() { return kAlone; }
+
     __device__ __forceinline__ int over_G(int r) const { return static_cast<int>((static_cast<uint64_t>(r) * G_mul) >> G_shift); }
     __device__ __forceinline__ int page_index(int token) const {  // token / page_size
         return static_cast<int>((static_cast<uint64_t>(token) * a.page_mul) >> a.page_shift);
     }
+};
+
+struct PassArgs : SplitArgs {
+    __device__ __forceinline__ int pass() const { return a.pass; }
+};
+struct PrefixArgs : SplitArgs {
+    __device__ static constexpr int pass() { return kPrefixes; }
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -60,12 +71,14 @@ __device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, 
 // The three kernels of a call with shared prefixes follow one another closely.  The first waits for what the stream did
 // before the call; each then lets the next one start as soon as there is room; the one over the requests' own tokens,
 // which needs nothing from the one before, ends after it, so that the join, which waits for its end, has both.
-__device__ __forceinline__ void let_next_start(const AttnArgs& a) {
-    if (a.pass == kPrefixes) asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (a.pass != kAlone) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+template <class SP>
+__device__ __forceinline__ void let_next_start(const SP& sp) {
+    if (sp.pass() == kPrefixes) asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (sp.pass() != kAlone) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
-__device__ __forceinline__ void end_after_the_one_before(const AttnArgs& a) {
-    if (a.pass == kOwn) asm volatile("griddepcontrol.wait;" ::: "memory");
+template <class SP>
+__device__ __forceinline__ void end_after_the_one_before(const SP& sp) {
+    if (sp.pass() == kOwn) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // --------------------------------------------------------------- work list
@@ -94,12 +107,12 @@ __device__ __forceinline__ int first_own(const AttnArgs& a, int b, int len, int 
     return a.group_starts[lo] <= b && b < a.group_starts[lo + 1] && static_cast<long long>(len) - n >= prefix ? prefix : 0;
 }
 
-template <int TILE, int ROWS>
-__device__ __forceinline__ Request request(const SplitArgs& sp, int b) {
+template <int TILE, int ROWS, class SP>
+__device__ __forceinline__ Request request(const SP& sp, int b) {
     const AttnArgs& a = sp.a;
     Request r;
     const int len = a.lens[b];
-    if (a.pass == kPrefixes) {
+    if (sp.pass() == kPrefixes) {
         const int first = min(max(a.group_starts[b], 0), a.requests), end = min(max(a.group_starts[b + 1], first), a.requests);
         const int T = static_cast<int>(a.T);
         r.start = a.starts ? min(max(a.starts[first], 0), T) : first * sp.rows_each;
@@ -113,15 +126,15 @@ __device__ __forceinline__ Request request(const SplitArgs& sp, int b) {
         r.start = b * r.n;
     }
     const int most = static_cast<int>(min(static_cast<long long>(a.width) * a.page_size,
-                                          static_cast<long long>(a.pass == kPrefixes ? kMostShared : kMaxLength)));
+                                          static_cast<long long>(sp.pass() == kPrefixes ? kMostShared : kMaxLength)));
     if (len < 0 || len > most) record_status(a.status, kStatusInvalid);
     r.len = min(max(len, 0), most);
     const long long low = a.window > 0 ? static_cast<long long>(r.len) - r.n - a.window + 1 : 0;
     r.low = static_cast<int>(max(low, 0ll));
-    if (a.pass == kPrefixes && r.len == 0) r.n = 0;
-    if (a.pass == kOwn) r.low = min(first_own(a, b, len, r.n), r.len);
+    if (sp.pass() == kPrefixes && r.len == 0) r.n = 0;
+    if (sp.pass() == kOwn) r.low = min(first_own(a, b, len, r.n), r.len);
     // Every row sees all of a prefix.
-    r.before = a.pass == kPrefixes ? r.len : r.len - r.n;
+    r.before = sp.pass() == kPrefixes ? r.len : r.len - r.n;
     // A request without tokens still has its rows of zeros to write: one tile.
     r.tiles = max(1, (r.len + TILE - 1) / TILE - r.low / TILE);
     r.row_tiles = (r.n * sp.G + ROWS - 1) / ROWS;
@@ -183,8 +196,8 @@ struct Walk {
     // The total work, and the request that the CTA's piece begins in: each
     // thread sums a stretch of the requests, then one scan over the threads.
     // False (for the whole CTA) where there is no piece.
-    template <int THREADS>
-    __device__ __forceinline__ bool find(const SplitArgs& sp) {
+    template <int THREADS, class SP>
+    __device__ __forceinline__ bool find(const SP& sp) {
         __shared__ long long s_sum[THREADS / 32];
         __shared__ long long s_before;
         __shared__ int s_at;
@@ -226,7 +239,8 @@ struct Walk {
         return true;
     }
 
-    __device__ __forceinline__ bool next(const SplitArgs& sp, Item& s) {
+    template <class SP>
+    __device__ __forceinline__ bool next(const SP& sp, Item& s) {
         while (at < end && b < sp.a.B) {
             if (!known) rq = request<TILE, ROWS>(sp, b);
             known = true;
@@ -251,7 +265,7 @@ struct Walk {
             s.start = rq.start;
             s.n = rq.n;
             s.before = rq.before;
-            s.shared = sp.a.pass == kOwn && rq.low > 0;
+            s.shared = sp.pass() == kOwn && rq.low > 0;
             s.tiles = rq.tiles;
             const int low_tile = rq.low / TILE;
             s.tok0 = max(rq.low, (low_tile + s.tile0) * TILE);
@@ -264,18 +278,20 @@ struct Walk {
 
 // ------------------------------------------------------------------- output
 // What a pass of a call with shared prefixes leaves of a row.
-__device__ __forceinline__ float4 row_sums(const SplitArgs& sp, const Item& it, bool none, float m, float l) {
-    const int kind = sp.a.pass == kPrefixes ? 0 : none ? kRowEmpty : it.shared ? kRowShared : kRowAlone;
+template <class SP>
+__device__ __forceinline__ float4 row_sums(const SP& sp, const Item& it, bool none, float m, float l) {
+    const int kind = sp.pass() == kPrefixes ? 0 : none ? kRowEmpty : it.shared ? kRowShared : kRowAlone;
     return make_float4(m + sp.lift, fminf(l, 3e38f), __int_as_float(kind), 0.f);
 }
 
 // n values of a row's output from column col on: `v` over `l`, weights of
 // reference m.  A row that sees nothing is zeros; one whose scores are all −∞
 // has no value (0 / 0).
-__device__ __forceinline__ void put_row(const SplitArgs& sp, const Item& it, int row, int col, const float* v, int n, float m, float l) {
+template <class SP>
+__device__ __forceinline__ void put_row(const SP& sp, const Item& it, int row, int col, const float* v, int n, float m, float l) {
     const int j = sp.over_G(row), head = it.h * sp.G + row - j * sp.G;
     const bool none = it.before + j < 0;
-    if (sp.a.pass != kAlone) {
+    if (sp.pass() != kAlone) {
         const size_t at = static_cast<size_t>(it.start + j) * sp.a.q_heads + head;
         if (col == 0) sp.a.sums[at] = row_sums(sp, it, none, m, l);
         float* const to = sp.a.sum_values + at * sp.a.head_dim + col;
@@ -334,8 +350,8 @@ struct Parts {
 
     // A warp (number `warp` of WARPS) joins NP parts of 16 / NP rows at a time, all loads at once: parts k0, k0 +
     // step, ... (n of them) into the output or into part k0.
-    template <int WARPS, int NP>
-    __device__ __forceinline__ void join_rows(const SplitArgs& sp, const Item& it, int warp, int lane, int k0, int n, int step, bool last) const {
+    template <int WARPS, int NP, class SP>
+    __device__ __forceinline__ void join_rows(const SP& sp, const Item& it, int warp, int lane, int k0, int n, int step, bool last) const {
         constexpr int NR = 16 / NP, V = D / 32;  // V neighbouring values of a lane
         const int y_lane = (lane & 15) / NP, i_lane = lane & (NP - 1);
         for (int r = warp * NR; r < ROWS && it.row0 + r < it.rows; r += WARPS * NR) {

@@ -94,7 +94,7 @@ struct Shape {
 };
 
 template <int D, bool Q8>
-__global__ void __launch_bounds__(Shape<D, Q8>::kThreads, 1) attn_prefix_kernel(const __grid_constant__ SplitArgs sp, const __grid_constant__ Boxes boxes) {
+__global__ void __launch_bounds__(Shape<D, Q8>::kThreads, 1) attn_prefix_kernel(const __grid_constant__ PrefixArgs sp, const __grid_constant__ Boxes boxes) {
     using S = Shape<D, Q8>;
     constexpr int TT = kTile, NS = S::kStages, kLoadWarps = S::kLoadWarps, kMmaWarp = S::kMmaWarp;
     extern __shared__ uint8_t smem_raw[];
@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(Shape<D, Q8>::kThreads, 1) attn_prefix_kernel(
         mbar_init(smem_addr(&s_queries), kRowThreads);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    let_next_start(a);
+    let_next_start(sp);
     Walk<TT, kRows, kFixed> walk;
     if (!walk.template find<S::kThreads>(sp)) return;
     if (warp == kMmaWarp) tmem_alloc(smem_addr(&s_tmem), kTmemCols);
@@ -661,7 +661,7 @@ cudaError_t run(const SplitArgs& sp, int grid, cudaStream_t stream) {
         if (err != cudaSuccess) return err;
         ready[device & (kMaxDevices - 1)].store(true, std::memory_order_relaxed);
     }
-    return launch_pass(attn_prefix_kernel<D, Q8>, grid, S::kThreads, S::kSmem, stream, true, sp, Q8 ? Boxes{} : boxes_of(sp.a));
+    return launch_pass(attn_prefix_kernel<D, Q8>, grid, S::kThreads, S::kSmem, stream, true, PrefixArgs{sp}, Q8 ? Boxes{} : boxes_of(sp.a));
 }
 
 // -------------------------------------------------------------------- join

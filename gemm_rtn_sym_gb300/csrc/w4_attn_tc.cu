@@ -71,8 +71,8 @@ struct Shape {
 
 __device__ __forceinline__ void rows_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kSoftmaxWarps * 32) : "memory"); }
 
-template <int D, bool Q8>
-__global__ void __launch_bounds__(Shape<D, Q8>::kThreads, 1) attn_tc_kernel(const __grid_constant__ SplitArgs sp) {
+template <int D, bool Q8, class SP>
+__global__ void __launch_bounds__(Shape<D, Q8>::kThreads, 1) attn_tc_kernel(const __grid_constant__ SP sp) {
     using S = Shape<D, Q8>;
     constexpr int TT = S::kTile, NS = S::kSlots, kLoadWarps = S::kLoadWarps, kMmaWarp = S::kMmaWarp;
     extern __shared__ uint8_t smem_raw[];
@@ -102,10 +102,10 @@ __global__ void __launch_bounds__(Shape<D, Q8>::kThreads, 1) attn_tc_kernel(cons
         mbar_init(smem_addr(&s_queries), kSoftmaxWarps * 32);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    let_next_start(a);
+    let_next_start(sp);
     Walk<TT, kRows, kFixed> walk;
     if (!walk.template find<S::kThreads>(sp)) {
-        end_after_the_one_before(a);
+        end_after_the_one_before(sp);
         return;
     }
     if (warp == kMmaWarp) tmem_alloc(smem_addr(&s_tmem), kTmemCols);
@@ -542,7 +542,7 @@ __global__ void __launch_bounds__(Shape<D, Q8>::kThreads, 1) attn_tc_kernel(cons
             __nv_bfloat16* const to = a.out.data + (live ? (it.start + j) * a.out.token_stride + (it.h * sp.G + row - j * sp.G) * a.out.head_stride : 0);
             // 32 of the row's values from column c on, weights of reference top with the sum `total`
             auto put = [&](int c, const uint32_t (&v)[32], float top, float total) {
-                if (a.pass != kAlone) {
+                if (sp.pass() != kAlone) {
                     const size_t at = static_cast<size_t>(it.start + j) * a.q_heads + it.h * sp.G + row - j * sp.G;
                     if (c == 0) a.sums[at] = row_sums(sp, it, none, top, total);
 #pragma unroll
@@ -634,38 +634,45 @@ __global__ void __launch_bounds__(Shape<D, Q8>::kThreads, 1) attn_tc_kernel(cons
         tc_fence_after();
         tmem_dealloc(tmem, kTmemCols);
     }
-    end_after_the_one_before(a);
+    end_after_the_one_before(sp);
 }
 
-template <int D, bool Q8>
-cudaError_t run(const SplitArgs& sp, int grid, cudaStream_t stream) {
+template <int D, bool Q8, class SP>
+cudaError_t run(const SP& sp, int grid, cudaStream_t stream) {
     using S = Shape<D, Q8>;
     static std::atomic<bool> ready[kMaxDevices];  // the kernel may use its shared memory on this device
     int device = 0;
     cudaError_t err = cudaGetDevice(&device);
     if (err != cudaSuccess) return err;
     if (!ready[device & (kMaxDevices - 1)].load(std::memory_order_relaxed)) {
-        err = cudaFuncSetAttribute(attn_tc_kernel<D, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+        err = cudaFuncSetAttribute(attn_tc_kernel<D, Q8, SP>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
         if (err != cudaSuccess) return err;
         ready[device & (kMaxDevices - 1)].store(true, std::memory_order_relaxed);
     }
-    return launch_pass(attn_tc_kernel<D, Q8>, grid, S::kThreads, S::kSmem, stream, sp.a.pass != kAlone, sp);
+    return launch_pass(attn_tc_kernel<D, Q8, SP>, grid, S::kThreads, S::kSmem, stream, !std::is_same<SP, SplitArgs>::value, sp);
+}
+
+template <class SP>
+cudaError_t run_dim(const SP& sp, bool q8, int grid, cudaStream_t stream) {
+    if (sp.a.head_dim <= 64) return q8 ? run<64, true>(sp, grid, stream) : run<64, false>(sp, grid, stream);
+    if (sp.a.head_dim <= 128) return q8 ? run<128, true>(sp, grid, stream) : run<128, false>(sp, grid, stream);
+    return q8 ? run<256, true>(sp, grid, stream) : run<256, false>(sp, grid, stream);
 }
 
 }  // namespace
 
 size_t attn_tc_partial_floats(int head_dim) { return partial_floats(kRows, head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256); }
 
-cudaError_t launch_attn_tc(const SplitArgs& sp, bool q8, const DeviceInfo& dev, cudaStream_t stream) {
+cudaError_t launch_attn_tc(const SplitArgs& sp, bool pass, bool q8, const DeviceInfo& dev, cudaStream_t stream) {
     const AttnArgs& a = sp.a;
     const int tile = a.head_dim <= 128 ? 128 : 64;
     // At least as many units as the batch can have: a CTA for each, where they are few.
     const double reach = std::min(static_cast<double>(a.width) * a.page_size, a.window > 0 ? static_cast<double>(a.window) + a.T : 1e18);
     const double most = static_cast<double>(a.kv_heads) * (a.B + static_cast<double>(a.T) * sp.G / kRows) * (reach / tile + 2 + kFixed);
     const int grid = static_cast<int>(std::min<double>(std::min(dev.sm_count, kMaxTcCtas), most));
-    if (a.head_dim <= 64) return q8 ? run<64, true>(sp, grid, stream) : run<64, false>(sp, grid, stream);
-    if (a.head_dim <= 128) return q8 ? run<128, true>(sp, grid, stream) : run<128, false>(sp, grid, stream);
-    return q8 ? run<256, true>(sp, grid, stream) : run<256, false>(sp, grid, stream);
+    if (!pass) return run_dim(sp, q8, grid, stream);
+    const PassArgs args = {sp};
+    return run_dim(args, q8, grid, stream);
 }
 
 }  // namespace w4

@@ -28,6 +28,7 @@ struct JoinArgs {
 cudaError_t launch_attn_join(JoinArgs a, cudaStream_t stream);
 // kPrefixes for head_dim up to 128.  Leaves the parts of shared items for the join.
 cudaError_t launch_attn_prefix(const SplitArgs& sp, bool q8, const DeviceInfo& dev, cudaStream_t stream);
-cudaError_t launch_attn_tc(const SplitArgs& sp, bool q8, const DeviceInfo& dev, cudaStream_t stream);
+// pass: one of a call with shared prefixes.
+cudaError_t launch_attn_tc(const SplitArgs& sp, bool pass, bool q8, const DeviceInfo& dev, cudaStream_t stream);
 
 }  // namespace w4
