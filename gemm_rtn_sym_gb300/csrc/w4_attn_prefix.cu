@@ -208,15 +208,21 @@ __global__ void __launch_bounds__(Shape<D, Q8>::kThreads, 1) attn_prefix_kernel(
         uint32_t scaled = 0;  // tiles whose scales are in shared memory
         const uint32_t raw = ring + 2 * NS * S::kHalf + ((warp - kRowWarps) * kMine * kChunks + lane) * 16;
         int asked = 0, raw_ask = 0, raw_take = 0;
-        // What the codes on their way are: keys or values or none, with the scales of the lane's token.
+        // What the codes on their way are: keys or values, or none.
         struct Half {
             bool key, any;
-            __nv_bfloat16 k, v;
         };
         Half way[2] = {};
+        // The scales of the lane's token, in the tile found last and in the one before it, as they come: they are moved and
+        // converted a stage after they were asked for, so that nothing waits for them.
+        struct Scales {
+            __nv_bfloat16 k, v;
+        };
+        const Scales none = {__ushort_as_bfloat16(0), __ushort_as_bfloat16(0)};
+        Scales found = none, older = none;
         static_assert(S::kAhead == 2, "two halves on their way");
         // Asks for half a stage of codes (or, past the last, for nothing) and turns that of kAhead before.
-        auto half_stage = [&](const Half& half, long long off) {
+        auto half_stage = [&](Half half, long long off) {
             if (half.any) {
                 const uint8_t* src = static_cast<const uint8_t*>(half.key ? a.k : a.v) + load_c * 16;
 #pragma unroll
@@ -253,8 +259,8 @@ __global__ void __launch_bounds__(Shape<D, Q8>::kThreads, 1) attn_prefix_kernel(
                 if (now.key) {
                     const int buffer = scaled++ & 3;
                     if (lane < kMine) {
-                        s_scale[Q8 ? buffer : 0][0][Q8 ? my_row + lane : 0] = __bfloat162float(now.k) * sp.scale_log2;
-                        s_scale[Q8 ? buffer : 0][1][Q8 ? my_row + lane : 0] = __bfloat162float(now.v);
+                        s_scale[Q8 ? buffer : 0][0][Q8 ? my_row + lane : 0] = __bfloat162float(older.k) * sp.scale_log2;
+                        s_scale[Q8 ? buffer : 0][1][Q8 ? my_row + lane : 0] = __bfloat162float(older.v);
                     }
                     mbar_arrive(smem_addr(&s_scaled[buffer]));
                 }
@@ -272,12 +278,10 @@ __global__ void __launch_bounds__(Shape<D, Q8>::kThreads, 1) attn_prefix_kernel(
             };
             int page_next = -1;
             long long off = -1, off1 = -1, off2 = -1;  // of the lane's token: in the tile found last, one and two before
-            Half found = {};
             auto find = [&](int i) {
                 const int tok = token_of(i), page = page_next;
                 page_next = page_of(i + 1);
                 off = -1;
-                found.k = found.v = __ushort_as_bfloat16(0);
                 if (tok >= it.tok1) return;
                 if (page < 0 || page >= a.pages) {
                     record_status(a.status, kStatusInvalid);
@@ -356,11 +360,11 @@ __global__ void __launch_bounds__(Shape<D, Q8>::kThreads, 1) attn_prefix_kernel(
                     next_page = box_page(i + 1);
                     copy_box(true, i, page0);
                 } else {
+                    older = found;
+                    found = none;
                     if (i < tiles) find(i);
-                    found.key = true;
-                    found.any = i < tiles;
                     if constexpr (Q8)
-                        half_stage(found, off);
+                        half_stage({true, i < tiles}, off);
                     else if (i < tiles)
                         copy(true, off);
                     else
