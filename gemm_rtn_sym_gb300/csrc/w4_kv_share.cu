@@ -63,9 +63,10 @@ __global__ void __launch_bounds__(kThreads) kv_let_go_kernel(KvPagesArgs a) {
     }
 }
 
-constexpr int kMarkWords = 256, kMarked = kMarkWords * 32, kMarkEach = kMarked / kThreads;  // words and entries that a CTA takes at a time
+constexpr int kMarkWords = 64, kMarked = kMarkWords * 32;  // words and entries that a CTA takes at a time
 
-// The marked entries' pages go to the ring, in the order of the entries.  A CTA counts the marks before its own.
+// The marked entries' pages go to the ring, in the order of the entries.  A CTA
+// counts the marks before its own (a bit for each entry that there could be).
 __global__ void __launch_bounds__(kThreads) kv_give_back_kernel(KvPagesArgs a) {
     __shared__ long long s_first[kThreads], s_warp[33];
     __shared__ int s_want[kThreads], s_before[kMarkWords];
@@ -74,50 +75,40 @@ __global__ void __launch_bounds__(kThreads) kv_give_back_kernel(KvPagesArgs a) {
     const int tid = threadIdx.x;
     const long long tail = a.range[1];
     const long long tail_at = static_cast<long long>(static_cast<uint64_t>(tail) % static_cast<uint64_t>(a.pages));
-    // (of all entries, marked or not)
-    long long entries = 0;
-    for (int base = 0; base < a.B; base += kThreads) {
-        entries += scan_given(a, base, min(a.B - base, kThreads), s_first, s_want, s_warp);
-        __syncthreads();
-    }
-    const long long words = (entries + 31) / 32;
-    auto marks = [&](long long from, long long to) {  // in words from .. to − 1
-        long long n = 0, total;
-        for (long long w = from + tid; w < to; w += kThreads) n += __popc(a.marks[w]);
-        block_sum_before(n, s_warp, total);
-        __syncthreads();
-        return total;
-    };
-    if (blockIdx.x == 0) {
-        const long long given = marks(0, words);
-        if (tid == 0) a.range_out[1] = tail + given;
-    }
+    const long long words = (static_cast<long long>(a.B) * a.width + 31) / 32;
     for (long long w0 = static_cast<long long>(blockIdx.x) * kMarkWords; w0 < words; w0 += static_cast<long long>(gridDim.x) * kMarkWords) {
-        const long long given = marks(0, w0);
         const unsigned word = tid < kMarkWords && w0 + tid < words ? a.marks[w0 + tid] : 0;
-        long long total;
-        const long long before = block_sum_before(__popc(word), s_warp, total);
+        long long n = 0, given, mine;
+#pragma unroll 8
+        for (long long w = tid; w < w0; w += kThreads) n += __popc(a.marks[w]);
+        block_sum_before(n, s_warp, given);
+        __syncthreads();
+        const long long before = block_sum_before(__popc(word), s_warp, mine);
         if (tid < kMarkWords) {
             s_words[tid] = word;
             s_before[tid] = static_cast<int>(before);
         }
+        if (tid == 0 && w0 + kMarkWords >= words) a.range_out[1] = tail + given + mine;
         __syncthreads();
+        if (mine == 0) continue;
         long long done = 0;  // entries of the requests before `base`
         for (int base = 0; base < a.B; base += kThreads) {
-            const int n = min(a.B - base, kThreads);
-            const long long mine = scan_given(a, base, n, s_first, s_want, s_warp);
+            const int m = min(a.B - base, kThreads);
+            const long long all = scan_given(a, base, m, s_first, s_want, s_warp);
+            if (done + all > w0 * 32 && done < (w0 + kMarkWords) * 32) {
 #pragma unroll
-            for (int j = 0; j < kMarkEach; ++j) {
-                const int e = j * kThreads + tid;
-                const long long r = w0 * 32 + e - done;
-                if (r >= 0 && r < mine && s_words[e >> 5] >> (e & 31) & 1) {
-                    const int i = last_at_most(s_first, n, r);
-                    long long at = tail_at + (given + s_before[e >> 5] + __popc(s_words[e >> 5] & ((1u << (e & 31)) - 1))) % a.pages;
-                    if (at >= a.pages) at -= a.pages;
-                    a.ring[at] = a.table[(base + i) * a.table_stride + s_want[i] + (r - s_first[i])];
+                for (int e0 = 0; e0 < kMarked; e0 += kThreads) {
+                    const int e = e0 + tid;
+                    const long long r = w0 * 32 + e - done;
+                    if (r >= 0 && r < all && s_words[e >> 5] >> (e & 31) & 1) {
+                        const int i = last_at_most(s_first, m, r);
+                        long long at = tail_at + (given + s_before[e >> 5] + __popc(s_words[e >> 5] & ((1u << (e & 31)) - 1))) % a.pages;
+                        if (at >= a.pages) at -= a.pages;
+                        a.ring[at] = a.table[(base + i) * a.table_stride + s_want[i] + (r - s_first[i])];
+                    }
                 }
             }
-            done += mine;
+            done += all;
             __syncthreads();
         }
     }
