@@ -827,7 +827,7 @@ size_t attn_decode_workspace_bytes(int32_t B, int64_t T, int32_t q_heads, int32_
 // Whether the pass leaves parts of its items for the join.
 static bool in_parts(const AttnArgs& a, bool q8) {
     const int G = a.q_heads / a.kv_heads;
-    return a.pass == kPrefixes && a.head_dim <= 128 && many_rows(a.B, a.T, G, a.kv_heads, dim_of(a.head_dim), q8);
+    return a.pass == kPrefixes && many_rows(a.B, a.T, G, a.kv_heads, dim_of(a.head_dim), q8);
 }
 
 cudaError_t launch_attn_decode(AttnArgs a, bool q8, void* workspace, const DeviceInfo& dev, cudaStream_t stream) {
@@ -844,7 +844,7 @@ cudaError_t launch_attn_decode(AttnArgs a, bool q8, void* workspace, const Devic
     sp.scale_log2 = std::max(std::fabs(a.scale) * 1.4426950408889634f, 1e-30f);
     sp.flip = a.scale < 0.f ? 0x80008000u : 0u;
     if (many_rows(a.B, a.T, sp.G, a.kv_heads, dim_of(a.head_dim), q8))
-        return in_parts(a, q8) ? launch_attn_prefix(sp, q8, dev, stream) : launch_attn_tc(sp, a.pass != kAlone, q8, dev, stream);
+        return in_parts(a, q8) && a.head_dim <= 128 ? launch_attn_prefix(sp, q8, dev, stream) : launch_attn_tc(sp, a.pass != kAlone, q8, dev, stream);
     sp.lift = q8 ? kLift : 0.f;
     if (a.pass == kAlone) return q8 ? run_dim<true>(sp, dev, stream) : run_dim<false>(sp, dev, stream);
     const PassArgs pass = {sp};

@@ -750,7 +750,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const __grid
 }  // namespace
 
 cudaError_t launch_attn_join(JoinArgs a, cudaStream_t stream) {
-    a.D = a.head_dim <= 64 ? 64 : 128;
+    a.D = a.head_dim <= 64 ? 64 : a.head_dim <= 128 ? 128 : 256;
     a.part_floats = partial_floats(kRows, a.D);
     const long long rows = static_cast<long long>(a.T) * a.q_heads;
     const unsigned grid = static_cast<unsigned>((rows + kJoinWarps - 1) / kJoinWarps);

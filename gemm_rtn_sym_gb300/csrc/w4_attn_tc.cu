@@ -533,8 +533,15 @@ __global__ void __launch_bounds__(Shape<D, Q8>::kThreads, 1) attn_tc_kernel(cons
             tc_fence_after();
             const bool whole = it.whole(), none = it.before + j < 0;
             const Parts<kRows, D> parts(sp, walk, it, kFixed);
-            float* const part = parts.at(static_cast<int>(blockIdx.x) - parts.first);
-            if (!whole && live) {
+            const int k_own = static_cast<int>(blockIdx.x) - parts.first;
+            float* const part = parts.at(k_own);
+            const bool leave = sp.pass() == kPrefixes && !whole;  // for the join, row by row
+            if (leave && live) {
+                reinterpret_cast<float2*>(part)[tid] = make_float2(m * unit, fminf(l, 3e38f));
+                if (k_own == 0)
+                    a.sums[static_cast<size_t>(it.start + j) * a.q_heads + it.h * sp.G + row - j * sp.G] =
+                        make_float4(0.f, 0.f, __int_as_float(parts.count), __int_as_float(parts.first << 8 | tid));
+            } else if (!whole && live) {
                 part[tid] = m * unit;
                 part[kRows + tid] = fminf(l, 3e38f);
             }
@@ -564,7 +571,10 @@ __global__ void __launch_bounds__(Shape<D, Q8>::kThreads, 1) attn_tc_kernel(cons
             for (int c = 0; c < D; c += 32) {
                 uint32_t v[32];
                 tmem_ld32(mine + S::kColO + c, v);
-                if (live && !whole) {
+                if (live && leave) {
+#pragma unroll
+                    for (int x = 0; x < 32; x += 4) *reinterpret_cast<uint4*>(part + 2 * kRows + tid * D + c + x) = make_uint4(v[x], v[x + 1], v[x + 2], v[x + 3]);
+                } else if (live && !whole) {
 #pragma unroll
                     for (int x = 0; x < 32; ++x) part[(2 + c + x) * kRows + tid] = __uint_as_float(v[x]);
                 } else if (live) {
@@ -575,7 +585,7 @@ __global__ void __launch_bounds__(Shape<D, Q8>::kThreads, 1) attn_tc_kernel(cons
             tc_fence_before();
             rows_sync();
             // Parts as [reference, sum, D columns][row], so that neighbouring threads' rows lie side by side.
-            if (!whole)
+            if (!whole && !leave)
                 parts.finish(sp, s_last, rows_sync, [&](int k0, int n, int step, bool last) {
                     // This CTA's own part is still in tensor memory (the item's, when it is a group's that is joined).
                     const int own = step == 1 ? static_cast<int>(blockIdx.x) - parts.first - k0 : -1;

@@ -26,7 +26,7 @@ struct JoinArgs {
     size_t part_floats;
 };
 cudaError_t launch_attn_join(JoinArgs a, cudaStream_t stream);
-// kPrefixes for head_dim up to 128.  Leaves the parts of shared items for the join.
+// kPrefixes for head_dim up to 128.  Like the other kernel in that pass, it leaves the parts of shared items for the join.
 cudaError_t launch_attn_prefix(const SplitArgs& sp, bool q8, const DeviceInfo& dev, cudaStream_t stream);
 // pass: one of a call with shared prefixes.
 cudaError_t launch_attn_tc(const SplitArgs& sp, bool pass, bool q8, const DeviceInfo& dev, cudaStream_t stream);
