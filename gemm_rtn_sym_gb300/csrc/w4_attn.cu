@@ -765,6 +765,20 @@ bool many_rows(int32_t B, int64_t T, int G, int32_t kv_heads, int D, bool q8) {
     return average_rows(B, T, G) > (few ? 2 * limit : limit);
 }
 
+// The same for a pass over prefixes, whose parts a kernel of its own joins, so that
+// few heads are no reason to stay here.  µs of the whole call, here and there,
+// one prefix of 16385 tokens, 8 key-value heads (4 of 256):
+// head_dim 64, 24 rows: 32 and 32; 32: 37 and 32.  128, 16 rows: 26 and 33; 24: 38
+// and 34.  256, 16 rows: 37 and 40; 24: 51 and 41.  Format 8: 64, 96 rows: 41 and
+// 40.  128, 48 rows: 43 and 45; 64: 46 and 46; 96: 58 and 47.  256, 64 rows: 53 and
+// 53; 96: 66 and 57.  Twelve prefixes of 1500 tokens: 128, 24 rows: 37 and 40; 32: 41
+// and 42; 48: 50 and 45; 256, 16 rows: 32 and 38; 24: 41 and 37; format 8, 128, 48
+// rows: 55 and 59; 64: 65 and 64.
+bool many_rows_behind(int32_t groups, int64_t T, int G, int D, bool q8) {
+    const int limit = q8 ? (D == 64 ? 96 : D == 128 ? 56 : 64) : D == 256 ? 16 : 24;
+    return average_rows(groups, T, G) > limit;
+}
+
 // Warps (of 16 rows) that share a stage.  With two, 17 to 32 rows are one pass
 // over the cache instead of two: 69 and 475 µs for 76 and 932 at head_dim 256,
 // 32 rows, in the two calls above, but 243 for 301 only where 64 is the
@@ -816,18 +830,21 @@ cudaError_t run_dim(const SP& sp, const DeviceInfo& dev, cudaStream_t stream) {
 
 }  // namespace
 
-size_t attn_decode_workspace_bytes(int32_t B, int64_t T, int32_t q_heads, int32_t kv_heads, int32_t head_dim, bool q8) {
+static size_t workspace_bytes(int32_t B, int64_t T, int32_t q_heads, int32_t kv_heads, int32_t head_dim, bool q8, bool prefixes) {
     const int G = q_heads / kv_heads, D = dim_of(head_dim);
     if (B <= 0) B = 1;
-    const bool many = many_rows(B, T, G, kv_heads, D, q8);
+    const bool many = prefixes ? many_rows_behind(B, T, G, D, q8) : many_rows(B, T, G, kv_heads, D, q8);
     const size_t part = many ? attn_tc_partial_floats(head_dim) : partial_floats(16 * row_warps(B, T, G, q8), D);
     return 2 * (kMaxCtas * sizeof(unsigned long long) + (many ? kMaxTcCtas : kMaxCtas) * part * sizeof(float));
 }
 
-// Whether the pass leaves parts of its items for the join.
+size_t attn_decode_workspace_bytes(int32_t B, int64_t T, int32_t q_heads, int32_t kv_heads, int32_t head_dim, bool q8) {
+    return workspace_bytes(B, T, q_heads, kv_heads, head_dim, q8, false);
+}
+
+// Whether the pass is that over prefixes of many rows, which leaves the parts of its items for the join.
 static bool in_parts(const AttnArgs& a, bool q8) {
-    const int G = a.q_heads / a.kv_heads;
-    return a.pass == kPrefixes && many_rows(a.B, a.T, G, a.kv_heads, dim_of(a.head_dim), q8);
+    return a.pass == kPrefixes && many_rows_behind(a.B, a.T, a.q_heads / a.kv_heads, dim_of(a.head_dim), q8);
 }
 
 cudaError_t launch_attn_decode(AttnArgs a, bool q8, void* workspace, const DeviceInfo& dev, cudaStream_t stream) {
@@ -843,8 +860,8 @@ cudaError_t launch_attn_decode(AttnArgs a, bool q8, void* workspace, const Devic
     // largest score is then that of the unscaled products, and hidden ones stay at −∞.
     sp.scale_log2 = std::max(std::fabs(a.scale) * 1.4426950408889634f, 1e-30f);
     sp.flip = a.scale < 0.f ? 0x80008000u : 0u;
-    if (many_rows(a.B, a.T, sp.G, a.kv_heads, dim_of(a.head_dim), q8))
-        return in_parts(a, q8) && a.head_dim <= 128 ? launch_attn_prefix(sp, q8, dev, stream) : launch_attn_tc(sp, a.pass != kAlone, q8, dev, stream);
+    if (a.pass == kPrefixes ? in_parts(a, q8) : many_rows(a.B, a.T, sp.G, a.kv_heads, dim_of(a.head_dim), q8))
+        return a.pass == kPrefixes && a.head_dim <= 128 ? launch_attn_prefix(sp, q8, dev, stream) : launch_attn_tc(sp, a.pass != kAlone, q8, dev, stream);
     sp.lift = q8 ? kLift : 0.f;
     if (a.pass == kAlone) return q8 ? run_dim<true>(sp, dev, stream) : run_dim<false>(sp, dev, stream);
     const PassArgs pass = {sp};
@@ -859,7 +876,7 @@ size_t padded(size_t bytes) { return (bytes + 255) / 256 * 256; }
 size_t attn_shared_workspace_bytes(int32_t B, int64_t T, int32_t q_heads, int32_t kv_heads, int32_t head_dim, bool q8,
                                    int32_t groups) {
     const size_t rows = static_cast<size_t>(T) * q_heads;
-    return padded(attn_decode_workspace_bytes(groups, T, q_heads, kv_heads, head_dim, q8)) +
+    return padded(workspace_bytes(groups, T, q_heads, kv_heads, head_dim, q8, true)) +
            padded(attn_decode_workspace_bytes(B, T, q_heads, kv_heads, head_dim, q8)) + 2 * padded(rows * sizeof(float4)) + 2 * padded(rows * head_dim * sizeof(float));
 }
 
@@ -871,7 +888,7 @@ cudaError_t launch_attn_shared(AttnArgs a, const SharedArgs& shared, bool q8, vo
         at += padded(bytes);
         return p;
     };
-    void* const first = take(attn_decode_workspace_bytes(shared.groups, a.T, a.q_heads, a.kv_heads, a.head_dim, q8));
+    void* const first = take(workspace_bytes(shared.groups, a.T, a.q_heads, a.kv_heads, a.head_dim, q8, true));
     void* const second = take(attn_decode_workspace_bytes(a.B, a.T, a.q_heads, a.kv_heads, a.head_dim, q8));
     const size_t rows = static_cast<size_t>(a.T) * a.q_heads;
     AttnArgs p = a;
