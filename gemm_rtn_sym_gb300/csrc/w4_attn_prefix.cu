@@ -29,6 +29,8 @@
 #include <cstdint>
 #include <type_traits>
 
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -633,19 +635,37 @@ __global__ void __launch_bounds__(Shape<D, Q8>::kThreads, 1) attn_prefix_kernel(
     }
 }
 
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+    static const PFN_cuTensorMapEncodeTiled_v12000 found = [] {
+        cudaDriverEntryPointQueryResult q;
+        void* fn = nullptr;
+        const bool there = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+                           q == cudaDriverEntryPointSuccess;
+        return there ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn) : nullptr;
+    }();
+    return found;
+}
+
 // Boxes of the cache's pages, where they serve: whole rows of 64 values, and tiles of whole pages or pages of whole
-// tiles, at eight rows or more a box (what the swizzle repeats after).
+// tiles, at eight rows or more a box (what the swizzle repeats after).  Values past head_dim and pages out of range
+// read as zeros.
 Boxes boxes_of(const AttnArgs& a) {
     Boxes b = {};
     const int P = a.page_size, tokens = P % kTile == 0 ? kTile : P < kTile && kTile % P == 0 ? P : 0;
-    if (tokens < 8 || a.head_dim < 64) return b;
+    if (tokens < 8 || a.head_dim < 64 || !encoder()) return b;
     // (a dimension of one has no stride of its own)
-    const int64_t heads = a.kv_heads > 1 ? a.head_stride * 2 : a.head_dim * 2, places = a.token_stride * 2;
-    const int64_t pages = a.pages > 1 ? a.page_stride * 2 : 16;
+    const cuuint64_t heads = a.kv_heads > 1 ? a.head_stride * 2 : a.head_dim * 2, places = a.token_stride * 2, pages = a.pages > 1 ? a.page_stride * 2 : 16;
     b.heads_inside = heads <= places;
-    const bool ok = encode_pages_map(&b.k, a.k, a.head_dim, a.kv_heads, heads, P, places, a.pages, pages, tokens, b.heads_inside) == cudaSuccess &&
-                    encode_pages_map(&b.v, a.v, a.head_dim, a.kv_heads, heads, P, places, a.pages, pages, tokens, b.heads_inside) == cudaSuccess;
-    b.tokens = ok ? tokens : 0;
+    const cuuint64_t H = a.kv_heads, size = P;
+    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(a.head_dim), b.heads_inside ? H : size, b.heads_inside ? size : H, static_cast<cuuint64_t>(a.pages)};
+    const cuuint64_t strides[3] = {b.heads_inside ? heads : places, b.heads_inside ? places : heads, pages};
+    const cuuint32_t n = tokens, box[4] = {64u, b.heads_inside ? 1u : n, b.heads_inside ? n : 1u, 1u}, each[4] = {1, 1, 1, 1};
+    for (int i = 0; i < 2; ++i)
+        if (encoder()(i ? &b.v : &b.k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(i ? a.v : a.k), dims, strides, box, each,
+                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return b;  // (strides past what a map can say: row by row)
+    b.tokens = tokens;
     return b;
 }
 

@@ -505,24 +505,6 @@ cudaError_t encode_x_stage_map(CUtensorMap* map, const void* x, int64_t M, int64
     return cudaSuccess;
 }
 
-cudaError_t encode_pages_map(CUtensorMap* map, const void* x, int64_t head_dim, int64_t heads, int64_t head_stride,
-                             int64_t page_size, int64_t token_stride, int64_t pages, int64_t page_stride, int tokens,
-                             bool heads_inside) {
-    if (cudaError_t e = get_encoder()) return e;
-    const cuuint64_t h = static_cast<cuuint64_t>(heads), p = static_cast<cuuint64_t>(page_size);
-    const cuuint64_t hs = static_cast<cuuint64_t>(head_stride), ts = static_cast<cuuint64_t>(token_stride);
-    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(head_dim), heads_inside ? h : p, heads_inside ? p : h, static_cast<cuuint64_t>(pages)};
-    const cuuint64_t strides[3] = {heads_inside ? hs : ts, heads_inside ? ts : hs, static_cast<cuuint64_t>(page_stride)};
-    const cuuint32_t n = static_cast<cuuint32_t>(tokens);
-    const cuuint32_t box[4] = {64u, heads_inside ? 1u : n, heads_inside ? n : 1u, 1u};
-    const cuuint32_t estr[4] = {1, 1, 1, 1};
-    if (g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(x), dims, strides, box, estr,
-                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-        return cudaErrorInvalidValue;
-    return cudaSuccess;
-}
-
 namespace {
 
 int smem_bytes(int bm) {

@@ -98,13 +98,6 @@ cudaError_t encode_x_stage_map(CUtensorMap* map, const void* x, int64_t M, int64
 cudaError_t encode_codes_stage_map(CUtensorMap* map, const void* packed, int64_t N, int64_t K, int rows,
                                    int groups, CUtensorMapSwizzle swizzle);
 
-// 4-D tensor map over bf16 pages of a cache (strides in bytes): boxes of one head's `tokens` tokens of a page x 64
-// values, 128-byte swizzle, values past head_dim and pages out of range read as zeros.  heads_inside: heads are
-// dimension 1 and tokens dimension 2; else the other way round.
-cudaError_t encode_pages_map(CUtensorMap* map, const void* x, int64_t head_dim, int64_t heads, int64_t head_stride,
-                             int64_t page_size, int64_t token_stride, int64_t pages, int64_t page_stride, int tokens,
-                             bool heads_inside);
-
 // One problem of a grouped matmul (validated by the C ABI layer).  zeros:
 // int8 zero − 8 per group of the affine formats, or null.
 struct GroupedSpec {
