@@ -183,6 +183,8 @@ struct Item {
     __device__ __forceinline__ bool whole() const { return tile0 == 0 && tile1 == tiles; }
 };
 
+constexpr int kShort = 8;  // tiles of an item that is not worth cutting
+
 // Walks the items of a CTA's piece.
 template <int TILE, int ROWS, int FIXED>
 struct Walk {
@@ -254,8 +256,14 @@ struct Walk {
             const int weight = rq.tiles + FIXED;
             const int line = static_cast<int>(quotient(at - before, weight));
             s.unit = before + static_cast<long long>(line) * weight;
-            s.tile0 = max(0, static_cast<int>(at - s.unit) - FIXED);
-            s.tile1 = static_cast<int>(min(static_cast<long long>(weight), end - s.unit)) - FIXED;
+            int from = static_cast<int>(at - s.unit), to = static_cast<int>(min(static_cast<long long>(weight), end - s.unit));
+            if (sp.pass() == kOwn && rq.tiles <= kShort) {
+                // Few tokens: all of them to the piece that has most of the item's units.
+                from = 2 * from < weight ? 0 : weight;
+                to = 2 * to < weight ? 0 : weight;
+            }
+            s.tile0 = max(0, from - FIXED);
+            s.tile1 = to - FIXED;
             at = s.unit + weight;
             if (s.tile1 <= s.tile0) continue;  // the piece ends in the item's fixed units
             s.b = b;
