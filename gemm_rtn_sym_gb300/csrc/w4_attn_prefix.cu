@@ -49,9 +49,9 @@ constexpr int kRowWarps = 8, kRowThreads = kRowWarps * 32;
 constexpr int kFixed = 4;  // an item's fixed cost in tiles
 constexpr uint32_t kTmemCols = 512, kColO = 256;
 
-template <int REGS>
+template <class S, bool Q8>
 __device__ __forceinline__ void fewer_registers() {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
+    if (Q8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kOtherRegs));
 }
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w, uint32_t bar) {
@@ -78,13 +78,12 @@ static_assert(kRows == kTile, "one offset for queries and keys");
 
 template <int D, bool Q8>
 struct Shape {
-    // Warpgroups: two of rows, the copies', and the products' warp with three that only make up its group.
-    static constexpr int kLoadWarps = Q8 ? 8 : 4, kMmaWarp = kRowWarps + kLoadWarps, kThreads = 32 * (kMmaWarp + 4);
-    // Registers: in format 16 a row's 128 scores stay in its thread's, and the other warpgroups leave theirs for that.
-    // The sum is what the block is launched with, which the launch checks: a thread that asks for more than there are
-    // waits for ever.
-    static constexpr int kLaunchRegs = Q8 ? 96 : 128, kRowRegs = Q8 ? 144 : 192, kOtherRegs = 64;
-    static_assert(2 * kRowRegs + (kLoadWarps / 4 + 1) * kOtherRegs == kThreads / 128 * kLaunchRegs, "all there are");
+    // Format 8: whole warpgroups (three warps only make up the last one), so that the rows' can have more registers than
+    // the others.  The sum is what the block is launched with, which the launch checks: a thread that asks for more than
+    // there are waits for ever.  (81 µs without for 64 rows of 40 heads behind 16385 tokens: 86.  Format 16 has enough.)
+    static constexpr int kLoadWarps = Q8 ? 8 : 4, kMmaWarp = kRowWarps + kLoadWarps, kThreads = 32 * (kMmaWarp + (Q8 ? 4 : 1));
+    static constexpr int kLaunchRegs = 96, kRowRegs = 144, kOtherRegs = 64;
+    static_assert(!Q8 || 2 * kRowRegs + (kLoadWarps / 4 + 1) * kOtherRegs == kThreads / 128 * kLaunchRegs, "all there are");
     static constexpr int kHalf = kTile * D * 2;       // keys or values of a tile
     static constexpr int kStages = Q8 ? 2 : 3;        // of keys and values, what shared memory holds at D = 128
     static constexpr int kQ = kRows * D * 2;
@@ -139,7 +138,7 @@ __global__ void __launch_bounds__(Shape<D, Q8>::kThreads, 1) attn_prefix_kernel(
 
     if (warp >= kMmaWarp) {
         // ------------------------------------------------------ products
-        fewer_registers<S::kOtherRegs>();  // (one instruction for all of a group's warps)
+        fewer_registers<S, Q8>();  // (one instruction for all of a group's warps)
         // A factor below zero turns the queries' signs over.
         const uint32_t qk_idesc = idesc_bf16(TT) | (sp.flip ? 1u << 13 : 0u), pv_idesc = idesc_bf16(D) | 1u << 16;  // B (values) N-major
         Turn stage;
@@ -186,7 +185,7 @@ __global__ void __launch_bounds__(Shape<D, Q8>::kThreads, 1) attn_prefix_kernel(
         }
     } else if (warp >= kRowWarps) {
         // -------------------------------------------------------- copies
-        fewer_registers<S::kOtherRegs>();
+        fewer_registers<S, Q8>();
         // A warp copies TT / kLoadWarps tokens of each tile; lane l knows token l of them.
         // Format 8: into slots of codes, which the lane that copied them turns to bf16, kAhead half tiles later.
         constexpr int kMine = TT / kLoadWarps, kSub = Q8 ? 1 : kMine / 16, kChunks = D * (Q8 ? 1 : 2) / 16;
@@ -393,7 +392,7 @@ __global__ void __launch_bounds__(Shape<D, Q8>::kThreads, 1) attn_prefix_kernel(
         cp_async_wait_all();
     } else {
         // ------------------------------------------- a row in every thread
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::kRowRegs));
+        if (Q8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::kRowRegs));
         auto rows_sync = [] { asm volatile("bar.sync 1, %0;" ::"n"(kRowThreads) : "memory"); };
         const int group = warp >> 2, own_row = tid & (kRows - 1);
         const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16), scores = lanes + group * TT, out = lanes + kColO + group * D;
@@ -411,7 +410,7 @@ __global__ void __launch_bounds__(Shape<D, Q8>::kThreads, 1) attn_prefix_kernel(
             }
         };
         Item it;
-        bool more = walk.next(sp, it), first = true;
+        bool more = walk.next(sp, it);
         if (more) ask(it);
         while (more) {
             const int tiles = tiles_of<TT>(it);
@@ -425,29 +424,23 @@ __global__ void __launch_bounds__(Shape<D, Q8>::kThreads, 1) attn_prefix_kernel(
                 for (int c = 0; c < D; c += 32) tmem_st32(out + c, zero);
                 tmem_wait_st();
             }
-            auto queries_there = [&] {
-                cp_async_wait_all();
-                fence_async_smem();
-                tc_fence_before();
-                mbar_arrive(smem_addr(&s_queries));
-            };
-            if (!first) queries_there();
+            cp_async_wait_all();
+            fence_async_smem();
+            tc_fence_before();
+            mbar_arrive(smem_addr(&s_queries));
             float m = -INFINITY, l = 0.f;  // reference score, unscaled (format 8: to base 2); sum of the weights
             const float unit = Q8 ? 1.f : sp.scale_log2;
-            // The first of a CTA's tiles has one before it that leaves nothing behind: its instructions, which are in no cache
-            // yet, arrive while queries and tokens do.
-            for (int i = first ? group - 2 : group; i < tiles; i += 2) {
-                const bool real = i >= 0;
+            for (int i = group; i < tiles; i += 2, ++tile) {
                 const int there = it.tok1 - it.tok0 - i * TT;  // columns that are tokens
-                if (real) wait_or_report(smem_addr(&s_scores[group]), tile & 1, alive, a.status);
+                wait_or_report(smem_addr(&s_scores[group]), tile & 1, alive, a.status);
                 tc_fence_after();
                 const uint32_t buffer = (four + i) & 3;
-                if (Q8 && real) wait_or_report(smem_addr(&s_scaled[buffer]), (four + i) >> 2 & 1, alive, a.status);
+                if (Q8) wait_or_report(smem_addr(&s_scaled[buffer]), (four + i) >> 2 & 1, alive, a.status);
                 const float(*const scale)[Q8 ? TT : 4] = s_scale[Q8 ? buffer : 0];
-                // Format 16 holds the 128 scores, format 8 (which has less room) reads them twice.
-                constexpr int kHeld = Q8 ? 1 : TT / 32;
-                uint32_t v[kHeld][32];
-                auto take = [&](uint32_t(&u)[32], int c) {  // 32 scores, read and waited for
+                // A tile's scores are read twice, 32 at a time in rolled loops: held in 128 registers in between, with all
+                // loops unrolled, they cost as much in instructions that the caches do not have (a fifth of all stalls).
+                auto take = [&](uint32_t(&u)[32], int c) {
+                    tmem_ld32(scores + 32 * c, u);
                     if (Q8)
 #pragma unroll
                         for (int x = 0; x < 32; x += 4) {
@@ -471,23 +464,11 @@ __global__ void __launch_bounds__(Shape<D, Q8>::kThreads, 1) attn_prefix_kernel(
                         for (int y = 0; y < 4; ++y)
                             most[y] = fmaxf(most[y], fmaxf(__uint_as_float(u[x + 2 * y]), __uint_as_float(u[x + 2 * y + 1])));
                 };
-                if constexpr (!Q8) {
-#pragma unroll
-                    for (int c = 0; c < TT / 32; ++c) tmem_ld32_async(scores + 32 * c, v[c]);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int c = 0; c < TT / 32; ++c) {
-                        reg_fence32(v[c]);
-                        take(v[c], c);
-                        larger(v[c]);
-                    }
-                } else {
 #pragma unroll 2
-                    for (int c = 0; c < TT / 32; ++c) {
-                        tmem_ld32(scores + 32 * c, v[0]);
-                        take(v[0], c);
-                        larger(v[0]);
-                    }
+                for (int c = 0; c < TT / 32; ++c) {
+                    uint32_t u[32];
+                    take(u, c);
+                    larger(u);
                 }
                 const float grown = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
                 const float by = (grown - m) * unit;
@@ -528,31 +509,19 @@ __global__ void __launch_bounds__(Shape<D, Q8>::kThreads, 1) attn_prefix_kernel(
                         w[x >> 1] = __byte_perm(u0, u1, 0x7632);
                         w[16 + (x >> 1)] = __byte_perm(__float_as_uint(first_of(left)), __float_as_uint(second_of(left)), 0x7632);
                     }
-                    if (real) tmem_st32(scores + 32 * c, w);
+                    tmem_st32(scores + 32 * c, w);
                 };
-                if constexpr (!Q8) {
-#pragma unroll
-                    for (int c = 0; c < TT / 32; ++c) weigh(v[c], c);
-                } else {
 #pragma unroll 2
-                    for (int c = 0; c < TT / 32; ++c) {
-                        tmem_ld32(scores + 32 * c, v[0]);
-                        take(v[0], c);
-                        weigh(v[0], c);
-                    }
+                for (int c = 0; c < TT / 32; ++c) {
+                    uint32_t u[32];
+                    take(u, c);
+                    weigh(u, c);
                 }
                 l = (first_of(sums[0]) + second_of(sums[0])) + (first_of(sums[1]) + second_of(sums[1]));
-                if (!real) {
-                    m = -INFINITY, l = 0.f;
-                    queries_there();
-                    continue;
-                }
                 tmem_wait_st();
                 tc_fence_before();
                 mbar_arrive(smem_addr(&s_weights[group]));
-                ++tile;
             }
-            first = false;
             four += tiles;
             // ---- the two groups' sums
             wait_or_report(smem_addr(&s_values), items++ & 1, alive, a.status);
@@ -680,7 +649,7 @@ cudaError_t run(const SplitArgs& sp, int grid, cudaStream_t stream) {
         cudaFuncAttributes attributes;
         err = cudaFuncGetAttributes(&attributes, attn_prefix_kernel<D, Q8>);
         if (err != cudaSuccess) return err;
-        if (attributes.numRegs != S::kLaunchRegs) return cudaErrorInvalidConfiguration;
+        if (Q8 && attributes.numRegs != S::kLaunchRegs) return cudaErrorInvalidConfiguration;
         err = cudaFuncSetAttribute(attn_prefix_kernel<D, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
         if (err != cudaSuccess) return err;
         ready[device & (kMaxDevices - 1)].store(true, std::memory_order_relaxed);
