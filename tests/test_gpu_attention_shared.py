@@ -350,6 +350,64 @@ def test_a_cache_past_2_to_the_32_bytes(cuda_lib):
     case.check(out)
 
 
+@pytest.mark.parametrize("format", [16, 8])
+@pytest.mark.parametrize("order,P", [("token", 1), ("token", 3), ("token", 8), ("head", 8), ("head", 16), ("pair", 24), ("pair", 32), ("head", 64),
+                                     ("token", 128), ("head", 256), ("pair", 256), ("token", 384), ("token", 700)])
+def test_page_sizes_and_orders_of_many_rows(cuda_lib, order, P, format):
+    """Whole tiles in boxes, where pages divide tiles or tiles pages, and by rows; ends inside of a page and of a tile."""
+    groups = [(300, members(*range(1, 41))), (512, members(*range(20, 50))), (97, members(*[3] * 30))]
+    for Hq, H, D in ((10, 2, 128), (24, 3, 64), (8, 1, 80)):
+        case = Case(groups, Hq, H, D, P, after=members(50, 8), order=order, format=format, seed=P + D)
+        case.check(case.run())
+
+
+@pytest.mark.parametrize("format", [16, 8])
+@pytest.mark.parametrize("length", [1, 8, 127, 128, 129, 256, 384, 385, 511, 512, 513, 640, 900])
+def test_prefix_lengths_of_many_rows(cuda_lib, length, format):
+    """One to eight tiles, for each of the two groups of rows that take them in turn."""
+    for Hq, H, D in ((16, 2, 128), (8, 1, 64), (8, 1, 256)):
+        case = Case([(length, members(*[1, 5, 30] * 12))], Hq, H, D, 16, format=format, seed=length)
+        case.check(case.run(starts=None))
+
+
+@pytest.mark.parametrize("format", [16, 8])
+@pytest.mark.parametrize("P", [16, 24])
+def test_numbers_out_of_range_under_many_rows(cuda_lib, P, format):
+    case = Case([(300, members(*[9] * 40)), (300, members(*[9] * 40))], 8, 1, 128, P, after=members(30), format=format, seed=15)
+    table = case.prefix_table.copy()
+    table[0, 1], table[0, 2], table[0, 5] = 10 ** 6, -1, case.k.shape[0]
+    last = slice(int(case.starts[case.group_starts[1]]), None)
+    case.check(case.run(status=w4.W4_ERR_INVALID_ARG, prefix_table=gpu(table)), rows=last)
+    case.check(case.run())
+
+
+@pytest.mark.parametrize("where", ["k", "v"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_not_finite_values_under_many_rows(cuda_lib, where, value):
+    """They reach every row behind their prefix, through its head, and no other row."""
+    case = Case([(300, members(*[5] * 40)), (200, members(*[6] * 40))], 16, 2, 128, 16, after=members(12), seed=16)
+    clean = case.run()
+    (case.k if where == "k" else case.v)[int(case.prefix_table[0, 9]), 3, 1, 77] = value
+    got = case.run()
+    spoilt = torch.zeros(got.shape, dtype=torch.bool, device=DEV)
+    spoilt[:40, 8:, :] = where == "k"
+    spoilt[:40, 8:, 77] = True
+    if where == "v" or value != value:
+        assert (~torch.isfinite(got[spoilt])).all()
+    assert torch.equal(got[~spoilt].view(torch.int16), clean[~spoilt].view(torch.int16))
+
+
+def test_a_cache_past_2_to_the_32_bytes_under_many_rows(cuda_lib):
+    """Tiles in boxes and by rows, at the far end of a cache of 4.6 GB."""
+    for P in (16, 24):
+        case = Case([(300, members(*range(3, 43)))], 8, 1, 128, P, seed=17)
+        pages, far = case.k.shape[0], 280000 * 32 // P
+        both = torch.zeros((2, far, P, 1, 128), dtype=torch.bfloat16, device=DEV)
+        both[0, far - pages:], both[1, far - pages:] = case.k, case.v
+        shift = lambda t: gpu(np.where(t >= 0, t + far - pages, -1))  # noqa: E731
+        case.check(case.run(k_cache=both[0], v_cache=both[1], block_table=shift(case.table), prefix_table=shift(case.prefix_table)))
+
+
 def test_checks_of_the_binding(cuda_lib):
     case = Case(FEW, 8, 2, 128, 16, seed=14)
     kw = case.args()
