@@ -222,3 +222,24 @@ def test_checks_of_the_binding(cuda_lib):
             w4.w4_kv_append_norm(case.q, case.k, case.v, qw, kw, *rope, case.kc, case.vc, slots)
     with pytest.raises(w4.W4Error):
         w4.w4_kv_append_norm(case.q, case.k, case.v, case.qw, case.kw_, *rope, case.kc, case.vc, slots, eps=0.0)
+
+
+def test_no_tokens_and_two_streams_at_once(cuda_lib):
+    case = Case(0, 4, 2, 128, 64, seed=12)
+    case.check(case.run())
+    cases = [Case(n, 8, 2, 128, 128, seed=13 + n) for n in (40, 1300)]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    args = [(c.q, c.k, c.v, c.qw, c.kw_, gpu(c.positions), torch.tensor(c.cos, device=DEV), torch.tensor(c.sin, device=DEV), c.kc, c.vc,
+             gpu(c.slots, torch.int64)) for c in cases]
+    torch.cuda.synchronize()
+    outs = [[], []]
+    for _ in range(10):
+        for s, c, a, out in zip(streams, cases, args, outs):
+            with torch.cuda.stream(s):
+                out.append(w4.w4_kv_append_norm(*a, **c.kw))
+    torch.cuda.synchronize()
+    assert w4.w4_last_device_status() == 0
+    for c, out in zip(cases, outs):
+        c.check(out[0])
+        assert all(torch.equal(x.view(torch.int16), out[0].view(torch.int16)) for x in out)

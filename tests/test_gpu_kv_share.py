@@ -420,3 +420,86 @@ def test_calls_on_another_stream(cuda_lib):
         pool.step([0, 91, 33])
         pool.compact()
     pool.consistent()
+
+
+def test_captured_release_of_many_pages(cuda_lib):
+    """The kernels with a workspace: two captured calls, replayed in turn and again, and an eager call in between."""
+    width, n = 6000, 23900
+    pools = [Pool(4, width, width + 200, 4, seed=s) for s in (21, 22)]
+    for pool in pools:
+        pool.step([n, 0, 0, 70])
+        pool.fork([-1, 0, 0, -1], [0, n - 1, n // 2, 0])
+    target = gpu([0, n // 3, 0, 71])
+    graphs, start, outs = [], [], []
+    for pool in pools:
+        start.append([x.clone() for x in (pool.t, pool.h, pool.r)])
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(w4.w4_kv_pages(pool.l, target, pool.t, pool.r, pool.f, 4, 1, holders=pool.h))
+        graphs.append(graph)
+    want = [SO.pages_held(p.lens, target.tolist(), p.table, p.ring, p.free, 4, 1, p.holders) for p in pools]
+    for turn in range(3):
+        for i in (0, 1):
+            for x, before in zip((pools[i].t, pools[i].h, pools[i].r), start[i]):
+                x.copy_(before)
+            graphs[i].replay()
+            if turn == 1:
+                t, h, r = (x.clone() for x in start[1 - i])
+                w4.w4_kv_pages(pools[1 - i].l, target, t, r, pools[1 - i].f, 4, 1, holders=h)
+                same(h, want[1 - i]["holders"])
+        finish()
+        for pool, out, w in zip(pools, outs, want):
+            for x, name in ((out[0], "new_lens"), (out[4], "free_range"), (pool.t, "table"), (pool.r, "ring"), (pool.h, "holders")):
+                same(x, w[name], name)
+
+
+def test_releases_on_two_streams_at_once(cuda_lib):
+    width, n = 6000, 23900
+    pools = [Pool(4, width, width + 200, 4, seed=s) for s in (31, 32)]
+    for pool in pools:
+        pool.step([n, 0, 0, 0])
+        pool.fork([-1, 0, 0, -1], [0, n - 1, n // 2, 0])
+    target = [0, 5, 0, 0]
+    want = [SO.pages_held(p.lens, target, p.table, p.ring, p.free, 4, 0, p.holders) for p in pools]
+    target = gpu(target)
+    streams, calls = [torch.cuda.Stream() for _ in pools], [[], []]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s, pool, got in zip(streams, pools, calls):
+            with torch.cuda.stream(s):
+                state = [x.clone() for x in (pool.t, pool.r, pool.h)]
+                got.append((*state, w4.w4_kv_pages(pool.l, target, *state[:2], pool.f, 4, 0, holders=state[2])[4]))
+    finish()
+    for got, w in zip(calls, want):
+        for t, r, h, left in got:
+            same(t, w["table"]), same(r, w["ring"]), same(h, w["holders"]), same(left, w["free_range"])
+
+
+def test_calls_of_nothing(cuda_lib):
+    """No requests, no tokens, no copies."""
+    pool = Pool(0, 4, 10, 16, head=3)
+    pool.step([])
+    pool.fork([], [])
+    pool.compact()
+    pool.step([], tokens=5)
+    pool = Pool(3, 4, 1, 16)
+    pool.step([0, 0, 0])
+    pool.fork([-1, 0, 1], [0, 0, 0])
+    copies = pool.compact()
+    assert copies.shape == (3, 0)
+    k, v = paged(1, 16, 2, 64, "token", 1.0, 0)
+    w4.w4_kv_copy(k, v, copies)
+    finish()
+
+
+def test_the_same_source_and_the_same_page_many_times(cuda_lib):
+    """Every request forks the first one; the entries of one page let go together."""
+    B = 1500
+    pool = Pool(B, 3, 2 * B, 16, seed=5)
+    pool.step([40] + [0] * (B - 1))
+    pool.fork([-1] + [0] * (B - 1), [0] + [40 - i % 41 for i in range(B - 1)])
+    pool.consistent()
+    pool.step([40 if b in (7, 900) else 0 for b in range(B)], tokens=80)
+    pool.consistent()
+    pool.step([0] * B)
+    assert pool.free[1] - pool.free[0] == 2 * B
