@@ -49,6 +49,16 @@ constexpr int kRowWarps = 8, kRowThreads = kRowWarps * 32;
 constexpr int kFixed = 4;  // an item's fixed cost in tiles
 constexpr uint32_t kTmemCols = 512, kColO = 256;
 
+// Waits, as a warp, suspended between tests (polls, which the other kernel's longer stages do not notice, took issue
+// slots here: 1 % of the pass); as wait_or_report otherwise.
+__device__ __forceinline__ void wait_or_report_suspended(uint32_t bar, uint32_t parity, bool& alive, unsigned* status) {
+    if (!alive || __all_sync(~0u, mbar_wait_suspend(bar, parity))) return;
+    record_status(status, kStatusTimeout);
+    alive = false;
+    mbar_wait(bar, parity);
+    __syncwarp();
+}
+
 template <class S, bool Q8>
 __device__ __forceinline__ void fewer_registers() {
     if (Q8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kOtherRegs));
@@ -145,13 +155,13 @@ __global__ void __launch_bounds__(Shape<D, Q8>::kThreads, 1) attn_prefix_kernel(
         uint32_t summed[2] = {0, 0}, items = 0;  // tiles of each group so far
         for (Item it; warp == kMmaWarp && walk.next(sp, it);) {
             const int tiles = tiles_of<TT>(it);
-            wait_or_report(smem_addr(&s_queries), items++ & 1, alive, a.status);
+            wait_or_report_suspended(smem_addr(&s_queries), items++ & 1, alive, a.status);
             // Stage i: the values of tile i − 2, then the keys of tile i, whose scores go where those weights are: those
             // products are issued before, and the tensor cores take a thread's products in their order.
             for (int i = 0; i < tiles + 2; ++i) {
                 const int w = i & 1;
-                wait_or_report(smem_addr(&s_full[stage.place]), stage.round, alive, a.status);
-                if (i >= 2) wait_or_report(smem_addr(&s_weights[w]), summed[w]++ & 1, alive, a.status);
+                wait_or_report_suspended(smem_addr(&s_full[stage.place]), stage.round, alive, a.status);
+                if (i >= 2) wait_or_report_suspended(smem_addr(&s_weights[w]), summed[w]++ & 1, alive, a.status);
                 fence_async_smem();  // the copies were made through the generic proxy
                 tc_fence_after();
                 const uint32_t keys = ring + stage.place * 2 * S::kHalf, vals = keys + S::kHalf;
@@ -196,7 +206,7 @@ __global__ void __launch_bounds__(Shape<D, Q8>::kThreads, 1) attn_prefix_kernel(
         stage.round = 1;  // the ring's first round finds its stages free
         auto place_of = [&](bool key) { return ring + (2 * stage.place + !key) * S::kHalf; };
         auto begin = [&](bool key) {  // keys come first
-            if (key) wait_or_report(smem_addr(&s_empty[stage.place]), stage.round, alive, a.status);
+            if (key) wait_or_report_suspended(smem_addr(&s_empty[stage.place]), stage.round, alive, a.status);
         };
         auto end = [&](bool key) {
             if (!key) stage.step(NS);
@@ -432,29 +442,23 @@ __global__ void __launch_bounds__(Shape<D, Q8>::kThreads, 1) attn_prefix_kernel(
             const float unit = Q8 ? 1.f : sp.scale_log2;
             for (int i = group; i < tiles; i += 2, ++tile) {
                 const int there = it.tok1 - it.tok0 - i * TT;  // columns that are tokens
-                wait_or_report(smem_addr(&s_scores[group]), tile & 1, alive, a.status);
+                wait_or_report_suspended(smem_addr(&s_scores[group]), tile & 1, alive, a.status);
                 tc_fence_after();
                 const uint32_t buffer = (four + i) & 3;
-                if (Q8) wait_or_report(smem_addr(&s_scaled[buffer]), (four + i) >> 2 & 1, alive, a.status);
+                if (Q8) wait_or_report_suspended(smem_addr(&s_scaled[buffer]), (four + i) >> 2 & 1, alive, a.status);
                 const float(*const scale)[Q8 ? TT : 4] = s_scale[Q8 ? buffer : 0];
                 // A tile's scores are read twice, 32 at a time in rolled loops: held in 128 registers in between, with all
                 // loops unrolled, they cost as much in instructions that the caches do not have (a fifth of all stalls).
-                auto take = [&](uint32_t(&u)[32], int c) {
-                    tmem_ld32(scores + 32 * c, u);
-                    if (Q8)
-#pragma unroll
-                        for (int x = 0; x < 32; x += 4) {
-                            const float4 f = *reinterpret_cast<const float4*>(&scale[0][Q8 ? 32 * c + x : 0]);
-                            u[x] = __float_as_uint(__uint_as_float(u[x]) * f.x);
-                            u[x + 1] = __float_as_uint(__uint_as_float(u[x + 1]) * f.y);
-                            u[x + 2] = __float_as_uint(__uint_as_float(u[x + 2]) * f.z);
-                            u[x + 3] = __float_as_uint(__uint_as_float(u[x + 3]) * f.w);
-                        }
+                // A tile's scores are read twice, 32 at a time in rolled loops: held in 128 registers in between, with all
+                // loops unrolled, they cost as much in instructions that the caches do not have (a fifth of all stalls).
+                auto hide = [&](uint32_t(&u)[32], int c) {  // (in a loop of its own: selects in every tile cost 7 %)
                     if (there < TT)
 #pragma unroll
                         for (int x = 0; x < 32; ++x)
                             if (32 * c + x >= there) u[x] = 0xFF800000u;  // −∞
                 };
+                // Factors of two tokens' scores to base 2.
+                auto units = [&](int column) { return Q8 ? *reinterpret_cast<const uint64_t*>(&scale[0][Q8 ? column : 0]) : two(unit, unit); };
                 // ---- reference
                 float most[4] = {m, -INFINITY, -INFINITY, -INFINITY};
                 auto larger = [&](const uint32_t(&u)[32]) {
@@ -467,7 +471,15 @@ __global__ void __launch_bounds__(Shape<D, Q8>::kThreads, 1) attn_prefix_kernel(
 #pragma unroll 2
                 for (int c = 0; c < TT / 32; ++c) {
                     uint32_t u[32];
-                    take(u, c);
+                    tmem_ld32(scores + 32 * c, u);
+                    if (Q8)
+#pragma unroll
+                        for (int x = 0; x < 32; x += 2) {
+                            const uint64_t s = mul2(two(__uint_as_float(u[x]), __uint_as_float(u[x + 1])), units(32 * c + x));
+                            u[x] = __float_as_uint(first_of(s));
+                            u[x + 1] = __float_as_uint(second_of(s));
+                        }
+                    hide(u, c);
                     larger(u);
                 }
                 const float grown = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
@@ -490,14 +502,14 @@ __global__ void __launch_bounds__(Shape<D, Q8>::kThreads, 1) attn_prefix_kernel(
                 }
                 const float ref = m == -INFINITY ? 0.f : m * unit;
                 // ---- weights, over the scores: of 32 tokens the upper halves in 16 columns, then the lower ones
-                const uint64_t by_unit = two(unit, unit), from = two(-ref, -ref);
+                const uint64_t from = two(-ref, -ref);
                 uint64_t sums[2] = {two(l, 0.f), 0};
                 auto weigh = [&](const uint32_t(&u)[32], int c) {
                     uint32_t w[32];
 #pragma unroll
                     for (int x = 0; x < 32; x += 2) {
                         uint64_t s = two(__uint_as_float(u[x]), __uint_as_float(u[x + 1]));
-                        s = Q8 ? add2(s, from) : fma2(s, by_unit, from);
+                        if (!Q8) s = fma2(s, units(0), from);
                         uint64_t p = two(ex2(first_of(s)), ex2(second_of(s)));
                         sums[x >> 1 & 1] = add2(sums[x >> 1 & 1], p);
                         if (Q8) p = mul2(p, *reinterpret_cast<const uint64_t*>(&scale[1][Q8 ? 32 * c + x : 0]));
@@ -514,7 +526,15 @@ __global__ void __launch_bounds__(Shape<D, Q8>::kThreads, 1) attn_prefix_kernel(
 #pragma unroll 2
                 for (int c = 0; c < TT / 32; ++c) {
                     uint32_t u[32];
-                    take(u, c);
+                    tmem_ld32(scores + 32 * c, u);
+                    if (Q8)
+#pragma unroll
+                        for (int x = 0; x < 32; x += 2) {
+                            const uint64_t s = fma2(two(__uint_as_float(u[x]), __uint_as_float(u[x + 1])), units(32 * c + x), from);
+                            u[x] = __float_as_uint(first_of(s));
+                            u[x + 1] = __float_as_uint(second_of(s));
+                        }
+                    hide(u, c);
                     weigh(u, c);
                 }
                 l = (first_of(sums[0]) + second_of(sums[0])) + (first_of(sums[1]) + second_of(sums[1]));
@@ -524,7 +544,7 @@ __global__ void __launch_bounds__(Shape<D, Q8>::kThreads, 1) attn_prefix_kernel(
             }
             four += tiles;
             // ---- the two groups' sums
-            wait_or_report(smem_addr(&s_values), items++ & 1, alive, a.status);
+            wait_or_report_suspended(smem_addr(&s_values), items++ & 1, alive, a.status);
             tc_fence_after();
             tc_fence_before();
             if (group == 1) s_stats[own_row] = make_float2(m * unit, l);
