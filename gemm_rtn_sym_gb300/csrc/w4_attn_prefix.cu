@@ -14,15 +14,36 @@
 // an item's end their sums meet: a row's two threads share its lane of tensor
 // memory, and each writes half of its columns.
 //
-// Warps 0 to 7 hold the rows, the next ones copy the tokens' rows by cp.async
-// from pages of any size into a ring of slots, in the order that the products
-// take them: K0, K1, V0, K2, V1, ...; the last warp issues the products.
+// Warps 0 to 7 hold the rows, the next ones bring keys and values, the last one
+// issues the products.  A stage of the ring is the keys of tile i and the values
+// of tile i − 2: the tensor cores take one thread's products in their order, so
+// that the scores of tile i may go where the weights of tile i − 2 were as soon
+// as the products of those are issued.  Whole tiles come by TMA, a page (or 128
+// tokens of one) and 64 columns at a time, where page sizes divide a tile or
+// are multiples of it; an item's end and pages of other sizes come row by row by
+// cp.async.  (All rows by cp.async: 1 to 3 % longer.)
 // Tensor memory: S of even and of odd tiles from column 0, then the two O.
 //
 // Format 8: codes are exact as bf16, so the products are those of format 16,
 // with the key scales applied to the scores and the value scales to the
 // weights.  Codes arrive in slots of their own and eight warps turn them to
 // bf16.
+//
+// The work is the list of (group, head, 128 rows) and their tiles in equal
+// pieces over the SMs; parts of items stay where they are, for the join.
+//
+// Measured.  64 rows of 40 query and 8 key-value heads of 128 behind 16385
+// tokens, 67 MB: 40 µs of 58 for all three kernels; 13 are the bytes, 11 the
+// products at the measured rates, and 20 the products as they are (each weight
+// twice, 320 rows to a head as 384).  Tensor pipe 42 % active, issue 39 %: a tile
+// is 2800 cycles, of which the products are 1536, and two groups of rows do not
+// hide the rest from one another: their exponentials, roundings and maxima, 640
+// instructions to a row at the least, and the hand-overs between the three
+// kinds of warps.  Twelve prefixes of 300 to 8192 tokens in format 8, 40 rows of 64
+// heads behind each: 68 of 131 µs, bound by instructions (issue 54 %), the codes'
+// turn to bf16 among them.
+// No faster: the next scores on their way while these are weighed (58.9 for
+// 59.4), the joins' work by the CTA that ends an item (25 to 40 µs more).
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -683,7 +704,8 @@ constexpr int kJoinWarps = 4, kJoinBatch = 8;
 // One warp to a row: its own tokens' sums, and those of its prefix, from
 // wherever they are, on one reference, into its output.  (The CTA that
 // finishes an item last, as in the other kernels, would read its parts alone:
-// 19 of 66 KB where one prefix's 8 heads are shared by 152 SMs.)
+// 19 of 66 KB where one prefix's 8 heads are shared by 152 SMs.)  2 of the 58
+// µs and 9 of the 131 above: 2560 rows of 128, each in about 7 parts.
 template <int V>  // float4 of a lane: head_dim ≤ 128 · V
 __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const __grid_constant__ JoinArgs a) {
     asm volatile("griddepcontrol.wait;" ::: "memory");

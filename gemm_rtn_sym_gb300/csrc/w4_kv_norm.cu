@@ -7,6 +7,13 @@
 // A row is read once and written once; its sum of squares is a few shuffles
 // among the lanes that hold it.  Done apart, the norm would read and write the
 // queries and keys once more, and round them once more.
+//
+// Measured, 40 query and 8 key-value heads of 128 in bf16: 16001 tokens 87 µs,
+// 0.80 of the rate of a plain copy (78.8 without norms); 208 tokens, 64 and 8
+// heads, 5.5 (4.3); one token, 16 and 4 heads of 256, 3.0 (2.6).  Long prompts
+// are bound by what a row takes on the way, shuffles, products and roundings
+// (issue 64 %, loads' latency 45 % of the stalls at 14 of 64 resident warps);
+// few tokens by one chain of latencies.
 #include <algorithm>
 #include <cmath>
 #include <cstdint>

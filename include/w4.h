@@ -675,7 +675,7 @@ int w4_attn_decode(const w4_kv_cache* cache, int32_t B, int64_t T, int32_t q_hea
  * groups then claim have no meaning); a prefix length past prefix_width ·
  * page_size (or 2³⁰) counts as that.  T: at most 2³⁰.
  * workspace: w4_attn_decode_shared_workspace_bytes(...) bytes; the rest as for
- * w4_attn_decode.  Deterministic.  Two launches.
+ * w4_attn_decode.  Deterministic.  Three launches.
  */
 size_t w4_attn_decode_shared_workspace_bytes(const w4_kv_cache* cache, int32_t B, int64_t T, int32_t q_heads,
                                              int32_t groups);
