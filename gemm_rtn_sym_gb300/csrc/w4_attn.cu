@@ -768,14 +768,15 @@ bool many_rows(int32_t B, int64_t T, int G, int32_t kv_heads, int D, bool q8) {
 // The same for a pass over prefixes, whose parts a kernel of its own joins, so that
 // few heads are no reason to stay here.  µs of the whole call, here and there,
 // one prefix of 16385 tokens, 8 key-value heads (4 of 256):
-// head_dim 64, 24 rows: 32 and 32; 32: 37 and 32.  128, 16 rows: 26 and 33; 24: 38
-// and 34.  256, 16 rows: 37 and 40; 24: 51 and 41.  Format 8: 64, 96 rows: 41 and
-// 40.  128, 48 rows: 43 and 45; 64: 46 and 46; 96: 58 and 47.  256, 64 rows: 53 and
-// 53; 96: 66 and 57.  Twelve prefixes of 1500 tokens: 128, 24 rows: 37 and 40; 32: 41
-// and 42; 48: 50 and 45; 256, 16 rows: 32 and 38; 24: 41 and 37; format 8, 128, 48
-// rows: 55 and 59; 64: 65 and 64.
+// head_dim 64, 16 rows: 22 and 29; 24: 32 and 29.  128, 16 rows: 26 and 30; 24: 39
+// and 31.  256, 16 rows: 38 and 40; 24: 51 and 41.  Format 8: 64, 64 rows: 33 and
+// 36; 96: 40 and 37.  128, 32 rows: 36 and 42; 40: 42 and 42; 48: 42 and 42; 64: 45
+// and 43.  256, 48 rows: 50 and 51; 64: 53 and 53; 96: 64 and 56.  Twelve prefixes
+// of 1500 tokens: 128, 16 rows: 27 and 34; 24: 37 and 35; 256, 16 rows: 31 and 37;
+// 24: 41 and 37; format 8, 128, 40 rows: 51 and 52; 48: 55 and 53; 64: 65 and 60.
+// (From 17 rows on, two warps share a stage here, and format 8 takes 16 at a time.)
 bool many_rows_behind(int32_t groups, int64_t T, int G, int D, bool q8) {
-    const int limit = q8 ? (D == 64 ? 96 : D == 128 ? 56 : 64) : D == 256 ? 16 : 24;
+    const int limit = !q8 ? 16 : D == 64 ? 80 : D == 128 ? 40 : 56;
     return average_rows(groups, T, G) > limit;
 }
 
