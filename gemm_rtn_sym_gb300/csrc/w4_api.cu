@@ -690,9 +690,10 @@ int kv_pages(const int32_t* lens, const int32_t* target, int32_t B, int32_t page
     if (any_meet(outs, 9, ins, 3)) return W4_ERR_INVALID_ARG;
     const DeviceInfo* dev;
     if (const int s = usable_device(&dev)) return s;
-    unsigned* const words = need > 0 ? static_cast<unsigned*>(workspace) : nullptr;
+    long long* const given = need > 0 ? static_cast<long long*>(workspace) : nullptr;
+    unsigned* const words = given ? reinterpret_cast<unsigned*>(given + 1) : nullptr;
     const KvPagesArgs a = {lens, target, B, page_size, free_pages, pages, free_range, block_table, table_stride, width,
-                           T, holders, words, words ? words + pages : nullptr, new_lens, starts, slots, positions, free_range_out, dev->status, 0, 0};
+                           T, holders, given, words, words ? words + pages : nullptr, new_lens, starts, slots, positions, free_range_out, dev->status, 0, 0};
     return to_status(launch_kv_pages(a, *dev, static_cast<cudaStream_t>(stream)));
 }
 

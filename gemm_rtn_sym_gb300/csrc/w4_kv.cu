@@ -149,10 +149,14 @@ __global__ void __launch_bounds__(kPagesThreads) kv_pages_kernel(KvPagesArgs a) 
             a.slots[t] = slot;
             a.positions[t] = pos;
         }
-        for (long long r = carry.back + static_cast<long long>(blockIdx.x) * threads + tid; !HELD && r < total.back; r += step) {
+        for (long long r = carry.back + static_cast<long long>(blockIdx.x) * threads + tid; (!HELD || a.last) && r < total.back; r += step) {
             const int i = last_at_most(s_back, n, r);
+            const int page = a.table[(base + i) * a.table_stride + s_want[i] + (r - s_back[i])];
             // The table may claim more pages than the pool has; each entry of the ring is then written again.
-            *ring(tail_at, r < a.pages ? r : r % a.pages) = a.table[(base + i) * a.table_stride + s_want[i] + (r - s_back[i])];
+            if (!HELD)
+                *ring(tail_at, r < a.pages ? r : r % a.pages) = page;
+            else if (page >= 0 && page < a.pages)
+                a.last[page] = 0;
         }
         carry = total;
         __syncthreads();
@@ -168,9 +172,9 @@ __global__ void __launch_bounds__(kPagesThreads) kv_pages_kernel(KvPagesArgs a) 
         if (!HELD) a.range_out[1] = tail + carry.back;
     }
     if (HELD && a.last) {
-        const long long step = static_cast<long long>(gridDim.x) * threads, words = (static_cast<long long>(a.B) * a.width + 31) / 32;
-        for (long long i = static_cast<long long>(blockIdx.x) * threads + tid; i < a.pages; i += step) a.last[i] = 0;
+        const long long step = static_cast<long long>(gridDim.x) * threads, words = (carry.back + 31) / 32;
         for (long long i = static_cast<long long>(blockIdx.x) * threads + tid; i < words; i += step) a.marks[i] = 0;
+        if (blockIdx.x == 0 && tid == 0) *a.given = carry.back;
     } else if (HELD && gridDim.x == 1) {
         __syncthreads();
         release_pages(a);
@@ -360,7 +364,8 @@ cudaError_t launch_kv_pages(KvPagesArgs a, const DeviceInfo& dev, cudaStream_t s
     // Small CTAs' barriers cost less, but each thread scans one request at a time: 3.2 µs with 256 threads and 4.2 with
     // 1024 for 64 requests (a token each), 3.6 and 4.7 for 256, 5.5 and 4.8 for 384, 9.4 and 5.6 for 1000.
     const int threads = a.B <= 256 ? 256 : kPagesThreads;
-    const int64_t blocks = (a.T + threads - 1) / threads;
+    // (a table of many entries: as many as could be let go of, whose words are cleared here)
+    const int64_t work = a.last ? std::max(a.T, static_cast<int64_t>(a.B) * a.width) : a.T, blocks = (work + threads - 1) / threads;
     const int grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(blocks, dev.sm_count * (kPagesThreads / threads))));
     if (!a.holders) {
         kv_pages_kernel<false><<<grid, threads, 0, stream>>>(a);

@@ -25,8 +25,9 @@ struct KvPagesArgs {
     int32_t width;
     int64_t T;
     int32_t* holders;  // nullptr: every page has one
-    unsigned* last;    // nullptr where the table has few entries; else a word for each page,
-    unsigned* marks;   // and a bit for each entry
+    long long* given;  // nullptr where the table has few entries; else the number of entries that are let go of,
+    unsigned* last;    // a word for each page,
+    unsigned* marks;   // and a bit for each entry that is let go of
     int32_t* new_lens;
     int32_t* starts;
     int64_t* slots;

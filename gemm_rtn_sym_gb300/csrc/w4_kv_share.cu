@@ -30,12 +30,14 @@ __global__ void __launch_bounds__(kThreads) kv_release_kernel(KvPagesArgs a) {
 // Entries by all CTAs at once.  Each leaves its number in its page's word if
 // that is the largest so far, and then counts the page's holders down: whoever
 // finds the last of them finds the number of the last entry there as well, and
-// marks that entry.  (600 of 1000 requests of up to 4097 tokens that end: this
-// kernel 8 µs, the pages' 8, the next 10; 21 in all, since they overlap.)
+// marks that entry.  What is read and written, here, before and after, follows
+// the entries that are let go of, not the table's size: the pages' kernel
+// leaves their number, clears the words of their pages and a mark for each.
 __global__ void __launch_bounds__(kThreads) kv_let_go_kernel(KvPagesArgs a) {
     __shared__ long long s_first[kThreads], s_warp[33];
     __shared__ int s_want[kThreads];
     pdl_start();
+    if (*a.given == 0) return;
     const int tid = threadIdx.x;
     long long before = 0;
     for (int base = 0; base < a.B; base += kThreads) {
@@ -65,55 +67,50 @@ __global__ void __launch_bounds__(kThreads) kv_let_go_kernel(KvPagesArgs a) {
     }
 }
 
-constexpr int kMarkWords = 64, kMarked = kMarkWords * 32;  // words and entries that a CTA takes at a time
-
 // The marked entries' pages go to the ring, in the order of the entries.  A CTA
-// counts the marks before its own (a bit for each entry that there could be).
+// has one run of the entries: it counts the marks before the run once, and
+// carries the count on through the run.
 __global__ void __launch_bounds__(kThreads) kv_give_back_kernel(KvPagesArgs a) {
     __shared__ long long s_first[kThreads], s_warp[33];
-    __shared__ int s_want[kThreads], s_before[kMarkWords];
-    __shared__ unsigned s_words[kMarkWords];
+    __shared__ int s_want[kThreads];
     pdl_start();
     const int tid = threadIdx.x;
-    const long long tail = a.range[1];
+    const long long tail = a.range[1], entries = *a.given;
     const long long tail_at = static_cast<long long>(static_cast<uint64_t>(tail) % static_cast<uint64_t>(a.pages));
-    const long long words = (static_cast<long long>(a.B) * a.width + 31) / 32;
-    for (long long w0 = static_cast<long long>(blockIdx.x) * kMarkWords; w0 < words; w0 += static_cast<long long>(gridDim.x) * kMarkWords) {
-        const unsigned word = tid < kMarkWords && w0 + tid < words ? a.marks[w0 + tid] : 0;
-        long long n = 0, given, mine;
+    // (runs of whole blocks of entries, so that they begin with a word of marks)
+    const long long run = ((entries + gridDim.x - 1) / gridDim.x + kThreads - 1) / kThreads * kThreads;
+    const long long from = blockIdx.x * run, to = min(from + run, entries);
+    if (from >= entries) {
+        if (entries == 0 && blockIdx.x == 0 && tid == 0) a.range_out[1] = tail;
+        return;
+    }
+    long long n = 0, given;
 #pragma unroll 8
-        for (long long w = tid; w < w0; w += kThreads) n += __popc(a.marks[w]);
-        block_sum_before(n, s_warp, given);
-        __syncthreads();
-        const long long before = block_sum_before(__popc(word), s_warp, mine);
-        if (tid < kMarkWords) {
-            s_words[tid] = word;
-            s_before[tid] = static_cast<int>(before);
-        }
-        if (tid == 0 && w0 + kMarkWords >= words) a.range_out[1] = tail + given + mine;
-        __syncthreads();
-        if (mine == 0) continue;
-        long long done = 0;  // entries of the requests before `base`
-        for (int base = 0; base < a.B; base += kThreads) {
-            const int m = min(a.B - base, kThreads);
-            const long long all = scan_given(a, base, m, s_first, s_want, s_warp);
-            if (done + all > w0 * 32 && done < (w0 + kMarkWords) * 32) {
-#pragma unroll
-                for (int e0 = 0; e0 < kMarked; e0 += kThreads) {
-                    const int e = e0 + tid;
-                    const long long r = w0 * 32 + e - done;
-                    if (r >= 0 && r < all && s_words[e >> 5] >> (e & 31) & 1) {
-                        const int i = last_at_most(s_first, m, r);
-                        long long at = tail_at + (given + s_before[e >> 5] + __popc(s_words[e >> 5] & ((1u << (e & 31)) - 1))) % a.pages;
-                        if (at >= a.pages) at -= a.pages;
-                        a.ring[at] = a.table[(base + i) * a.table_stride + s_want[i] + (r - s_first[i])];
-                    }
-                }
+    for (long long w = tid; w < from / 32; w += kThreads) n += __popc(a.marks[w]);
+    block_sum_before(n, s_warp, given);
+    __syncthreads();
+    long long done = 0;  // entries of the requests before `base`
+    for (int base = 0; base < a.B && done < to; base += kThreads) {
+        const int m = min(a.B - base, kThreads);
+        const long long all = scan_given(a, base, m, s_first, s_want, s_warp), end = min(done + all, to);
+        for (long long r0 = max(done, from); r0 < end; r0 += kThreads) {
+            const long long r = r0 + tid;
+            const bool marked = r < end && (a.marks[r >> 5] >> (r & 31) & 1);
+            long long count;
+            const long long before = block_sum_before(marked, s_warp, count);
+            if (marked) {
+                const int i = last_at_most(s_first, m, r - done);
+                long long at = tail_at + (given + before) % a.pages;
+                if (at >= a.pages) at -= a.pages;
+                a.ring[at] = a.table[(base + i) * a.table_stride + s_want[i] + (r - done - s_first[i])];
             }
-            done += all;
+            given += count;
             __syncthreads();
         }
+        done += all;
+        __syncthreads();
     }
+    if (to == entries && tid == 0) a.range_out[1] = tail + given;
 }
 
 // -------------------------------------------------------------------- fork
@@ -440,13 +437,14 @@ cudaError_t launch_kv_release(const KvPagesArgs& a, const DeviceInfo& dev, cudaS
     }
     auto ctas = [&](int64_t each) { return static_cast<int>(std::min<int64_t>((entries + each - 1) / each, dev.sm_count)); };
     const cudaError_t err = launch_pass(kv_let_go_kernel, ctas(kThreads), kThreads, 0, stream, true, a);
-    return err != cudaSuccess ? err : launch_pass(kv_give_back_kernel, ctas(kMarked), kThreads, 0, stream, true, a);
+    return err != cudaSuccess ? err : launch_pass(kv_give_back_kernel, ctas(kThreads), kThreads, 0, stream, true, a);
 }
 
-// Words for each page and a bit for each entry of the table, where more pages may go back than one CTA should see to.
+// The number of entries that are let go of, a word for each page and a bit for each entry of the table, where more pages may
+// go back than one CTA should see to.
 size_t kv_held_workspace_bytes(int32_t B, int32_t width, int64_t pages) {
     const int64_t entries = static_cast<int64_t>(B) * width;
-    return entries <= kFewEntries ? 0 : static_cast<size_t>(pages + (entries + 31) / 32) * 4;
+    return entries <= kFewEntries ? 0 : sizeof(long long) + static_cast<size_t>(pages + (entries + 31) / 32) * 4;
 }
 
 cudaError_t launch_kv_fork(KvForkArgs a, const DeviceInfo& dev, cudaStream_t stream) {

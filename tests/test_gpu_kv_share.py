@@ -503,3 +503,57 @@ def test_the_same_source_and_the_same_page_many_times(cuda_lib):
     pool.consistent()
     pool.step([0] * B)
     assert pool.free[1] - pool.free[0] == 2 * B
+
+
+@pytest.mark.parametrize("B,width", [(5, 130000), (2600, 300)])
+def test_more_entries_let_go_than_the_grid_has_blocks(cuda_lib, B, width):
+    """400000 entries in one call: every CTA has several blocks of them; then a few, and none, of the same table."""
+    pages, n = 2 * width + 400000, 4 * (width - 10)
+    pool = Pool(B, width, pages, 4, seed=B)
+    parents = max(1, B // 8)
+    lens = np.where(np.arange(B) < parents, n, 0)
+    pool.step(lens)
+    child = np.arange(B) >= parents
+    keep = np.where(child, n - np.arange(B) % 7 * 10, 0)
+    pool.fork(np.where(child, np.arange(B) % parents, -1), keep)
+    pool.consistent()
+    back = pool.free[1] - pool.free[0]
+    pool.step(np.where(np.arange(B) % 11 == 3, 50, np.where(np.arange(B) % 13 == 5, pool.lens, 0)))
+    pool.consistent()
+    assert pool.free[1] - pool.free[0] > back
+    pool.step(pool.lens - np.minimum(pool.lens, 9))
+    pool.consistent()
+    pool.step(pool.lens)
+    pool.step(np.zeros(B, np.int32))
+    assert pool.free[1] - pool.free[0] == pages
+
+
+@pytest.mark.parametrize("ends", [0, 3])
+def test_the_time_of_a_step_follows_what_is_let_go_of(cuda_lib, ends):
+    """1000 requests of a few hundred tokens whose tables have room for two million: a step that lets go of nothing, or of
+    three requests' pages, takes microseconds (a walk over the table's 131 million entries would take a hundred times the limit)."""
+    B, width, P, pages = 1000, 131072, 16, 40000
+    lens = gpu(np.arange(B) % 500 + 17)
+    table = torch.full((B, width), -1, dtype=torch.int32, device=DEV)
+    free, ring = gpu([0, pages], torch.int64), gpu(np.arange(pages))
+    holders = gpu(np.zeros(pages))
+    total = int(lens.sum())
+    lens, *_, free = w4.w4_kv_pages(gpu(np.zeros(B)), lens, table, ring, free, P, total, holders=holders)
+    target = (lens + 1) * gpu(np.arange(B) >= ends)
+    want = SO.pages_held(lens.tolist(), target.tolist(), table[:, :40].cpu().numpy(), ring.cpu().numpy(), free.tolist(), P, B, holders.cpu().numpy())
+    state = [x.clone() for x in (ring, holders)]
+    got = w4.w4_kv_pages(lens, target, table, state[0], free, P, B, holders=state[1])
+    finish()
+    for x, name in ((got[0], "new_lens"), (got[4], "free_range"), (state[0], "ring"), (state[1], "holders"), (table[:, :40], "table")):
+        same(x, want[name], name)
+    times = []
+    for _ in range(10):
+        for x, old in zip(state, (ring, holders)):
+            x.copy_(old)
+        begin, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        begin.record()
+        w4.w4_kv_pages(lens, target, table, state[0], free, P, B, holders=state[1])
+        end.record()
+        torch.cuda.synchronize()
+        times.append(begin.elapsed_time(end) * 1e3)
+    assert min(times) < 500, f"{min(times):.0f} us"
