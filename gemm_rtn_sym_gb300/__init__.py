@@ -604,6 +604,13 @@ def _compiled():
     return _fast
 
 
+def _result(done, name: str):
+    """What a compiled function returned; a status (an int) is an error that came up at a launch."""
+    if type(done) is int:
+        raise W4Error(done, name)
+    return done
+
+
 def w4_kv_pages(lens: torch.Tensor, target: torch.Tensor, block_table: torch.Tensor, free_pages: torch.Tensor,
                 free_range: torch.Tensor, page_size: int, tokens: int, new_lens: torch.Tensor | None = None,
                 starts: torch.Tensor | None = None, slots: torch.Tensor | None = None,
@@ -619,7 +626,7 @@ def w4_kv_pages(lens: torch.Tensor, target: torch.Tensor, block_table: torch.Ten
         done = _compiled().kv_pages_held(lens, target, block_table, free_pages, free_range, page_size, tokens, holders,
                                         new_lens, starts, slots, positions, free_range_out)
         if done is not NotImplemented:
-            return done
+            return _result(done, "w4_kv_pages_held")
     index = _device_index(block_table, "block_table")
     stride = _strides(block_table, "block_table", torch.int32, 2, index)[0]
     B, width = block_table.shape
@@ -674,7 +681,7 @@ def w4_kv_fork(lens: torch.Tensor, source: torch.Tensor, keep: torch.Tensor, blo
     done = _compiled().kv_fork(lens, source, keep, block_table, holders, free_pages, free_range, page_size, new_lens, copies,
                               free_range_out)
     if done is not NotImplemented:
-        return done
+        return _result(done, "w4_kv_fork")
     index = _device_index(block_table, "block_table")
     stride = _strides(block_table, "block_table", torch.int32, 2, index)[0]
     B, width = block_table.shape
@@ -698,7 +705,7 @@ def w4_kv_compact(lens: torch.Tensor, block_table: torch.Tensor, holders: torch.
     done = _compiled().kv_compact(lens, block_table, holders, free_range, page_size, new_table, new_holders, free_pages,
                                  free_range_out, copies)
     if done is not NotImplemented:
-        return done
+        return _result(done, "w4_kv_compact")
     index = _device_index(block_table, "block_table")
     stride = _strides(block_table, "block_table", torch.int32, 2, index)[0]
     B, width = block_table.shape
@@ -717,7 +724,7 @@ def w4_kv_copy(k_cache: torch.Tensor, v_cache: torch.Tensor, copies: torch.Tenso
                v_scales: torch.Tensor | None = None) -> None:
     """Copies the first copies[2][i] tokens of page copies[0][i] to page copies[1][i] (int32 [3, n]; −1, −1: nothing), keys,
     values and scales."""
-    if _compiled().kv_copy(k_cache, v_cache, copies, k_scales, v_scales) is None:
+    if _result(_compiled().kv_copy(k_cache, v_cache, copies, k_scales, v_scales), "w4_kv_copy") is None:
         return
     index = _device_index(k_cache, "k_cache")
     cache = _kv_cache(k_cache, v_cache, k_scales, v_scales, index)
@@ -800,7 +807,7 @@ def w4_kv_append_norm(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, 
     done = _compiled().kv_append_norm(q, k, v, q_weight, k_weight, positions, cos, sin, k_cache, v_cache, slots, eps,
                                      unit_offset, sections, cycled, paired, k_scales, v_scales, q_out)
     if done is not NotImplemented:
-        return done[0]
+        return _result(done, "w4_kv_append_norm")[0]
     return _append("w4_kv_append_norm", q, k, v, positions, cos, sin, k_cache, v_cache, slots, sections, cycled, paired,
                    k_scales, v_scales, q_out, (q_weight, k_weight, eps, unit_offset))
 
@@ -878,7 +885,7 @@ def w4_attn_decode_shared(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
         done = _compiled().attn_decode_shared(q, k_cache, v_cache, block_table, lens, group_starts, prefix_table, prefix_lens,
                                              starts, k_scales, v_scales, scale, out)
         if done is not NotImplemented:
-            return done[0]
+            return _result(done, "w4_attn_decode_shared")[0]
     index = _device_index(q, "q")
     cache = _kv_cache(k_cache, v_cache, k_scales, v_scales, index)
     stride = _strides(block_table, "block_table", torch.int32, 2, index)[0]

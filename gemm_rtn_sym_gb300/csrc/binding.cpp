@@ -6,7 +6,9 @@
 // function here takes its Python counterpart's arguments, in its order, and
 // handles the usual case: the tensors are what they should be, on the current
 // device.  Anything else, and any call that the library refuses, it leaves
-// alone (NotImplemented) to the Python function, which says what is wrong.
+// alone (NotImplemented) to the Python function, which says what is wrong.  Any
+// other status (an int) is the end of the call: some of its kernels may run
+// already, and a second call would change pages and holders once more.
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/ops/empty.h>
@@ -111,6 +113,12 @@ struct Call {
     }
 };
 
+// What a call that did not work out returns.
+PyObject* failed(int status) {
+    if (status == W4_ERR_INVALID_ARG || status == W4_ERR_MISALIGNED || status == W4_ERR_UNSUPPORTED) Py_RETURN_NOTIMPLEMENTED;  // before any launch
+    return PyLong_FromLong(status);
+}
+
 // Outputs, in their order: the caller's, or new ones.
 struct Outputs {
     Call& call;
@@ -137,7 +145,7 @@ struct Outputs {
         return static_cast<V*>(t->data_ptr());
     }
     PyObject* done(int status) {
-        if (status != W4_OK) Py_RETURN_NOTIMPLEMENTED;
+        if (status != W4_OK) return failed(status);
         PyObject* const t = tuple;
         tuple = nullptr;
         return t;
@@ -328,7 +336,7 @@ PyObject* kv_copy(PyObject*, PyObject* const* args, Py_ssize_t n) {
         const Tensor* const copies = c.typed(2, kInt, 2);
         if (!c.ok || copies->size(0) != 3 || !copies->is_contiguous() || copies->size(1) > INT32_MAX) Py_RETURN_NOTIMPLEMENTED;
         const int status = run([&] { return w4_kv_copy(&cache, copies->const_data_ptr<int32_t>(), static_cast<int32_t>(copies->size(1)), c.stream); });
-        if (status != W4_OK) Py_RETURN_NOTIMPLEMENTED;
+        if (status != W4_OK) return failed(status);
         Py_RETURN_NONE;
     });
 }
