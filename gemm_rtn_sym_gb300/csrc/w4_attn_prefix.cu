@@ -16,9 +16,10 @@
 //
 // Warps 0 to 7 hold the rows, the next ones bring keys and values, the last one
 // issues the products.  A stage of the ring is the keys of tile i and the values
-// of tile i − 2: the tensor cores take one thread's products in their order, so
-// that the scores of tile i may go where the weights of tile i − 2 were as soon
-// as the products of those are issued.  Whole tiles come by TMA, a page (or 128
+// of tile i − 2.  The scores of tile i go where the weights of tile i − 2 were,
+// and are issued when the products of those are complete: the order in which
+// products are carried out is a promise for those of one shape into one
+// accumulator only.  Whole tiles come by TMA, a page (or 128
 // tokens of one) and 64 columns at a time, where page sizes divide a tile or
 // are multiples of it; an item's end and pages of other sizes come row by row by
 // cp.async.  (All rows by cp.async: 1 to 3 % longer.)
@@ -130,8 +131,9 @@ __global__ void __launch_bounds__(Shape<D, Q8>::kThreads, 1) attn_prefix_kernel(
     using S = Shape<D, Q8>;
     constexpr int TT = kTile, NS = S::kStages, kLoadWarps = S::kLoadWarps, kMmaWarp = S::kMmaWarp;
     extern __shared__ uint8_t smem_raw[];
-    // By the tile's group: its scores are there, its weights; all of an item's products are in O.
-    __shared__ __align__(8) uint64_t s_full[NS], s_empty[NS], s_scores[2], s_weights[2], s_values, s_queries;
+    // By the tile's group: its scores are there, its weights; a tile's weights have been used; all of an item's products
+    // are in O.
+    __shared__ __align__(8) uint64_t s_full[NS], s_empty[NS], s_scores[2], s_weights[2], s_used, s_values, s_queries;
     // Format 8, for four tiles: the tokens' key scales (times that of the scores) and value scales.  Where a tile's
     // keys find their stage free, the weights of four tiles before have been used.
     __shared__ __align__(8) uint64_t s_scaled[4];
@@ -152,6 +154,7 @@ __global__ void __launch_bounds__(Shape<D, Q8>::kThreads, 1) attn_prefix_kernel(
             mbar_init(smem_addr(&s_weights[i]), kRowThreads / 2);
         }
         for (int i = 0; i < 4; ++i) mbar_init(smem_addr(&s_scaled[i]), kLoadWarps * 32);
+        mbar_init(smem_addr(&s_used), 1);
         mbar_init(smem_addr(&s_values), 1);
         mbar_init(smem_addr(&s_queries), kRowThreads);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -173,12 +176,11 @@ __global__ void __launch_bounds__(Shape<D, Q8>::kThreads, 1) attn_prefix_kernel(
         // A factor below zero turns the queries' signs over.
         const uint32_t qk_idesc = idesc_bf16(TT) | (sp.flip ? 1u << 13 : 0u), pv_idesc = idesc_bf16(D) | 1u << 16;  // B (values) N-major
         Turn stage;
-        uint32_t summed[2] = {0, 0}, items = 0;  // tiles of each group so far
+        uint32_t summed[2] = {0, 0}, used = 0, items = 0;  // tiles of each group so far
         for (Item it; warp == kMmaWarp && walk.next(sp, it);) {
             const int tiles = tiles_of<TT>(it);
             wait_or_report_suspended(smem_addr(&s_queries), items++ & 1, alive, a.status);
-            // Stage i: the values of tile i − 2, then the keys of tile i, whose scores go where those weights are: those
-            // products are issued before, and the tensor cores take a thread's products in their order.
+            // Stage i: the values of tile i − 2, then the keys of tile i, whose scores go where those weights are.
             for (int i = 0; i < tiles + 2; ++i) {
                 const int w = i & 1;
                 wait_or_report_suspended(smem_addr(&s_full[stage.place]), stage.round, alive, a.status);
@@ -186,8 +188,8 @@ __global__ void __launch_bounds__(Shape<D, Q8>::kThreads, 1) attn_prefix_kernel(
                 fence_async_smem();  // the copies were made through the generic proxy
                 tc_fence_after();
                 const uint32_t keys = ring + stage.place * 2 * S::kHalf, vals = keys + S::kHalf;
-                if (elect_one()) {
-                    if (i >= 2) {
+                if (i >= 2) {
+                    if (elect_one()) {
                         // Sixteen tokens' weights: 8 columns of their upper halves, 16 columns further the lower ones.
                         const uint32_t to = tmem + kColO + w * D, weights = tmem + w * TT;
                         const uint32_t low = vals >> 4 | (TT * 128 >> 4) << 16;
@@ -197,7 +199,13 @@ __global__ void __launch_bounds__(Shape<D, Q8>::kThreads, 1) attn_prefix_kernel(
                             mma_bf16_tmem_a(to, weights + (ks >> 1) * 32 + (ks & 1) * 8, desc, pv_idesc, 1);
                             mma_bf16_tmem_a(to, weights + (ks >> 1) * 32 + (ks & 1) * 8 + 16, desc, pv_idesc, 1);
                         }
+                        if (i < tiles) mma_commit(smem_addr(&s_used));
                     }
+                    __syncwarp();
+                    if (i < tiles) wait_or_report_suspended(smem_addr(&s_used), used++ & 1, alive, a.status);
+                    tc_fence_after();
+                }
+                if (elect_one()) {
                     if (i < tiles) {
                         const uint32_t to = tmem + w * TT, q_low = q_smem >> 4 | 1u << 16, k_low = keys >> 4 | 1u << 16;
 #pragma unroll

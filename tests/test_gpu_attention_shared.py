@@ -416,3 +416,14 @@ def test_checks_of_the_binding(cuda_lib):
                                ("lens", kw["lens"].cpu(), TypeError), ("starts", kw["starts"][1:], ValueError)):
         with pytest.raises(error):
             w4.w4_attn_decode_shared(**{**kw, name: value})
+
+
+@pytest.mark.parametrize("format", [16, 8])
+@pytest.mark.parametrize("Hq,H,D", [(16, 1, 128), (16, 2, 64), (48, 2, 128)])
+def test_long_prefixes_of_many_rows_in_every_run(cuda_lib, Hq, H, D, format):
+    """Scores and weights of dozens of tiles take turns in tensor memory: the same bits each time, and the right ones."""
+    case = Case([(9000, members(*[3] * 9)), (4000, members(*[2] * 12)), (257, members(*[1] * 10))], Hq, H, D, 16, format=format, seed=D + Hq)
+    first = case.run()
+    case.check(first)
+    for _ in range(20):
+        assert torch.equal(case.run().view(torch.int16), first.view(torch.int16))
