@@ -38,7 +38,7 @@ W4_PATH_AUTO, W4_PATH_SMALL_M, W4_PATH_TENSOR = 0, 1, 2
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _lib = None
-_fast = None
+_fast = _fast_error = None
 _lock = threading.Lock()
 
 _i64, _i32, _vp, _sz = ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p, ctypes.c_size_t
@@ -144,8 +144,9 @@ def library_path() -> str:
 
 
 def load() -> ctypes.CDLL:
-    """Load libw4.so (built by gemm_rtn_sym_gb300.build) and the compiled module beside it; raises if absent."""
-    global _lib, _fast
+    """Load libw4.so (built by gemm_rtn_sym_gb300.build), raises if absent, and the compiled module beside it, whose calls
+    raise where it cannot be imported."""
+    global _lib, _fast, _fast_error
     with _lock:
         if _lib is None:
             path = library_path()
@@ -160,7 +161,7 @@ def load() -> ctypes.CDLL:
             try:
                 _fast = importlib.import_module("._binding", __name__)
             except ImportError as e:
-                raise RuntimeError(f"{_PKG}/_binding.so cannot be loaded: build it with `python -m gemm_rtn_sym_gb300.build`") from e
+                _fast_error = e
             _lib = lib
     return _lib
 
@@ -601,6 +602,8 @@ def _compiled():
     """The compiled module: its functions return NotImplemented where a call is not the usual one."""
     if _fast is None:
         load()
+        if _fast is None:
+            raise RuntimeError(f"{_PKG}/_binding.so cannot be loaded: build it with `python -m gemm_rtn_sym_gb300.build`") from _fast_error
     return _fast
 
 

@@ -2,12 +2,15 @@
 
 Each .cu file under csrc/ is compiled in parallel to an object under _build/,
 then linked into gemm_rtn_sym_gb300/libw4.so.  csrc/binding.cpp becomes the
-extension module gemm_rtn_sym_gb300/_binding.so, which calls the library.  IEEE division and no
+extension module gemm_rtn_sym_gb300/_binding.so, which calls the library; it is
+left out where torch is not there, as for a user of the C library alone
+(``python gemm_rtn_sym_gb300/build.py``).  IEEE division and no
 flush-to-zero are required by the quantiser, so no fast-math flags are used.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -48,6 +51,10 @@ def _compile(src: str, extra: list[str]) -> str:
     return obj
 
 
+def _have_torch() -> bool:
+    return importlib.util.find_spec("torch") is not None
+
+
 def _compile_binding() -> str:
     """Object of the extension module (host code against torch's headers)."""
     import torch
@@ -79,11 +86,12 @@ def _link_binding(obj: str) -> None:
 
 
 def build(verbose: bool = False, extra: list[str] | None = None) -> str:
-    """Compile and link libw4.so; returns its path."""
+    """Compile and link libw4.so and the extension module; returns the library's path.  The library is there also where
+    the module cannot be built, which raises."""
     os.makedirs(BUILD, exist_ok=True)
     srcs = sources()
     with cf.ThreadPoolExecutor(max_workers=min(12, len(srcs) + 1)) as ex:
-        binding = ex.submit(_compile_binding)
+        binding = ex.submit(_compile_binding) if _have_torch() else None
         objs = list(ex.map(lambda s: _compile(s, list(extra or [])), srcs))
     tmp = LIB + ".tmp"
     cmd = [nvcc()] + ARCH + ["-shared", "-cudart", "shared", "-Xlinker", "-soname=libw4.so", "-o", tmp] + objs
@@ -91,9 +99,10 @@ def build(verbose: bool = False, extra: list[str] | None = None) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    _link_binding(binding.result())
+    if binding is not None:
+        _link_binding(binding.result())
     if verbose:
-        print(f"built {LIB}")
+        print(f"built {LIB}" + ("" if binding is not None else " (no torch: without the extension module)"))
     return LIB
 
 
