@@ -12,6 +12,7 @@ from __future__ import annotations
 import concurrent.futures as cf
 import importlib.util
 import os
+import re
 import shutil
 import subprocess
 import sysconfig
@@ -42,13 +43,34 @@ def sources() -> list[str]:
     return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cu"))
 
 
-def _compile(src: str, extra: list[str]) -> str:
+def _compile(src: str, extra: list[str]) -> tuple[str, str]:
+    """The object of a source, and what the assembler says about its kernels."""
     obj = os.path.join(BUILD, os.path.basename(src)[:-3] + ".o")
-    cmd = [nvcc()] + NVCC_FLAGS + extra + ["-c", src, "-o", obj]
+    cmd = [nvcc()] + NVCC_FLAGS + extra + ["-Xptxas", "-v", "-c", src, "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"nvcc failed for {src}:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
-    return obj
+    return obj, r.stderr
+
+
+#: Kernels whose warps hand registers to one another, by their name in the object, and what a thread has to be launched with
+#: (kLaunchRegs beside them): with fewer, the warps that ask for more would wait for ever, so that the calls refuse to launch.
+SHARED_OUT = {"attn_prefix_kernelILi64ELb1E": 96, "attn_prefix_kernelILi128ELb1E": 96}
+
+
+def registers(text: str) -> dict[str, int]:
+    """Registers of each kernel in what the assembler says."""
+    found = re.findall(r"Compiling entry function '(\w+)'.*?Used (\d+) registers", text, re.S)
+    return {name: int(n) for name, n in found}
+
+
+def _check_registers(text: str) -> None:
+    have = registers(text)
+    for part, wanted in SHARED_OUT.items():
+        got = {n for name, n in have.items() if part in name}
+        if got - {wanted}:
+            raise RuntimeError(f"this compiler gives {part} {sorted(got)} registers instead of {wanted}: attention over shared "
+                               "prefixes in 8 bits will be refused (the library is there for all else)")
 
 
 def _have_torch() -> bool:
@@ -92,15 +114,19 @@ def build(verbose: bool = False, extra: list[str] | None = None) -> str:
     srcs = sources()
     with cf.ThreadPoolExecutor(max_workers=min(12, len(srcs) + 1)) as ex:
         binding = ex.submit(_compile_binding) if _have_torch() else None
-        objs = list(ex.map(lambda s: _compile(s, list(extra or [])), srcs))
+        made = list(ex.map(lambda s: _compile(s, list(extra or [])), srcs))
     tmp = LIB + ".tmp"
-    cmd = [nvcc()] + ARCH + ["-shared", "-cudart", "shared", "-Xlinker", "-soname=libw4.so", "-o", tmp] + objs
+    cmd = [nvcc()] + ARCH + ["-shared", "-cudart", "shared", "-Xlinker", "-soname=libw4.so", "-o", tmp] + [obj for obj, _ in made]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
     if binding is not None:
         _link_binding(binding.result())
+    said = "".join(text for _, text in made)
+    with open(os.path.join(BUILD, "kernels.txt"), "w") as f:
+        f.write(said)
+    _check_registers(said)
     if verbose:
         print(f"built {LIB}" + ("" if binding is not None else " (no torch: without the extension module)"))
     return LIB
