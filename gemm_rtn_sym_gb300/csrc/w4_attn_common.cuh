@@ -174,7 +174,7 @@ struct Cut {
 // `tiles`, for the rows from row0 on (of `rows`) of head h of request b.
 struct Item {
     int b, h, row0, rows;
-    int start, n, before;
+    int start, before;
     bool shared;     // the rows' sums over a shared prefix join
     int tok0, tok1;
     int tile0, tile1, tiles;
@@ -271,7 +271,6 @@ struct Walk {
             s.row0 = (line - s.h * rq.row_tiles) * ROWS;
             s.rows = rq.n * sp.G;
             s.start = rq.start;
-            s.n = rq.n;
             s.before = rq.before;
             s.shared = sp.pass() == kOwn && rq.low > 0;
             s.tiles = rq.tiles;

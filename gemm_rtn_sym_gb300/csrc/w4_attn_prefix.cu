@@ -478,8 +478,6 @@ __global__ void __launch_bounds__(Shape<D, Q8>::kThreads, 1) attn_prefix_kernel(
                 const float(*const scale)[Q8 ? TT : 4] = s_scale[Q8 ? buffer : 0];
                 // A tile's scores are read twice, 32 at a time in rolled loops: held in 128 registers in between, with all
                 // loops unrolled, they cost as much in instructions that the caches do not have (a fifth of all stalls).
-                // A tile's scores are read twice, 32 at a time in rolled loops: held in 128 registers in between, with all
-                // loops unrolled, they cost as much in instructions that the caches do not have (a fifth of all stalls).
                 auto hide = [&](uint32_t(&u)[32], int c) {  // (in a loop of its own: selects in every tile cost 7 %)
                     if (there < TT)
 #pragma unroll

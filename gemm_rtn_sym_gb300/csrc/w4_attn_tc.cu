@@ -535,7 +535,8 @@ __global__ void __launch_bounds__(Shape<D, Q8>::kThreads, 1) attn_tc_kernel(cons
             const Parts<kRows, D> parts(sp, walk, it, kFixed);
             const int k_own = static_cast<int>(blockIdx.x) - parts.first;
             float* const part = parts.at(k_own);
-            const bool leave = sp.pass() == kPrefixes && !whole;  // for the join, row by row
+            // For the join, row by row.  (Up to 128 values a head, prefixes have a kernel of their own.)
+            const bool leave = D > 128 && sp.pass() == kPrefixes && !whole;
             if (leave && live) {
                 reinterpret_cast<float2*>(part)[tid] = make_float2(m * unit, fminf(l, 3e38f));
                 if (k_own == 0)

@@ -427,3 +427,61 @@ def test_long_prefixes_of_many_rows_in_every_run(cuda_lib, Hq, H, D, format):
     case.check(first)
     for _ in range(20):
         assert torch.equal(case.run().view(torch.int16), first.view(torch.int16))
+
+
+@pytest.mark.parametrize("format", [16, 8])
+@pytest.mark.parametrize("Hq,H,D", [(8, 1, 128), (8, 1, 64), (16, 2, 256), (24, 2, 80)])
+@pytest.mark.parametrize("scale", [None, -0.3, 0.0, 1e-3])
+def test_scales_of_both_signs_and_zero_under_many_rows(cuda_lib, Hq, H, D, scale, format):
+    """The kernels of many rows: queries' signs turned over, every weight 1; whole tiles and an item's end."""
+    case = Case([(200, members(*[5] * 40)), (300, members(*[2, 9] * 20)), (128, members(*[3] * 40))], Hq, H, D, 16, format=format, seed=D)
+    case.check(case.run(scale=scale), scale=scale)
+
+
+@pytest.mark.parametrize("Hq,H", [(8, 2), (16, 1)])
+@pytest.mark.parametrize("starts", [[-5, 4, 4, 4, 4, 4], [0, 99, 99, 99, 99, 99], [9, 7, 5, 3, 1, 0], [3, 6, 0, 2, 2, 2], [5, 9, 0, 3, 3, 3],
+                                    [-2 ** 31, 2 ** 31 - 1, 0, 0, 0, 0], [2 ** 31 - 1] * 6, [-1] * 6])
+def test_group_starts_that_fall_or_pass_the_batch(cuda_lib, Hq, H, starts):
+    """Requests of one prefix whose tables have its pages, too: whichever of them stand in a group, and in which, the rows
+    are the same.  (No request stands in two groups here.)"""
+    case = Case([(64, members(5, 1, 30, 9, 2, 70, 1, 1, 16))], Hq, H, 128, 16, seed=18)
+    table = case.table.copy()
+    table[:, :4] = case.prefix_table[0, :4]
+    kw = dict(group_starts=gpu(starts), prefix_table=gpu(np.repeat(case.prefix_table, 5, 0)), prefix_lens=gpu([64] * 5), block_table=gpu(table))
+    case.check(case.run(**kw))
+    case.check(case.run(**kw, starts=None))
+
+
+def test_a_negative_prefix_length_is_none(cuda_lib):
+    case = Case(FEW, 8, 2, 128, 16, before=members(20), after=members(30), seed=12)
+    lens = case.prefix_lens.copy()
+    lens[0] = -3
+    out = case.run(status=w4.W4_ERR_INVALID_ARG, prefix_lens=gpu(lens))
+    case.check(out, rows=slice(0, 1))
+    case.check(out, rows=slice(int(case.starts[case.group_starts[1]]), None))
+
+
+@pytest.mark.parametrize("Hq,H", [(8, 2), (64, 1)])
+def test_what_the_stream_did_before_is_seen_by_every_kernel(cuda_lib, Hq, H):
+    """Tables, lengths, queries and pages that change right before each call."""
+    cases = [Case([(m, members(*own)) for m, own in groups], Hq, H, 128, 16, after=members(9), seed=40 + i)
+             for i, groups in enumerate([((100, (5, 30, 1)), (33, (2, 8))), ((130, (90, 2, 3)), (64, (1, 50)))])]
+    width, prefix_width = max(c.table.shape[1] for c in cases), max(c.prefix_table.shape[1] for c in cases)
+    for c in cases:
+        c.table = np.pad(c.table, ((0, 0), (0, width - c.table.shape[1])), constant_values=-1)
+        c.prefix_table = np.pad(c.prefix_table, ((0, 0), (0, prefix_width - c.prefix_table.shape[1])), constant_values=-1)
+    pages = max(c.k.shape[0] for c in cases)
+    kw = cases[0].args()
+    kw["k_cache"], kw["v_cache"] = (torch.zeros((pages, 16, H, 128), dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    args = [c.args() for c in cases]
+    torch.cuda.synchronize()
+    outs = []
+    for i in range(60):
+        for name, x in args[i % 2].items():
+            (kw[name][:x.shape[0]] if name.endswith("cache") else kw[name]).copy_(x)
+        outs.append(w4.w4_attn_decode_shared(**kw))
+    torch.cuda.synchronize()
+    assert w4.w4_last_device_status() == 0
+    for i, c in enumerate(cases):
+        c.check(outs[i])
+        assert all(torch.equal(x.view(torch.int16), outs[i].view(torch.int16)) for x in outs[i::2])
