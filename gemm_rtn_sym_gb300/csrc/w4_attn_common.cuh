@@ -70,10 +70,13 @@ __device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, 
 
 // The three kernels of a call with shared prefixes follow one another closely.  The first waits for what the stream did
 // before the call; each then lets the next one start as soon as there is room; the one over the requests' own tokens,
-// which needs nothing from the one before, ends after it, so that the join, which waits for its end, has both.
+// which needs nothing from the one before, ends after it, so that the join, which waits for its end, has both.  It begins
+// when every CTA of the first has seen the stream's work before the call end, and discards what its SM may hold from
+// before that (waiting by itself, it would wait for the first kernel, too).
 template <class SP>
 __device__ __forceinline__ void let_next_start(const SP& sp) {
     if (sp.pass() == kPrefixes) asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (sp.pass() == kOwn) asm volatile("fence.acq_rel.gpu;" ::: "memory");
     if (sp.pass() != kAlone) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 template <class SP>
