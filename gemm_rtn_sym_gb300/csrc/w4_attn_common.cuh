@@ -186,7 +186,12 @@ struct Item {
     __device__ __forceinline__ bool whole() const { return tile0 == 0 && tile1 == tiles; }
 };
 
-constexpr int kShort = 8;  // tiles of an item that is not worth cutting
+// Tiles of an item of a request's own tokens that is not worth cutting.  µs of the whole call behind a prefix of about 2000
+// tokens, cut and whole (requests × own tokens): one row each, 40 and 8 heads: 4 × 60 25 and 22, 16 × 250 30 and 28, 64 ×
+// 250 42 and 39; 8 and 1 heads, as few items as requests: 4 × 470 18.5 and 20.4, 16 × 470 19.7 and 22.0.  13 rows, 64 and
+// 8 heads: 1 × 1000 46 and 43, 16 × 1000 89 and 66, in 8 bits 93 and 80 (4 × 1000: 52 and 56); 8 and 1 heads: 4 × 470 31
+// and 26, in 8 bits 33 and 30.  (Half as many tiles: 4 × 500 in verify passes of 5 rows 44, whole 35.)
+constexpr int kShort = 8;
 
 // Walks the items of a CTA's piece.
 template <int TILE, int ROWS, int FIXED>

@@ -284,7 +284,12 @@ template <int THREADS, int LPR>
 cudaError_t append(const KvAppendArgs& a, const KvNorm& norm, const Axes& axes, bool q8, int64_t tokens, int sm_count, cudaStream_t stream) {
     const int per_cta = THREADS / LPR;
     auto slices = [&](int rows) { return (rows + per_cta - 1) / per_cta; };
-    const int y = a.T * 2 >= sm_count ? 1 : slices(a.q_heads) + 2 * slices(a.kv_heads);
+    // Few tokens: a CTA for every THREADS / LPR rows of a kind, as long as all of them fit the SMs at once.  A CTA for a
+    // token and for a slice, in bf16: 64 and 8 heads of 128, 6 slices, 4.9 and 2.7 µs for 1 token, 5.1 and 4.1 for 100,
+    // 5.1 and 5.2 for 112, 5.8 and 7.7 for 208; 40 and 8 heads, 5 slices, 4.7 and 4.0 for 120, 4.8 and 5.0 for 128; 16
+    // and 4 of 256, 4 slices, 4.6 and 4.2 for 151, 5.2 and 5.7 for 208.  Into a cache in 8 bits: 64 and 8 heads 6.6 and
+    // 4.8 for 100, 6.8 and 6.9 for 151; 16 and 4 of 256 6.3 and 4.9 for 151.
+    const int all = slices(a.q_heads) + 2 * slices(a.kv_heads), y = a.T * 2 >= sm_count && a.T * all > tokens ? 1 : all;
     // A few CTAs may start before the kernel ahead of them ends (3.3 to 3.0 µs for one token, one call after another);
     // many would take its SMs' room (5.5 to 7.0 for 208 tokens, 87 to 91 for 16001).
     const dim3 grid(static_cast<unsigned>(std::min(a.T, tokens)), static_cast<unsigned>(y));

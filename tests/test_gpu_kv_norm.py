@@ -243,3 +243,11 @@ def test_no_tokens_and_two_streams_at_once(cuda_lib):
     for c, out in zip(cases, outs):
         c.check(out[0])
         assert all(torch.equal(x.view(torch.int16), out[0].view(torch.int16)) for x in out)
+
+
+@pytest.mark.parametrize("Hq,H,D", [(64, 8, 128), (40, 8, 128), (16, 4, 256), (9, 1, 64)])
+@pytest.mark.parametrize("format", [16, 8])
+def test_both_sides_of_the_shares_of_a_token(cuda_lib, Hq, H, D, format):
+    """A CTA for some of a token's rows, or for all of them."""
+    for T in (76, 101, 102, 121, 122, 151, 152, 153):
+        check(Case(T, Hq, H, D, 64, format=format, seed=T))
