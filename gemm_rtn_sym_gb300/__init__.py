@@ -883,7 +883,7 @@ def w4_attn_decode_shared(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
     [groups + 1]) begin with the prefix_lens[g] tokens (int32 [groups]) in the pages prefix_table[g] (int32 [groups,
     width]), which are read once for all of them; what follows is in their own pages, at the places that block_table has
     for it.  lens counts the prefix.  Requests outside of the groups, and those whose new tokens do not all lie behind the
-    prefix, are attended over their own pages."""
+    prefix, are attended over their own pages.  Few requests behind a short prefix are faster by w4_attn_decode (w4.h)."""
     if workspace is None:
         done = _compiled().attn_decode_shared(q, k_cache, v_cache, block_table, lens, group_starts, prefix_table, prefix_lens,
                                              starts, k_scales, v_scales, scale, out)

@@ -768,12 +768,12 @@ bool many_rows(int32_t B, int64_t T, int G, int32_t kv_heads, int D, bool q8) {
 // The same for a pass over prefixes, whose parts a kernel of its own joins, so that
 // few heads are no reason to stay here.  µs of the whole call, here and there,
 // one prefix of 16385 tokens, 8 key-value heads (4 of 256):
-// head_dim 64, 16 rows: 22 and 29; 24: 32 and 29.  128, 16 rows: 26 and 30; 24: 39
-// and 31.  256, 16 rows: 38 and 40; 24: 51 and 41.  Format 8: 64, 64 rows: 33 and
-// 36; 96: 40 and 37.  128, 32 rows: 36 and 42; 40: 42 and 42; 48: 42 and 42; 64: 45
-// and 43.  256, 48 rows: 50 and 51; 64: 53 and 53; 96: 64 and 56.  Twelve prefixes
-// of 1500 tokens: 128, 16 rows: 27 and 34; 24: 37 and 35; 256, 16 rows: 31 and 37;
-// 24: 41 and 37; format 8, 128, 40 rows: 51 and 52; 48: 55 and 53; 64: 65 and 60.
+// head_dim 64, 16 rows: 23 and 30; 24: 33 and 30.  128, 16 rows: 27 and 32; 24: 39
+// and 32.  256, 16 rows: 39 and 40; 24: 52 and 41.  Format 8: 64, 64 rows: 34 and
+// 36; 96: 41 and 37.  128, 32 rows: 36 and 42; 40: 42 and 42; 48: 42 and 42; 64: 45
+// and 43.  256, 48 rows: 50 and 51; 64: 53 and 52; 96: 64 and 55.  Twelve prefixes
+// of 1500 tokens: 128, 16 rows: 28 and 35; 24: 37 and 36; 256, 16 rows: 33 and 37;
+// 24: 42 and 37; format 8, 128, 40 rows: 51 and 53; 48: 54 and 54; 64: 65 and 62.
 // (From 17 rows on, two warps share a stage here, and format 8 takes 16 at a time.)
 bool many_rows_behind(int32_t groups, int64_t T, int G, int D, bool q8) {
     const int limit = !q8 ? 16 : D == 64 ? 80 : D == 128 ? 40 : 56;

@@ -34,17 +34,20 @@
 // pieces over the SMs; parts of items stay where they are, for the join.
 //
 // Measured.  64 rows of 40 query and 8 key-value heads of 128 behind 16385
-// tokens, 67 MB: 40 µs of 58 for all three kernels; 13 are the bytes, 11 the
+// tokens, 67 MB: 42 µs of 60 for all three kernels; 13 are the bytes, 11 the
 // products at the measured rates, and 20 the products as they are (each weight
-// twice, 320 rows to a head as 384).  Tensor pipe 42 % active, issue 39 %: a tile
-// is 2800 cycles, of which the products are 1536, and two groups of rows do not
+// twice, 320 rows to a head as 384).  Tensor pipe 38 % active, issue 37 %: a tile
+// is 3000 cycles, of which the products are 1536, and two groups of rows do not
 // hide the rest from one another: their exponentials, roundings and maxima, 640
-// instructions to a row at the least, and the hand-overs between the three
-// kinds of warps.  Twelve prefixes of 300 to 8192 tokens in format 8, 40 rows of 64
-// heads behind each: 68 of 131 µs, bound by instructions (issue 54 %), the codes'
-// turn to bf16 among them.
+// instructions to a row at the least, the hand-overs between the three
+// kinds of warps, and the pause between a tile's second product and the scores
+// that go over its weights (3 µs of the 60; 17 of 121 for 128 rows of 64 heads,
+// whose tensor cores have no other pause).  Twelve prefixes of 300 to 8192 tokens
+// in format 8, 20 to 40 rows of 64 heads behind each: 70 of 134 µs, bound by
+// instructions (issue 53 %), the codes' turn to bf16 among them.
 // No faster: the next scores on their way while these are weighed (58.9 for
-// 59.4), the joins' work by the CTA that ends an item (25 to 40 µs more).
+// 59.4), the joins' work by the CTA that ends an item (25 to 40 µs more), polling
+// instead of a suspended wait for the second product (62.1 for 61.4).
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -710,8 +713,8 @@ constexpr int kJoinWarps = 4, kJoinBatch = 8;
 // One warp to a row: its own tokens' sums, and those of its prefix, from
 // wherever they are, on one reference, into its output.  (The CTA that
 // finishes an item last, as in the other kernels, would read its parts alone:
-// 19 of 66 KB where one prefix's 8 heads are shared by 152 SMs.)  2 of the 58
-// µs and 9 of the 131 above: 2560 rows of 128, each in about 7 parts.
+// 19 of 66 KB where one prefix's 8 heads are shared by 152 SMs.)  2 of the 60
+// µs and 9 of the 134 above: 2560 rows of 128, each in about 7 parts.
 template <int V>  // float4 of a lane: head_dim ≤ 128 · V
 __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const __grid_constant__ JoinArgs a) {
     asm volatile("griddepcontrol.wait;" ::: "memory");

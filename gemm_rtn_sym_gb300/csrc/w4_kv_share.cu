@@ -34,7 +34,7 @@ __global__ void __launch_bounds__(kThreads) kv_release_kernel(KvPagesArgs a) {
 // the entries that are let go of, not the table's size: the pages' kernel
 // leaves their number, clears the words of their pages and a mark for each.
 // 600 of 1000 requests of up to 4097 tokens that end: this kernel 9 µs, the
-// pages' 11, the next 8, 24 in all, since they overlap.  A step of 1000 requests
+// pages' 11, the next 8, 22 in all, since they overlap.  A step of 1000 requests
 // in which none ends: 11 µs, with tables of 260 entries and of 8192.
 __global__ void __launch_bounds__(kThreads) kv_let_go_kernel(KvPagesArgs a) {
     __shared__ long long s_first[kThreads], s_warp[33];
